@@ -88,7 +88,7 @@ def draw(rng):
     case = {"op": op, "experts": experts, "top_k": min(experts, rng.randint(1, 8)),
             "spread": rng.choice([0.0, 0.5, 1.0]), "pad": rng.choice([0, 0, 33]), "tokens": _log(rng, 1, 4096)}
     if op == "geglu":
-        return {**case, "n": 8 * _log(rng, 8, 88), "k": k, "tanh": rng.random() < 0.5,
+        return {**case, "n": 16 * _log(rng, 4, 44), "k": k, "tanh": rng.random() < 0.5,
                 "keep": rng.random() < 0.5, "dtype": dtype}
     n, k = (n, 8 * _log(rng, 8, 176)) if rng.random() < 0.5 else (8 * _log(rng, 8, 176), k)
     case = {**case, "n": n, "k": k, "dtype": dtype, "out": rng.choice([dtype, "f32"])}

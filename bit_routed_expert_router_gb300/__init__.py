@@ -21,6 +21,7 @@ MOE_FILE_DIRECT = 1
 MOE_STAGING_HOST, MOE_STAGING_DEVICE, MOE_STAGING_FUSED = 0, 1, 2
 MOE_CACHE_LRU, MOE_CACHE_LFU = 0, 1
 MOE_GELU_ERF, MOE_GELU_TANH = 0, 1
+MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
 HOOK_FAIL_NEXT_COPY, HOOK_WAIT_LIMIT_US, HOOK_PDL, HOOK_PERSISTENT, HOOK_TIMELINE, HOOK_FREE_BYTES = 1, 2, 3, 4, 5, 6
 HOOK_PREFILL_TC = 7
 HOOK_CLUSTER = 9
@@ -100,6 +101,18 @@ _SIGS = {
     "moe_test_hook": (C.c_int, [C.c_void_p, C.c_int, C.c_int64]),
     "moe_route_noalloc": (C.c_int, [C.POINTER(MoeConfig), C.c_void_p, C.c_void_p, C.c_int, C.c_void_p,
                                     C.c_void_p, C.c_void_p, C.c_void_p]),
+    "moe_grouped_mm": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
+                                 C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p]),
+    "moe_grouped_wgrad": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_void_p,
+                                    C.c_int, C.c_int, C.c_int, C.c_void_p, C.c_int, C.c_void_p]),
+    "moe_grouped_geglu": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
+                                    C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p]),
+    "moe_geglu_grad": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_int,
+                                 C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p]),
+    "moe_lora_mm": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int, C.c_int, C.c_void_p,
+                              C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p,
+                              C.c_uint64, C.c_void_p]),
+    "moe_grouped_sync": (C.c_int, [C.c_void_p]),
     "moe_profile": (C.c_int, [C.c_void_p, C.c_int]),
     "moe_get_profile": (C.c_int, [C.c_void_p, C.POINTER(MoeKernelTime), C.c_int]),
     "moe_status_string": (C.c_char_p, [C.c_int]),
@@ -291,6 +304,122 @@ def moe_route_noalloc(cfg: MoeConfig, router_w, h, B: int, logit_bias, ids, gate
     """Routing without any device allocation (see include/moe.h); every buffer is the caller's."""
     return lib().moe_route_noalloc(C.byref(cfg), _ptr(router_w), _ptr(h), B, _ptr(logit_bias), _ptr(ids),
                                    _ptr(gates), _stream(stream))
+
+
+# ---------------------------------------------------------------- 16-bit operators (no context)
+#
+# Sizes, strides and types come from the tensors.  Tensors that do not fit together (shape, type, device, a last
+# dimension that is not contiguous) return MOE_EINVAL like the library's own checks.  The call runs on the tensors'
+# device, on `stream` or that device's current stream.
+
+_DTYPE = None   # torch dtype -> MOE_BF16 / MOE_F16 / MOE_F32
+
+
+def _dtype(t) -> int:
+    global _DTYPE
+    if _DTYPE is None:
+        import torch
+        _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+    return _DTYPE.get(t.dtype, -1)
+
+
+def _rows(t, cols: int, device) -> bool:
+    """A matrix of `cols` contiguous values a row on `device`."""
+    return t.dim() == 2 and t.shape[1] == cols and t.stride(1) == 1 and t.device == device
+
+
+def _ld(t) -> int:
+    # the row stride of a single row says nothing
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _whole(t, dtype: str, device, *shape) -> bool:
+    """A contiguous tensor of this shape and type on `device`."""
+    return tuple(t.shape) == shape and str(t.dtype) == dtype and t.is_contiguous() and t.device == device
+
+
+def _call(fn, device, stream, *args) -> int:
+    import torch
+    if device.type != "cuda":
+        return MOE_EINVAL
+    if device.index == torch.cuda.current_device():
+        return fn(*args, _stream(stream))
+    with torch.cuda.device(device):
+        return fn(*args, _stream(stream))
+
+
+def moe_grouped_mm(x, offsets, w, y, transpose: bool = False, stream=None) -> int:
+    """y[r] = w[e] x[r] (or w[e]^T x[r]) for the rows of each expert; w [E, n, k], offsets int32 [E + 1]."""
+    if w.dim() != 3 or x.dim() != 2 or y.dim() != 2 or not w.is_contiguous():
+        return MOE_EINVAL
+    (E, n, k), dev = w.shape, w.device
+    into, out = (n, k) if transpose else (k, n)
+    if not (_rows(x, into, dev) and _rows(y, out, dev) and y.shape[0] == x.shape[0] and x.dtype == w.dtype and
+            _whole(offsets, "torch.int32", dev, E + 1)):
+        return MOE_EINVAL
+    return _call(lib().moe_grouped_mm, dev, stream, _dtype(x), int(transpose), _ptr(x), _ld(x), x.shape[0],
+                 _ptr(offsets), E, _ptr(w), n, k, _ptr(y), _ld(y), _dtype(y))
+
+
+def moe_grouped_wgrad(dy, x, offsets, dw, stream=None) -> int:
+    """dw[e] = sum over the rows of each expert of dy[r] x[r]^T; dw [E, n, k], all of it written."""
+    if dw.dim() != 3 or x.dim() != 2 or dy.dim() != 2 or not dw.is_contiguous():
+        return MOE_EINVAL
+    (E, n, k), dev = dw.shape, dw.device
+    if not (_rows(x, k, dev) and _rows(dy, n, dev) and dy.shape[0] == x.shape[0] and x.dtype == dy.dtype and
+            _whole(offsets, "torch.int32", dev, E + 1)):
+        return MOE_EINVAL
+    return _call(lib().moe_grouped_wgrad, dev, stream, _dtype(x), _ptr(dy), _ld(dy), _ptr(x), _ld(x), x.shape[0],
+                 _ptr(offsets), E, n, k, _ptr(dw), _dtype(dw))
+
+
+def moe_grouped_geglu(x, offsets, w, a, h=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
+    """a[r] = GELU(g) u, [g, u] = w[e] x[r]; w [E, 2 f, k]; h [m, 2 f] (optional) receives [g, u]."""
+    if w.dim() != 3 or x.dim() != 2 or a.dim() != 2 or not w.is_contiguous() or w.shape[1] % 2:
+        return MOE_EINVAL
+    (E, n, k), dev = w.shape, w.device
+    if not (_rows(x, k, dev) and _rows(a, n // 2, dev) and a.shape[0] == x.shape[0] and
+            x.dtype == w.dtype == a.dtype and _whole(offsets, "torch.int32", dev, E + 1)):
+        return MOE_EINVAL
+    if h is not None and not (_rows(h, n, dev) and h.shape[0] == x.shape[0] and h.dtype == x.dtype):
+        return MOE_EINVAL
+    return _call(lib().moe_grouped_geglu, dev, stream, _dtype(x), gelu_variant, _ptr(x), _ld(x), x.shape[0],
+                 _ptr(offsets), E, _ptr(w), n // 2, k, _ptr(a), _ld(a), _ptr(h), 0 if h is None else _ld(h))
+
+
+def moe_geglu_grad(h, da, dh, n_rows=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
+    """dh = [da u GELU'(g), da GELU(g)] for h = [g, u]; n_rows: int32 tensor of one value, the rows to do."""
+    if da.dim() != 2:
+        return MOE_EINVAL
+    (m, f), dev = da.shape, da.device
+    if not (_rows(h, 2 * f, dev) and _rows(da, f, dev) and _rows(dh, 2 * f, dev) and h.shape[0] == dh.shape[0] == m and
+            h.dtype == da.dtype == dh.dtype):
+        return MOE_EINVAL
+    if n_rows is not None and not (n_rows.numel() == 1 and str(n_rows.dtype) == "torch.int32" and n_rows.device == dev):
+        return MOE_EINVAL
+    return _call(lib().moe_geglu_grad, dev, stream, _dtype(h), gelu_variant, _ptr(h), _ld(h), _ptr(da), _ld(da), m, f,
+                 _ptr(n_rows), _ptr(dh), _ld(dh))
+
+
+def moe_lora_mm(x, w, ids, a, b, scale, y, workspace, stream=None) -> int:
+    """y[t] = w x[t] + scale[i] b[i] (a[i] x[t]), i = ids[t]; w [n, k], a [N, rank, k], b [N, n, rank], scale fp32
+    [N], ids int32 [t] (-1: no adapter), workspace: a tensor of at least 4 * t * rank bytes."""
+    if w.dim() != 2 or x.dim() != 2 or y.dim() != 2 or a.dim() != 3 or not w.is_contiguous():
+        return MOE_EINVAL
+    (n, k), (N, rank, _), dev, dt = w.shape, a.shape, w.device, str(w.dtype)
+    t = x.shape[0]
+    if not (_rows(x, k, dev) and _rows(y, n, dev) and y.shape[0] == t and x.dtype == w.dtype == y.dtype and
+            _whole(a, dt, dev, N, rank, k) and _whole(b, dt, dev, N, n, rank) and
+            _whole(scale, "torch.float32", dev, N) and _whole(ids, "torch.int32", dev, t) and
+            workspace.is_contiguous() and workspace.device == dev):
+        return MOE_EINVAL
+    return _call(lib().moe_lora_mm, dev, stream, _dtype(x), _ptr(x), _ld(x), t, _ptr(w), n, k, _ptr(ids), _ptr(a),
+                 _ptr(b), _ptr(scale), N, rank, _ptr(y), _ld(y), _ptr(workspace),
+                 workspace.numel() * workspace.element_size())
+
+
+def moe_grouped_sync(stream=None) -> int:
+    return lib().moe_grouped_sync(_stream(stream))
 
 
 def moe_profile(ctx, enable: bool) -> int:

@@ -1,0 +1,210 @@
+// Kernels around the 16-bit grouped products: the gradient of the gated
+// product, and the down half of the per-request adapters.
+#include <algorithm>
+
+#include "common.cuh"
+#include "grouped.h"
+
+namespace moe {
+
+namespace {
+
+template <bool kBf16>
+__device__ __forceinline__ float2 to_floats(uint32_t v) {
+  if (kBf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  return make_float2(half_lo(v), half_hi(v));
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t to_pair(float a, float b) {
+  if (kBf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// GELU(g) and its derivative.  With P the normal distribution function and p
+// its density: g P(g) and P(g) + g p(g).  The tanh form: with t = tanh(s),
+// s = c (g + 0.044715 g^3): g (1 + t) / 2 and (1 + t) / 2 + g (1 - t^2) s' / 2.
+template <int kGelu>
+__device__ __forceinline__ float2 gelu_and_slope(float g) {
+  if (kGelu == 1) {
+    const float c = 0.7978845608028654f, g2 = g * g;
+    const float t = tanhf(c * g * (1.f + 0.044715f * g2));
+    const float half = 0.5f + 0.5f * t;
+    return make_float2(g * half, half + 0.5f * g * (1.f - t * t) * c * (1.f + 0.134145f * g2));
+  }
+  const float half = 0.5f + 0.5f * erff(g * 0.7071067811865476f);
+  return make_float2(g * half, half + g * 0.3989422804014327f * expf(-0.5f * g * g));
+}
+
+// dh = [da u GELU'(g), da GELU(g)] for h = [g, u]: 16-byte loads and stores,
+// eight features a thread.  Memory-bound: 10 bytes in and out per feature and
+// about 30 operations.
+template <bool kBf16, int kGelu>
+__global__ void __launch_bounds__(256) k_gated_grad(const uint16_t* h, long long ldh,
+                                                    const uint16_t* da, long long ldda, uint16_t* dh,
+                                                    long long lddh, int m, int f, const int32_t* n_rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int rows = n_rows ? min(*n_rows, m) : m, words = f / 8;
+  const long long total = static_cast<long long>(rows) * words;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long r = i / words;
+    const int c = static_cast<int>(i - r * words) * 8;
+    const uint4 gv = *reinterpret_cast<const uint4*>(h + r * ldh + c);
+    const uint4 uv = *reinterpret_cast<const uint4*>(h + r * ldh + f + c);
+    const uint4 dv = *reinterpret_cast<const uint4*>(da + r * ldda + c);
+    const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w}, d[4] = {dv.x, dv.y, dv.z, dv.w};
+    uint32_t dg[4], du[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const float2 gg = to_floats<kBf16>(g[w]), uu = to_floats<kBf16>(u[w]), dd = to_floats<kBf16>(d[w]);
+      const float2 a = gelu_and_slope<kGelu>(gg.x), b = gelu_and_slope<kGelu>(gg.y);
+      dg[w] = to_pair<kBf16>(dd.x * uu.x * a.y, dd.y * uu.y * b.y);
+      du[w] = to_pair<kBf16>(dd.x * a.x, dd.y * b.x);
+    }
+    *reinterpret_cast<uint4*>(dh + r * lddh + c) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+    *reinterpret_cast<uint4*>(dh + r * lddh + f + c) = make_uint4(du[0], du[1], du[2], du[3]);
+  }
+}
+
+// ------------------------------------------------------------------ adapters: u = s A x
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+constexpr int kDownWarps = 8, kDownRows = 32;
+
+// A CTA: 16 rank rows x 32 rows of x, for the distinct adapters number z,
+// z + gridDim.z, ... of those rows.  The warps split the reduction (64 values
+// at a time) and add through shared memory in warp order.  A lane's fragments
+// are 16 consecutive values of a row, loaded as two 16-byte words; the order
+// of k inside a 64 is the same in both operands, which is all a product needs.
+// Each adapter's products are written for its own rows only.
+template <bool kBf16>
+__global__ void __launch_bounds__(32 * kDownWarps)
+    k_adapter_down(const uint16_t* __restrict__ x, long long ldx, int t, const uint16_t* __restrict__ a,
+                   const float* __restrict__ scale, const int32_t* __restrict__ ids, int n_adapters, int rank, int k,
+                   uint16_t* u) {
+  __shared__ float red[kDownWarps][16][kDownRows + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+  const int row0 = blockIdx.x * kDownRows, r0 = blockIdx.y * 16;
+  int id = -1;
+  if (row0 + lane < t) {
+    id = ids[row0 + lane];
+    if (id < 0 || id >= n_adapters) id = -1;
+  }
+  uint32_t left = __ballot_sync(0xFFFFFFFFu, id >= 0);
+  for (int nth = 0; left; ++nth) {
+    const int ad = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
+    const uint32_t same = __ballot_sync(0xFFFFFFFFu, id == ad);
+    left &= ~same;
+    if (nth % static_cast<int>(gridDim.z) != static_cast<int>(blockIdx.z)) continue;
+    const uint16_t* arow = a + (static_cast<size_t>(ad) * rank + r0 + g) * k;
+    const bool has0 = r0 + g < rank, has1 = r0 + 8 + g < rank;
+    float acc[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
+    for (int k0 = 64 * warp; k0 < k; k0 += 64 * kDownWarps) {
+      uint32_t w0[8], w1[8];
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int at = k0 + 16 * t4 + 8 * hh;
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const uint4 p = has0 && at < k ? __ldg(reinterpret_cast<const uint4*>(arow + at)) : z;
+        const uint4 q = has1 && at < k ? __ldg(reinterpret_cast<const uint4*>(arow + 8 * static_cast<size_t>(k) + at)) : z;
+        w0[4 * hh] = p.x, w0[4 * hh + 1] = p.y, w0[4 * hh + 2] = p.z, w0[4 * hh + 3] = p.w;
+        w1[4 * hh] = q.x, w1[4 * hh + 1] = q.y, w1[4 * hh + 2] = q.z, w1[4 * hh + 3] = q.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!((same >> (8 * j)) & 0xFFu)) continue;
+        const int row = min(row0 + 8 * j + g, t - 1);   // rows of others: their columns are not used
+        uint32_t b[8];
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const int at = k0 + 16 * t4 + 8 * hh;
+          const uint4 p = at < k ? __ldg(reinterpret_cast<const uint4*>(x + row * ldx + at)) : make_uint4(0, 0, 0, 0);
+          b[4 * hh] = p.x, b[4 * hh + 1] = p.y, b[4 * hh + 2] = p.z, b[4 * hh + 3] = p.w;
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint32_t af[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
+          if (kBf16)
+            mma_bf16(acc[j], af, b[2 * s], b[2 * s + 1]);
+          else
+            mma_f16(acc[j], af, b[2 * s], b[2 * s + 1]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[warp][g + 8 * (i >> 1)][8 * j + 2 * t4 + (i & 1)] = acc[j][i];
+    __syncthreads();
+    const float sc = scale[ad];
+    for (int i = tid; i < 16 * kDownRows; i += 32 * kDownWarps) {
+      const int r = i & 15, c = i >> 4;
+      if (!((same >> c) & 1u) || r0 + r >= rank) continue;
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDownWarps; ++w) v += red[w][r][c];
+      v *= sc;
+      // bf16 value and bf16 remainder: 16 significant bits, so u's rounding is far below the output's
+      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+      uint16_t* dst = u + static_cast<size_t>(row0 + c) * 2 * rank + r0 + r;
+      dst[0] = __bfloat16_as_ushort(hi);
+      dst[rank] = float_to_bf16_bits(isfinite(v) ? v - __bfloat162float(hi) : 0.f);
+    }
+    __syncthreads();
+  }
+}
+
+template <typename K, typename... A>
+bool launch_pdl(K kernel, dim3 grid, int threads, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+}  // namespace
+
+bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const void* da, long long ldda, void* dh,
+                       long long lddh, int m, int f, const int32_t* n_rows, cudaStream_t s) {
+  const long long words = static_cast<long long>(m) * (f / 8);
+  const dim3 grid(static_cast<unsigned>(std::min<long long>((words + 255) / 256, 1 << 20)));
+  const auto kernel = bf16 ? (gelu == 1 ? k_gated_grad<true, 1> : k_gated_grad<true, 0>)
+                           : (gelu == 1 ? k_gated_grad<false, 1> : k_gated_grad<false, 0>);
+  return launch_pdl(kernel, grid, 256, s, static_cast<const uint16_t*>(h), ldh, static_cast<const uint16_t*>(da), ldda,
+                    static_cast<uint16_t*>(dh), lddh, m, f, n_rows);
+}
+
+bool launch_adapter_down(bool bf16, const void* x, long long ldx, int t, const void* a, const float* scale,
+                         const int32_t* ids, int n_adapters, int rank, int k, uint16_t* u, cudaStream_t s) {
+  const int blocks = (t + kDownRows - 1) / kDownRows, mt = (rank + 15) / 16;
+  // CTAs that share a block's distinct adapters: up to one each while the grid is small
+  const int shares = std::max(1, std::min({std::min(t, kDownRows), n_adapters, 1024 / std::max(1, blocks * mt)}));
+  const auto kernel = bf16 ? k_adapter_down<true> : k_adapter_down<false>;
+  return launch_pdl(kernel, dim3(blocks, mt, shares), 32 * kDownWarps, s, static_cast<const uint16_t*>(x), ldx, t,
+                    static_cast<const uint16_t*>(a), scale, ids, n_adapters, rank, k, u);
+}
+
+}  // namespace moe

@@ -1,0 +1,822 @@
+// 16-bit products grouped by expert with ragged sizes, on tcgen05.
+//
+//   forward     y[r, n]     = sum_k W[e][n, k] x[r, k]          rows r of expert e
+//   gradient    dx[r, k]    = sum_n W[e][n, k] dy[r, n]
+//   weights     dW[e][n, k] = sum_{r of e} dy[r, n] x[r, k]
+//
+// bf16 or fp16 operands, fp32 accumulators in tensor memory, one rounding at
+// the store.  The weights' features are the MMA's M side and the rows its N
+// side, so a ragged group costs its rows rounded up to 32 (16 in the small
+// kernel) instead of to a tile of 128 or 256: an expert's rows are cut into
+// equal parts of at most 256 and each part's N is set per instruction.
+//
+// k_grouped: persistent, pairs of CTAs (one CTA per SM).  A pair computes 256
+// features x up to 256 rows with cta_group::2 MMAs; each CTA stages its 128
+// features and half of the rows, so a staged byte feeds twice the products
+// that it would in a lone CTA.  Two accumulators of 256 columns: the epilogue
+// of one tile overlaps the next tile's products.  Roles: warp 0 loads, warp 1
+// of the even CTA issues, warps 2-5 store, warp 6 (weights only) clears the
+// rows behind a group's end in the last stage.
+//
+// k_grouped_small: few rows per expert (decode).  The weights are read once
+// and nothing else matters, so a CTA takes 128 features x up to 64 rows, the
+// reduction split over a cluster whose CTAs add their accumulators through
+// distributed shared memory in rank order (no atomics, no workspace).
+#include <algorithm>
+#include <type_traits>
+
+#include "grouped.h"
+#include "tc16.cuh"
+#include "tensor_map.h"
+
+namespace moe {
+
+namespace {
+
+using namespace tc16;
+
+__device__ uint32_t g_grouped_err;
+
+constexpr int kMaxE = 1024;
+constexpr int kStages = 6;
+constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
+constexpr int kHalf = 16384;
+constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 32 bytes: multiples of 16, and the
+constexpr int kEpiPitch16 = 48;      // 16-byte words of eight rows hit all 32 banks
+constexpr int kAccCols = 256;
+
+struct BigSmem {
+  uint8_t stage[kStages][kStageBytes];
+  uint8_t epi[4][2][16 * kEpiPitch16];
+  uint64_t full[kStages], empty[kStages], tail[kStages];
+  uint64_t acc_full[2], acc_empty[2], drain;
+  uint32_t tmem;
+  volatile int abort;
+  int off[kMaxE + 1];    // clamped to [0, m]
+  int tiles[kMaxE + 1];  // column tiles before each expert
+};
+static_assert(sizeof(BigSmem) + 1024 <= 227 * 1024, "one CTA per SM");
+static_assert(16 * kEpiPitch16 >= 8 * kEpiPitch && kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0, "staged rows");
+
+__device__ __forceinline__ uint32_t* err_word() { return &g_grouped_err; }
+
+// Bounded wait that also ends when another role of the CTA gave up.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  if (try_wait_cluster(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (try_wait_cluster(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > kSpinLimitCycles) {
+      *abort = 1;
+      atomicOr(err_word(), ERR_WAIT_TIMEOUT);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float gelu(float v, int variant) {
+  if (variant == 1) return 0.5f * v * (1.f + tanhf(0.7978845608028654f * (v + 0.044715f * v * v * v)));
+  return 0.5f * v * (1.f + erff(v * 0.7071067811865476f));
+}
+
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
+  if (bf16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void store_out(void* y, long long i, float v, int f32, int bf16) {
+  if (f32)
+    static_cast<float*>(y)[i] = v;
+  else if (bf16)
+    static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(y)[i] = __float2half_rn(v);
+}
+
+// Row range of expert e: inside [0, m] whatever the offsets hold.
+__device__ __forceinline__ int clamp_off(int v, int m) { return min(max(v, 0), m); }
+
+struct Tile {
+  int e, f0;         // expert, first feature
+  int c0, cols, n;   // first column (a row of x, or of this expert's gradient), columns, columns rounded up for the MMA
+  int row0, rows;    // GM_WGRAD: the expert's rows
+  int steps;         // k64 steps
+};
+
+// Tile t of the launch in the order expert, feature tile, column tile: the
+// pairs that run together share an expert's rows and weights through L2.
+template <int kMode, int kFeat>
+__device__ __forceinline__ bool tile_at(const BigSmem& S, const GmParams& p, int t, int& e, Tile& T) {
+  const int ft = (p.feat + kFeat - 1) / kFeat;
+  if constexpr (kMode == GM_WGRAD) {
+    const int ct = (p.cols + 255) / 256, per = ft * ct;
+    e = t / per;
+    if (e >= p.E) return false;
+    const int rem = t - e * per, c = rem / ft;
+    T.e = e;
+    T.f0 = (rem - c * ft) * kFeat;
+    T.c0 = c * 256;
+    T.cols = min(256, p.cols - T.c0);
+    T.n = 256;
+    T.row0 = S.off[e];
+    T.rows = max(S.off[e + 1] - T.row0, 0);
+    T.steps = (T.rows + 63) / 64;
+    return true;
+  } else {
+    while (e < p.E && S.tiles[e + 1] * ft <= t) ++e;
+    if (e >= p.E) return false;
+    const int nt = S.tiles[e + 1] - S.tiles[e], rem = t - S.tiles[e] * ft, f = rem / nt, c = rem - f * nt;
+    const int lo = S.off[e], rows = S.off[e + 1] - lo;
+    const int width = ((rows + nt - 1) / nt + 31) & ~31;
+    T.e = e;
+    T.f0 = f * kFeat;
+    T.c0 = lo + c * width;
+    T.cols = min(width, lo + rows - T.c0);
+    T.n = (T.cols + 31) & ~31;
+    T.row0 = T.rows = 0;
+    T.steps = (p.red + 63) / 64;
+    return true;
+  }
+}
+
+// ------------------------------------------------------------------ adapter term of the epilogue
+
+// Two fp16 values as the exact sum of two bf16 pairs.
+__device__ __forceinline__ void split_f16x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
+  // an fp16 value has 11 significant bits: bf16 hi (8) + lo (the other 3) is exact
+  const float a = half_lo(v), b = half_hi(v);
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack16(a - __low2float(h), b - __high2float(h), 1);
+}
+
+// v[mb][4j + i] += (B[id] u)[feature][row] for the 32 columns at c0.  The
+// fragments of the accumulator are those of an m16n8k16 product, so the term
+// is one: B's rows are its A operand, u (two bf16 halves, about 16 bits) its B
+// operand.  Each distinct adapter of the 32 rows is one pass whose result is
+// added to its own rows only, so nothing that one request's adapter holds
+// reaches another's output.
+__device__ __forceinline__ void add_adapters(float (&v)[2][16], const GmParams& p, int row0, int cols, int f0, int lane) {
+  const int g = lane >> 2, t4 = lane & 3;
+  int id = -1;
+  if (lane < cols) {
+    id = p.ids[row0 + lane];
+    if (id < 0 || id >= p.n_adapters) id = -1;
+  }
+  uint32_t left = __ballot_sync(0xFFFFFFFFu, id >= 0);
+  while (left) {
+    const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
+    const uint32_t same = __ballot_sync(0xFFFFFFFFu, id == a);
+    left &= ~same;
+    float d[2][16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) d[0][i] = d[1][i] = 0.f;
+    const uint16_t* b = p.b + static_cast<size_t>(a) * p.feat * p.rank;
+    for (int k = 0; k < p.rank; k += 16) {
+      const bool upper = k + 8 < p.rank;   // a rank of 8 mod 16 ends in half a step
+      uint32_t af[2][4];
+#pragma unroll
+      for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int f = min(f0 + 16 * mb + 8 * r + g, p.feat - 1);   // rows past the end are never stored
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(b + static_cast<size_t>(f) * p.rank + k + 2 * t4);
+          af[mb][r] = __ldg(src);
+          af[mb][2 + r] = upper ? __ldg(src + 4) : 0u;
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (!((same >> (8 * j)) & 0xFFu)) continue;
+        const int row = row0 + min(8 * j + g, cols - 1);
+        const uint16_t* u = p.u + static_cast<size_t>(row) * 2 * p.rank + k + 2 * t4;
+        const uint32_t* uh = reinterpret_cast<const uint32_t*>(u);
+        const uint32_t* ul = reinterpret_cast<const uint32_t*>(u + p.rank);
+        const uint32_t h0 = __ldcg(uh), h1 = upper ? __ldcg(uh + 4) : 0u;
+        const uint32_t l0 = __ldcg(ul), l1 = upper ? __ldcg(ul + 4) : 0u;
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb) {
+          float c[4] = {d[mb][4 * j], d[mb][4 * j + 1], d[mb][4 * j + 2], d[mb][4 * j + 3]};
+          if (p.bf16) {
+            mma_bf16(c, af[mb], h0, h1);
+            mma_bf16(c, af[mb], l0, l1);
+          } else {
+            uint32_t bh[4], bl[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) split_f16x2(af[mb][i], bh[i], bl[i]);
+            mma_bf16(c, bh, h0, h1);
+            mma_bf16(c, bh, l0, l1);
+            mma_bf16(c, bl, h0, h1);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[mb][4 * j + i] = c[i];
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if ((same >> (8 * j + 2 * t4 + (i & 1))) & 1u) {
+          v[0][4 * j + i] += d[0][4 * j + i];
+          v[1][4 * j + i] += d[1][4 * j + i];
+        }
+  }
+}
+
+// ------------------------------------------------------------------ the persistent kernel
+
+// 8 columns x 32 features through shared memory, then one 16-byte store per
+// lane: 64 contiguous bytes of each column.
+__device__ __forceinline__ void store_8x32(uint32_t buf, const float (&v)[2][16], int j, int bf16, uint16_t* out,
+                                           long long ld, int cols, int feats, int lane) {
+  __syncwarp();   // the previous reads of this buffer are done
+  stmatrix4_trans(buf + (lane & 7) * kEpiPitch + (lane >> 3) * 16, pack16(v[0][4 * j], v[0][4 * j + 1], bf16),
+                  pack16(v[0][4 * j + 2], v[0][4 * j + 3], bf16), pack16(v[1][4 * j], v[1][4 * j + 1], bf16),
+                  pack16(v[1][4 * j + 2], v[1][4 * j + 3], bf16));
+  __syncwarp();
+  const int c = lane >> 2, f = 8 * (lane & 3);
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "r"(buf + c * kEpiPitch + (lane & 3) * 16)
+               : "memory");
+  if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+}
+
+// 16 columns x 16 features (fragments j and j + 1 of one 16-row block).
+__device__ __forceinline__ void store_16x16(uint32_t buf, const float (&v)[16], int j, int bf16, uint16_t* out,
+                                            long long ld, int cols, int feats, int lane) {
+  __syncwarp();
+  const int blk = lane >> 3;   // blocks: (fragment j, features 0-7), (j, 8-15), (j + 1, 0-7), (j + 1, 8-15)
+  stmatrix4_trans(buf + ((blk >> 1) * 8 + (lane & 7)) * (kEpiPitch16) + (blk & 1) * 16,
+                  pack16(v[4 * j], v[4 * j + 1], bf16), pack16(v[4 * j + 2], v[4 * j + 3], bf16),
+                  pack16(v[4 * j + 4], v[4 * j + 5], bf16), pack16(v[4 * j + 6], v[4 * j + 7], bf16));
+  __syncwarp();
+  const int c = lane >> 1, f = 8 * (lane & 1);
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "r"(buf + c * kEpiPitch16 + (lane & 1) * 16)
+               : "memory");
+  if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+}
+
+template <int kMode, int kEpi>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
+    k_grouped(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, GmParams p) {
+  constexpr bool kTa = kMode != GM_FWD, kTb = kMode == GM_WGRAD;
+  constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;   // features of a pair's tile
+  extern __shared__ uint8_t smem_raw[];
+  BigSmem& S = *reinterpret_cast<BigSmem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+
+  if (tid == 0) {
+    prefetch_map(&map_a);
+    prefetch_map(&map_b);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&S.full[i], kMode == GM_WGRAD ? 2 : 1);
+      mbar_init(&S.empty[i], 1);
+      mbar_init(&S.tail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.acc_full[i], 1);
+      mbar_init(&S.acc_empty[i], 8);
+    }
+    mbar_init(&S.drain, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
+  if (kEpi != GM_ADAPT) pdl_wait();   // adapters: only their u rows come from the previous kernel
+  pdl_trigger();
+  for (int e = tid; e <= p.E; e += blockDim.x)
+    S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
+  __syncthreads();
+  if (kMode != GM_WGRAD && warp == 0) {
+    int base = 0;
+    if (lane == 0) S.tiles[0] = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int c = e < p.E ? (max(S.off[e + 1] - S.off[e], 0) + 255) / 256 : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, c, d);
+        if (lane >= d) c += o;
+      }
+      if (e < p.E) S.tiles[e + 1] = base + c;
+      base += __shfl_sync(0xFFFFFFFFu, c, 31);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers are initialised
+  fence_after();
+  const uint32_t tmem = S.tmem;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t lead_full = map_rank(smem_u32(S.full), 0);
+      uint32_t it = 0;
+      int e = 0;
+      Tile T;
+      for (int t = first; !S.abort && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+        const int half = T.n / 2;
+        const uint32_t bytes = kHalf + half * 128;
+        for (int ks = 0; ks < T.steps; ++ks, ++it) {
+          const int s = it % kStages;
+          if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
+          uint32_t bar = lead_full + 8 * s;
+          if (kMode == GM_WGRAD) {
+            if (ks == T.steps - 1 && (T.rows & 15)) {   // warp 6 sees these bytes first
+              bar = smem_u32(&S.tail[s]);
+              mbar_arrive_expect_tx(&S.tail[s], bytes);
+            } else {
+              arrive_expect_cluster(bar, bytes);
+            }
+          } else if (rank == 0) {
+            mbar_arrive_expect_tx(&S.full[s], 2 * bytes);
+          }
+          const uint32_t a = smem_u32(S.stage[s]), b = a + kHalf;
+          if (kMode == GM_WGRAD) {
+            const int row = T.row0 + 64 * ks;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              load_2d<true>(a + 8192 * i, &map_a, T.f0 + 128 * rank + 64 * i, row, bar);
+              load_2d<true>(b + 8192 * i, &map_b, T.c0 + 128 * rank + 64 * i, row, bar);
+            }
+          } else {
+            if (kEpi == GM_GATED) {
+              load_5d<true>(a, &map_a, 64 * ks, 0, 0, (T.f0 + 64 * static_cast<int>(rank)) / 16, T.e, bar);
+            } else if (kMode == GM_FWD) {
+              load_3d<true>(a, &map_a, 64 * ks, T.f0 + 128 * rank, T.e, bar);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                load_3d<true>(a + 8192 * i, &map_a, T.f0 + 128 * rank + 64 * i, 64 * ks, T.e, bar);
+            }
+            for (int i = 0; i < half; i += 16)
+              load_2d<true>(b + 128 * i, &map_b, 64 * ks, T.c0 + rank * half + i, bar);
+          }
+        }
+      }
+      if (S.abort && rank == 0)   // copies already issued land before the pair leaves
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+          mbar_wait_bounded(&S.full[i % kStages], (i / kStages) & 1, err_word());
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      uint32_t it = 0, count = 0;
+      int e = 0;
+      bool ok = true;
+      Tile T;
+      for (int t = first; ok && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+        if (T.steps == 0) continue;
+        const int buf = count & 1;
+        ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort);
+        fence_after();
+        const uint32_t d = tmem + buf * kAccCols, idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb);
+        const int red = kMode == GM_WGRAD ? T.rows : p.red;
+        for (int ks = 0; ok && ks < T.steps; ++ks, ++it) {
+          const int s = it % kStages;
+          if (!(ok = wait_bar(&S.full[s], (it / kStages) & 1, &S.abort))) break;
+          fence_after();
+          const uint32_t a = smem_u32(S.stage[s]);
+          const uint64_t da = tile_desc<kTa>(a), db = tile_desc<kTb>(a + kHalf);
+          const int nk = (min(64, red - 64 * ks) + 15) / 16;
+          for (int kk = 0; kk < nk; ++kk)
+            mma<true>(d, da + kk * kStep16<kTa>, db + kk * kStep16<kTb>, idesc, (ks | kk) != 0);
+          commit_pair(&S.empty[s], 3);
+        }
+        if (ok) commit_pair(&S.acc_full[buf], 3);
+        ++count;
+      }
+      if (!ok) {   // the products in flight read shared memory: wait for them
+        commit_pair(&S.drain, 1);
+        mbar_wait_bounded(&S.drain, 0, err_word());
+      }
+    }
+  } else if (warp < 6) {
+    const int q = warp & 3;   // the tensor-memory lanes this warp may read
+    const uint32_t buf0 = smem_u32(S.epi[q][0]), buf1 = smem_u32(S.epi[q][1]);
+    const uint32_t lead_empty = map_rank(smem_u32(S.acc_empty), 0);
+    uint32_t count = 0;
+    int e = 0;
+    Tile T;
+    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+      // first feature of this warp's 32 lanes (GM_GATED: 16 gate and 16 up lanes of 16 features)
+      const int f0 = T.f0 + (kEpi == GM_GATED ? 64 * rank + 16 * q : 128 * rank + 32 * q);
+      const int feats = p.feat - f0;
+      const int buf = count & 1;
+      if (T.steps && !wait_bar(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
+      fence_after();
+      const long long out0 =
+          (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
+      for (int c0 = 0; c0 < T.cols; c0 += 32) {
+        float v[2][16];
+        if (T.steps) {
+          ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
+        }
+        const int cols = T.cols - c0;
+        if (kEpi == GM_ADAPT) {
+          if (c0 == 0) pdl_wait();
+          add_adapters(v, p, T.c0 + c0, min(cols, 32), f0, lane);
+        }
+        if (feats <= 0) continue;   // the warp's features end before this tile does
+        if (kEpi == GM_GATED) {
+          uint16_t* y = static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy;
+          if (p.h) {
+            uint16_t* h = static_cast<uint16_t*>(p.h) + static_cast<long long>(T.c0 + c0) * p.ldh + f0;
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              if (8 * j >= cols) break;
+              store_16x16(buf0, v[0], j, p.bf16, h + 8 * j * p.ldh, p.ldh, cols - 8 * j, feats, lane);
+              store_16x16(buf1, v[1], j, p.bf16, h + p.feat + 8 * j * p.ldh, p.ldh, cols - 8 * j, feats, lane);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[0][i] = gelu(v[0][i], p.gelu) * v[1][i];
+#pragma unroll
+          for (int j = 0; j < 4; j += 2) {
+            if (8 * j >= cols) break;
+            store_16x16(j ? buf1 : buf0, v[0], j, p.bf16, y + 8 * j * p.ldy, p.ldy, cols - 8 * j, feats, lane);
+          }
+        } else if (p.out_f32) {
+          float* y = static_cast<float*>(p.y) + out0 + c0 * p.ldy;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+#pragma unroll
+              for (int mb = 0; mb < 2; ++mb) {
+                const int f = 16 * mb + 8 * (i >> 1) + (lane >> 2);
+                if (c < cols && f < feats) y[c * p.ldy + f] = v[mb][4 * j + i];
+              }
+            }
+        } else {
+          uint16_t* y = static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (8 * j >= cols) break;
+            store_8x32((j & 1) ? buf1 : buf0, v, j, p.bf16, y + 8 * j * p.ldy, p.ldy, cols - 8 * j, feats, lane);
+          }
+        }
+      }
+      if (T.steps) {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
+        ++count;
+      }
+    }
+  } else if (kMode == GM_WGRAD) {
+    // rows behind the group's end in its last stage belong to another expert (or to nobody, and may hold
+    // anything): cleared in both operands, up to the end of the last k16 step that is issued
+    const uint32_t lead_full = map_rank(smem_u32(S.full), 0);
+    uint32_t it = 0, phases = 0;
+    int e = 0;
+    Tile T;
+    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+      it += T.steps;
+      if (!(T.rows & 15)) continue;
+      const int s = (it - 1) % kStages, lo = ((T.rows - 1) & 63) + 1, hi = (lo + 15) & ~15;
+      if (!wait_bar(&S.tail[s], (phases >> s) & 1, &S.abort)) break;
+      phases ^= 1u << s;
+      for (int i = lane; i < (hi - lo) * 32; i += 32) {   // four blocks of 64 x 128 bytes, eight 16-byte words a row
+        const int blk = (i & 31) >> 3, word = i & 7, row = lo + (i >> 5);
+        *reinterpret_cast<uint4*>(S.stage[s] + 8192 * blk + 128 * row + 16 * word) = make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(lead_full + 8 * s);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  cluster_sync();   // no CTA leaves while the other may still arrive on its barriers or read its stages
+  fence_after();
+  if (warp == 1) tmem_free<true>(tmem, 2 * kAccCols);
+}
+
+// ------------------------------------------------------------------ few rows per expert
+
+constexpr int kSmallCols = 64;                   // most columns of a tile
+constexpr int kSmallRing = 73728;                // 3 CTAs per SM: 4 stages of 16 columns, 3 of 64
+constexpr int kSmallPitch = 132;                 // floats between reduced columns
+static_assert(kSmallCols * kSmallPitch * 4 <= kSmallRing, "the reduction reuses the ring");
+
+template <int kMode, int kEpi>
+__global__ void __launch_bounds__(192)
+    k_grouped_small(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, GmParams p,
+                    int split) {
+  constexpr bool kTa = kMode == GM_DGRAD;
+  constexpr int kFeat = kEpi == GM_GATED ? 64 : 128;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[8], empty[8], acc_full;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ int s_tile[4];   // expert, first row, rows
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank()), f0 = blockIdx.x / split * kFeat;
+
+  if (kEpi != GM_ADAPT) pdl_wait();   // adapters: nothing before the u rows comes from the previous kernel
+  pdl_trigger();
+  if (warp == 0) {
+    // column tile blockIdx.y: an expert's rows in equal parts of at most kSmallCols
+    int base = 0, found = 0;
+    for (int e0 = 0; e0 < p.E && !found; e0 += 32) {
+      const int e = e0 + lane;
+      int lo = 0, hi = 0;
+      if (e < p.E) {
+        lo = p.offsets ? clamp_off(p.offsets[e], p.m) : 0;
+        hi = p.offsets ? clamp_off(p.offsets[e + 1], p.m) : p.m;
+      }
+      const int rows = max(hi - lo, 0), nt = (rows + kSmallCols - 1) / kSmallCols;
+      int c = nt;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, c, d);
+        if (lane >= d) c += o;
+      }
+      const int at = static_cast<int>(blockIdx.y) - (base + c - nt);
+      const bool mine = at >= 0 && at < nt;
+      if (mine) {
+        const int width = ((rows + nt - 1) / nt + 15) & ~15;
+        s_tile[0] = e;
+        s_tile[1] = lo + at * width;
+        s_tile[2] = min(width, rows - at * width);
+      }
+      found = __any_sync(0xFFFFFFFFu, mine);
+      base += __shfl_sync(0xFFFFFFFFu, c, 31);
+    }
+    if (lane == 0) {
+      if (!found) s_tile[2] = 0;
+      s_abort = 0;
+      for (int i = 0; i < 8; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      mbar_init(&acc_full, 1);
+      fence_mbar_init();
+      prefetch_map(&map_a);
+      prefetch_map(&map_b);
+    }
+  } else if (warp == 1) {
+    tmem_alloc<false>(&s_tmem, kSmallCols);
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  const int expert = s_tile[0], row0 = s_tile[1], rows = s_tile[2];
+  if (rows <= 0) {   // no such tile: the same for every CTA of the cluster
+    if (warp == 1) tmem_free<false>(tmem, kSmallCols);
+    return;
+  }
+  const int n = (rows + 15) & ~15;
+  const int bytes = kHalf + n * 128, stages = min(8, kSmallRing / bytes);
+  const int all = (p.red + 63) / 64, k0 = all * rank / split, steps = all * (rank + 1) / split - k0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int ks = 0;
+      for (; ks < steps; ++ks) {
+        const int s = ks % stages;
+        if (!wait_bar(&empty[s], ((ks / stages) & 1) ^ 1, &s_abort)) break;
+        const uint32_t a = smem_u32(ring) + s * bytes, bar = smem_u32(&full[s]);
+        mbar_arrive_expect_tx(&full[s], bytes);
+        const int k = 64 * (k0 + ks);
+        if (kEpi == GM_GATED) {
+          load_5d<false>(a, &map_a, k, 0, 0, f0 / 16, expert, bar);
+        } else if (kMode == GM_FWD) {
+          load_3d<false>(a, &map_a, k, f0, expert, bar);
+        } else {
+          load_3d<false>(a, &map_a, f0, k, expert, bar);
+          load_3d<false>(a + 8192, &map_a, f0 + 64, k, expert, bar);
+        }
+        for (int i = 0; i < n; i += 16) load_2d<false>(a + kHalf + 128 * i, &map_b, k, row0 + i, bar);
+      }
+      if (s_abort)
+        for (int i = max(0, ks - stages); i < ks; ++i)
+          mbar_wait_bounded(&full[i % stages], (i / stages) & 1, err_word());
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = instr_desc(p.bf16, 128, n, kTa, false);
+      for (int ks = 0; ks < steps; ++ks) {
+        const int s = ks % stages;
+        if (!wait_bar(&full[s], (ks / stages) & 1, &s_abort)) break;
+        fence_after();
+        const uint32_t a = smem_u32(ring) + s * bytes;
+        const uint64_t da = tile_desc<kTa>(a), db = tile_desc<false>(a + kHalf);
+        const int nk = (min(64, p.red - 64 * (k0 + ks)) + 15) / 16;
+        for (int kk = 0; kk < nk; ++kk)
+          mma<false>(tmem, da + kk * kStep16<kTa>, db + kk * kStep16<false>, idesc, (ks | kk) != 0);
+        commit(&empty[s]);
+      }
+      commit(&acc_full);   // after every product above, also when a wait ran out
+    }
+  }
+  __syncwarp();
+  float* part = reinterpret_cast<float*>(ring);   // [column][kSmallPitch], after every product has read the ring
+  bool ok = true;
+  if (warp >= 2) {
+    ok = mbar_wait_bounded(&acc_full, 0, err_word()) && !s_abort;
+    fence_after();
+    const int q = warp & 3;
+    if (ok)
+      for (int c = 0; c < n; c += 16) {
+        float v[16];
+        ld_cols16(tmem + c + (static_cast<uint32_t>(32 * q) << 16), v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) part[(c + i) * kSmallPitch + 32 * q + lane] = v[i];
+      }
+    fence_before();
+  }
+  if (split > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (warp >= 2 && ok) {
+    if (kEpi == GM_ADAPT) pdl_wait();
+    const int i = tid - 64, fi = kEpi == GM_GATED ? i & 63 : i, f = f0 + fi;
+    const int step = kEpi == GM_GATED ? 2 * split : split;
+    const uint32_t base = smem_u32(part);
+    for (int c = kEpi == GM_GATED ? 2 * rank + (i >> 6) : rank; c < rows; c += step) {
+      const int lane_of = kEpi == GM_GATED ? (fi >> 4) * 32 + (fi & 15) : fi;
+      float v = 0.f, up = 0.f;
+      for (int r = 0; r < split; ++r) {
+        const uint32_t at = map_rank(base, r) + (c * kSmallPitch + lane_of) * 4;
+        v += ld_cluster_f32(at);
+        if (kEpi == GM_GATED) up += ld_cluster_f32(at + 64);
+      }
+      if (f >= p.feat) continue;
+      const long long row = row0 + c;
+      if (kEpi == GM_GATED) {
+        if (p.h) {
+          store_out(p.h, row * p.ldh + f, v, 0, p.bf16);
+          store_out(p.h, row * p.ldh + p.feat + f, up, 0, p.bf16);
+        }
+        v = gelu(v, p.gelu) * up;
+      }
+      if (kEpi == GM_ADAPT) {
+        const int id = p.ids[row];
+        if (id >= 0 && id < p.n_adapters) {
+          const uint4* b = reinterpret_cast<const uint4*>(p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank);
+          const uint4* u = reinterpret_cast<const uint4*>(p.u + static_cast<size_t>(row) * 2 * p.rank);
+          float d = 0.f;
+          for (int j = 0; j < p.rank / 8; ++j) {
+            const uint4 bv = __ldg(b + j), hi = __ldcg(u + j), lo = __ldcg(u + p.rank / 8 + j);
+            const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w},
+                           lw[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const float b0 = p.bf16 ? __uint_as_float(bw[w] << 16) : half_lo(bw[w]);
+              const float b1 = p.bf16 ? __uint_as_float(bw[w] & 0xFFFF0000u) : half_hi(bw[w]);
+              d += b0 * (__uint_as_float(hw[w] << 16) + __uint_as_float(lw[w] << 16));
+              d += b1 * (__uint_as_float(hw[w] & 0xFFFF0000u) + __uint_as_float(lw[w] & 0xFFFF0000u));
+            }
+          }
+          v += d;
+        }
+      }
+      store_out(p.y, row * p.ldy + f, v, p.out_f32, p.bf16);
+    }
+  }
+  if (split > 1)
+    cluster_sync();   // the others may still read this CTA's part
+  else
+    __syncthreads();
+  if (warp == 1) tmem_free<false>(tmem, kSmallCols);
+}
+
+// ------------------------------------------------------------------ launches
+
+struct DeviceInfo {
+  int sms = 0;
+};
+
+bool device_info(DeviceInfo* d) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(&d->sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+// rows [rows][cols] of 16-bit values, `ld` apart, in boxes of box_rows x 64
+bool map_rows(CUtensorMap* m, const void* base, int cols, int rows, long long ld, int box_rows, bool bf16) {
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(ld) * 2};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  return encode_tiles(m, base, 2, dim, stride, box, bf16);
+}
+
+bool map_weights(CUtensorMap* m, const void* base, int E, int n, int k, int box_rows, bool bf16) {
+  const cuuint64_t dim[3] = {static_cast<cuuint64_t>(k), static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(E)};
+  const cuuint64_t stride[2] = {static_cast<cuuint64_t>(k) * 2, static_cast<cuuint64_t>(k) * n * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 1};
+  return encode_tiles(m, base, 3, dim, stride, box, bf16);
+}
+
+// [E][2][f][k] seen as blocks of 16 features: a box is 64 k x 16 gate and the
+// same 16 up rows of four blocks, so each warp's 32 accumulator lanes hold
+// both halves of 16 features.
+bool map_gated(CUtensorMap* m, const void* base, int E, int f, int k, bool bf16) {
+  const cuuint64_t row = static_cast<cuuint64_t>(k) * 2;
+  const cuuint64_t dim[5] = {static_cast<cuuint64_t>(k), 16, 2, static_cast<cuuint64_t>(f / 16),
+                             static_cast<cuuint64_t>(E)};
+  const cuuint64_t stride[4] = {row, row * f, row * 16, row * 2 * f};
+  const cuuint32_t box[5] = {64, 16, 2, 4, 1};
+  return encode_tiles(m, base, 5, dim, stride, box, bf16);
+}
+
+template <typename K>
+bool launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const CUtensorMap& a,
+            const CUtensorMap& b, const GmParams& p, int split) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return false;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = split ? 2 : 1;   // the persistent kernel's cluster is part of its type
+  if constexpr (std::is_same_v<K, void (*)(CUtensorMap, CUtensorMap, GmParams)>)
+    return cudaLaunchKernelEx(&cfg, kernel, a, b, p) == cudaSuccess;
+  else
+    return cudaLaunchKernelEx(&cfg, kernel, a, b, p, split) == cudaSuccess;
+}
+
+template <int kMode, int kEpi>
+bool launch_big(const CUtensorMap& a, const CUtensorMap& b, const GmParams& p, int sms, cudaStream_t s) {
+  constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;
+  const long long ft = (p.feat + kFeat - 1) / kFeat;
+  const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
+                                         : std::min(p.E, p.m) + static_cast<long long>(p.m) / 256;
+  const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
+  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), 224, sizeof(BigSmem) + 1024, 2, s, a, b, p, 0);
+}
+
+template <int kMode, int kEpi>
+bool launch_small(const CUtensorMap& a, const CUtensorMap& b, const GmParams& p, int sms, cudaStream_t s) {
+  constexpr int kFeat = kEpi == GM_GATED ? 64 : 128;
+  const int ft = (p.feat + kFeat - 1) / kFeat, tiles = std::min(p.E, p.m) + p.m / kSmallCols;
+  const int steps = (p.red + 63) / 64;
+  int split = 1;   // CTAs that share a tile's reduction: enough for three CTAs on every SM, at least two k64 steps each
+  while (split < 8 && 2 * split * ft * static_cast<long long>(tiles) <= 3 * sms && 4 * split <= steps) split *= 2;
+  return launch(k_grouped_small<kMode, kEpi>, dim3(ft * split, tiles), 192, kSmallRing + 1024, split, s, a, b, p, split);
+}
+
+// Few rows per expert: the small kernel.  Its tiles re-read an expert's weights (from L2) for every 64 rows.
+bool few_rows(const GmParams& p) { return p.m <= (p.offsets ? 4 * static_cast<long long>(p.E) : 64); }
+
+}  // namespace
+
+bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, cudaStream_t s) {
+  DeviceInfo d;
+  if (!device_info(&d)) return false;
+  CUtensorMap a, b;
+  if (mode == GM_WGRAD) {
+    if (!map_rows(&a, o.x, o.k, p.m, o.ldx, 64, p.bf16) || !map_rows(&b, o.w, o.n, p.m, o.ldw, 64, p.bf16)) return false;
+    return launch_big<GM_WGRAD, GM_PLAIN>(a, b, p, d.sms, s);
+  }
+  if (!map_rows(&b, o.x, mode == GM_FWD ? o.k : o.n, p.m, o.ldx, 16, p.bf16)) return false;
+  if (epi == GM_GATED ? !map_gated(&a, o.w, p.E, p.feat, o.k, p.bf16)
+                      : !map_weights(&a, o.w, p.E, o.n, o.k, mode == GM_FWD ? 128 : 64, p.bf16))
+    return false;
+  const bool small = few_rows(p);
+  if (mode == GM_DGRAD)
+    return small ? launch_small<GM_DGRAD, GM_PLAIN>(a, b, p, d.sms, s) : launch_big<GM_DGRAD, GM_PLAIN>(a, b, p, d.sms, s);
+  if (epi == GM_GATED)
+    return small ? launch_small<GM_FWD, GM_GATED>(a, b, p, d.sms, s) : launch_big<GM_FWD, GM_GATED>(a, b, p, d.sms, s);
+  if (epi == GM_ADAPT)
+    return small ? launch_small<GM_FWD, GM_ADAPT>(a, b, p, d.sms, s) : launch_big<GM_FWD, GM_ADAPT>(a, b, p, d.sms, s);
+  return small ? launch_small<GM_FWD, GM_PLAIN>(a, b, p, d.sms, s) : launch_big<GM_FWD, GM_PLAIN>(a, b, p, d.sms, s);
+}
+
+bool grouped_error(cudaStream_t s, uint32_t* err) {
+  const uint32_t zero = 0;
+  if (cudaStreamSynchronize(s) != cudaSuccess) return false;
+  if (cudaMemcpyFromSymbol(err, g_grouped_err, sizeof(*err)) != cudaSuccess) return false;
+  return *err == 0 || cudaMemcpyToSymbol(g_grouped_err, &zero, sizeof(zero)) == cudaSuccess;
+}
+
+}  // namespace moe

@@ -26,11 +26,11 @@
 
 #include "expert_file.h"
 
-#include <cudaTypedefs.h>
 
 #include "internal.h"
 #include "kernels.h"
 #include "staging.h"
+#include "tensor_map.h"
 
 using namespace moe;
 
@@ -458,22 +458,6 @@ moe_status check_ready(moe_ctx* ctx, int l0, int l1) {
   for (int l = l0; l < l1; ++l)
     if (!ctx->L[l].ready) return fail(ctx, MOE_ESTATE, "layer %d is not initialised", l);
   return MOE_OK;
-}
-
-// cuTensorMapEncodeTiled, looked up through the runtime so that the library
-// does not link libcuda itself (it loads on machines without a driver).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
-    cudaDriverEntryPointQueryResult q{};
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-            cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || !fn)
-      return nullptr;
-    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  }
-  return encode;
 }
 
 // 3-D tensor map over the down regions of n_mat matrices seen as 32-bit words:

@@ -72,6 +72,7 @@ enum { MOE_FILE_DIRECT = 1 };   /* moe_set_expert_file flag: read misses with O_
 enum { MOE_STAGING_HOST = 0, MOE_STAGING_DEVICE = 1, MOE_STAGING_FUSED = 2 };   /* moe_set_staging modes */
 enum { MOE_CACHE_LRU = 0, MOE_CACHE_LFU = 1 };
 enum { MOE_GELU_ERF = 0, MOE_GELU_TANH = 1 };
+enum { MOE_BF16 = 0, MOE_F16 = 1, MOE_F32 = 2 };   /* value types of the 16-bit operators */
 
 /* Model dimensions.  Constraints (checked by moe_create): d, f and f_shared
  * are multiples of 64; group == 64; 1 <= top_k <= n_experts <= 256;
@@ -426,6 +427,81 @@ int64_t moe_shared_bytes(const moe_config *cfg);
 
 moe_status moe_route_noalloc(const moe_config *cfg, const uint16_t *router_w, const void *h, int B,
                              const float *logit_bias, int32_t *ids, float *gates, void *stream);
+
+/* ---- 16-bit operators over rows grouped by expert, and per-request adapters ----
+ *
+ * For experts kept in bf16 or fp16 (before quantisation, or in layers left
+ * unquantised) and for training them.  They take no context: every buffer is
+ * the caller's device memory on the current CUDA device, nothing is allocated
+ * or kept between calls, and the calls return without synchronising (they can
+ * be captured).  Common rules:
+ *   dtype        MOE_BF16 or MOE_F16, the type of every 16-bit tensor of the
+ *                call; out_dtype is the same or MOE_F32
+ *   rows         [m][ld], ld >= the row's length, ld a multiple of 8, 16-byte
+ *                aligned; 0 <= m <= 2^24 (0: nothing to do)
+ *   n, k         8 .. 65536, multiples of 8 (f of moe_grouped_geglu: multiples
+ *                of 16 up to 32768); weights 16-byte aligned and contiguous
+ *   offsets      device int32 [n_experts + 1], 1 <= n_experts <= 1024: the rows
+ *                of expert e are [offsets[e], offsets[e + 1]), empty groups
+ *                included (the counts of moe_route_noalloc's ids, summed up).
+ *                Rows before offsets[0] and from offsets[n_experts] on are
+ *                neither read into any result nor written.  Offsets that are
+ *                not non-decreasing or reach past m give undefined outputs, but
+ *                every access stays inside the given tensors.
+ * Products are accumulated in fp32 and rounded once, to the output's type; a
+ * result past the type's range is infinite.  No output may overlap an input.
+ * Results do not depend on timing: no atomics are used.
+ * MOE_EINVAL for an argument outside these rules (checked before anything is
+ * enqueued), MOE_ECUDA for a failed CUDA call (there is no context to poison). */
+
+/* y[r] = W[e] x[r] (transpose = 0: x [m][k], y [m][n]) or W[e]^T x[r]
+ * (transpose = 1: x [m][n], y [m][k], the gradient with respect to the input)
+ * for the rows r of each expert e, W [n_experts][n][k]. */
+moe_status moe_grouped_mm(int dtype, int transpose, const void *x, int64_t ldx, int m, const int32_t *offsets,
+                          int n_experts, const void *w, int n, int k, void *y, int64_t ldy, int out_dtype,
+                          void *stream);
+
+/* dw[e] = sum over the rows r of expert e of dy[r] x[r]^T, dw [n_experts][n][k]
+ * contiguous, dy [m][n], x [m][k]: the gradient of moe_grouped_mm with respect
+ * to its weights.  All of dw is written (zeros for an empty expert). */
+moe_status moe_grouped_wgrad(int dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int m,
+                             const int32_t *offsets, int n_experts, int n, int k, void *dw, int out_dtype,
+                             void *stream);
+
+/* The gate/up half of an expert: a[r] = GELU(g) * u with g = W[e][0 .. f) x[r]
+ * and u = W[e][f .. 2f) x[r], W [n_experts][2 f][k], a [m][f]; gelu_variant as
+ * in moe_config.  a is computed from the fp32 g and u.  h ([m][2 f], or NULL)
+ * receives [g, u], what moe_geglu_grad needs. */
+moe_status moe_grouped_geglu(int dtype, int gelu_variant, const void *x, int64_t ldx, int m, const int32_t *offsets,
+                             int n_experts, const void *w, int f, int k, void *a, int64_t lda, void *h, int64_t ldh,
+                             void *stream);
+
+/* dh = [da u GELU'(g), da GELU(g)] for rows h = [g, u] ([m][2 f]), da [m][f],
+ * dh [m][2 f] (dh may be h itself).  n_rows: device int32, the rows to do (at
+ * most m; offsets + n_experts of the grouped calls), or NULL for all m.  f is
+ * a multiple of 8 up to 32768. */
+moe_status moe_geglu_grad(int dtype, int gelu_variant, const void *h, int64_t ldh, const void *da, int64_t ldda, int m,
+                          int f, const int32_t *n_rows, void *dh, int64_t lddh, void *stream);
+
+/* A shared projection with a low-rank adapter per request:
+ *   y[t] = W x[t] + scale[i] B[i] (A[i] x[t]),  i = ids[t]
+ * W [n][k], A [n_adapters][rank][k], B [n_adapters][n][rank], scale fp32
+ * [n_adapters], ids int32 [t]; a row whose id is outside [0, n_adapters) (-1)
+ * has no adapter.  Rows are in any order; 8 <= rank <= 128, a multiple of 8
+ * (an adapter of a smaller rank ends in zeros).  A x is held in fp32 and
+ * handed on as the sum of two bf16 values (16 significant bits).  Non-finite
+ * values in an adapter reach the rows of its own requests only (as infinities
+ * or NaN).  workspace: at least 4 t rank bytes of device memory, 16-byte
+ * aligned, contents undefined before and after; calls that may run at the same
+ * time (other streams, captured graphs) need one each. */
+moe_status moe_lora_mm(int dtype, const void *x, int64_t ldx, int t, const void *w, int n, int k, const int32_t *ids,
+                       const void *a, const void *b, const float *scale, int n_adapters, int rank, void *y, int64_t ldy,
+                       void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* Synchronise `stream`, then report whether a bounded device wait of these
+ * operators ran out on the current device since the last call (MOE_ETIMEOUT:
+ * outputs since then are undefined), as moe_sync does for a context. */
+moe_status moe_grouped_sync(void *stream);
 
 /* Per-kernel timing.  While enabled, decode and prefill calls launch their
  * kernels one by one (no graph replay), record a CUDA event pair around every

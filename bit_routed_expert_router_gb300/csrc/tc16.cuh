@@ -9,6 +9,14 @@
 namespace moe {
 namespace tc16 {
 
+// One lane of a converged warp.  Unlike lane == 0, the compiler knows that a
+// branch on it has one active thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // ------------------------------------------------------------------ clusters and barriers
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -38,8 +46,9 @@ __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
+// (relaxed: the arrival publishes nothing but the byte count)
 __device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
 

@@ -312,110 +312,128 @@ def moe_route_noalloc(cfg: MoeConfig, router_w, h, B: int, logit_bias, ids, gate
 # dimension that is not contiguous) return MOE_EINVAL like the library's own checks.  The call runs on the tensors'
 # device, on `stream` or that device's current stream.
 
-_DTYPE = None   # torch dtype -> MOE_BF16 / MOE_F16 / MOE_F32
+_DTYPE = _INT32 = _FLOAT32 = _current_device = _raw_stream = None   # from torch, on the first call
 
 
-def _dtype(t) -> int:
-    global _DTYPE
-    if _DTYPE is None:
-        import torch
-        _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
-    return _DTYPE.get(t.dtype, -1)
-
-
-def _rows(t, cols: int, device) -> bool:
-    """A matrix of `cols` contiguous values a row on `device`."""
-    return t.dim() == 2 and t.shape[1] == cols and t.stride(1) == 1 and t.device == device
-
-
-def _ld(t) -> int:
-    # the row stride of a single row says nothing
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _whole(t, dtype: str, device, *shape) -> bool:
-    """A contiguous tensor of this shape and type on `device`."""
-    return tuple(t.shape) == shape and str(t.dtype) == dtype and t.is_contiguous() and t.device == device
-
-
-def _call(fn, device, stream, *args) -> int:
+def _from_torch() -> None:
+    global _DTYPE, _INT32, _FLOAT32, _current_device, _raw_stream
     import torch
-    if device.type != "cuda":
+    _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
+    _INT32, _FLOAT32, _current_device = torch.int32, torch.float32, torch.cuda.current_device
+    # the stream's handle without the 3 us of a torch.cuda.Stream object: these calls start kernels of 10 us
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _rows(t, rows: int, cols: int, dev: int) -> bool:
+    """A [rows, cols] matrix on device `dev` whose rows are contiguous."""
+    return t.shape == (rows, cols) and t.stride(1) == 1 and t.get_device() == dev
+
+
+def _ld(t, rows: int, cols: int) -> int:
+    # the row stride of a single row says nothing
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _whole(t, dtype, dev: int, *shape) -> bool:
+    """A contiguous tensor of this shape and type on device `dev`."""
+    return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
+
+
+def _call(fn, dev: int, stream, *args) -> int:
+    if dev < 0:
         return MOE_EINVAL
-    if device.index == torch.cuda.current_device():
-        return fn(*args, _stream(stream))
-    with torch.cuda.device(device):
-        return fn(*args, _stream(stream))
+    if stream is None:
+        stream = _raw_stream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == _current_device():
+        return fn(*args, stream)
+    import torch
+    with torch.cuda.device(dev):
+        return fn(*args, stream)
 
 
 def moe_grouped_mm(x, offsets, w, y, transpose: bool = False, stream=None) -> int:
     """y[r] = w[e] x[r] (or w[e]^T x[r]) for the rows of each expert; w [E, n, k], offsets int32 [E + 1]."""
-    if w.dim() != 3 or x.dim() != 2 or y.dim() != 2 or not w.is_contiguous():
+    if _DTYPE is None:
+        _from_torch()
+    if w.dim() != 3 or x.dim() != 2:
         return MOE_EINVAL
-    (E, n, k), dev = w.shape, w.device
+    (E, n, k), m, dev, dt = w.shape, x.shape[0], w.get_device(), w.dtype
     into, out = (n, k) if transpose else (k, n)
-    if not (_rows(x, into, dev) and _rows(y, out, dev) and y.shape[0] == x.shape[0] and x.dtype == w.dtype and
-            _whole(offsets, "torch.int32", dev, E + 1)):
+    if not (_rows(x, m, into, dev) and _rows(y, m, out, dev) and x.dtype is dt and w.is_contiguous() and
+            _whole(offsets, _INT32, dev, E + 1)):
         return MOE_EINVAL
-    return _call(lib().moe_grouped_mm, dev, stream, _dtype(x), int(transpose), _ptr(x), _ld(x), x.shape[0],
-                 _ptr(offsets), E, _ptr(w), n, k, _ptr(y), _ld(y), _dtype(y))
+    return _call(lib().moe_grouped_mm, dev, stream, _DTYPE.get(dt, -1), 1 if transpose else 0, x.data_ptr(),
+                 _ld(x, m, into), m, offsets.data_ptr(), E, w.data_ptr(), n, k, y.data_ptr(), _ld(y, m, out),
+                 _DTYPE.get(y.dtype, -1))
 
 
 def moe_grouped_wgrad(dy, x, offsets, dw, stream=None) -> int:
     """dw[e] = sum over the rows of each expert of dy[r] x[r]^T; dw [E, n, k], all of it written."""
-    if dw.dim() != 3 or x.dim() != 2 or dy.dim() != 2 or not dw.is_contiguous():
+    if _DTYPE is None:
+        _from_torch()
+    if dw.dim() != 3 or x.dim() != 2:
         return MOE_EINVAL
-    (E, n, k), dev = dw.shape, dw.device
-    if not (_rows(x, k, dev) and _rows(dy, n, dev) and dy.shape[0] == x.shape[0] and x.dtype == dy.dtype and
-            _whole(offsets, "torch.int32", dev, E + 1)):
+    (E, n, k), m, dev, dt = dw.shape, x.shape[0], dw.get_device(), x.dtype
+    if not (_rows(x, m, k, dev) and _rows(dy, m, n, dev) and dy.dtype is dt and dw.is_contiguous() and
+            _whole(offsets, _INT32, dev, E + 1)):
         return MOE_EINVAL
-    return _call(lib().moe_grouped_wgrad, dev, stream, _dtype(x), _ptr(dy), _ld(dy), _ptr(x), _ld(x), x.shape[0],
-                 _ptr(offsets), E, n, k, _ptr(dw), _dtype(dw))
+    return _call(lib().moe_grouped_wgrad, dev, stream, _DTYPE.get(dt, -1), dy.data_ptr(), _ld(dy, m, n), x.data_ptr(),
+                 _ld(x, m, k), m, offsets.data_ptr(), E, n, k, dw.data_ptr(), _DTYPE.get(dw.dtype, -1))
 
 
 def moe_grouped_geglu(x, offsets, w, a, h=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
     """a[r] = GELU(g) u, [g, u] = w[e] x[r]; w [E, 2 f, k]; h [m, 2 f] (optional) receives [g, u]."""
-    if w.dim() != 3 or x.dim() != 2 or a.dim() != 2 or not w.is_contiguous() or w.shape[1] % 2:
+    if _DTYPE is None:
+        _from_torch()
+    if w.dim() != 3 or x.dim() != 2 or w.shape[1] % 2:
         return MOE_EINVAL
-    (E, n, k), dev = w.shape, w.device
-    if not (_rows(x, k, dev) and _rows(a, n // 2, dev) and a.shape[0] == x.shape[0] and
-            x.dtype == w.dtype == a.dtype and _whole(offsets, "torch.int32", dev, E + 1)):
+    (E, n, k), m, dev, dt = w.shape, x.shape[0], w.get_device(), w.dtype
+    f = n // 2
+    if not (_rows(x, m, k, dev) and _rows(a, m, f, dev) and x.dtype is dt and a.dtype is dt and w.is_contiguous() and
+            _whole(offsets, _INT32, dev, E + 1)):
         return MOE_EINVAL
-    if h is not None and not (_rows(h, n, dev) and h.shape[0] == x.shape[0] and h.dtype == x.dtype):
+    if h is not None and not (_rows(h, m, n, dev) and h.dtype is dt):
         return MOE_EINVAL
-    return _call(lib().moe_grouped_geglu, dev, stream, _dtype(x), gelu_variant, _ptr(x), _ld(x), x.shape[0],
-                 _ptr(offsets), E, _ptr(w), n // 2, k, _ptr(a), _ld(a), _ptr(h), 0 if h is None else _ld(h))
+    return _call(lib().moe_grouped_geglu, dev, stream, _DTYPE.get(dt, -1), gelu_variant, x.data_ptr(), _ld(x, m, k), m,
+                 offsets.data_ptr(), E, w.data_ptr(), f, k, a.data_ptr(), _ld(a, m, f),
+                 None if h is None else h.data_ptr(), 0 if h is None else _ld(h, m, n))
 
 
 def moe_geglu_grad(h, da, dh, n_rows=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
     """dh = [da u GELU'(g), da GELU(g)] for h = [g, u]; n_rows: int32 tensor of one value, the rows to do."""
+    if _DTYPE is None:
+        _from_torch()
     if da.dim() != 2:
         return MOE_EINVAL
-    (m, f), dev = da.shape, da.device
-    if not (_rows(h, 2 * f, dev) and _rows(da, f, dev) and _rows(dh, 2 * f, dev) and h.shape[0] == dh.shape[0] == m and
-            h.dtype == da.dtype == dh.dtype):
+    (m, f), dev, dt = da.shape, da.get_device(), da.dtype
+    if not (_rows(h, m, 2 * f, dev) and _rows(da, m, f, dev) and _rows(dh, m, 2 * f, dev) and h.dtype is dt and
+            dh.dtype is dt):
         return MOE_EINVAL
-    if n_rows is not None and not (n_rows.numel() == 1 and str(n_rows.dtype) == "torch.int32" and n_rows.device == dev):
+    if n_rows is not None and not (n_rows.numel() == 1 and n_rows.dtype is _INT32 and n_rows.get_device() == dev):
         return MOE_EINVAL
-    return _call(lib().moe_geglu_grad, dev, stream, _dtype(h), gelu_variant, _ptr(h), _ld(h), _ptr(da), _ld(da), m, f,
-                 _ptr(n_rows), _ptr(dh), _ld(dh))
+    return _call(lib().moe_geglu_grad, dev, stream, _DTYPE.get(dt, -1), gelu_variant, h.data_ptr(), _ld(h, m, 2 * f),
+                 da.data_ptr(), _ld(da, m, f), m, f, None if n_rows is None else n_rows.data_ptr(), dh.data_ptr(),
+                 _ld(dh, m, 2 * f))
 
 
 def moe_lora_mm(x, w, ids, a, b, scale, y, workspace, stream=None) -> int:
     """y[t] = w x[t] + scale[i] b[i] (a[i] x[t]), i = ids[t]; w [n, k], a [N, rank, k], b [N, n, rank], scale fp32
     [N], ids int32 [t] (-1: no adapter), workspace: a tensor of at least 4 * t * rank bytes."""
-    if w.dim() != 2 or x.dim() != 2 or y.dim() != 2 or a.dim() != 3 or not w.is_contiguous():
+    if _DTYPE is None:
+        _from_torch()
+    if w.dim() != 2 or x.dim() != 2 or a.dim() != 3:
         return MOE_EINVAL
-    (n, k), (N, rank, _), dev, dt = w.shape, a.shape, w.device, str(w.dtype)
-    t = x.shape[0]
-    if not (_rows(x, k, dev) and _rows(y, n, dev) and y.shape[0] == t and x.dtype == w.dtype == y.dtype and
-            _whole(a, dt, dev, N, rank, k) and _whole(b, dt, dev, N, n, rank) and
-            _whole(scale, "torch.float32", dev, N) and _whole(ids, "torch.int32", dev, t) and
-            workspace.is_contiguous() and workspace.device == dev):
+    (n, k), (N, rank, _), t, dev, dt = w.shape, a.shape, x.shape[0], w.get_device(), w.dtype
+    if not (_rows(x, t, k, dev) and _rows(y, t, n, dev) and x.dtype is dt and y.dtype is dt and w.is_contiguous() and
+            _whole(a, dt, dev, N, rank, k) and _whole(b, dt, dev, N, n, rank) and _whole(scale, _FLOAT32, dev, N) and
+            _whole(ids, _INT32, dev, t) and workspace.is_contiguous() and workspace.get_device() == dev):
         return MOE_EINVAL
-    return _call(lib().moe_lora_mm, dev, stream, _dtype(x), _ptr(x), _ld(x), t, _ptr(w), n, k, _ptr(ids), _ptr(a),
-                 _ptr(b), _ptr(scale), N, rank, _ptr(y), _ld(y), _ptr(workspace),
-                 workspace.numel() * workspace.element_size())
+    return _call(lib().moe_lora_mm, dev, stream, _DTYPE.get(dt, -1), x.data_ptr(), _ld(x, t, k), t, w.data_ptr(), n, k,
+                 ids.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), N, rank, y.data_ptr(), _ld(y, t, n),
+                 workspace.data_ptr(), workspace.numel() * workspace.element_size())
 
 
 def moe_grouped_sync(stream=None) -> int:

@@ -15,7 +15,7 @@
 // features and half of the rows, so a staged byte feeds twice the products
 // that it would in a lone CTA.  Two accumulators of 256 columns: the epilogue
 // of one tile overlaps the next tile's products.  Roles: warp 0 loads, warp 1
-// of the even CTA issues, warps 2-5 store, warp 6 (weights only) clears the
+// of the even CTA issues, warps 2-9 store, warp 10 (weights only) clears the
 // rows behind a group's end in the last stage.  The loading and issuing
 // threads are elected (elect.sync): with lane == 0 in its place an MMA took
 // 170 cycles whatever its N, against 135 for N = 256 and 87 for N = 160.
@@ -45,11 +45,15 @@ constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns 
 constexpr int kHalf = 16384;
 constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 32 bytes: multiples of 16, and the
 constexpr int kEpiPitch16 = 48;      // 16-byte words of eight rows hit all 32 banks
+constexpr int kPitch32 = 36;          // floats between staged rows of 32
+constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memory lanes, 32 columns in turn
+constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
+constexpr int kBigThreads = 32 * (2 + kEpiWarps + 1);
 constexpr int kAccCols = 256;
 
 struct BigSmem {
   uint8_t stage[kStages][kStageBytes];
-  uint8_t epi[4][2][16 * kEpiPitch16];
+  uint8_t epi[kEpiWarps][kEpiBytes];
   uint64_t full[kStages], empty[kStages], tail[kStages];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
@@ -58,7 +62,7 @@ struct BigSmem {
   int tiles[kMaxE + 1];  // column tiles before each expert
 };
 static_assert(sizeof(BigSmem) + 1024 <= 227 * 1024, "one CTA per SM");
-static_assert(16 * kEpiPitch16 >= 8 * kEpiPitch && kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0, "staged rows");
+static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes >= 8 * kPitch32 * 4 && kEpiBytes % 16 == 0 && kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0, "staged rows");
 
 __device__ __forceinline__ uint32_t* err_word() { return &g_grouped_err; }
 
@@ -245,44 +249,85 @@ __device__ __forceinline__ void add_adapters(float (&v)[2][16], const GmParams& 
 
 // ------------------------------------------------------------------ the persistent kernel
 
-// 8 columns x 32 features through shared memory, then one 16-byte store per
-// lane: 64 contiguous bytes of each column.
-__device__ __forceinline__ void store_8x32(uint32_t buf, const float (&v)[2][16], int j, int bf16, uint16_t* out,
-                                           long long ld, int cols, int feats, int lane) {
-  __syncwarp();   // the previous reads of this buffer are done
-  stmatrix4_trans(buf + (lane & 7) * kEpiPitch + (lane >> 3) * 16, pack16(v[0][4 * j], v[0][4 * j + 1], bf16),
-                  pack16(v[0][4 * j + 2], v[0][4 * j + 3], bf16), pack16(v[1][4 * j], v[1][4 * j + 1], bf16),
-                  pack16(v[1][4 * j + 2], v[1][4 * j + 3], bf16));
-  __syncwarp();
-  const int c = lane >> 2, f = 8 * (lane & 3);
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 w;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-               : "r"(buf + c * kEpiPitch + (lane & 3) * 16)
-               : "memory");
-  if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+  return w;
 }
 
-// 16 columns x 16 features (fragments j and j + 1 of one 16-row block).
-__device__ __forceinline__ void store_16x16(uint32_t buf, const float (&v)[16], int j, int bf16, uint16_t* out,
-                                            long long ld, int cols, int feats, int lane) {
+// The stores of one warp: 32 columns of its accumulator lanes as fragments,
+// turned through the warp's own shared memory so that every lane stores 16
+// bytes.  All of a tensor's fragments are staged before the first is read
+// back: one warp barrier each way, and four independent loads and stores.
+
+// 32 features x 32 columns of 16-bit values: 64 contiguous bytes of a column.
+__device__ __forceinline__ void store_32x32(uint32_t buf, const float (&v)[2][16], int bf16, uint16_t* out, long long ld,
+                                            int cols, int feats, int lane) {
+  __syncwarp();   // earlier reads of this buffer are done
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    stmatrix4_trans(buf + j * 8 * kEpiPitch + (lane & 7) * kEpiPitch + (lane >> 3) * 16,
+                    pack16(v[0][4 * j], v[0][4 * j + 1], bf16), pack16(v[0][4 * j + 2], v[0][4 * j + 3], bf16),
+                    pack16(v[1][4 * j], v[1][4 * j + 1], bf16), pack16(v[1][4 * j + 2], v[1][4 * j + 3], bf16));
   __syncwarp();
+  const int f = 8 * (lane & 3);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = 8 * j + (lane >> 2);
+    const uint4 w = lds128(buf + c * kEpiPitch + (lane & 3) * 16);
+    if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+  }
+}
+
+// 32 features x 32 columns of fp32: 128 contiguous bytes of a column, eight
+// columns at a time.
+__device__ __forceinline__ void store_32x32_f32(uint32_t buf, const float (&v)[2][16], float* out, long long ld, int cols,
+                                                int feats, int lane) {
+  const int g = lane >> 2, t4 = lane & 3, f = 4 * (lane & 7);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (8 * j >= cols) break;
+    __syncwarp();
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + ((2 * t4 + (i & 1)) * kPitch32 + 16 * mb + 8 * (i >> 1) + g) * 4),
+                     "f"(v[mb][4 * j + i])
+                     : "memory");
+    __syncwarp();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int c = 4 * half + (lane >> 3);
+      const uint4 w = lds128(buf + (c * kPitch32 + f) * 4);
+      if (8 * j + c < cols && f < feats) *reinterpret_cast<uint4*>(out + (8 * j + c) * ld + f) = w;
+    }
+  }
+}
+
+// 16 features x 32 columns of 16-bit values (one 16-row block): staged here ...
+__device__ __forceinline__ void stage_16x32(uint32_t buf, const float (&v)[16], int bf16, int lane) {
   const int blk = lane >> 3;   // blocks: (fragment j, features 0-7), (j, 8-15), (j + 1, 0-7), (j + 1, 8-15)
-  stmatrix4_trans(buf + ((blk >> 1) * 8 + (lane & 7)) * (kEpiPitch16) + (blk & 1) * 16,
-                  pack16(v[4 * j], v[4 * j + 1], bf16), pack16(v[4 * j + 2], v[4 * j + 3], bf16),
-                  pack16(v[4 * j + 4], v[4 * j + 5], bf16), pack16(v[4 * j + 6], v[4 * j + 7], bf16));
-  __syncwarp();
-  const int c = lane >> 1, f = 8 * (lane & 1);
-  uint4 w;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-               : "r"(buf + c * kEpiPitch16 + (lane & 1) * 16)
-               : "memory");
-  if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+#pragma unroll
+  for (int j = 0; j < 4; j += 2)
+    stmatrix4_trans(buf + (8 * j + (blk >> 1) * 8 + (lane & 7)) * kEpiPitch16 + (blk & 1) * 16,
+                    pack16(v[4 * j], v[4 * j + 1], bf16), pack16(v[4 * j + 2], v[4 * j + 3], bf16),
+                    pack16(v[4 * j + 4], v[4 * j + 5], bf16), pack16(v[4 * j + 6], v[4 * j + 7], bf16));
+}
+
+// ... and stored: 32 contiguous bytes of a column.
+__device__ __forceinline__ void store_16x32(uint32_t buf, uint16_t* out, long long ld, int cols, int feats, int lane) {
+  const int f = 8 * (lane & 1);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int c = 16 * i + (lane >> 1);
+    const uint4 w = lds128(buf + c * kEpiPitch16 + (lane & 1) * 16);
+    if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+  }
 }
 
 template <int kMode, int kEpi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
     k_grouped(const __grid_constant__ GmMaps maps, GmParams p) {
   constexpr bool kTa = kMode != GM_FWD, kTb = kMode == GM_WGRAD;
   constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;   // features of a pair's tile
@@ -301,7 +346,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.acc_full[i], 1);
-      mbar_init(&S.acc_empty[i], 8);
+      mbar_init(&S.acc_empty[i], 2 * kEpiWarps);
     }
     mbar_init(&S.drain, 1);
     S.abort = 0;
@@ -348,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
           if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
           uint32_t bar = lead_full + 8 * s;
           if (kMode == GM_WGRAD) {
-            if (ks == T.steps - 1 && (T.rows & 15)) {   // warp 6 sees these bytes first
+            if (ks == T.steps - 1 && (T.rows & 15)) {   // warp 10 sees these bytes first
               bar = smem_u32(&S.tail[s]);
               mbar_arrive_expect_tx(&S.tail[s], bytes);
             } else {
@@ -399,7 +444,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
         for (int ks = 0; ok && ks < T.steps; ++ks, ++it) {
           const int s = it % kStages;
           const uint32_t par = (it / kStages) & 1;
-          if (kMode == GM_WGRAD && ks == T.steps - 1 && (T.rows & 15))   // rows cleared by warp 6 of both CTAs
+          if (kMode == GM_WGRAD && ks == T.steps - 1 && (T.rows & 15))   // rows cleared by warp 10 of both CTAs
             ok = wait_bar<true>(&S.full[s], par, &S.abort);
           else
             ok = wait_bar(&S.full[s], par, &S.abort);
@@ -420,9 +465,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
         mbar_wait_bounded(&S.drain, 0, err_word());
       }
     }
-  } else if (warp < 6) {
+  } else if (warp < 2 + kEpiWarps) {
     const int q = warp & 3;   // the tensor-memory lanes this warp may read
-    const uint32_t buf0 = smem_u32(S.epi[q][0]), buf1 = smem_u32(S.epi[q][1]);
+    const uint32_t buf16 = smem_u32(S.epi[warp - 2]);
     const uint32_t lead_empty = map_rank(smem_u32(S.acc_empty), 0);
     uint32_t count = 0;
     int e = 0;
@@ -430,13 +475,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
     for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
       // first feature of this warp's 32 lanes (GM_GATED: 16 gate and 16 up lanes of 16 features)
       const int f0 = T.f0 + (kEpi == GM_GATED ? 64 * rank + 16 * q : 128 * rank + 32 * q);
-      const int feats = p.feat - f0;
-      const int buf = count & 1;
+      const int feats = p.feat - f0;   // none or less: the output ends before this warp's features do
+      const int buf = count & 1, c_first = 32 * ((warp - 2) >> 2);
       if (T.steps && !wait_bar(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
       fence_after();
       const long long out0 =
           (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
-      for (int c0 = 0; c0 < T.cols; c0 += 32) {
+      if (kEpi == GM_ADAPT) pdl_wait();   // the u rows
+      for (int c0 = c_first; c0 < T.cols; c0 += 64) {
         float v[2][16];
         if (T.steps) {
           ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
@@ -444,50 +490,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(224, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
         }
+        if (feats <= 0) continue;
         const int cols = T.cols - c0;
-        if (kEpi == GM_ADAPT) {
-          if (c0 == 0) pdl_wait();
-          add_adapters(v, p, T.c0 + c0, min(cols, 32), f0, lane);
-        }
-        if (feats <= 0) continue;   // the warp's features end before this tile does
+        if (kEpi == GM_ADAPT) add_adapters(v, p, T.c0 + c0, min(cols, 32), f0, lane);
         if (kEpi == GM_GATED) {
-          uint16_t* y = static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy;
+          __syncwarp();
           if (p.h) {
             uint16_t* h = static_cast<uint16_t*>(p.h) + static_cast<long long>(T.c0 + c0) * p.ldh + f0;
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-              if (8 * j >= cols) break;
-              store_16x16(buf0, v[0], j, p.bf16, h + 8 * j * p.ldh, p.ldh, cols - 8 * j, feats, lane);
-              store_16x16(buf1, v[1], j, p.bf16, h + p.feat + 8 * j * p.ldh, p.ldh, cols - 8 * j, feats, lane);
-            }
+            stage_16x32(buf16, v[0], p.bf16, lane);
+            stage_16x32(buf16 + 32 * kEpiPitch16, v[1], p.bf16, lane);
+            __syncwarp();
+            store_16x32(buf16, h, p.ldh, cols, feats, lane);
+            store_16x32(buf16 + 32 * kEpiPitch16, h + p.feat, p.ldh, cols, feats, lane);
+            __syncwarp();
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = gelu(v[0][i], p.gelu) * v[1][i];
-#pragma unroll
-          for (int j = 0; j < 4; j += 2) {
-            if (8 * j >= cols) break;
-            store_16x16(j ? buf1 : buf0, v[0], j, p.bf16, y + 8 * j * p.ldy, p.ldy, cols - 8 * j, feats, lane);
-          }
+          stage_16x32(buf16, v[0], p.bf16, lane);
+          __syncwarp();
+          store_16x32(buf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         } else if (p.out_f32) {
-          float* y = static_cast<float*>(p.y) + out0 + c0 * p.ldy;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int c = 8 * j + 2 * (lane & 3) + (i & 1);
-#pragma unroll
-              for (int mb = 0; mb < 2; ++mb) {
-                const int f = 16 * mb + 8 * (i >> 1) + (lane >> 2);
-                if (c < cols && f < feats) y[c * p.ldy + f] = v[mb][4 * j + i];
-              }
-            }
+          store_32x32_f32(buf16, v, static_cast<float*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         } else {
-          uint16_t* y = static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (8 * j >= cols) break;
-            store_8x32((j & 1) ? buf1 : buf0, v, j, p.bf16, y + 8 * j * p.ldy, p.ldy, cols - 8 * j, feats, lane);
-          }
+          store_32x32(buf16, v, p.bf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         }
       }
       if (T.steps) {
@@ -788,7 +813,7 @@ bool launch_big(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s) 
   const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
                                          : std::min(p.E, p.m) + static_cast<long long>(p.m) / 256;
   const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
-  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), 224, sizeof(BigSmem) + 1024, 2, s, maps, p, 0);
+  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), kBigThreads, sizeof(BigSmem) + 1024, 2, s, maps, p, 0);
 }
 
 template <int kMode, int kEpi>

@@ -40,7 +40,6 @@ using namespace tc16;
 __device__ uint32_t g_grouped_err;
 
 constexpr int kMaxE = 1024;
-constexpr int kStages = 6;
 constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
 constexpr int kHalf = 16384;
 constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 32 bytes: multiples of 16, and the
@@ -51,9 +50,19 @@ constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kBigThreads = 32 * (2 + kEpiWarps + 1);
 constexpr int kAccCols = 256;
 
+// The weight gradient's tiles have few stages each and store far more than they
+// load: two buffers a warp for TMA stores, and a stage less.
+template <int kMode>
+struct BigCfg {
+  static constexpr int kStages = kMode == GM_WGRAD ? 5 : 6;
+  static constexpr int kEpiBytes = kMode == GM_WGRAD ? 4096 : moe::kEpiBytes;
+};
+
+template <int kMode>
 struct BigSmem {
+  static constexpr int kStages = BigCfg<kMode>::kStages;
   uint8_t stage[kStages][kStageBytes];
-  uint8_t epi[kEpiWarps][kEpiBytes];
+  alignas(1024) uint8_t epi[kEpiWarps][BigCfg<kMode>::kEpiBytes];
   uint64_t full[kStages], empty[kStages], tail[kStages];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
@@ -61,8 +70,11 @@ struct BigSmem {
   int off[kMaxE + 1];    // clamped to [0, m]
   int tiles[kMaxE + 1];  // column tiles before each expert
 };
-static_assert(sizeof(BigSmem) + 1024 <= 227 * 1024, "one CTA per SM");
-static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes >= 8 * kPitch32 * 4 && kEpiBytes % 16 == 0 && kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0, "staged rows");
+static_assert(sizeof(BigSmem<GM_FWD>) + 1024 <= 227 * 1024 && sizeof(BigSmem<GM_WGRAD>) + 1024 <= 227 * 1024,
+              "one CTA per SM");
+static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes >= 8 * kPitch32 * 4 && kEpiBytes % 16 == 0 &&
+                  kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0,
+              "staged rows");
 
 __device__ __forceinline__ uint32_t* err_word() { return &g_grouped_err; }
 
@@ -130,7 +142,7 @@ struct Tile {
 // Tile t of the launch in the order expert, feature tile, column tile: the
 // pairs that run together share an expert's rows and weights through L2.
 template <int kMode, int kFeat>
-__device__ __forceinline__ bool tile_at(const BigSmem& S, const GmParams& p, int t, int& e, Tile& T) {
+__device__ __forceinline__ bool tile_at(const BigSmem<kMode>& S, const GmParams& p, int t, int& e, Tile& T) {
   const int ft = (p.feat + kFeat - 1) / kFeat;
   if constexpr (kMode == GM_WGRAD) {
     const int ct = (p.cols + 255) / 256, per = ft * ct;
@@ -305,6 +317,53 @@ __device__ __forceinline__ void store_32x32_f32(uint32_t buf, const float (&v)[2
   }
 }
 
+// The weight gradient's stores: swizzled rows of 32 features in one of two
+// buffers, which the TMA engine writes out while the other is filled.  A
+// 64-byte segment of each column per warp and ordinary store kept the LSU's
+// data pipe at 66% and the kernel at 138 us (507 MB of fp16).
+__device__ __forceinline__ void tma_store_32x32(uint32_t buf, const float (&v)[2][16], const GmParams& p,
+                                                const CUtensorMap* map, int f0, int c0, int cols, int e, int lane,
+                                                bool lead, uint32_t& n_stores) {
+  const int g = lane >> 2, t4 = lane & 3;
+  if (p.out_f32) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {   // 16 columns of 128 bytes
+      if (16 * half >= cols) break;
+      if (lead) store_wait<1>();
+      __syncwarp();
+      const uint32_t at = buf + 2048 * (n_stores++ & 1);   // the store before last has read it
+#pragma unroll
+      for (int j = 2 * half; j < 2 * half + 2; ++j)
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 8 * (j & 1) + 2 * t4 + (i & 1), word = 4 * mb + 2 * (i >> 1) + (g >> 2);
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128 * c + 16 * (word ^ (c & 7)) + 4 * (g & 3)),
+                         "f"(v[mb][4 * j + i])
+                         : "memory");
+          }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lead) store_3d(map, at, f0, c0 + 16 * half, e);
+    }
+  } else {
+    const uint32_t at = buf + 2048 * (n_stores++ & 1);
+    if (lead) store_wait<1>();
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = 8 * j + (lane & 7);
+      stmatrix4_trans(at + 64 * c + 16 * ((lane >> 3) ^ ((c >> 1) & 3)), pack16(v[0][4 * j], v[0][4 * j + 1], p.bf16),
+                      pack16(v[0][4 * j + 2], v[0][4 * j + 3], p.bf16), pack16(v[1][4 * j], v[1][4 * j + 1], p.bf16),
+                      pack16(v[1][4 * j + 2], v[1][4 * j + 3], p.bf16));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lead) store_3d(map, at, f0, c0, e);
+  }
+}
+
 // 16 features x 32 columns of 16-bit values (one 16-row block): staged here ...
 __device__ __forceinline__ void stage_16x32(uint32_t buf, const float (&v)[16], int bf16, int lane) {
   const int blk = lane >> 3;   // blocks: (fragment j, features 0-7), (j, 8-15), (j + 1, 0-7), (j + 1, 8-15)
@@ -332,7 +391,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
   constexpr bool kTa = kMode != GM_FWD, kTb = kMode == GM_WGRAD;
   constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;   // features of a pair's tile
   extern __shared__ uint8_t smem_raw[];
-  BigSmem& S = *reinterpret_cast<BigSmem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
+  using Smem = BigSmem<kMode>;
+  constexpr int kStages = Smem::kStages;
+  Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
@@ -469,7 +530,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
     const int q = warp & 3;   // the tensor-memory lanes this warp may read
     const uint32_t buf16 = smem_u32(S.epi[warp - 2]);
     const uint32_t lead_empty = map_rank(smem_u32(S.acc_empty), 0);
-    uint32_t count = 0;
+    const bool lead = kMode == GM_WGRAD && elect_one();
+    uint32_t count = 0, n_stores = 0;
     int e = 0;
     Tile T;
     for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
@@ -493,7 +555,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
         if (feats <= 0) continue;
         const int cols = T.cols - c0;
         if (kEpi == GM_ADAPT) add_adapters(v, p, T.c0 + c0, min(cols, 32), f0, lane);
-        if (kEpi == GM_GATED) {
+        if (kMode == GM_WGRAD) {
+          tma_store_32x32(buf16, v, p, &maps.b[1], f0, T.c0 + c0, cols, T.e, lane, lead, n_stores);
+        } else if (kEpi == GM_GATED) {
           __syncwarp();
           if (p.h) {
             uint16_t* h = static_cast<uint16_t*>(p.h) + static_cast<long long>(T.c0 + c0) * p.ldh + f0;
@@ -522,6 +586,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
         ++count;
       }
     }
+    if (lead) store_wait<0>();   // the last stores have read this CTA's shared memory
   } else if (kMode == GM_WGRAD) {
     // rows behind the group's end in its last stage belong to another expert (or to nobody, and may hold
     // anything): cleared in both operands, up to the end of the last k16 step that is issued
@@ -813,7 +878,7 @@ bool launch_big(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s) 
   const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
                                          : std::min(p.E, p.m) + static_cast<long long>(p.m) / 256;
   const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
-  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), kBigThreads, sizeof(BigSmem) + 1024, 2, s, maps, p, 0);
+  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), kBigThreads, sizeof(BigSmem<kMode>) + 1024, 2, s, maps, p, 0);
 }
 
 template <int kMode, int kEpi>
@@ -838,6 +903,10 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
   if (mode == GM_WGRAD) {
     if (!map_rows(&maps.a, o.x, o.k, p.m, o.ldx, 64, p.bf16) || !map_rows(&maps.b[0], o.w, o.n, p.m, o.ldw, 64, p.bf16))
       return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(o.k) * (p.out_f32 ? 4 : 2);
+    const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
+    const cuuint64_t stride[2] = {row, row * o.n};
+    if (!encode_store(&maps.b[1], p.y, dim, stride, p.out_f32 ? 16 : 32, p.out_f32, p.bf16)) return false;
     return launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);

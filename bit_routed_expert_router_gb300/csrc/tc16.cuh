@@ -120,6 +120,23 @@ __device__ __forceinline__ void load_5d(uint32_t dst, const CUtensorMap* map, in
         : "memory");
 }
 
+// ------------------------------------------------------------------ TMA stores
+
+// What a box reaches past the tensor is not written.  One thread commits the
+// stores it issued as a group and waits until at most kLeft groups still read
+// shared memory.
+__device__ __forceinline__ void store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void store_wait() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+
 // ------------------------------------------------------------------ tcgen05
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }

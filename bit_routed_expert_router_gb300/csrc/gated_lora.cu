@@ -80,24 +80,75 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-constexpr int kDownWarps = 8, kDownRows = 32;
+constexpr int kDownWarps = 16, kDownRows = 32;
 
-// A CTA: 16 rank rows x 32 rows of x, for the distinct adapters number z,
-// z + gridDim.z, ... of those rows.  The warps split the reduction (64 values
-// at a time) and add through shared memory in warp order.  A lane's fragments
-// are 16 consecutive values of a row, loaded as two 16-byte words; the order
-// of k inside a 64 is the same in both operands, which is all a product needs.
-// Each adapter's products are written for its own rows only.
-template <bool kBf16>
+// acc += A x for 16 rank rows and 8 kNg rows of x over the 64-value pieces k0,
+// k0 + step, ... of the reduction.  A lane's fragments are 16 consecutive
+// values of a row, loaded as two 16-byte words; the order of k inside a 64 is
+// the same in both operands, which is all a product needs.  The next piece's
+// loads are issued before this one's products.
+template <bool kBf16, int kNg>
+__device__ __forceinline__ void down_products(float (&acc)[4][4], const uint16_t* arow, bool has0, bool has1,
+                                              const uint16_t* const (&xrow)[4], int k, int k0, int step, int t4) {
+  struct Piece {
+    uint4 a[2][2], x[kNg][2];
+  };
+  const auto load = [&](Piece& P, int at0) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const int at = at0 + 16 * t4 + 8 * hh;
+      const bool in = at < k;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      P.a[0][hh] = in && has0 ? __ldg(reinterpret_cast<const uint4*>(arow + at)) : zero;
+      P.a[1][hh] = in && has1 ? __ldg(reinterpret_cast<const uint4*>(arow + 8 * static_cast<size_t>(k) + at)) : zero;
+#pragma unroll
+      for (int j = 0; j < kNg; ++j) P.x[j][hh] = in ? __ldg(reinterpret_cast<const uint4*>(xrow[j] + at)) : zero;
+    }
+  };
+  const auto multiply = [&](const Piece& P) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t af[4] = {s ? P.a[0][hh].z : P.a[0][hh].x, s ? P.a[1][hh].z : P.a[1][hh].x,
+                                s ? P.a[0][hh].w : P.a[0][hh].y, s ? P.a[1][hh].w : P.a[1][hh].y};
+#pragma unroll
+        for (int j = 0; j < kNg; ++j) {
+          const uint32_t b0 = s ? P.x[j][hh].z : P.x[j][hh].x, b1 = s ? P.x[j][hh].w : P.x[j][hh].y;
+          if (kBf16)
+            mma_bf16(acc[j], af, b0, b1);
+          else
+            mma_f16(acc[j], af, b0, b1);
+        }
+      }
+  };
+  Piece cur, next;
+  load(cur, k0);
+  for (; k0 < k; k0 += 2 * step) {
+    load(next, k0 + step);
+    multiply(cur);
+    load(cur, k0 + 2 * step);
+    multiply(next);
+  }
+}
+
+// A CTA: 16 kMt rank rows x 32 rows of x, for the distinct adapters number z,
+// z + gridDim.z, ... of those rows.  An adapter's rows are gathered, so that
+// its products cost 8 rows at a time whatever their order.  Warps: kMt tiles
+// of 16 ranks, the others split the reduction and are added in order through
+// shared memory.
+template <bool kBf16, int kMt>
 __global__ void __launch_bounds__(32 * kDownWarps)
     k_adapter_down(const uint16_t* __restrict__ x, long long ldx, int t, const uint16_t* __restrict__ a,
                    const float* __restrict__ scale, const int32_t* __restrict__ ids, int n_adapters, int rank, int k,
                    uint16_t* u) {
-  __shared__ float red[kDownWarps][16][kDownRows + 1];
+  constexpr int kSplit = kDownWarps / kMt;
+  __shared__ float red[kSplit][16 * kMt][kDownRows + 1];
+  __shared__ uint8_t list[kDownWarps][kDownRows];   // a warp's own copy: the adapter's rows in order
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int row0 = blockIdx.x * kDownRows, r0 = blockIdx.y * 16;
+  const int row0 = blockIdx.x * kDownRows, r0 = blockIdx.y * 16 * kMt, r1 = r0 + 16 * (warp % kMt), part = warp / kMt;
   int id = -1;
   if (row0 + lane < t) {
     id = ids[row0 + lane];
@@ -109,61 +160,47 @@ __global__ void __launch_bounds__(32 * kDownWarps)
     const uint32_t same = __ballot_sync(0xFFFFFFFFu, id == ad);
     left &= ~same;
     if (nth % static_cast<int>(gridDim.z) != static_cast<int>(blockIdx.z)) continue;
-    const uint16_t* arow = a + (static_cast<size_t>(ad) * rank + r0 + g) * k;
-    const bool has0 = r0 + g < rank, has1 = r0 + 8 + g < rank;
+    const int rows = __popc(same), groups = (rows + 7) / 8;
+    __syncwarp();
+    if (id == ad) list[warp][__popc(same & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
+    __syncwarp();
+    const float sc = scale[ad];
+    const uint16_t* arow = a + (static_cast<size_t>(ad) * rank + r1 + g) * k;
+    const uint16_t* xrow[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)   // the last group repeats its last row
+      xrow[j] = x + static_cast<long long>(row0 + list[warp][min(8 * j + g, rows - 1)]) * ldx;
     float acc[4][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    for (int k0 = 64 * warp; k0 < k; k0 += 64 * kDownWarps) {
-      uint32_t w0[8], w1[8];
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const int at = k0 + 16 * t4 + 8 * hh;
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        const uint4 p = has0 && at < k ? __ldg(reinterpret_cast<const uint4*>(arow + at)) : z;
-        const uint4 q = has1 && at < k ? __ldg(reinterpret_cast<const uint4*>(arow + 8 * static_cast<size_t>(k) + at)) : z;
-        w0[4 * hh] = p.x, w0[4 * hh + 1] = p.y, w0[4 * hh + 2] = p.z, w0[4 * hh + 3] = p.w;
-        w1[4 * hh] = q.x, w1[4 * hh + 1] = q.y, w1[4 * hh + 2] = q.z, w1[4 * hh + 3] = q.w;
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (!((same >> (8 * j)) & 0xFFu)) continue;
-        const int row = min(row0 + 8 * j + g, t - 1);   // rows of others: their columns are not used
-        uint32_t b[8];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const int at = k0 + 16 * t4 + 8 * hh;
-          const uint4 p = at < k ? __ldg(reinterpret_cast<const uint4*>(x + row * ldx + at)) : make_uint4(0, 0, 0, 0);
-          b[4 * hh] = p.x, b[4 * hh + 1] = p.y, b[4 * hh + 2] = p.z, b[4 * hh + 3] = p.w;
-        }
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const uint32_t af[4] = {w0[2 * s], w1[2 * s], w0[2 * s + 1], w1[2 * s + 1]};
-          if (kBf16)
-            mma_bf16(acc[j], af, b[2 * s], b[2 * s + 1]);
-          else
-            mma_f16(acc[j], af, b[2 * s], b[2 * s + 1]);
-        }
-      }
+    if (r1 < rank) {
+      const bool has0 = r1 + g < rank, has1 = r1 + 8 + g < rank;
+      const int k0 = 64 * part, step = 64 * kSplit;
+      if (groups == 1)
+        down_products<kBf16, 1>(acc, arow, has0, has1, xrow, k, k0, step, t4);
+      else if (groups == 2)
+        down_products<kBf16, 2>(acc, arow, has0, has1, xrow, k, k0, step, t4);
+      else
+        down_products<kBf16, 4>(acc, arow, has0, has1, xrow, k, k0, step, t4);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][g + 8 * (i >> 1)][8 * j + 2 * t4 + (i & 1)] = acc[j][i];
+      for (int i = 0; i < 4; ++i)
+        red[part][16 * (warp % kMt) + g + 8 * (i >> 1)][8 * j + 2 * t4 + (i & 1)] = acc[j][i];
     __syncthreads();
-    const float sc = scale[ad];
-    for (int i = tid; i < 16 * kDownRows; i += 32 * kDownWarps) {
-      const int r = i & 15, c = i >> 4;
-      if (!((same >> c) & 1u) || r0 + r >= rank) continue;
+    for (int i = tid; i < 16 * kMt * rows; i += 32 * kDownWarps) {
+      const int r = i % (16 * kMt), c = i / (16 * kMt);
+      if (r0 + r >= rank) continue;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kDownWarps; ++w) v += red[w][r][c];
+      for (int w = 0; w < kSplit; ++w) v += red[w][r][c];
       v *= sc;
       // bf16 value and bf16 remainder: 16 significant bits, so u's rounding is far below the output's
       const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      uint16_t* dst = u + static_cast<size_t>(row0 + c) * 2 * rank + r0 + r;
+      uint16_t* dst = u + static_cast<size_t>(row0 + list[warp][c]) * 2 * rank + r0 + r;
       dst[0] = __bfloat16_as_ushort(hi);
       dst[rank] = float_to_bf16_bits(isfinite(v) ? v - __bfloat162float(hi) : 0.f);
     }
@@ -199,11 +236,15 @@ bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const 
 
 bool launch_adapter_down(bool bf16, const void* x, long long ldx, int t, const void* a, const float* scale,
                          const int32_t* ids, int n_adapters, int rank, int k, uint16_t* u, cudaStream_t s) {
-  const int blocks = (t + kDownRows - 1) / kDownRows, mt = (rank + 15) / 16;
-  // CTAs that share a block's distinct adapters: up to one each while the grid is small
-  const int shares = std::max(1, std::min({std::min(t, kDownRows), n_adapters, 1024 / std::max(1, blocks * mt)}));
-  const auto kernel = bf16 ? k_adapter_down<true> : k_adapter_down<false>;
-  return launch_pdl(kernel, dim3(blocks, mt, shares), 32 * kDownWarps, s, static_cast<const uint16_t*>(x), ldx, t,
+  // Few rows: a CTA for every 16 rank rows, and up to one for each distinct adapter of its 32 rows.  Many: all of the
+  // rank rows in one CTA, which then reads the rows of x once.
+  const int blocks = (t + kDownRows - 1) / kDownRows;
+  const bool many = blocks >= 64;
+  const int mt = (rank + 15) / 16, parts = many ? (mt + 3) / 4 : mt;
+  const int shares = std::max(1, std::min({std::min(t, kDownRows), n_adapters, 512 / (blocks * parts)}));
+  const auto kernel = bf16 ? (many ? k_adapter_down<true, 4> : k_adapter_down<true, 1>)
+                           : (many ? k_adapter_down<false, 4> : k_adapter_down<false, 1>);
+  return launch_pdl(kernel, dim3(blocks, parts, shares), 32 * kDownWarps, s, static_cast<const uint16_t*>(x), ldx, t,
                     static_cast<const uint16_t*>(a), scale, ids, n_adapters, rank, k, u);
 }
 

@@ -44,7 +44,6 @@ constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns 
 constexpr int kHalf = 16384;
 constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 32 bytes: multiples of 16, and the
 constexpr int kEpiPitch16 = 48;      // 16-byte words of eight rows hit all 32 banks
-constexpr int kPitch32 = 36;          // floats between staged rows of 32
 constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memory lanes, 32 columns in turn
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kBigThreads = 32 * (2 + kEpiWarps + 1);
@@ -72,7 +71,7 @@ struct BigSmem {
 };
 static_assert(sizeof(BigSmem<GM_FWD>) + 1024 <= 227 * 1024 && sizeof(BigSmem<GM_WGRAD>) + 1024 <= 227 * 1024,
               "one CTA per SM");
-static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes >= 8 * kPitch32 * 4 && kEpiBytes % 16 == 0 &&
+static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
                   kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0,
               "staged rows");
 
@@ -108,15 +107,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
   }
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ void store_out(void* y, long long i, float v, int f32, int bf16) {
-  if (f32)
-    static_cast<float*>(y)[i] = v;
-  else if (bf16)
-    static_cast<__nv_bfloat16*>(y)[i] = __float2bfloat16_rn(v);
-  else
-    static_cast<__half*>(y)[i] = __float2half_rn(v);
 }
 
 // Row range of expert e: inside [0, m] whatever the offsets hold.
@@ -186,14 +176,48 @@ __device__ __forceinline__ void split_f16x2(uint32_t v, uint32_t& hi, uint32_t& 
   lo = pack16(a - __low2float(h), b - __high2float(h), 1);
 }
 
-// v[mb][4j + i] += (B[id] u)[feature][row] for the 32 columns at c0.  The
-// fragments of the accumulator are those of an m16n8k16 product, so the term
-// is one: B's rows are its A operand, u (two bf16 halves, about 16 bits) its B
-// operand.  Each distinct adapter of the 32 rows is one pass whose result is
-// added to its own rows only, so nothing that one request's adapter holds
-// reaches another's output.
-__device__ __forceinline__ void add_adapters(float (&v)[2][16], const GmParams& p, int row0, int cols, int f0, int lane) {
-  const int g = lane >> 2, t4 = lane & 3;
+// B's fragments of one adapter for a warp's 32 features, up to 64 ranks.  The
+// order of the ranks inside a product is free as long as both operands share
+// it: lane quarter t4 takes the 4 ceil(rank / 16) consecutive ranks from
+// t4 times that on, so that a k16 step's share is one 8-byte word of a row.
+constexpr int kRankSteps = 4;
+struct AdapterFrags {
+  int id = -1;
+  uint32_t a[kRankSteps][2][4];
+};
+
+__device__ __forceinline__ int rank_at(int steps, int step, int t4) { return 4 * (steps * t4 + step); }
+
+__device__ __forceinline__ void load_adapter(AdapterFrags& F, const GmParams& p, int id, int f0, int step0, int lane) {
+  const int g = lane >> 2, t4 = lane & 3, steps = (p.rank + 15) / 16;
+  const uint16_t* b = p.b + static_cast<size_t>(id) * p.feat * p.rank;
+#pragma unroll
+  for (int s = 0; s < kRankSteps; ++s) {
+    const int at = rank_at(steps, step0 + s, t4);
+#pragma unroll
+    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int f = min(f0 + 16 * mb + 8 * r + g, p.feat - 1);   // rows past the end are never stored
+        const bool in = step0 + s < steps && at < p.rank;
+        const uint2 w = in ? __ldg(reinterpret_cast<const uint2*>(b + static_cast<size_t>(f) * p.rank + at))
+                           : make_uint2(0, 0);
+        F.a[s][mb][r] = w.x;
+        F.a[s][mb][2 + r] = w.y;
+      }
+  }
+}
+
+// v[mb][4j + i] += (B[id] u)[feature][row] for the 32 columns at row0.  The
+// accumulator's fragments are those of an m16n8k16 product, so the term is
+// one: B's rows are its A operand, u (two bf16 halves, 16 bits) its B operand.
+// Each distinct adapter of the 32 rows is one pass whose result is added to
+// its own rows only, so nothing that one request's adapter holds reaches
+// another's output.  The last adapter's fragments stay in registers: rows of a
+// prompt share theirs.  Two chains a product (the halves) hide its latency.
+__device__ __forceinline__ void add_adapters(float (&v)[2][16], AdapterFrags& F, const GmParams& p, int row0, int cols,
+                                             int f0, int lane) {
+  const int g = lane >> 2, t4 = lane & 3, steps = (p.rank + 15) / 16;
   int id = -1;
   if (lane < cols) {
     id = p.ids[row0 + lane];
@@ -204,58 +228,46 @@ __device__ __forceinline__ void add_adapters(float (&v)[2][16], const GmParams& 
     const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
     const uint32_t same = __ballot_sync(0xFFFFFFFFu, id == a);
     left &= ~same;
-    float d[2][16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) d[0][i] = d[1][i] = 0.f;
-    const uint16_t* b = p.b + static_cast<size_t>(a) * p.feat * p.rank;
-    for (int k = 0; k < p.rank; k += 16) {
-      const bool upper = k + 8 < p.rank;   // a rank of 8 mod 16 ends in half a step
-      uint32_t af[2][4];
-#pragma unroll
-      for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int f = min(f0 + 16 * mb + 8 * r + g, p.feat - 1);   // rows past the end are never stored
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(b + static_cast<size_t>(f) * p.rank + k + 2 * t4);
-          af[mb][r] = __ldg(src);
-          af[mb][2 + r] = upper ? __ldg(src + 4) : 0u;
-        }
+    for (int step0 = 0; step0 < steps; step0 += kRankSteps) {
+      if (F.id != a || steps > kRankSteps) load_adapter(F, p, a, f0, step0, lane);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (!((same >> (8 * j)) & 0xFFu)) continue;
-        const int row = row0 + min(8 * j + g, cols - 1);
-        const uint16_t* u = p.u + static_cast<size_t>(row) * 2 * p.rank + k + 2 * t4;
-        const uint32_t* uh = reinterpret_cast<const uint32_t*>(u);
-        const uint32_t* ul = reinterpret_cast<const uint32_t*>(u + p.rank);
-        const uint32_t h0 = __ldcg(uh), h1 = upper ? __ldcg(uh + 4) : 0u;
-        const uint32_t l0 = __ldcg(ul), l1 = upper ? __ldcg(ul + 4) : 0u;
+        // rows past the end and of other adapters: their columns are not used
+        const uint16_t* u = p.u + static_cast<size_t>(row0 + min(8 * j + g, cols - 1)) * 2 * p.rank;
+        uint2 hi[kRankSteps], lo[kRankSteps];
+#pragma unroll
+        for (int s = 0; s < kRankSteps; ++s) {
+          const int at = rank_at(steps, step0 + s, t4);
+          const bool in = step0 + s < steps && at < p.rank;
+          hi[s] = in ? __ldcg(reinterpret_cast<const uint2*>(u + at)) : make_uint2(0, 0);
+          lo[s] = in ? __ldcg(reinterpret_cast<const uint2*>(u + p.rank + at)) : make_uint2(0, 0);
+        }
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
-          float c[4] = {d[mb][4 * j], d[mb][4 * j + 1], d[mb][4 * j + 2], d[mb][4 * j + 3]};
-          if (p.bf16) {
-            mma_bf16(c, af[mb], h0, h1);
-            mma_bf16(c, af[mb], l0, l1);
-          } else {
-            uint32_t bh[4], bl[4];
+          float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) split_f16x2(af[mb][i], bh[i], bl[i]);
-            mma_bf16(c, bh, h0, h1);
-            mma_bf16(c, bh, l0, l1);
-            mma_bf16(c, bl, h0, h1);
+          for (int s = 0; s < kRankSteps; ++s) {
+            if (step0 + s >= steps) continue;
+            if (p.bf16) {
+              mma_bf16(c, F.a[s][mb], hi[s].x, hi[s].y);
+              mma_bf16(d, F.a[s][mb], lo[s].x, lo[s].y);
+            } else {
+              uint32_t bh[4], bl[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) split_f16x2(F.a[s][mb][i], bh[i], bl[i]);
+              mma_bf16(c, bh, hi[s].x, hi[s].y);
+              mma_bf16(d, bh, lo[s].x, lo[s].y);
+              mma_bf16(d, bl, hi[s].x, hi[s].y);
+            }
           }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[mb][4 * j + i] = c[i];
+          for (int i = 0; i < 4; ++i)
+            if ((same >> (8 * j + 2 * t4 + (i & 1))) & 1u) v[mb][4 * j + i] += c[i] + d[i];
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if ((same >> (8 * j + 2 * t4 + (i & 1))) & 1u) {
-          v[0][4 * j + i] += d[0][4 * j + i];
-          v[1][4 * j + i] += d[1][4 * j + i];
-        }
+    F.id = a;
   }
 }
 
@@ -291,77 +303,26 @@ __device__ __forceinline__ void store_32x32(uint32_t buf, const float (&v)[2][16
   }
 }
 
-// 32 features x 32 columns of fp32: 128 contiguous bytes of a column, eight
-// columns at a time.
-__device__ __forceinline__ void store_32x32_f32(uint32_t buf, const float (&v)[2][16], float* out, long long ld, int cols,
-                                                int feats, int lane) {
-  const int g = lane >> 2, t4 = lane & 3, f = 4 * (lane & 7);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    if (8 * j >= cols) break;
-    __syncwarp();
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(buf + ((2 * t4 + (i & 1)) * kPitch32 + 16 * mb + 8 * (i >> 1) + g) * 4),
-                     "f"(v[mb][4 * j + i])
-                     : "memory");
-    __syncwarp();
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int c = 4 * half + (lane >> 3);
-      const uint4 w = lds128(buf + (c * kPitch32 + f) * 4);
-      if (8 * j + c < cols && f < feats) *reinterpret_cast<uint4*>(out + (8 * j + c) * ld + f) = w;
-    }
-  }
-}
-
 // The weight gradient's stores: swizzled rows of 32 features in one of two
 // buffers, which the TMA engine writes out while the other is filled.  A
 // 64-byte segment of each column per warp and ordinary store kept the LSU's
 // data pipe at 66% and the kernel at 138 us (507 MB of fp16).
 __device__ __forceinline__ void tma_store_32x32(uint32_t buf, const float (&v)[2][16], const GmParams& p,
-                                                const CUtensorMap* map, int f0, int c0, int cols, int e, int lane,
-                                                bool lead, uint32_t& n_stores) {
-  const int g = lane >> 2, t4 = lane & 3;
-  if (p.out_f32) {
+                                                const CUtensorMap* map, int f0, int c0, int e, int lane, bool lead,
+                                                uint32_t& n_stores) {
+  const uint32_t at = buf + 2048 * (n_stores++ & 1);
+  if (lead) store_wait<1>();
+  __syncwarp();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {   // 16 columns of 128 bytes
-      if (16 * half >= cols) break;
-      if (lead) store_wait<1>();
-      __syncwarp();
-      const uint32_t at = buf + 2048 * (n_stores++ & 1);   // the store before last has read it
-#pragma unroll
-      for (int j = 2 * half; j < 2 * half + 2; ++j)
-#pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = 8 * (j & 1) + 2 * t4 + (i & 1), word = 4 * mb + 2 * (i >> 1) + (g >> 2);
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + 128 * c + 16 * (word ^ (c & 7)) + 4 * (g & 3)),
-                         "f"(v[mb][4 * j + i])
-                         : "memory");
-          }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lead) store_3d(map, at, f0, c0 + 16 * half, e);
-    }
-  } else {
-    const uint32_t at = buf + 2048 * (n_stores++ & 1);
-    if (lead) store_wait<1>();
-    __syncwarp();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = 8 * j + (lane & 7);
-      stmatrix4_trans(at + 64 * c + 16 * ((lane >> 3) ^ ((c >> 1) & 3)), pack16(v[0][4 * j], v[0][4 * j + 1], p.bf16),
-                      pack16(v[0][4 * j + 2], v[0][4 * j + 3], p.bf16), pack16(v[1][4 * j], v[1][4 * j + 1], p.bf16),
-                      pack16(v[1][4 * j + 2], v[1][4 * j + 3], p.bf16));
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lead) store_3d(map, at, f0, c0, e);
+  for (int j = 0; j < 4; ++j) {
+    const int c = 8 * j + (lane & 7);
+    stmatrix4_trans(at + 64 * c + 16 * ((lane >> 3) ^ ((c >> 1) & 3)), pack16(v[0][4 * j], v[0][4 * j + 1], p.bf16),
+                    pack16(v[0][4 * j + 2], v[0][4 * j + 3], p.bf16), pack16(v[1][4 * j], v[1][4 * j + 1], p.bf16),
+                    pack16(v[1][4 * j + 2], v[1][4 * j + 3], p.bf16));
   }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lead) store_3d(map, at, f0, c0, e);
 }
 
 // 16 features x 32 columns of 16-bit values (one 16-row block): staged here ...
@@ -544,7 +505,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
       const long long out0 =
           (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
       if (kEpi == GM_ADAPT) pdl_wait();   // the u rows
+      AdapterFrags frags;
+      // the accumulator goes back as soon as this warp has read its last columns, before they are stored
+      const auto release = [&](int c0) {
+        if (!T.steps || c0 + 64 < T.cols) return;
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
+      };
+      if (c_first >= T.cols) release(c_first);
       for (int c0 = c_first; c0 < T.cols; c0 += 64) {
+        if (kEpi == GM_PLAIN && p.out_f32) {
+          // a lane holds one feature of 32 columns: each store of the warp is 128 contiguous bytes of a column,
+          // straight from the accumulator
+          float w[32];
+          if (T.steps) {
+            ld_cols32(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), w);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = 0.f;
+          }
+          release(c0);
+          float* y = static_cast<float*>(p.y) + out0 + c0 * p.ldy + lane;
+          const int cols = T.cols - c0;
+          if (lane < feats) {
+            if (cols >= 32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) y[i * p.ldy] = w[i];
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < cols) y[i * p.ldy] = w[i];
+            }
+          }
+          continue;
+        }
         float v[2][16];
         if (T.steps) {
           ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
@@ -552,11 +547,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
         }
+        release(c0);
         if (feats <= 0) continue;
         const int cols = T.cols - c0;
-        if (kEpi == GM_ADAPT) add_adapters(v, p, T.c0 + c0, min(cols, 32), f0, lane);
+        if (kEpi == GM_ADAPT) add_adapters(v, frags, p, T.c0 + c0, min(cols, 32), f0, lane);
         if (kMode == GM_WGRAD) {
-          tma_store_32x32(buf16, v, p, &maps.b[1], f0, T.c0 + c0, cols, T.e, lane, lead, n_stores);
+          tma_store_32x32(buf16, v, p, &maps.b[1], f0, T.c0 + c0, T.e, lane, lead, n_stores);
         } else if (kEpi == GM_GATED) {
           __syncwarp();
           if (p.h) {
@@ -573,18 +569,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
           stage_16x32(buf16, v[0], p.bf16, lane);
           __syncwarp();
           store_16x32(buf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
-        } else if (p.out_f32) {
-          store_32x32_f32(buf16, v, static_cast<float*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         } else {
           store_32x32(buf16, v, p.bf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         }
       }
-      if (T.steps) {
-        fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
-        ++count;
-      }
+      if (T.steps) ++count;
     }
     if (lead) store_wait<0>();   // the last stores have read this CTA's shared memory
   } else if (kMode == GM_WGRAD) {
@@ -620,8 +609,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
 
 constexpr int kSmallCols = 64;                   // most columns of a tile
 constexpr int kSmallRing = 73728;                // 3 CTAs per SM: 4 stages of 16 columns, 3 of 64
+constexpr int kMaxSplit = 8;                     // CTAs that share a tile's reduction
 constexpr int kSmallPitch = 132;                 // floats between reduced columns
 static_assert(kSmallCols * kSmallPitch * 4 <= kSmallRing, "the reduction reuses the ring");
+
+// (B[id] u)[row][f .. f + 4) in fp32; 0 for a row without an adapter.
+__device__ __forceinline__ float4 adapter_values(const GmParams& p, int row, int f) {
+  const int id = p.ids[row];
+  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  if (id >= 0 && id < p.n_adapters) {
+    const uint16_t* b = p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank;
+    const uint16_t* u = p.u + static_cast<size_t>(row) * 2 * p.rank;
+    for (int j = 0; j < p.rank; j += 8) {
+      const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(u + j));
+      const uint4 lo = __ldcg(reinterpret_cast<const uint4*>(u + p.rank + j));
+      const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+      uint4 bv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bv[i] = __ldg(reinterpret_cast<const uint4*>(b + static_cast<size_t>(i) * p.rank + j));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float u0 = __uint_as_float(hw[w] << 16) + __uint_as_float(lw[w] << 16);
+        const float u1 = __uint_as_float(hw[w] & 0xFFFF0000u) + __uint_as_float(lw[w] & 0xFFFF0000u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = w == 0 ? bv[i].x : w == 1 ? bv[i].y : w == 2 ? bv[i].z : bv[i].w;
+          d[i] += (p.bf16 ? __uint_as_float(v << 16) : half_lo(v)) * u0;
+          d[i] += (p.bf16 ? __uint_as_float(v & 0xFFFF0000u) : half_hi(v)) * u1;
+        }
+      }
+    }
+  }
+  return make_float4(d[0], d[1], d[2], d[3]);
+}
+
+// Four consecutive values of an output row.
+__device__ __forceinline__ void store_out4(void* y, long long i, float4 v, int f32, int bf16) {
+  if (f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(y) + i) = v;
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + i) = make_uint2(pack16(v.x, v.y, bf16), pack16(v.z, v.w, bf16));
+}
 
 template <int kMode, int kEpi>
 __global__ void __launch_bounds__(192)
@@ -637,49 +665,55 @@ __global__ void __launch_bounds__(192)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank()), f0 = blockIdx.x / split * kFeat;
 
-  if (kEpi != GM_ADAPT) pdl_wait();   // adapters: nothing before the u rows comes from the previous kernel
+  if (warp == 1) {
+    tmem_alloc<false>(&s_tmem, kSmallCols);
+  } else if (tid == 64) {
+    prefetch_map(&maps.a);
+    s_abort = 0;
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    fence_mbar_init();
+  }
+  if (kEpi != GM_ADAPT) pdl_wait();   // adapters: nothing but the u rows comes from the previous kernel
   pdl_trigger();
   if (warp == 0) {
-    // column tile blockIdx.y: an expert's rows in equal parts of at most kSmallCols
-    int base = 0, found = 0;
-    for (int e0 = 0; e0 < p.E && !found; e0 += 32) {
-      const int e = e0 + lane;
-      int lo = 0, hi = 0;
-      if (e < p.E) {
-        lo = p.offsets ? clamp_off(p.offsets[e], p.m) : 0;
-        hi = p.offsets ? clamp_off(p.offsets[e + 1], p.m) : p.m;
+    // column tile blockIdx.y: an expert's rows in equal parts of at most kSmallCols.  A lane takes four experts at
+    // a time, so that up to 128 experts' offsets are one round of loads.
+    int base = 0;
+    if (lane == 0) s_tile[2] = 0;
+    __syncwarp();
+    for (int e0 = 0; e0 < p.E; e0 += 128) {
+      int off[5], c = 0;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        const int e = min(e0 + 4 * lane + i, p.E);
+        off[i] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
       }
-      const int rows = max(hi - lo, 0), nt = (rows + kSmallCols - 1) / kSmallCols;
-      int c = nt;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) c += (max(off[i + 1] - off[i], 0) + kSmallCols - 1) / kSmallCols;
+      int before = c;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, c, d);
-        if (lane >= d) c += o;
+        const int o = __shfl_up_sync(0xFFFFFFFFu, before, d);
+        if (lane >= d) before += o;
       }
-      const int at = static_cast<int>(blockIdx.y) - (base + c - nt);
-      const bool mine = at >= 0 && at < nt;
-      if (mine) {
-        const int width = ((rows + nt - 1) / nt + 15) & ~15;
-        s_tile[0] = e;
-        s_tile[1] = lo + at * width;
-        s_tile[2] = min(width, rows - at * width);
+      int at = static_cast<int>(blockIdx.y) - (base + before - c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rows = max(off[i + 1] - off[i], 0), nt = (rows + kSmallCols - 1) / kSmallCols;
+        if (at >= 0 && at < nt) {
+          const int width = ((rows + nt - 1) / nt + 15) & ~15;
+          s_tile[0] = e0 + 4 * lane + i;
+          s_tile[1] = off[i] + at * width;
+          s_tile[2] = min(width, rows - at * width);
+        }
+        at -= nt;
       }
-      found = __any_sync(0xFFFFFFFFu, mine);
-      base += __shfl_sync(0xFFFFFFFFu, c, 31);
+      base += __shfl_sync(0xFFFFFFFFu, before, 31);
     }
-    if (lane == 0) {
-      if (!found) s_tile[2] = 0;
-      s_abort = 0;
-      for (int i = 0; i < 8; ++i) {
-        mbar_init(&full[i], 1);
-        mbar_init(&empty[i], 1);
-      }
-      mbar_init(&acc_full, 1);
-      fence_mbar_init();
-      prefetch_map(&maps.a);
-    }
-  } else if (warp == 1) {
-    tmem_alloc<false>(&s_tmem, kSmallCols);
   }
   fence_before();
   __syncthreads();
@@ -736,8 +770,29 @@ __global__ void __launch_bounds__(192)
   }
   __syncwarp();
   float* part = reinterpret_cast<float*>(ring);   // [column][kSmallPitch], after every product has read the ring
+  // Columns rank, rank + split, ... of the tile are this CTA's to finish, one warp (GM_GATED: half a warp) a column
+  // and four features a lane.
+  constexpr int kLanes = kFeat / 4;
+  const int i0 = tid - 64, fi = 4 * (i0 % kLanes), f = f0 + fi, first = rank + split * (i0 / kLanes);
+  const int step = split * (128 / kLanes);
+  constexpr int kEarly = kEpi == GM_ADAPT ? kSmallCols / kMaxSplit / 4 : 1;
+  float4 delta[kEarly];
   bool ok = true;
   if (warp >= 2) {
+    if (kEpi == GM_ADAPT && f < p.feat) {
+      // the adapters' rows come to L2 before the weights queue up in front of them; B u while the weights stream, for
+      // the first columns
+      for (int c = first; c < rows; c += step) {
+        const int id = p.ids[row0 + c];
+        if (id >= 0 && id < p.n_adapters)
+          for (int j = 0; j < 4 * p.rank; j += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank + j));
+      }
+      pdl_wait();
+#pragma unroll
+      for (int i = 0; i < kEarly; ++i)
+        if (first + i * step < rows) delta[i] = adapter_values(p, row0 + first + i * step, f);
+    }
     ok = mbar_wait_bounded(&acc_full, 0, err_word()) && !s_abort;
     fence_after();
     const int q = warp & 3;
@@ -755,49 +810,45 @@ __global__ void __launch_bounds__(192)
   else
     __syncthreads();
   if (warp >= 2 && ok) {
-    if (kEpi == GM_ADAPT) pdl_wait();
-    const int i = tid - 64, fi = kEpi == GM_GATED ? i & 63 : i, f = f0 + fi;
-    const int step = kEpi == GM_GATED ? 2 * split : split;
-    const uint32_t base = smem_u32(part);
-    for (int c = kEpi == GM_GATED ? 2 * rank + (i >> 6) : rank; c < rows; c += step) {
-      const int lane_of = kEpi == GM_GATED ? (fi >> 4) * 32 + (fi & 15) : fi;
-      float v = 0.f, up = 0.f;
-      for (int r = 0; r < split; ++r) {
-        const uint32_t at = map_rank(base, r) + (c * kSmallPitch + lane_of) * 4;
-        v += ld_cluster_f32(at);
-        if (kEpi == GM_GATED) up += ld_cluster_f32(at + 64);
+    const int lane_of = kEpi == GM_GATED ? (fi >> 4) * 32 + (fi & 15) : fi;
+    uint32_t from[kMaxSplit];   // these features' first column in each CTA's part
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r) from[r] = map_rank(smem_u32(part) + lane_of * 4, min(r, split - 1));
+    const auto add = [](float4& x, const float4& y) { x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w; };
+    const auto finish = [&](int c, const float4& term) {
+      const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 pv[kMaxSplit], pu[kMaxSplit], v = zero, up = zero;
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r) {   // every load before the first sum; the sum in rank order
+        pv[r] = ld_cluster_f32x4(from[r] + c * kSmallPitch * 4, r < split);
+        if (kEpi == GM_GATED) pu[r] = ld_cluster_f32x4(from[r] + c * kSmallPitch * 4 + 64, r < split);
       }
-      if (f >= p.feat) continue;
+#pragma unroll
+      for (int r = 0; r < kMaxSplit; ++r) {
+        add(v, pv[r]);
+        if (kEpi == GM_GATED) add(up, pu[r]);
+      }
       const long long row = row0 + c;
       if (kEpi == GM_GATED) {
         if (p.h) {
-          store_out(p.h, row * p.ldh + f, v, 0, p.bf16);
-          store_out(p.h, row * p.ldh + p.feat + f, up, 0, p.bf16);
+          store_out4(p.h, row * p.ldh + f, v, 0, p.bf16);
+          store_out4(p.h, row * p.ldh + p.feat + f, up, 0, p.bf16);
         }
-        v = gelu(v, p.gelu) * up;
+        v = make_float4(gelu(v.x, p.gelu) * up.x, gelu(v.y, p.gelu) * up.y, gelu(v.z, p.gelu) * up.z,
+                        gelu(v.w, p.gelu) * up.w);
       }
+      if (kEpi == GM_ADAPT) add(v, term);
+      store_out4(p.y, row * p.ldy + f, v, p.out_f32, p.bf16);
+    };
+    int c = first;
+    if (f < p.feat) {
       if (kEpi == GM_ADAPT) {
-        const int id = p.ids[row];
-        if (id >= 0 && id < p.n_adapters) {
-          const uint4* b = reinterpret_cast<const uint4*>(p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank);
-          const uint4* u = reinterpret_cast<const uint4*>(p.u + static_cast<size_t>(row) * 2 * p.rank);
-          float d = 0.f;
-          for (int j = 0; j < p.rank / 8; ++j) {
-            const uint4 bv = __ldg(b + j), hi = __ldcg(u + j), lo = __ldcg(u + p.rank / 8 + j);
-            const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w},
-                           lw[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const float b0 = p.bf16 ? __uint_as_float(bw[w] << 16) : half_lo(bw[w]);
-              const float b1 = p.bf16 ? __uint_as_float(bw[w] & 0xFFFF0000u) : half_hi(bw[w]);
-              d += b0 * (__uint_as_float(hw[w] << 16) + __uint_as_float(lw[w] << 16));
-              d += b1 * (__uint_as_float(hw[w] & 0xFFFF0000u) + __uint_as_float(lw[w] & 0xFFFF0000u));
-            }
-          }
-          v += d;
-        }
+        for (int i = 0; i < kEarly; ++i, c += step)
+          if (c < rows) finish(c, delta[i]);
       }
-      store_out(p.y, row * p.ldy + f, v, p.out_f32, p.bf16);
+      for (; c < rows; c += step)
+        finish(c, kEpi == GM_ADAPT ? adapter_values(p, row0 + c, f) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
   if (split > 1)
@@ -887,7 +938,7 @@ bool launch_small(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s
   const int ft = (p.feat + kFeat - 1) / kFeat, tiles = std::min(p.E, p.m) + p.m / kSmallCols;
   const int steps = (p.red + 63) / 64;
   int split = 1;   // CTAs that share a tile's reduction: enough for three CTAs on every SM, at least two k64 steps each
-  while (split < 8 && 2 * split * ft * static_cast<long long>(tiles) <= 3 * sms && 4 * split <= steps) split *= 2;
+  while (split < kMaxSplit && 2 * split * ft * static_cast<long long>(tiles) <= 3 * sms && 4 * split <= steps) split *= 2;
   return launch(k_grouped_small<kMode, kEpi>, dim3(ft * split, tiles), 192, kSmallRing + 1024, split, s, maps, p, split);
 }
 
@@ -903,10 +954,10 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
   if (mode == GM_WGRAD) {
     if (!map_rows(&maps.a, o.x, o.k, p.m, o.ldx, 64, p.bf16) || !map_rows(&maps.b[0], o.w, o.n, p.m, o.ldw, 64, p.bf16))
       return false;
-    const cuuint64_t row = static_cast<cuuint64_t>(o.k) * (p.out_f32 ? 4 : 2);
+    const cuuint64_t row = static_cast<cuuint64_t>(o.k) * 2;
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
     const cuuint64_t stride[2] = {row, row * o.n};
-    if (!encode_store(&maps.b[1], p.y, dim, stride, p.out_f32 ? 16 : 32, p.out_f32, p.bf16)) return false;
+    if (!p.out_f32 && !encode_store(&maps.b[1], p.y, dim, stride, p.bf16)) return false;
     return launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);

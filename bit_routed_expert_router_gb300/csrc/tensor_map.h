@@ -36,17 +36,13 @@ inline bool encode_tiles(CUtensorMap* m, const void* base, int rank, const cuuin
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A map for stores of 32 consecutive values: rows of 64 bytes (16-bit) or 128
-// bytes (fp32) in shared memory, swizzled over their own width.
-inline bool encode_store(CUtensorMap* m, void* base, const cuuint64_t (&dim)[3], const cuuint64_t (&stride)[2], int rows,
-                         bool f32, bool bf16) {
+// A map over bf16 or fp16 values for stores of 32 x 32: rows of 64 bytes in
+// shared memory, swizzled over their own width.
+inline bool encode_store(CUtensorMap* m, void* base, const cuuint64_t (&dim)[3], const cuuint64_t (&stride)[2], bool bf16) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  const cuuint32_t box[3] = {32, static_cast<cuuint32_t>(rows), 1}, ones[3] = {1, 1, 1};
-  return encode && encode(m, f32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                             : bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                          3, base, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+  const cuuint32_t box[3] = {32, 32, 1}, ones[3] = {1, 1, 1};
+  return encode && encode(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dim,
+                          stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -141,7 +141,7 @@ template <bool kBf16, int kMt>
 __global__ void __launch_bounds__(32 * kDownWarps)
     k_adapter_down(const uint16_t* __restrict__ x, long long ldx, int t, const uint16_t* __restrict__ a,
                    const float* __restrict__ scale, const int32_t* __restrict__ ids, int n_adapters, int rank, int k,
-                   uint16_t* u) {
+                   float* u) {
   constexpr int kSplit = kDownWarps / kMt;
   __shared__ float red[kSplit][16 * kMt][kDownRows + 1];
   __shared__ uint8_t list[kDownWarps][kDownRows];   // a warp's own copy: the adapter's rows in order
@@ -197,12 +197,7 @@ __global__ void __launch_bounds__(32 * kDownWarps)
       float v = 0.f;
 #pragma unroll
       for (int w = 0; w < kSplit; ++w) v += red[w][r][c];
-      v *= sc;
-      // bf16 value and bf16 remainder: 16 significant bits, so u's rounding is far below the output's
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      uint16_t* dst = u + static_cast<size_t>(row0 + list[warp][c]) * 2 * rank + r0 + r;
-      dst[0] = __bfloat16_as_ushort(hi);
-      dst[rank] = float_to_bf16_bits(isfinite(v) ? v - __bfloat162float(hi) : 0.f);
+      u[static_cast<size_t>(row0 + list[warp][c]) * rank + r0 + r] = v * sc;
     }
     __syncthreads();
   }
@@ -235,7 +230,7 @@ bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const 
 }
 
 bool launch_adapter_down(bool bf16, const void* x, long long ldx, int t, const void* a, const float* scale,
-                         const int32_t* ids, int n_adapters, int rank, int k, uint16_t* u, cudaStream_t s) {
+                         const int32_t* ids, int n_adapters, int rank, int k, float* u, cudaStream_t s) {
   // Few rows: a CTA for every 16 rank rows, and up to one for each distinct adapter of its 32 rows.  Many: all of the
   // rank rows in one CTA, which then reads the rows of x once.
   const int blocks = (t + kDownRows - 1) / kDownRows;

@@ -29,7 +29,7 @@ struct GmParams {
   int gelu = 0;
   const int32_t* ids = nullptr;       // GM_ADAPT: adapter of each row
   const uint16_t* b = nullptr;        // [n_adapters][feat][rank]
-  const uint16_t* u = nullptr;        // bf16 [m][2][rank]: s A x as a sum of two bf16 values
+  const float* u = nullptr;           // [m][rank]: s A x, 32-byte aligned
   int rank = 0, n_adapters = 0;
 };
 
@@ -52,8 +52,8 @@ bool grouped_error(cudaStream_t s, uint32_t* err);
 bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const void* da, long long ldda, void* dh,
                        long long lddh, int m, int f, const int32_t* n_rows, cudaStream_t s);
 
-// u[t] = scale[id] A[id] x[t] for every row with an adapter, as two bf16 halves.
+// u[t] = scale[id] A[id] x[t] for every row with an adapter.
 bool launch_adapter_down(bool bf16, const void* x, long long ldx, int t, const void* a, const float* scale,
-                         const int32_t* ids, int n_adapters, int rank, int k, uint16_t* u, cudaStream_t s);
+                         const int32_t* ids, int n_adapters, int rank, int k, float* u, cudaStream_t s);
 
 }  // namespace moe

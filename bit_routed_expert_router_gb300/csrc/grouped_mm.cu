@@ -46,30 +46,43 @@ constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 3
 constexpr int kEpiPitch16 = 48;      // 16-byte words of eight rows hit all 32 banks
 constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memory lanes, 32 columns in turn
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
-constexpr int kBigThreads = 32 * (2 + kEpiWarps + 1);
+constexpr int kUWarps = 4;           // adapters: warps that stage u
 constexpr int kAccCols = 256;
 
 // The weight gradient's tiles have few stages each and store far more than they
 // load: two buffers a warp for TMA stores, and a stage less.
-template <int kMode>
+template <int kMode, int kEpi>
 struct BigCfg {
   static constexpr int kStages = kMode == GM_WGRAD ? 5 : 6;
-  static constexpr int kEpiBytes = kMode == GM_WGRAD ? 4096 : moe::kEpiBytes;
+  static constexpr int kEpiBytes = kMode == GM_WGRAD ? 4096 : kEpi == GM_ADAPT ? 4 * 8 * kEpiPitch : moe::kEpiBytes;
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + (kEpi == GM_ADAPT ? kUWarps : kMode == GM_WGRAD ? 1 : 0));
 };
 
-template <int kMode>
+struct AdaptSmem {
+  int id[2][256];          // adapter of each column of a tile, -1 for none (tiles alternate)
+  int list[2][256];        // its distinct adapters, in order
+  int n_list[2], n_group[8];
+  volatile int broken[2];  // a value of the tile's B rows is not finite
+  uint64_t u_full[8], list_full[2], list_empty[2];
+};
+struct NoSmem {};
+
+template <int kMode, int kEpi>
 struct BigSmem {
-  static constexpr int kStages = BigCfg<kMode>::kStages;
+  static constexpr int kStages = BigCfg<kMode, kEpi>::kStages;
   uint8_t stage[kStages][kStageBytes];
-  alignas(1024) uint8_t epi[kEpiWarps][BigCfg<kMode>::kEpiBytes];
+  alignas(1024) uint8_t epi[kEpiWarps][BigCfg<kMode, kEpi>::kEpiBytes];
   uint64_t full[kStages], empty[kStages], tail[kStages];
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   volatile int abort;
-  int off[kMaxE + 1];    // clamped to [0, m]
-  int tiles[kMaxE + 1];  // column tiles before each expert
+  std::conditional_t<kEpi == GM_ADAPT, AdaptSmem, NoSmem> ad;
+  int off[(kEpi == GM_ADAPT ? 1 : kMaxE) + 1];    // clamped to [0, m]
+  int tiles[(kEpi == GM_ADAPT ? 1 : kMaxE) + 1];  // column tiles before each expert
 };
-static_assert(sizeof(BigSmem<GM_FWD>) + 1024 <= 227 * 1024 && sizeof(BigSmem<GM_WGRAD>) + 1024 <= 227 * 1024,
+static_assert(sizeof(BigSmem<GM_FWD, GM_PLAIN>) + 1024 <= 227 * 1024 &&
+                  sizeof(BigSmem<GM_FWD, GM_ADAPT>) + 1024 <= 227 * 1024 &&
+                  sizeof(BigSmem<GM_WGRAD, GM_PLAIN>) + 1024 <= 227 * 1024,
               "one CTA per SM");
 static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
                   kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0,
@@ -119,6 +132,7 @@ __device__ __forceinline__ int clamp_off(int v, int m) { return min(max(v, 0), m
 constexpr int kRowMaps = 8;
 struct GmMaps {
   CUtensorMap a;
+  CUtensorMap c;   // adapters: their B; weight gradient: the output
   CUtensorMap b[kRowMaps];
 };
 
@@ -131,8 +145,8 @@ struct Tile {
 
 // Tile t of the launch in the order expert, feature tile, column tile: the
 // pairs that run together share an expert's rows and weights through L2.
-template <int kMode, int kFeat>
-__device__ __forceinline__ bool tile_at(const BigSmem<kMode>& S, const GmParams& p, int t, int& e, Tile& T) {
+template <int kMode, int kFeat, typename Smem>
+__device__ __forceinline__ bool tile_at(const Smem& S, const GmParams& p, int t, int& e, Tile& T) {
   const int ft = (p.feat + kFeat - 1) / kFeat;
   if constexpr (kMode == GM_WGRAD) {
     const int ct = (p.cols + 255) / 256, per = ft * ct;
@@ -167,108 +181,90 @@ __device__ __forceinline__ bool tile_at(const BigSmem<kMode>& S, const GmParams&
 
 // ------------------------------------------------------------------ adapter term of the epilogue
 
-// Two fp16 values as the exact sum of two bf16 pairs.
-__device__ __forceinline__ void split_f16x2(uint32_t v, uint32_t& hi, uint32_t& lo) {
-  // an fp16 value has 11 significant bits: bf16 hi (8) + lo (the other 3) is exact
-  const float a = half_lo(v), b = half_hi(v);
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack16(a - __low2float(h), b - __high2float(h), 1);
+// Two fp32 values in one register pair, and d = a b + d on both at once.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ void fma_f32x2(uint64_t& d, uint64_t a, uint64_t b) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
-// B's fragments of one adapter for a warp's 32 features, up to 64 ranks.  The
-// order of the ranks inside a product is free as long as both operands share
-// it: lane quarter t4 takes the 4 ceil(rank / 16) consecutive ranks from
-// t4 times that on, so that a k16 step's share is one 8-byte word of a row.
-constexpr int kRankSteps = 4;
-struct AdapterFrags {
-  int id = -1;
-  uint32_t a[kRankSteps][2][4];
-};
-
-__device__ __forceinline__ int rank_at(int steps, int step, int t4) { return 4 * (steps * t4 + step); }
-
-__device__ __forceinline__ void load_adapter(AdapterFrags& F, const GmParams& p, int id, int f0, int step0, int lane) {
-  const int g = lane >> 2, t4 = lane & 3, steps = (p.rank + 15) / 16;
-  const uint16_t* b = p.b + static_cast<size_t>(id) * p.feat * p.rank;
+// Eight 16-bit values as four pairs of floats.
+__device__ __forceinline__ void widen8(uint64_t (&o)[4], uint4 v, int bf16) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int s = 0; s < kRankSteps; ++s) {
-    const int at = rank_at(steps, step0 + s, t4);
-#pragma unroll
-    for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int f = min(f0 + 16 * mb + 8 * r + g, p.feat - 1);   // rows past the end are never stored
-        const bool in = step0 + s < steps && at < p.rank;
-        const uint2 w = in ? __ldg(reinterpret_cast<const uint2*>(b + static_cast<size_t>(f) * p.rank + at))
-                           : make_uint2(0, 0);
-        F.a[s][mb][r] = w.x;
-        F.a[s][mb][2 + r] = w.y;
-      }
-  }
+  for (int i = 0; i < 4; ++i)
+    o[i] = bf16 ? pack_f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u))
+                : pack_f32x2(half_lo(w[i]), half_hi(w[i]));
 }
 
-// v[mb][4j + i] += (B[id] u)[feature][row] for the 32 columns at row0.  The
-// accumulator's fragments are those of an m16n8k16 product, so the term is
-// one: B's rows are its A operand, u (two bf16 halves, 16 bits) its B operand.
-// Each distinct adapter of the 32 rows is one pass whose result is added to
-// its own rows only, so nothing that one request's adapter holds reaches
-// another's output.  The last adapter's fragments stay in registers: rows of a
-// prompt share theirs.  Two chains a product (the halves) hide its latency.
-__device__ __forceinline__ void add_adapters(float (&v)[2][16], AdapterFrags& F, const GmParams& p, int row0, int cols,
-                                             int f0, int lane) {
-  const int g = lane >> 2, t4 = lane & 3, steps = (p.rank + 15) / 16;
-  int id = -1;
-  if (lane < cols) {
-    id = p.ids[row0 + lane];
-    if (id < 0 || id >= p.n_adapters) id = -1;
+// Eight floats of u, the same address in every lane.
+__device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
+  asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(o[0]), "=l"(o[1]), "=l"(o[2]), "=l"(o[3]) : "l"(u));
+}
+
+// ---- the adapters' term in the persistent kernel
+//
+// y = W x + B_i u is a longer reduction: behind the k64 steps of W and x come
+// steps whose features' operand is B_i and whose columns' operand is u, zero in
+// the rows of other adapters; one pair of steps (u as a value of the operands'
+// type and its remainder, 16 bits of bf16 or 22 of fp16) for each distinct
+// adapter of the tile's rows and 64 ranks.  Four warps of each CTA list the
+// tile's adapters, write u's steps and look through the B rows that TMA loaded
+// for them: a value that is not finite would reach every column (0 times
+// infinity), so it is cleared and the tile marked, and the storing warps put
+// NaN where it belongs.  (As mma.sync products in the epilogue the term took
+// the kernel from 45 to 115 us at 4096 rows and rank 64, since they wait for the
+// tcgen05 products; on the ordinary pipes 145, bound by broadcast loads.)
+
+// True if one of the 16-bit values of v is infinite or NaN (all exponent bits set).
+__device__ __forceinline__ uint32_t not_finite(uint32_t v, int bf16) {
+  const uint32_t mask = bf16 ? 0x7F807F80u : 0x7C007C00u, one = bf16 ? 0x00800080u : 0x04000400u;
+  return ((v & mask) + one) & 0x80008000u;
+}
+
+__device__ __noinline__ bool row_broken(const uint16_t* b, int rank, int bf16) {
+  uint32_t bad = 0;
+  for (int k = 0; k < rank; k += 8) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + k));
+    bad |= not_finite(w.x, bf16) | not_finite(w.y, bf16) | not_finite(w.z, bf16) | not_finite(w.w, bf16);
   }
-  uint32_t left = __ballot_sync(0xFFFFFFFFu, id >= 0);
-  while (left) {
-    const int a = __shfl_sync(0xFFFFFFFFu, id, __ffs(left) - 1);
-    const uint32_t same = __ballot_sync(0xFFFFFFFFu, id == a);
-    left &= ~same;
-    for (int step0 = 0; step0 < steps; step0 += kRankSteps) {
-      if (F.id != a || steps > kRankSteps) load_adapter(F, p, a, f0, step0, lane);
+  return bad != 0;
+}
+
+// Columns row0 .. and this warp's 32 features: NaN where the row's adapter has a value that is not finite.
+__device__ __forceinline__ void mark_broken(float (&v)[2][16], const GmParams& p, int row0, int cols, int f0, int lane) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (!((same >> (8 * j)) & 0xFFu)) continue;
-        // rows past the end and of other adapters: their columns are not used
-        const uint16_t* u = p.u + static_cast<size_t>(row0 + min(8 * j + g, cols - 1)) * 2 * p.rank;
-        uint2 hi[kRankSteps], lo[kRankSteps];
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int s = 0; s < kRankSteps; ++s) {
-          const int at = rank_at(steps, step0 + s, t4);
-          const bool in = step0 + s < steps && at < p.rank;
-          hi[s] = in ? __ldcg(reinterpret_cast<const uint2*>(u + at)) : make_uint2(0, 0);
-          lo[s] = in ? __ldcg(reinterpret_cast<const uint2*>(u + p.rank + at)) : make_uint2(0, 0);
-        }
+    for (int i = 0; i < 4; ++i) {
+      const int c = 8 * j + 2 * (lane & 3) + (i & 1);
+      const int id = c < cols ? p.ids[row0 + c] : -1;
+      if (id < 0 || id >= p.n_adapters) continue;
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int s = 0; s < kRankSteps; ++s) {
-            if (step0 + s >= steps) continue;
-            if (p.bf16) {
-              mma_bf16(c, F.a[s][mb], hi[s].x, hi[s].y);
-              mma_bf16(d, F.a[s][mb], lo[s].x, lo[s].y);
-            } else {
-              uint32_t bh[4], bl[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) split_f16x2(F.a[s][mb][i], bh[i], bl[i]);
-              mma_bf16(c, bh, hi[s].x, hi[s].y);
-              mma_bf16(d, bh, lo[s].x, lo[s].y);
-              mma_bf16(d, bl, hi[s].x, hi[s].y);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((same >> (8 * j + 2 * t4 + (i & 1))) & 1u) v[mb][4 * j + i] += c[i] + d[i];
-        }
+      for (int mb = 0; mb < 2; ++mb) {
+        const int f = f0 + 16 * mb + 8 * (i >> 1) + (lane >> 2);
+        if (f < p.feat && row_broken(p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank, p.rank, p.bf16))
+          v[mb][4 * j + i] = __uint_as_float(0x7FC00000u);
       }
     }
-    F.id = a;
+}
+
+// Eight values of u as the operands' type (kLo: what that leaves).
+template <bool kLo>
+__device__ __forceinline__ uint4 u_words(const float4& a, const float4& b, int bf16) {
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
+    if (kLo) {
+      const float h0 = bf16 ? __uint_as_float(w[i] << 16) : half_lo(w[i]);
+      const float h1 = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : half_hi(w[i]);
+      w[i] = pack16(isfinite(h0) ? v[2 * i] - h0 : 0.f, isfinite(h1) ? v[2 * i + 1] - h1 : 0.f, bf16);
+    }
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ------------------------------------------------------------------ the persistent kernel
@@ -347,12 +343,12 @@ __device__ __forceinline__ void store_16x32(uint32_t buf, uint16_t* out, long lo
 }
 
 template <int kMode, int kEpi>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>::kThreads, 1)
     k_grouped(const __grid_constant__ GmMaps maps, GmParams p) {
   constexpr bool kTa = kMode != GM_FWD, kTb = kMode == GM_WGRAD;
   constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;   // features of a pair's tile
   extern __shared__ uint8_t smem_raw[];
-  using Smem = BigSmem<kMode>;
+  using Smem = BigSmem<kMode, kEpi>;
   constexpr int kStages = Smem::kStages;
   Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -365,10 +361,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
       mbar_init(&S.full[i], kMode == GM_WGRAD ? 2 : 1);
       mbar_init(&S.empty[i], 1);
       mbar_init(&S.tail[i], 1);
+      if constexpr (kEpi == GM_ADAPT) mbar_init(&S.ad.u_full[i], 2 * kUWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.acc_full[i], 1);
       mbar_init(&S.acc_empty[i], 2 * kEpiWarps);
+      if constexpr (kEpi == GM_ADAPT) {
+        mbar_init(&S.ad.list_full[i], 1);
+        mbar_init(&S.ad.list_empty[i], kEpiWarps + (rank == 0 ? 2 : 1));   // and the loading and the issuing warp
+      }
     }
     mbar_init(&S.drain, 1);
     S.abort = 0;
@@ -377,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
   if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
   if (kEpi != GM_ADAPT) pdl_wait();   // adapters: only their u rows come from the previous kernel
   pdl_trigger();
-  for (int e = tid; e <= p.E; e += blockDim.x)
+  for (int e = tid; e <= p.E; e += BigCfg<kMode, kEpi>::kThreads)
     S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
   __syncthreads();
   if (kMode != GM_WGRAD && warp == 0) {
@@ -404,7 +405,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
   if (warp == 0) {
     if (elect_one()) {
       const uint32_t lead_full = map_rank(smem_u32(S.full), 0);
-      uint32_t it = 0;
+      uint32_t it = 0, n_tile = 0;
+      uint32_t extra = 0, fulls = 0, tails = 0;   // by stage: last loaded for an adapter's step; phases issued
       int e = 0;
       Tile T;
       for (int t = first; !S.abort && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
@@ -444,15 +446,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
             }
             load_2d<true>(b, &maps.b[half / 16 - 1], 64 * ks, T.c0 + rank * half, bar);
           }
+          extra &= ~(1u << s);
+          fulls ^= 1u << s;
+        }
+        if constexpr (kEpi == GM_ADAPT) {
+          const int lb = n_tile & 1;
+          if (wait_bar(&S.ad.list_full[lb], (n_tile >> 1) & 1, &S.abort)) {
+            for (int j = 0; j < S.ad.n_list[lb] && !S.abort; ++j)
+              for (int k = 0; k < p.rank && !S.abort; k += 64)
+                for (int h = 0; h < 2; ++h, ++it) {
+                  const int s = it % kStages;
+                  if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
+                  mbar_arrive_expect_tx(&S.tail[s], kHalf);
+                  load_3d<true>(smem_u32(S.stage[s]), &maps.c, k, T.f0 + 128 * rank, S.ad.list[lb][j],
+                                smem_u32(&S.tail[s]));
+                  extra |= 1u << s;
+                  tails ^= 1u << s;
+                }
+            mbarrier_arrive(&S.ad.list_empty[lb]);
+          }
+          ++n_tile;
         }
       }
-      if (S.abort && rank == 0)   // copies already issued land before the pair leaves
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-          mbar_wait_bounded(&S.full[i % kStages], (i / kStages) & 1, err_word());
+      if (S.abort)   // copies already issued land before the pair leaves
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
+          const int s = i % kStages;
+          if ((extra >> s) & 1u)
+            mbar_wait_bounded(&S.tail[s], ((tails >> s) & 1) ^ 1, err_word());
+          else if (rank == 0)
+            mbar_wait_bounded(&S.full[s], ((fulls >> s) & 1) ^ 1, err_word());
+        }
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      uint32_t it = 0, count = 0;
+      uint32_t it = 0, count = 0, fulls = 0, us = 0;   // fulls, us: phases seen, by stage
       int e = 0;
       bool ok = true;
       Tile T;
@@ -463,21 +490,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
         fence_after();
         const uint32_t d = tmem + buf * kAccCols, idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb);
         const int red = kMode == GM_WGRAD ? T.rows : p.red;
-        for (int ks = 0; ok && ks < T.steps; ++ks, ++it) {
-          const int s = it % kStages;
-          const uint32_t par = (it / kStages) & 1;
-          if (kMode == GM_WGRAD && ks == T.steps - 1 && (T.rows & 15))   // rows cleared by warp 10 of both CTAs
-            ok = wait_bar<true>(&S.full[s], par, &S.abort);
-          else
-            ok = wait_bar(&S.full[s], par, &S.abort);
-          if (!ok) break;
+        const auto multiply = [&](int s, int k, bool first_step) {   // k of the stage's 64
           fence_after();
           const uint32_t a = smem_u32(S.stage[s]);
           const uint64_t da = tile_desc<kTa>(a), db = tile_desc<kTb>(a + kHalf);
-          const int nk = (min(64, red - 64 * ks) + 15) / 16;
+          const int nk = (min(64, k) + 15) / 16;
           for (int kk = 0; kk < nk; ++kk)
-            mma<true>(d, da + kk * kStep16<kTa>, db + kk * kStep16<kTb>, idesc, (ks | kk) != 0);
+            mma<true>(d, da + kk * kStep16<kTa>, db + kk * kStep16<kTb>, idesc, !first_step || kk != 0);
           commit_pair(&S.empty[s], 3);
+        };
+        for (int ks = 0; ok && ks < T.steps; ++ks, ++it) {
+          const int s = it % kStages;
+          if (kMode == GM_WGRAD && ks == T.steps - 1 && (T.rows & 15))   // rows cleared by warp 10 of both CTAs
+            ok = wait_bar<true>(&S.full[s], (fulls >> s) & 1, &S.abort);
+          else
+            ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort);
+          if (!ok) break;
+          fulls ^= 1u << s;
+          multiply(s, red - 64 * ks, ks == 0);
+        }
+        if constexpr (kEpi == GM_ADAPT) {
+          ok = ok && wait_bar(&S.ad.list_full[buf], (count >> 1) & 1, &S.abort);
+          const int n_list = ok ? S.ad.n_list[buf] : 0;
+          for (int j = 0; ok && j < n_list; ++j)
+            for (int k = 0; ok && k < p.rank; k += 64)
+              for (int h = 0; h < 2; ++h, ++it) {
+                const int s = it % kStages;
+                if (!(ok = wait_bar<true>(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
+                us ^= 1u << s;
+                multiply(s, p.rank - k, false);
+              }
+          mbarrier_arrive(&S.ad.list_empty[buf]);
         }
         if (ok) commit_pair(&S.acc_full[buf], 3);
         ++count;
@@ -504,8 +547,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
       fence_after();
       const long long out0 =
           (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
-      if (kEpi == GM_ADAPT) pdl_wait();   // the u rows
-      AdapterFrags frags;
       // the accumulator goes back as soon as this warp has read its last columns, before they are stored
       const auto release = [&](int c0) {
         if (!T.steps || c0 + 64 < T.cols) return;
@@ -547,12 +588,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
         }
+        const int cols = T.cols - c0;
+        if constexpr (kEpi == GM_ADAPT)
+          if (S.ad.broken[buf] && feats > 0) mark_broken(v, p, T.c0 + c0, cols, f0, lane);
         release(c0);
         if (feats <= 0) continue;
-        const int cols = T.cols - c0;
-        if (kEpi == GM_ADAPT) add_adapters(v, frags, p, T.c0 + c0, min(cols, 32), f0, lane);
         if (kMode == GM_WGRAD) {
-          tma_store_32x32(buf16, v, p, &maps.b[1], f0, T.c0 + c0, T.e, lane, lead, n_stores);
+          tma_store_32x32(buf16, v, p, &maps.c, f0, T.c0 + c0, T.e, lane, lead, n_stores);
         } else if (kEpi == GM_GATED) {
           __syncwarp();
           if (p.h) {
@@ -573,10 +615,110 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kBigThreads, 1)
           store_32x32(buf16, v, p.bf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         }
       }
+      if constexpr (kEpi == GM_ADAPT) {
+        __syncwarp();
+        if (lane == 0) mbarrier_arrive(&S.ad.list_empty[buf]);
+      }
       if (T.steps) ++count;
     }
     if (lead) store_wait<0>();   // the last stores have read this CTA's shared memory
-  } else if (kMode == GM_WGRAD) {
+  } else if constexpr (kEpi == GM_ADAPT) {
+    const int i0 = tid - 32 * (2 + kEpiWarps);
+    const uint32_t lead_u = map_rank(smem_u32(S.ad.u_full), 0);
+    const auto meet = [] {
+      __syncwarp();
+      asm volatile("bar.sync 1, %0;" ::"n"(32 * kUWarps) : "memory");
+    };
+    uint32_t it = 0, n_tile = 0, tails = 0;
+    bool alive = true;   // the four warps meet at barriers: a wait that ran out ends the work, not the loops
+    int e = 0;
+    Tile T;
+    pdl_wait();   // the u rows
+    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
+      const int lb = n_tile & 1;
+      alive = alive && wait_bar(&S.ad.list_empty[lb], ((n_tile >> 1) & 1) ^ 1, &S.abort);
+      int* ids = S.ad.id[lb];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = i0 + 128 * i;
+        int id = c < T.cols ? p.ids[T.c0 + c] : -1;
+        if (id >= p.n_adapters || id < 0) id = -1;
+        ids[c] = id;
+      }
+      if (i0 == 0) S.ad.broken[lb] = 0;
+      meet();
+      bool first_of[2];
+      uint32_t firsts[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int c = i0 + 128 * i, id = ids[c];
+        bool seen = id < 0;
+        for (int b = 0; b < c && !seen; b += 4) {
+          const int4 o = *reinterpret_cast<const int4*>(ids + b);
+          seen = o.x == id || (b + 1 < c && o.y == id) || (b + 2 < c && o.z == id) || (b + 3 < c && o.w == id);
+        }
+        first_of[i] = !seen;
+        firsts[i] = __ballot_sync(0xFFFFFFFFu, !seen);
+        if (lane == 0) S.ad.n_group[4 * i + (i0 >> 5)] = __popc(firsts[i]);
+      }
+      meet();
+      int n = 0, at[2];
+#pragma unroll
+      for (int g = 0; g < 8; ++g) {
+        if (g == (i0 >> 5)) at[0] = n;
+        if (g == 4 + (i0 >> 5)) at[1] = n;
+        n += S.ad.n_group[g];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (first_of[i]) S.ad.list[lb][at[i] + __popc(firsts[i] & ((1u << lane) - 1u))] = ids[i0 + 128 * i];
+      if (i0 == 0) S.ad.n_list[lb] = n;
+      meet();
+      if (i0 == 0) mbarrier_arrive(&S.ad.list_full[lb]);
+
+      it += T.steps;
+      const int half = T.n / 2, c = rank * half + i0;   // this thread's column, one of this CTA's half
+      const int mine = i0 < half ? ids[c] : -1;
+      for (int j = 0; j < n; ++j) {
+        const int id = S.ad.list[lb][j];
+        for (int k = 0; k < p.rank; k += 64) {
+          float4 u[16];
+          const float* src = p.u + static_cast<size_t>(T.c0 + c) * p.rank + k;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            u[i] = mine == id && k + 4 * i < p.rank ? __ldcg(reinterpret_cast<const float4*>(src) + i)
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int h = 0; h < 2; ++h, ++it) {
+            const int s = it % kStages;
+            // the B rows have landed, so the stage was free (its own barrier's phase would be ambiguous here: these
+            // warps do not see the steps in between)
+            alive = alive && wait_bar(&S.tail[s], (tails >> s) & 1, &S.abort);
+            tails ^= 1u << s;
+            if (i0 < half) {
+              uint8_t* row = S.stage[s] + kHalf + 128 * i0;
+#pragma unroll
+              for (int w = 0; w < 8; ++w)
+                *reinterpret_cast<uint4*>(row + 16 * (w ^ (i0 & 7))) =
+                    h ? u_words<true>(u[2 * w], u[2 * w + 1], p.bf16) : u_words<false>(u[2 * w], u[2 * w + 1], p.bf16);
+            }
+            uint4* words = reinterpret_cast<uint4*>(S.stage[s]) + i0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              const uint4 v = words[128 * w];
+              if (not_finite(v.x, p.bf16) | not_finite(v.y, p.bf16) | not_finite(v.z, p.bf16) | not_finite(v.w, p.bf16)) {
+                words[128 * w] = make_uint4(0, 0, 0, 0);
+                S.ad.broken[lb] = 1;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(lead_u + 8 * s);
+          }
+        }
+      }
+    }
+  } else if constexpr (kMode == GM_WGRAD) {
     // rows behind the group's end in its last stage belong to another expert (or to nobody, and may hold
     // anything): cleared in both operands, up to the end of the last k16 step that is issued
     const uint32_t lead_full = map_rank(smem_u32(S.full), 0);
@@ -616,31 +758,27 @@ static_assert(kSmallCols * kSmallPitch * 4 <= kSmallRing, "the reduction reuses 
 // (B[id] u)[row][f .. f + 4) in fp32; 0 for a row without an adapter.
 __device__ __forceinline__ float4 adapter_values(const GmParams& p, int row, int f) {
   const int id = p.ids[row];
-  float d[4] = {0.f, 0.f, 0.f, 0.f};
+  uint64_t d[4] = {0, 0, 0, 0};
   if (id >= 0 && id < p.n_adapters) {
     const uint16_t* b = p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank;
-    const uint16_t* u = p.u + static_cast<size_t>(row) * 2 * p.rank;
+    const float* u = p.u + static_cast<size_t>(row) * p.rank;
+#pragma unroll 2
     for (int j = 0; j < p.rank; j += 8) {
-      const uint4 hi = __ldcg(reinterpret_cast<const uint4*>(u + j));
-      const uint4 lo = __ldcg(reinterpret_cast<const uint4*>(u + p.rank + j));
-      const uint32_t hw[4] = {hi.x, hi.y, hi.z, hi.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
-      uint4 bv[4];
+      uint64_t uw[4], bw[4];
+      load_u8(uw, u + j);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bv[i] = __ldg(reinterpret_cast<const uint4*>(b + static_cast<size_t>(i) * p.rank + j));
+      for (int i = 0; i < 4; ++i) {
+        widen8(bw, __ldg(reinterpret_cast<const uint4*>(b + static_cast<size_t>(i) * p.rank + j)), p.bf16);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float u0 = __uint_as_float(hw[w] << 16) + __uint_as_float(lw[w] << 16);
-        const float u1 = __uint_as_float(hw[w] & 0xFFFF0000u) + __uint_as_float(lw[w] & 0xFFFF0000u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t v = w == 0 ? bv[i].x : w == 1 ? bv[i].y : w == 2 ? bv[i].z : bv[i].w;
-          d[i] += (p.bf16 ? __uint_as_float(v << 16) : half_lo(v)) * u0;
-          d[i] += (p.bf16 ? __uint_as_float(v & 0xFFFF0000u) : half_hi(v)) * u1;
-        }
+        for (int w = 0; w < 4; ++w) fma_f32x2(d[i], bw[w], uw[w]);
       }
     }
   }
-  return make_float4(d[0], d[1], d[2], d[3]);
+  float s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    s[i] = __uint_as_float(static_cast<uint32_t>(d[i])) + __uint_as_float(static_cast<uint32_t>(d[i] >> 32));
+  return make_float4(s[0], s[1], s[2], s[3]);
 }
 
 // Four consecutive values of an output row.
@@ -929,7 +1067,7 @@ bool launch_big(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s) 
   const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
                                          : std::min(p.E, p.m) + static_cast<long long>(p.m) / 256;
   const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
-  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), kBigThreads, sizeof(BigSmem<kMode>) + 1024, 2, s, maps, p, 0);
+  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), BigCfg<kMode, kEpi>::kThreads, sizeof(BigSmem<kMode, kEpi>) + 1024, 2, s, maps, p, 0);
 }
 
 template <int kMode, int kEpi>
@@ -957,7 +1095,7 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
     const cuuint64_t row = static_cast<cuuint64_t>(o.k) * 2;
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
     const cuuint64_t stride[2] = {row, row * o.n};
-    if (!p.out_f32 && !encode_store(&maps.b[1], p.y, dim, stride, p.bf16)) return false;
+    if (!p.out_f32 && !encode_store(&maps.c, p.y, dim, stride, p.bf16)) return false;
     return launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);
@@ -966,6 +1104,7 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
   if (epi == GM_GATED ? !map_gated(&maps.a, o.w, p.E, p.feat, o.k, p.bf16)
                       : !map_weights(&maps.a, o.w, p.E, o.n, o.k, mode == GM_FWD ? 128 : 64, p.bf16))
     return false;
+  if (epi == GM_ADAPT && !small && !map_weights(&maps.c, p.b, p.n_adapters, p.feat, p.rank, 128, p.bf16)) return false;
   if (mode == GM_DGRAD)
     return small ? launch_small<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s) : launch_big<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s);
   if (epi == GM_GATED)

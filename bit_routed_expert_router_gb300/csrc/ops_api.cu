@@ -109,11 +109,11 @@ extern "C" moe_status moe_lora_mm(int dtype, const void* x, int64_t ldx, int t, 
   if (!w || !a || !b || (!ids && t > 0) || !scale || !aligned(w, 16) || !aligned(a, 16) || !aligned(b, 16) || !aligned(ids, 4) ||
       !aligned(scale, 4) || !rows_ok(x, t, ldx, k) || !rows_ok(y, t, ldy, n))
     return MOE_EINVAL;
-  if ((!workspace && t > 0) || !aligned(workspace, 16) || workspace_bytes < static_cast<uint64_t>(t) * rank * 4) return MOE_EINVAL;
+  if ((!workspace && t > 0) || !aligned(workspace, 32) || workspace_bytes < static_cast<uint64_t>(t) * rank * 4) return MOE_EINVAL;
   if (t == 0) return MOE_OK;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MOE_BF16;
-  uint16_t* u = static_cast<uint16_t*>(workspace);
+  float* u = static_cast<float*>(workspace);
   if (!moe::launch_adapter_down(bf16, x, ldx, t, a, scale, ids, n_adapters, rank, k, u, s)) return MOE_ECUDA;
   moe::GmOperands o;
   o.x = x, o.ldx = ldx, o.w = w, o.n = n, o.k = k;

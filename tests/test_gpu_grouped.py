@@ -270,7 +270,7 @@ def lora_reference(x, w, ids, a, b, scale):
 def lora_case(seed, t, n, k, N, rank, dtype, order, top=2):
     g = gen(seed)
     x, w = ints(g, dtype, t, k + 8, top=top)[:, :k], ints(g, dtype, n, k, top=top)
-    # few non-zero values in A and B: A x stays below 2^16 (what its two bf16 halves hold) and the sums below 2^24
+    # few non-zero values in A: A x stays below 2^16 (16 bits are handed on) and every sum below 2^24
     a = ints(g, dtype, N, rank, k) * (torch.rand(N, rank, k, generator=g, device="cuda") < 0.1)
     b = ints(g, dtype, N, n, rank)
     scale = torch.tensor([0.5, 1.0, 2.0], device="cuda")[torch.arange(N, device="cuda") % 3].contiguous()
@@ -304,8 +304,8 @@ def test_adapters(t, n, k, N, rank, order, dtype):
 @pytest.mark.parametrize("t", [40, 200])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_adapters_of_real_values(t, dtype):
-    """A x in two bf16 halves: off by 2^-17 of itself at most (half a step of the second half), and by the sum's
-    fp32 error as in test_products_of_real_values; then B's sum the same way, and one rounding."""
+    """The sums' fp32 errors as in test_products_of_real_values, A x and B's sum among them; A x handed on as two
+    bf16 values (half a step of the second: 2^-17); and one rounding."""
     g, n, k, N, rank = gen(t), 328, 1000, 5, 64
     x = torch.randn(t, k, generator=g, device="cuda").to(dtype)
     w = (torch.randn(n, k, generator=g, device="cuda") / k ** 0.5).to(dtype)
@@ -318,7 +318,7 @@ def test_adapters_of_real_values(t, dtype):
     ref = lora_reference(x, w, ids, a, b, scale)
     mag = lora_reference(x.abs(), w.abs(), ids, a.abs(), b.abs(), scale)
     err = (y.double() - ref).abs()
-    assert (err <= torch.finfo(dtype).eps / 2 * ref.abs() + 1.01 * ((k / 16 + rank + 8) * 17 * 2 ** -23 + 2 ** -16) * mag).all()
+    assert (err <= torch.finfo(dtype).eps / 2 * ref.abs() + 1.01 * ((k / 16 + rank + 8) * 17 * 2 ** -23 + 2 ** -17) * mag).all()
 
 
 @pytest.mark.parametrize("t", [30, 150])

@@ -58,12 +58,15 @@ struct BigCfg {
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (kEpi == GM_ADAPT ? kUWarps : kMode == GM_WGRAD ? 1 : 0));
 };
 
+constexpr int kLists = 4;
 struct AdaptSmem {
-  int id[2][256];          // adapter of each column of a tile, -1 for none (tiles alternate)
-  int list[2][256];        // its distinct adapters, in order
-  int n_list[2], n_group[8];
-  volatile int broken[2];  // a value of the tile's B rows is not finite
-  uint64_t u_full[8], list_full[2], list_empty[2];
+  int id[kLists][256];     // adapter of each column of a tile, -1 for none (tiles in turn)
+  int list[kLists][256];   // its distinct adapters, in order
+  int n_list[kLists], n_group[8];
+  // a value of the tile's B rows is not finite.  Sixteen tiles in turn: the listing warps follow the loading one, which
+  // is at most kStages steps, so as many tiles, ahead of the products, those two tiles ahead of the stores, and the lists one ahead of the loads
+  volatile int broken[16];
+  uint64_t u_full[8], list_full[kLists], list_empty[kLists];
 };
 struct NoSmem {};
 
@@ -217,6 +220,11 @@ __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
 // the kernel from 45 to 115 us at 4096 rows and rank 64, since they wait for the
 // tcgen05 products; on the ordinary pipes 145, bound by broadcast loads.)
 
+// The pairs are spread over the tile's reduction, so that the warps that write
+// them have the steps between for it: pair i of n comes before base step
+// pair_at(i, n).
+__device__ __forceinline__ int pair_at(int i, int n, int steps) { return max(1, (i + 1) * steps / (n + 1)); }
+
 // True if one of the 16-bit values of v is infinite or NaN (all exponent bits set).
 __device__ __forceinline__ uint32_t not_finite(uint32_t v, int bf16) {
   const uint32_t mask = bf16 ? 0x7F807F80u : 0x7C007C00u, one = bf16 ? 0x00800080u : 0x04000400u;
@@ -366,11 +374,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.acc_full[i], 1);
       mbar_init(&S.acc_empty[i], 2 * kEpiWarps);
-      if constexpr (kEpi == GM_ADAPT) {
-        mbar_init(&S.ad.list_full[i], 1);
-        mbar_init(&S.ad.list_empty[i], kEpiWarps + (rank == 0 ? 2 : 1));   // and the loading and the issuing warp
-      }
     }
+    if constexpr (kEpi == GM_ADAPT)
+      for (int i = 0; i < kLists; ++i) {
+        mbar_init(&S.ad.list_full[i], 1);
+        mbar_init(&S.ad.list_empty[i], rank == 0 ? 2 : 1);   // the loading and the issuing warp
+      }
     mbar_init(&S.drain, 1);
     S.abort = 0;
     fence_mbar_init();
@@ -412,7 +421,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       for (int t = first; !S.abort && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
         const int half = T.n / 2;
         const uint32_t bytes = kHalf + half * 128;
-        for (int ks = 0; ks < T.steps; ++ks, ++it) {
+        int pairs = 0, pair = 0;
+        [[maybe_unused]] const int lb = n_tile++ % kLists;
+        if constexpr (kEpi == GM_ADAPT) {
+          if (!wait_bar(&S.ad.list_full[lb], ((n_tile - 1) / kLists) & 1, &S.abort)) break;
+          pairs = S.ad.n_list[lb] * ((p.rank + 63) / 64);
+        }
+        for (int ks = 0; ks < T.steps || pair < pairs; ++ks) {
+          if constexpr (kEpi == GM_ADAPT) {
+            for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair)
+#pragma unroll
+              for (int h = 0; h < 2; ++h, ++it) {
+                const int s = it % kStages;
+                if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
+                const int block = pair / S.ad.n_list[lb];
+                mbar_arrive_expect_tx(&S.tail[s], kHalf);
+                load_3d<true>(smem_u32(S.stage[s]), &maps.c, 64 * block, T.f0 + 128 * rank,
+                              S.ad.list[lb][pair - block * S.ad.n_list[lb]], smem_u32(&S.tail[s]));
+                extra |= 1u << s;
+                tails ^= 1u << s;
+              }
+            if (S.abort) break;
+            if (ks >= T.steps) continue;
+          }
           const int s = it % kStages;
           if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
           uint32_t bar = lead_full + 8 * s;
@@ -448,25 +479,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           }
           extra &= ~(1u << s);
           fulls ^= 1u << s;
+          ++it;
         }
-        if constexpr (kEpi == GM_ADAPT) {
-          const int lb = n_tile & 1;
-          if (wait_bar(&S.ad.list_full[lb], (n_tile >> 1) & 1, &S.abort)) {
-            for (int j = 0; j < S.ad.n_list[lb] && !S.abort; ++j)
-              for (int k = 0; k < p.rank && !S.abort; k += 64)
-                for (int h = 0; h < 2; ++h, ++it) {
-                  const int s = it % kStages;
-                  if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
-                  mbar_arrive_expect_tx(&S.tail[s], kHalf);
-                  load_3d<true>(smem_u32(S.stage[s]), &maps.c, k, T.f0 + 128 * rank, S.ad.list[lb][j],
-                                smem_u32(&S.tail[s]));
-                  extra |= 1u << s;
-                  tails ^= 1u << s;
-                }
-            mbarrier_arrive(&S.ad.list_empty[lb]);
-          }
-          ++n_tile;
-        }
+        if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
       }
       if (S.abort)   // copies already issued land before the pair leaves
         for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
@@ -499,7 +514,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             mma<true>(d, da + kk * kStep16<kTa>, db + kk * kStep16<kTb>, idesc, !first_step || kk != 0);
           commit_pair(&S.empty[s], 3);
         };
-        for (int ks = 0; ok && ks < T.steps; ++ks, ++it) {
+        int pairs = 0, pair = 0;
+        [[maybe_unused]] const int lb = count % kLists;
+        if constexpr (kEpi == GM_ADAPT) {
+          ok = ok && wait_bar(&S.ad.list_full[lb], (count / kLists) & 1, &S.abort);
+          pairs = ok ? S.ad.n_list[lb] * ((p.rank + 63) / 64) : 0;
+        }
+        for (int ks = 0; ok && (ks < T.steps || pair < pairs); ++ks) {
+          if constexpr (kEpi == GM_ADAPT) {
+            for (; ok && pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair)
+#pragma unroll
+              for (int h = 0; h < 2; ++h, ++it) {
+                const int s = it % kStages;
+                if (!(ok = wait_bar<true>(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
+                us ^= 1u << s;
+                multiply(s, p.rank - 64 * (pair / S.ad.n_list[lb]), false);
+              }
+            if (!ok) break;
+            if (ks >= T.steps) continue;
+          }
           const int s = it % kStages;
           if (kMode == GM_WGRAD && ks == T.steps - 1 && (T.rows & 15))   // rows cleared by warp 10 of both CTAs
             ok = wait_bar<true>(&S.full[s], (fulls >> s) & 1, &S.abort);
@@ -508,20 +541,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           if (!ok) break;
           fulls ^= 1u << s;
           multiply(s, red - 64 * ks, ks == 0);
+          ++it;
         }
-        if constexpr (kEpi == GM_ADAPT) {
-          ok = ok && wait_bar(&S.ad.list_full[buf], (count >> 1) & 1, &S.abort);
-          const int n_list = ok ? S.ad.n_list[buf] : 0;
-          for (int j = 0; ok && j < n_list; ++j)
-            for (int k = 0; ok && k < p.rank; k += 64)
-              for (int h = 0; h < 2; ++h, ++it) {
-                const int s = it % kStages;
-                if (!(ok = wait_bar<true>(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
-                us ^= 1u << s;
-                multiply(s, p.rank - k, false);
-              }
-          mbarrier_arrive(&S.ad.list_empty[buf]);
-        }
+        if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
         if (ok) commit_pair(&S.acc_full[buf], 3);
         ++count;
       }
@@ -590,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         }
         const int cols = T.cols - c0;
         if constexpr (kEpi == GM_ADAPT)
-          if (S.ad.broken[buf] && feats > 0) mark_broken(v, p, T.c0 + c0, cols, f0, lane);
+          if (S.ad.broken[count & 15] && feats > 0) mark_broken(v, p, T.c0 + c0, cols, f0, lane);
         release(c0);
         if (feats <= 0) continue;
         if (kMode == GM_WGRAD) {
@@ -615,10 +637,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           store_32x32(buf16, v, p.bf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         }
       }
-      if constexpr (kEpi == GM_ADAPT) {
-        __syncwarp();
-        if (lane == 0) mbarrier_arrive(&S.ad.list_empty[buf]);
-      }
       if (T.steps) ++count;
     }
     if (lead) store_wait<0>();   // the last stores have read this CTA's shared memory
@@ -629,14 +647,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       __syncwarp();
       asm volatile("bar.sync 1, %0;" ::"n"(32 * kUWarps) : "memory");
     };
-    uint32_t it = 0, n_tile = 0, tails = 0;
+    uint32_t it = 0, tails = 0;
     bool alive = true;   // the four warps meet at barriers: a wait that ran out ends the work, not the loops
-    int e = 0;
-    Tile T;
-    pdl_wait();   // the u rows
-    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
-      const int lb = n_tile & 1;
-      alive = alive && wait_bar(&S.ad.list_empty[lb], ((n_tile >> 1) & 1) ^ 1, &S.abort);
+    // tile t's columns' adapters and which of them are the first of theirs
+    const auto make_list = [&](const Tile& T, uint32_t n_tile) {
+      const int lb = n_tile % kLists;
+      alive = alive && wait_bar(&S.ad.list_empty[lb], ((n_tile / kLists) & 1) ^ 1, &S.abort);
       int* ids = S.ad.id[lb];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -645,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         if (id >= p.n_adapters || id < 0) id = -1;
         ids[c] = id;
       }
-      if (i0 == 0) S.ad.broken[lb] = 0;
+      if (i0 == 0) S.ad.broken[n_tile & 15] = 0;
       meet();
       bool first_of[2];
       uint32_t firsts[2];
@@ -662,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         if (lane == 0) S.ad.n_group[4 * i + (i0 >> 5)] = __popc(firsts[i]);
       }
       meet();
-      int n = 0, at[2];
+      int n = 0, at[2] = {0, 0};
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         if (g == (i0 >> 5)) at[0] = n;
@@ -675,19 +691,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       if (i0 == 0) S.ad.n_list[lb] = n;
       meet();
       if (i0 == 0) mbarrier_arrive(&S.ad.list_full[lb]);
-
-      it += T.steps;
+    };
+    Tile T, next;
+    int e = 0;
+    bool more = tile_at<kMode, kFeat>(S, p, first, e, next);
+    if (more) make_list(next, 0);
+    pdl_wait();   // the u rows
+    uint32_t n_tile = 0;
+    for (int t = first; more; t += stride, ++n_tile) {
+      T = next;
+      more = tile_at<kMode, kFeat>(S, p, t + stride, e, next);
+      if (more) make_list(next, n_tile + 1);   // the loading warp needs it before this tile is done
+      const int lb = n_tile % kLists, n = S.ad.n_list[lb], blocks = (p.rank + 63) / 64, pairs = n * blocks;
       const int half = T.n / 2, c = rank * half + i0;   // this thread's column, one of this CTA's half
-      const int mine = i0 < half ? ids[c] : -1;
-      for (int j = 0; j < n; ++j) {
-        const int id = S.ad.list[lb][j];
-        for (int k = 0; k < p.rank; k += 64) {
-          float4 u[16];
-          const float* src = p.u + static_cast<size_t>(T.c0 + c) * p.rank + k;
+      const int mine = i0 < half ? S.ad.id[lb][c] : -1;
+      int at0 = 0;
+      for (int block = 0; block < blocks; ++block) {
+        uint4 hi[8], lo[8];
+        const float* src = p.u + static_cast<size_t>(T.c0 + c) * p.rank + 64 * block;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            u[i] = mine == id && k + 4 * i < p.rank ? __ldcg(reinterpret_cast<const float4*>(src) + i)
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < 8; ++w) {
+          const bool in = mine >= 0 && 64 * block + 8 * w < p.rank;
+          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 u0 = in ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * w) : zero;
+          const float4 u1 = in ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * w + 1) : zero;
+          hi[w] = u_words<false>(u0, u1, p.bf16);
+          lo[w] = u_words<true>(u0, u1, p.bf16);
+        }
+        for (int j = 0; j < n; ++j) {
+          const int at = pair_at(block * n + j, pairs, T.steps);   // base steps before this pair
+          it += at - at0;
+          at0 = at;
+          const bool use = mine == S.ad.list[lb][j];
+          bool scan = true;
 #pragma unroll
           for (int h = 0; h < 2; ++h, ++it) {
             const int s = it % kStages;
@@ -698,18 +734,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             if (i0 < half) {
               uint8_t* row = S.stage[s] + kHalf + 128 * i0;
 #pragma unroll
-              for (int w = 0; w < 8; ++w)
-                *reinterpret_cast<uint4*>(row + 16 * (w ^ (i0 & 7))) =
-                    h ? u_words<true>(u[2 * w], u[2 * w + 1], p.bf16) : u_words<false>(u[2 * w], u[2 * w + 1], p.bf16);
-            }
-            uint4* words = reinterpret_cast<uint4*>(S.stage[s]) + i0;
-#pragma unroll
-            for (int w = 0; w < 8; ++w) {
-              const uint4 v = words[128 * w];
-              if (not_finite(v.x, p.bf16) | not_finite(v.y, p.bf16) | not_finite(v.z, p.bf16) | not_finite(v.w, p.bf16)) {
-                words[128 * w] = make_uint4(0, 0, 0, 0);
-                S.ad.broken[lb] = 1;
+              for (int w = 0; w < 8; ++w) {
+                const uint4 v = h ? lo[w] : hi[w];
+                *reinterpret_cast<uint4*>(row + 16 * (w ^ (i0 & 7))) = use ? v : make_uint4(0, 0, 0, 0);
               }
+            }
+            if (scan) {   // the second step's rows are the first's
+              uint4* words = reinterpret_cast<uint4*>(S.stage[s]) + i0;
+              uint32_t any = 0;
+#pragma unroll
+              for (int w = 0; w < 8; ++w) {
+                const uint4 v = words[128 * w];
+                const uint32_t bad =
+                    not_finite(v.x, p.bf16) | not_finite(v.y, p.bf16) | not_finite(v.z, p.bf16) | not_finite(v.w, p.bf16);
+                if (bad) words[128 * w] = make_uint4(0, 0, 0, 0);
+                any |= bad;
+              }
+              if (any) S.ad.broken[n_tile & 15] = 1;
+              scan = any != 0;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -717,6 +759,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           }
         }
       }
+      it += T.steps - at0;
     }
   } else if constexpr (kMode == GM_WGRAD) {
     // rows behind the group's end in its last stage belong to another expert (or to nobody, and may hold

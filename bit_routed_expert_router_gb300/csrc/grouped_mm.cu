@@ -93,15 +93,12 @@ static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
 
 __device__ __forceinline__ uint32_t* err_word() { return &g_grouped_err; }
 
-// Bounded wait that also ends when another role of the CTA gave up.  What a
-// wait orders is asynchronous (TMA bytes, MMAs) except with kCluster, where
-// another CTA's ordinary writes are awaited.
-template <bool kCluster = false>
+// Bounded wait that also ends when another role of the CTA gave up.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (kCluster ? try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait(bar, parity)) return true;
     if (*abort) return false;
     if (clock64() - t0 > kSpinLimitCycles) {
       *abort = 1;
@@ -526,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
 #pragma unroll
               for (int h = 0; h < 2; ++h, ++it) {
                 const int s = it % kStages;
-                if (!(ok = wait_bar<true>(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
+                if (!(ok = wait_bar(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
                 us ^= 1u << s;
                 multiply(s, p.rank - 64 * (pair / S.ad.n_list[lb]), false);
               }
@@ -534,11 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             if (ks >= T.steps) continue;
           }
           const int s = it % kStages;
-          if (kMode == GM_WGRAD && ks == T.steps - 1 && (T.rows & 15))   // rows cleared by warp 10 of both CTAs
-            ok = wait_bar<true>(&S.full[s], (fulls >> s) & 1, &S.abort);
-          else
-            ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort);
-          if (!ok) break;
+          if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort))) break;
           fulls ^= 1u << s;
           multiply(s, red - 64 * ks, ks == 0);
           ++it;

@@ -49,26 +49,18 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, bool on) {
   return v;
 }
 
+// Arrival on a barrier of either CTA of a pair.  Its release is the CTA's own:
+// what it announces are tensor-memory reads and shared-memory writes of this
+// SM, which this SM's share of the pair's products waits for.  (At cluster
+// scope each arrival cost about a microsecond.)
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // (relaxed: the arrival publishes nothing but the byte count)
 __device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
-}
-
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
-      : "memory");
-  return ok != 0;
 }
 
 // ------------------------------------------------------------------ TMA loads

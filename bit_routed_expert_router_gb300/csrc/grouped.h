@@ -52,7 +52,9 @@ bool grouped_error(cudaStream_t s, uint32_t* err);
 bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const void* da, long long ldda, void* dh,
                        long long lddh, int m, int f, const int32_t* n_rows, cudaStream_t s);
 
-// u[t] = scale[id] A[id] x[t] for every row with an adapter.
+// u[t] = scale[id] A[id] x[t] for every row with an adapter: few rows, and many
+// (o.x, o.w = A; p: m, red, rank, n_adapters, ids, bf16).
+bool launch_adapter_down_many(const GmOperands& o, const GmParams& p, const float* scale, float* u, cudaStream_t s);
 bool launch_adapter_down(bool bf16, const void* x, long long ldx, int t, const void* a, const float* scale,
                          const int32_t* ids, int n_adapters, int rank, int k, float* u, cudaStream_t s);
 

@@ -1032,6 +1032,149 @@ __global__ void __launch_bounds__(192)
   if (warp == 1) tmem_free<false>(tmem, kSmallCols);
 }
 
+// ------------------------------------------------------------------ adapters' down half for many rows
+
+// u[t] = scale[i] A[i] x[t] for 64 rows of x a cluster.  The distinct adapters
+// of the rows go 128 / slot at a time (slot: the rank rounded up to a power of
+// two) as the MMA's 128 features, for all 64 rows; a row keeps its own
+// adapter's part.  The reduction is split over the cluster as above.
+constexpr int kDownCols = 64;
+constexpr int kDownStage = kHalf + kDownCols * 128;
+constexpr int kDownStages = 4;
+static_assert(kDownCols * kSmallPitch * 4 <= kDownStages * kDownStage, "the reduction reuses the ring");
+
+__global__ void __launch_bounds__(192)
+    k_adapter_down_many(const __grid_constant__ GmMaps maps, GmParams p, const float* scale, float* u, int slot, int split) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t full[kDownStages], empty[kDownStages], acc_full;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  __shared__ int s_n, s_list[kDownCols], s_nth[kDownCols];   // distinct adapters; which of them a row has, or -1
+  uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = static_cast<int>(cluster_rank()), row0 = blockIdx.y * kDownCols, rows = min(kDownCols, p.m - row0);
+  if (warp == 1) {
+    tmem_alloc<false>(&s_tmem, kDownCols);
+  } else if (tid == 64) {
+    prefetch_map(&maps.a);
+    prefetch_map(&maps.b[0]);
+    s_abort = 0;
+    for (int i = 0; i < kDownStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(&acc_full, 1);
+    fence_mbar_init();
+  }
+  pdl_wait();
+  pdl_trigger();
+  if (warp == 0) {
+    int id[2], nth[2] = {-1, -1}, n = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      id[i] = lane + 32 * i < rows ? p.ids[row0 + lane + 32 * i] : -1;
+      if (id[i] < 0 || id[i] >= p.n_adapters) id[i] = -1;
+    }
+    for (;;) {
+      const uint32_t open0 = __ballot_sync(0xFFFFFFFFu, id[0] >= 0 && nth[0] < 0);
+      const uint32_t open1 = __ballot_sync(0xFFFFFFFFu, id[1] >= 0 && nth[1] < 0);
+      if (!(open0 | open1)) break;
+      const int a = open0 ? __shfl_sync(0xFFFFFFFFu, id[0], __ffs(open0) - 1)
+                          : __shfl_sync(0xFFFFFFFFu, id[1], __ffs(open1) - 1);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (id[i] == a) nth[i] = n;
+      if (lane == 0) s_list[n] = a;
+      ++n;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) s_nth[lane + 32 * i] = nth[i];
+    if (lane == 0) s_n = n;
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  const int n = s_n, each = 128 / slot;   // adapters of a pass
+  const int all = (p.red + 63) / 64, k0 = all * rank / split, steps = all * (rank + 1) / split - k0;
+  float* part = reinterpret_cast<float*>(ring);
+  uint32_t from[kMaxSplit];
+#pragma unroll
+  for (int r = 0; r < kMaxSplit; ++r) from[r] = map_rank(smem_u32(part) + 16 * lane, min(r, split - 1));
+  uint32_t it = 0, pass = 0;
+  for (int a0 = each * blockIdx.z; a0 < n; a0 += each * gridDim.z, ++pass) {
+    const int na = min(each, n - a0);
+    const uint32_t bytes = na * slot * 128 + kDownCols * 128;
+    if (warp == 0) {
+      if (elect_one()) {
+        int ks = 0;
+        for (; ks < steps; ++ks) {
+          const uint32_t i = it + ks, s = i % kDownStages;
+          if (!wait_bar(&empty[s], ((i / kDownStages) & 1) ^ 1, &s_abort)) break;
+          const uint32_t a = smem_u32(ring) + s * kDownStage, bar = smem_u32(&full[s]);
+          mbar_arrive_expect_tx(&full[s], bytes);
+          for (int j = 0; j < na; ++j) load_3d<false>(a + j * slot * 128, &maps.a, 64 * (k0 + ks), 0, s_list[a0 + j], bar);
+          load_2d<false>(a + kHalf, &maps.b[0], 64 * (k0 + ks), row0, bar);
+        }
+        if (s_abort)
+          for (uint32_t i = it + ks - min(ks, kDownStages); i < it + ks; ++i)
+            mbar_wait_bounded(&full[i % kDownStages], (i / kDownStages) & 1, err_word());
+      }
+    } else if (warp == 1) {
+      if (elect_one()) {
+        const uint32_t idesc = instr_desc(p.bf16, 128, kDownCols, false, false);
+        for (int ks = 0; ks < steps; ++ks) {
+          const uint32_t i = it + ks, s = i % kDownStages;
+          if (!wait_bar(&full[s], (i / kDownStages) & 1, &s_abort)) break;
+          fence_after();
+          const uint32_t a = smem_u32(ring) + s * kDownStage;
+          const uint64_t da = tile_desc<false>(a), db = tile_desc<false>(a + kHalf);
+          const int nk = (min(64, p.red - 64 * (k0 + ks)) + 15) / 16;
+          for (int kk = 0; kk < nk; ++kk)
+            mma<false>(tmem, da + kk * kStep16<false>, db + kk * kStep16<false>, idesc, (ks | kk) != 0);
+          commit(&empty[s]);
+        }
+        commit(&acc_full);
+      }
+    }
+    __syncwarp();
+    it += steps;
+    bool ok = true;
+    if (warp >= 2) {
+      ok = mbar_wait_bounded(&acc_full, pass & 1, err_word()) && !s_abort;
+      fence_after();
+      const int q = warp & 3;
+      if (ok)
+        for (int c = 0; c < kDownCols; c += 16) {
+          float v[16];
+          ld_cols16(tmem + c + (static_cast<uint32_t>(32 * q) << 16), v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(c + i) * kSmallPitch + 32 * q + lane] = v[i];
+        }
+      fence_before();
+    }
+    cluster_sync();
+    fence_after();
+    if (warp >= 2 && ok)
+      for (int c = rank + split * (warp - 2); c < rows; c += 4 * split) {
+        const int nth = s_nth[c], r = 4 * lane - (nth - a0) * slot;   // this lane's four ranks of the row's adapter
+        if (nth < a0 || nth >= a0 + na || r < 0 || r >= min(slot, p.rank)) continue;
+        const float sc = scale[s_list[nth]];
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), pv[kMaxSplit];
+#pragma unroll
+        for (int j = 0; j < kMaxSplit; ++j) pv[j] = ld_cluster_f32x4(from[j] + c * kSmallPitch * 4, j < split);
+#pragma unroll
+        for (int j = 0; j < kMaxSplit; ++j) v.x += pv[j].x, v.y += pv[j].y, v.z += pv[j].z, v.w += pv[j].w;
+        v.x *= sc, v.y *= sc, v.z *= sc, v.w *= sc;
+        *reinterpret_cast<float4*>(u + static_cast<size_t>(row0 + c) * p.rank + r) = v;
+      }
+    fence_proxy_async_smem();   // the next pass's loads follow these accesses of the ring
+    cluster_sync();             // the others may still read this CTA's part
+  }
+  __syncthreads();
+  if (warp == 1) tmem_free<false>(tmem, kDownCols);
+}
+
 // ------------------------------------------------------------------ launches
 
 struct DeviceInfo {
@@ -1115,6 +1258,44 @@ bool launch_small(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s
   while (split < kMaxSplit && 2 * split * ft * static_cast<long long>(tiles) <= 3 * sms && 4 * split <= steps) split *= 2;
   return launch(k_grouped_small<kMode, kEpi>, dim3(ft * split, tiles), 192, kSmallRing + 1024, split, s, maps, p, split);
 }
+
+}  // namespace
+
+bool launch_adapter_down_many(const GmOperands& o, const GmParams& p, const float* scale, float* u, cudaStream_t s) {
+  int slot = 8;
+  while (slot < p.rank) slot *= 2;
+  GmMaps maps;
+  if (!map_weights(&maps.a, o.w, p.n_adapters, p.rank, o.k, slot, p.bf16) ||
+      !map_rows(&maps.b[0], o.x, o.k, p.m, o.ldx, kDownCols, p.bf16))
+    return false;
+  const int blocks = (p.m + kDownCols - 1) / kDownCols, steps = (o.k + 63) / 64, most = std::min(kDownCols, p.n_adapters);
+  DeviceInfo d;
+  if (!device_info(&d)) return false;
+  int split = 1;   // two CTAs an SM
+  while (split < kMaxSplit && 2 * split * blocks <= 2 * d.sms && 4 * split <= steps) split *= 2;
+  const int shares = std::max(1, std::min((most * slot + 127) / 128, 2 * d.sms / (split * blocks)));
+  const size_t smem = kDownStages * kDownStage + 1024;
+  if (cudaFuncSetAttribute(k_adapter_down_many, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
+      cudaSuccess)
+    return false;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(split, blocks, shares);
+  cfg.blockDim = dim3(192);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = split;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_adapter_down_many, maps, p, scale, u, slot, split) == cudaSuccess;
+}
+
+namespace {
 
 // Few rows per expert: the small kernel.  Its tiles re-read an expert's weights (from L2) for every 64 rows.
 bool few_rows(const GmParams& p) { return p.m <= (p.offsets ? 4 * static_cast<long long>(p.E) : 64); }

@@ -10,6 +10,7 @@
 namespace {
 
 constexpr int kMaxExperts = 1024, kMaxSide = 65536, kMaxRows = 1 << 24, kMaxRank = 128;
+constexpr int kManyRows = 256;   // adapters: from here on their down half runs on tcgen05
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 
@@ -114,13 +115,16 @@ extern "C" moe_status moe_lora_mm(int dtype, const void* x, int64_t ldx, int t, 
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MOE_BF16;
   float* u = static_cast<float*>(workspace);
-  if (!moe::launch_adapter_down(bf16, x, ldx, t, a, scale, ids, n_adapters, rank, k, u, s)) return MOE_ECUDA;
   moe::GmOperands o;
-  o.x = x, o.ldx = ldx, o.w = w, o.n = n, o.k = k;
+  o.x = x, o.ldx = ldx, o.w = a, o.n = n, o.k = k;
   moe::GmParams p;
   p.m = t, p.feat = n, p.red = k;
   p.y = y, p.ldy = ldy, p.bf16 = bf16;
   p.ids = ids, p.b = static_cast<const uint16_t*>(b), p.u = u, p.rank = rank, p.n_adapters = n_adapters;
+  if (t >= kManyRows ? !moe::launch_adapter_down_many(o, p, scale, u, s)
+                     : !moe::launch_adapter_down(bf16, x, ldx, t, a, scale, ids, n_adapters, rank, k, u, s))
+    return MOE_ECUDA;
+  o.w = w;
   return status(moe::launch_grouped(moe::GM_FWD, moe::GM_ADAPT, o, p, s));
 }
 

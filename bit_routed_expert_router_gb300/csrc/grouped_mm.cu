@@ -25,6 +25,7 @@
 // reduction split over a cluster whose CTAs add their accumulators through
 // distributed shared memory in rank order (no atomics, no workspace).
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "grouped.h"
@@ -55,14 +56,14 @@ template <int kMode, int kEpi>
 struct BigCfg {
   static constexpr int kStages = kMode == GM_WGRAD ? 5 : 6;
   static constexpr int kEpiBytes = kMode == GM_WGRAD ? 4096 : kEpi == GM_ADAPT ? 4 * 8 * kEpiPitch : moe::kEpiBytes;
-  static constexpr int kThreads = 32 * (2 + kEpiWarps + (kEpi == GM_ADAPT ? kUWarps : kMode == GM_WGRAD ? 1 : 0));
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + (kEpi == GM_ADAPT ? kUWarps + 1 : kMode == GM_WGRAD ? 1 : 0));
 };
 
 constexpr int kLists = 4;
 struct AdaptSmem {
   int id[kLists][256];     // adapter of each column of a tile, -1 for none (tiles in turn)
   int list[kLists][256];   // its distinct adapters, in order
-  int n_list[kLists], n_group[8];
+  int n_list[kLists];
   // a value of the tile's B rows is not finite.  Sixteen tiles in turn: the listing warps follow the loading one, which
   // is at most kStages steps, so as many tiles, ahead of the products, those two tiles ahead of the stores, and the lists one ahead of the loads
   volatile int broken[16];
@@ -106,6 +107,11 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
       return false;
     }
   }
+}
+
+// The same by a whole warp, which then agrees on the outcome.
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort));
 }
 
 __device__ __forceinline__ float gelu(float v, int variant) {
@@ -172,7 +178,7 @@ __device__ __forceinline__ bool tile_at(const Smem& S, const GmParams& p, int t,
     T.f0 = f * kFeat;
     T.c0 = lo + c * width;
     T.cols = min(width, lo + rows - T.c0);
-    T.n = (T.cols + 31) & ~31;
+    T.n = max((T.cols + 31) & ~31, 32);   // an MMA has columns whatever the parts are
     T.row0 = T.rows = 0;
     T.steps = (p.red + 63) / 64;
     return true;
@@ -375,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     if constexpr (kEpi == GM_ADAPT)
       for (int i = 0; i < kLists; ++i) {
         mbar_init(&S.ad.list_full[i], 1);
-        mbar_init(&S.ad.list_empty[i], rank == 0 ? 2 : 1);   // the loading and the issuing warp
+        mbar_init(&S.ad.list_empty[i], kUWarps + (rank == 0 ? 2 : 1));   // and the loading and the issuing warp
       }
     mbar_init(&S.drain, 1);
     S.abort = 0;
@@ -558,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       const int f0 = T.f0 + (kEpi == GM_GATED ? 64 * rank + 16 * q : 128 * rank + 32 * q);
       const int feats = p.feat - f0;   // none or less: the output ends before this warp's features do
       const int buf = count & 1, c_first = 32 * ((warp - 2) >> 2);
-      if (T.steps && !wait_bar(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
+      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
       fence_after();
       const long long out0 =
           (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
@@ -633,69 +639,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       if (T.steps) ++count;
     }
     if (lead) store_wait<0>();   // the last stores have read this CTA's shared memory
+  } else if (kEpi == GM_ADAPT && warp == 2 + kEpiWarps + kUWarps) {
+    if constexpr (kEpi == GM_ADAPT) {
+      // lists the distinct adapters of the tiles, ahead of the other roles
+      uint32_t n_tile = 0;
+      int e = 0;
+      Tile T;
+      for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
+        const int lb = n_tile % kLists;
+        if (!wait_bar_warp(&S.ad.list_empty[lb], ((n_tile / kLists) & 1) ^ 1, &S.abort)) break;
+        int id[8];
+        uint32_t open[8];   // columns whose adapter is not listed yet, 32 at a time
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = 32 * i + lane;
+          id[i] = c < T.cols ? p.ids[T.c0 + c] : -1;
+          if (id[i] >= p.n_adapters || id[i] < 0) id[i] = -1;
+          S.ad.id[lb][c] = id[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) open[i] = __ballot_sync(0xFFFFFFFFu, id[i] >= 0);
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          while (open[i]) {
+            const int a = __shfl_sync(0xFFFFFFFFu, id[i], __ffs(open[i]) - 1);
+#pragma unroll
+            for (int k = i; k < 8; ++k) open[k] &= ~__ballot_sync(0xFFFFFFFFu, id[k] == a);
+            if (lane == 0) S.ad.list[lb][n] = a;
+            ++n;
+          }
+        if (lane == 0) {
+          S.ad.n_list[lb] = n;
+          S.ad.broken[n_tile & 15] = 0;
+        }
+        __syncwarp();
+        if (lane == 0) mbarrier_arrive(&S.ad.list_full[lb]);
+      }
+    }
   } else if constexpr (kEpi == GM_ADAPT) {
     const int i0 = tid - 32 * (2 + kEpiWarps);
     const uint32_t lead_u = map_rank(smem_u32(S.ad.u_full), 0);
-    const auto meet = [] {
-      __syncwarp();
-      asm volatile("bar.sync 1, %0;" ::"n"(32 * kUWarps) : "memory");
-    };
-    uint32_t it = 0, tails = 0;
-    bool alive = true;   // the four warps meet at barriers: a wait that ran out ends the work, not the loops
-    // tile t's columns' adapters and which of them are the first of theirs
-    const auto make_list = [&](const Tile& T, uint32_t n_tile) {
-      const int lb = n_tile % kLists;
-      alive = alive && wait_bar(&S.ad.list_empty[lb], ((n_tile / kLists) & 1) ^ 1, &S.abort);
-      int* ids = S.ad.id[lb];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = i0 + 128 * i;
-        int id = c < T.cols ? p.ids[T.c0 + c] : -1;
-        if (id >= p.n_adapters || id < 0) id = -1;
-        ids[c] = id;
-      }
-      if (i0 == 0) S.ad.broken[n_tile & 15] = 0;
-      meet();
-      bool first_of[2];
-      uint32_t firsts[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = i0 + 128 * i, id = ids[c];
-        bool seen = id < 0;
-        for (int b = 0; b < c && !seen; b += 4) {
-          const int4 o = *reinterpret_cast<const int4*>(ids + b);
-          seen = o.x == id || (b + 1 < c && o.y == id) || (b + 2 < c && o.z == id) || (b + 3 < c && o.w == id);
-        }
-        first_of[i] = !seen;
-        firsts[i] = __ballot_sync(0xFFFFFFFFu, !seen);
-        if (lane == 0) S.ad.n_group[4 * i + (i0 >> 5)] = __popc(firsts[i]);
-      }
-      meet();
-      int n = 0, at[2] = {0, 0};
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        if (g == (i0 >> 5)) at[0] = n;
-        if (g == 4 + (i0 >> 5)) at[1] = n;
-        n += S.ad.n_group[g];
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (first_of[i]) S.ad.list[lb][at[i] + __popc(firsts[i] & ((1u << lane) - 1u))] = ids[i0 + 128 * i];
-      if (i0 == 0) S.ad.n_list[lb] = n;
-      meet();
-      if (i0 == 0) mbarrier_arrive(&S.ad.list_full[lb]);
-    };
-    Tile T, next;
+    uint32_t it = 0, tails = 0, n_tile = 0;
+    bool alive = true;
     int e = 0;
-    bool more = tile_at<kMode, kFeat>(S, p, first, e, next);
-    if (more) make_list(next, 0);
+    Tile T;
     pdl_wait();   // the u rows
-    uint32_t n_tile = 0;
-    for (int t = first; more; t += stride, ++n_tile) {
-      T = next;
-      more = tile_at<kMode, kFeat>(S, p, t + stride, e, next);
-      if (more) make_list(next, n_tile + 1);   // the loading warp needs it before this tile is done
-      const int lb = n_tile % kLists, n = S.ad.n_list[lb], blocks = (p.rank + 63) / 64, pairs = n * blocks;
+    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
+      const int lb = n_tile % kLists;
+      if (!wait_bar_warp(&S.ad.list_full[lb], (n_tile / kLists) & 1, &S.abort)) break;
+      const int n = S.ad.n_list[lb], blocks = (p.rank + 63) / 64, pairs = n * blocks;
       const int half = T.n / 2, c = rank * half + i0;   // this thread's column, one of this CTA's half
       const int mine = i0 < half ? S.ad.id[lb][c] : -1;
       int at0 = 0;
@@ -722,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             const int s = it % kStages;
             // the B rows have landed, so the stage was free (its own barrier's phase would be ambiguous here: these
             // warps do not see the steps in between)
-            alive = alive && wait_bar(&S.tail[s], (tails >> s) & 1, &S.abort);
+            alive = alive && wait_bar_warp(&S.tail[s], (tails >> s) & 1, &S.abort);
             tails ^= 1u << s;
             if (i0 < half) {
               uint8_t* row = S.stage[s] + kHalf + 128 * i0;
@@ -753,6 +746,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         }
       }
       it += T.steps - at0;
+      __syncwarp();
+      if (lane == 0) mbarrier_arrive(&S.ad.list_empty[lb]);
     }
   } else if constexpr (kMode == GM_WGRAD) {
     // rows behind the group's end in its last stage belong to another expert (or to nobody, and may hold
@@ -765,7 +760,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       it += T.steps;
       if (!(T.rows & 15)) continue;
       const int s = (it - 1) % kStages, lo = ((T.rows - 1) & 63) + 1, hi = (lo + 15) & ~15;
-      if (!wait_bar(&S.tail[s], (phases >> s) & 1, &S.abort)) break;
+      if (!wait_bar_warp(&S.tail[s], (phases >> s) & 1, &S.abort)) break;
       phases ^= 1u << s;
       for (int i = lane; i < (hi - lo) * 32; i += 32) {   // four blocks of 64 x 128 bytes, eight 16-byte words a row
         const int blk = (i & 31) >> 3, word = i & 7, row = lo + (i >> 5);
@@ -967,7 +962,7 @@ __global__ void __launch_bounds__(192)
       for (int i = 0; i < kEarly; ++i)
         if (first + i * step < rows) delta[i] = adapter_values(p, row0 + first + i * step, f);
     }
-    ok = mbar_wait_bounded(&acc_full, 0, err_word()) && !s_abort;
+    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full, 0, err_word()) && !s_abort);
     fence_after();
     const int q = warp & 3;
     if (ok)
@@ -1141,7 +1136,7 @@ __global__ void __launch_bounds__(192)
     it += steps;
     bool ok = true;
     if (warp >= 2) {
-      ok = mbar_wait_bounded(&acc_full, pass & 1, err_word()) && !s_abort;
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full, pass & 1, err_word()) && !s_abort);
       fence_after();
       const int q = warp & 3;
       if (ok)
@@ -1176,6 +1171,8 @@ __global__ void __launch_bounds__(192)
 }
 
 // ------------------------------------------------------------------ launches
+
+constexpr int kMaxKernels = 16;
 
 struct DeviceInfo {
   int sms = 0;
@@ -1214,11 +1211,30 @@ bool map_gated(CUtensorMap* m, const void* base, int E, int f, int k, bool bf16)
   return encode_tiles(m, base, 5, dim, stride, box, bf16);
 }
 
+// Dynamic shared memory past 48 KB has to be allowed once for a kernel and device.
+template <typename K>
+bool allow_smem(K kernel, size_t smem) {
+  static std::atomic<uint64_t> done[kMaxKernels];   // devices, by kernel
+  static std::atomic<const void*> known[kMaxKernels];
+  int dev = 0, i = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const void* id = reinterpret_cast<const void*>(kernel);
+  for (; i < kMaxKernels; ++i) {
+    const void* at = known[i].load(std::memory_order_acquire);
+    if (at == id || (!at && known[i].compare_exchange_strong(at, id)) || at == id) break;
+  }
+  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+  if (i < kMaxKernels && (done[i].load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return false;
+  if (i < kMaxKernels) done[i].fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
 template <typename K>
 bool launch(K kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s, const GmMaps& maps,
             const GmParams& p, int split) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return false;
+  if (!allow_smem(kernel, smem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -1246,7 +1262,8 @@ bool launch_big(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s) 
   const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
                                          : std::min(p.E, p.m) + static_cast<long long>(p.m) / 256;
   const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
-  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), BigCfg<kMode, kEpi>::kThreads, sizeof(BigSmem<kMode, kEpi>) + 1024, 2, s, maps, p, 0);
+  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), BigCfg<kMode, kEpi>::kThreads,
+                sizeof(BigSmem<kMode, kEpi>) + 1024, 2, s, maps, p, 0);
 }
 
 template <int kMode, int kEpi>
@@ -1254,8 +1271,12 @@ bool launch_small(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s
   constexpr int kFeat = kEpi == GM_GATED ? 64 : 128;
   const int ft = (p.feat + kFeat - 1) / kFeat, tiles = std::min(p.E, p.m) + p.m / kSmallCols;
   const int steps = (p.red + 63) / 64;
-  int split = 1;   // CTAs that share a tile's reduction: enough for three CTAs on every SM, at least two k64 steps each
-  while (split < kMaxSplit && 2 * split * ft * static_cast<long long>(tiles) <= 3 * sms && 4 * split <= steps) split *= 2;
+  // CTAs that share a tile's reduction: up to three on every SM (two with adapters, whose many columns make the sum over
+  // the cluster dearer: 48 rows 17.7 us against 18.8), at least two k64 steps each
+  constexpr int kPerSm = kEpi == GM_ADAPT ? 2 : 3;
+  int split = 1;
+  while (split < kMaxSplit && 2 * split * ft * static_cast<long long>(tiles) <= kPerSm * sms && 4 * split <= steps)
+    split *= 2;
   return launch(k_grouped_small<kMode, kEpi>, dim3(ft * split, tiles), 192, kSmallRing + 1024, split, s, maps, p, split);
 }
 
@@ -1271,13 +1292,13 @@ bool launch_adapter_down_many(const GmOperands& o, const GmParams& p, const floa
   const int blocks = (p.m + kDownCols - 1) / kDownCols, steps = (o.k + 63) / 64, most = std::min(kDownCols, p.n_adapters);
   DeviceInfo d;
   if (!device_info(&d)) return false;
-  int split = 1;   // two CTAs an SM
-  while (split < kMaxSplit && 2 * split * blocks <= 2 * d.sms && 4 * split <= steps) split *= 2;
+  // one CTA an SM from the split, two with the shares of the adapters: measured 58 / 93 us (one adapter / runs of 41
+  // rows, 4096 rows) against 62 / 97 with twice the split
+  int split = 1;
+  while (split < kMaxSplit && 2 * split * blocks <= d.sms && 4 * split <= steps) split *= 2;
   const int shares = std::max(1, std::min((most * slot + 127) / 128, 2 * d.sms / (split * blocks)));
   const size_t smem = kDownStages * kDownStage + 1024;
-  if (cudaFuncSetAttribute(k_adapter_down_many, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) !=
-      cudaSuccess)
-    return false;
+  if (!allow_smem(k_adapter_down_many, smem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(split, blocks, shares);
   cfg.blockDim = dim3(192);
@@ -1316,7 +1337,9 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
     return launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);
-  for (int i = 0; i < (small ? kSmallCols / 16 : kRowMaps); ++i)
+  // a tile has at most all of the rows, and at most kSmallCols or 256 (half of them a CTA)
+  const int largest = small ? (std::min(p.m, kSmallCols) + 15) / 16 : ((std::min(p.m, 256) + 31) & ~31) / 32;
+  for (int i = 0; i < largest; ++i)
     if (!map_rows(&maps.b[i], o.x, mode == GM_FWD ? o.k : o.n, p.m, o.ldx, 16 * (i + 1), p.bf16)) return false;
   if (epi == GM_GATED ? !map_gated(&maps.a, o.w, p.E, p.feat, o.k, p.bf16)
                       : !map_weights(&maps.a, o.w, p.E, o.n, o.k, mode == GM_FWD ? 128 : 64, p.bf16))

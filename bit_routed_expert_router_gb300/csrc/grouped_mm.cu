@@ -394,11 +394,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
   __syncthreads();
   if (kMode != GM_WGRAD && warp == 0) {
+    // Parts of at most 256 rows; of 128 or 64 where the tiles then still are one round of the pairs, which few tiles of
+    // 256 would leave idle (256 rows and 2816 features: 11 tiles for 76 pairs).
+    int n128 = 0, n64 = 0, width = 256;
+    for (int e = lane; e < p.E; e += 32) {
+      const int rows = max(S.off[e + 1] - S.off[e], 0);
+      n128 += (rows + 127) / 128;
+      n64 += (rows + 63) / 64;
+    }
+    n128 = __reduce_add_sync(0xFFFFFFFFu, n128);
+    n64 = __reduce_add_sync(0xFFFFFFFFu, n64);
+    const int ft = (p.feat + kFeat - 1) / kFeat;
+    if (n64 * ft <= stride)
+      width = 64;
+    else if (n128 * ft <= stride)
+      width = 128;
     int base = 0;
     if (lane == 0) S.tiles[0] = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
-      int c = e < p.E ? (max(S.off[e + 1] - S.off[e], 0) + 255) / 256 : 0;
+      int c = e < p.E ? (max(S.off[e + 1] - S.off[e], 0) + width - 1) / width : 0;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int o = __shfl_up_sync(0xFFFFFFFFu, c, d);
@@ -1260,7 +1275,7 @@ bool launch_big(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s) 
   constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;
   const long long ft = (p.feat + kFeat - 1) / kFeat;
   const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
-                                         : std::min(p.E, p.m) + static_cast<long long>(p.m) / 256;
+                                         : std::min(p.E, p.m) + static_cast<long long>(p.m) / 64;   // most parts, of 64
   const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
   return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), BigCfg<kMode, kEpi>::kThreads,
                 sizeof(BigSmem<kMode, kEpi>) + 1024, 2, s, maps, p, 0);
@@ -1318,8 +1333,15 @@ bool launch_adapter_down_many(const GmOperands& o, const GmParams& p, const floa
 
 namespace {
 
-// Few rows per expert: the small kernel.  Its tiles re-read an expert's weights (from L2) for every 64 rows.
-bool few_rows(const GmParams& p) { return p.m <= (p.offsets ? 4 * static_cast<long long>(p.E) : 64); }
+// Few rows per expert: the small kernel.  Its tiles re-read an expert's weights (from L2) for every 64 rows, and its
+// adapters cost a row's rank times the features on the ordinary pipes.  Small against persistent kernel, 128 experts:
+// gated 2816 -> 704 at 4 rows an expert 125 us against 133, at 16 157 against 162, at 32 164 against 176; down 704 -> 2816
+// 68 / 68, 83 / 82, 92 / 86.  Adapters at 2816 x 2816: 128 rows of rank 16 16 us against 24, of rank 64 30 against 26;
+// 256 rows of rank 16 27 against 31.
+bool few_rows(const GmParams& p) {
+  if (p.offsets) return p.m <= 16 * static_cast<long long>(p.E);
+  return p.m <= 64 || (p.m <= 256 && p.m * p.rank <= 4096);
+}
 
 }  // namespace
 

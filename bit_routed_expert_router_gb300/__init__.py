@@ -331,8 +331,7 @@ def _rows(t, rows: int, cols: int, dev: int) -> bool:
 
 
 def _ld(t, rows: int, cols: int) -> int:
-    # the row stride of a single row says nothing
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    return t.stride(0) if rows > 1 else cols   # the row stride of a single row says nothing
 
 
 def _whole(t, dtype, dev: int, *shape) -> bool:

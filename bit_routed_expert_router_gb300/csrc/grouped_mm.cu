@@ -388,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
-  if (kEpi != GM_ADAPT) pdl_wait();   // adapters: only their u rows come from the previous kernel
+  pdl_wait();
   pdl_trigger();
   for (int e = tid; e <= p.E; e += BigCfg<kMode, kEpi>::kThreads)
     S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
@@ -699,7 +699,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     bool alive = true;
     int e = 0;
     Tile T;
-    pdl_wait();   // the u rows
     for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
       const int lb = n_tile % kLists;
       if (!wait_bar_warp(&S.ad.list_full[lb], (n_tile / kLists) & 1, &S.abort)) break;

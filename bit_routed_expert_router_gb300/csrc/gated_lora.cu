@@ -3,6 +3,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "gelu16.cuh"
 #include "grouped.h"
 
 namespace moe {
@@ -25,61 +26,33 @@ __device__ __forceinline__ uint32_t to_pair(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// GELU(g) and its derivative.  With P the normal distribution function and p
-// its density: g P(g) and P(g) + g p(g).  The tanh form: with t = tanh(s),
-// s = c (g + 0.044715 g^3): g (1 + t) / 2 and (1 + t) / 2 + g (1 - t^2) s' / 2.
-template <int kGelu>
-__device__ __forceinline__ float2 gelu_and_slope(float g) {
-  if (kGelu == 1) {
-    const float c = 0.7978845608028654f, g2 = g * g;
-    const float t = tanhf(c * g * (1.f + 0.044715f * g2));
-    const float half = 0.5f + 0.5f * t;
-    return make_float2(g * half, half + 0.5f * g * (1.f - t * t) * c * (1.f + 0.134145f * g2));
-  }
-  const float half = 0.5f + 0.5f * erff(g * 0.7071067811865476f);
-  return make_float2(g * half, half + g * 0.3989422804014327f * expf(-0.5f * g * g));
-}
-
 // dh = [da u GELU'(g), da GELU(g)] for h = [g, u]: 16-byte loads and stores,
-// eight features a word, kWords words a thread whose loads are issued together.
-// Memory-bound: 10 bytes in and out per feature and about 30 operations.
-template <bool kBf16, int kGelu, int kWords>
+// eight features a thread.  Memory-bound: 10 bytes in and out per feature and
+// about 30 operations; two words a thread were slower (41 us against 38 at
+// 32,768 x 704).
+template <bool kBf16, int kGelu>
 __global__ void __launch_bounds__(256) k_gated_grad(const uint16_t* h, long long ldh, const uint16_t* da, long long ldda,
                                                     uint16_t* dh, long long lddh, int m, int f, const int32_t* n_rows) {
   pdl_wait();
   pdl_trigger();
   const int rows = n_rows ? min(*n_rows, m) : m, words = f / 8;
-  const long long total = static_cast<long long>(rows) * words, stride = gridDim.x * 256LL;
-  for (long long i0 = blockIdx.x * 256LL + threadIdx.x; i0 < total; i0 += kWords * stride) {
-    uint4 gv[kWords], uv[kWords], dv[kWords];
-    long long row[kWords];
-    int col[kWords];
+  const long long i = blockIdx.x * 256LL + threadIdx.x, r = i / words;
+  if (r >= rows) return;
+  const int c = static_cast<int>(i - r * words) * 8;
+  const uint4 gv = *reinterpret_cast<const uint4*>(h + r * ldh + c);
+  const uint4 uv = *reinterpret_cast<const uint4*>(h + r * ldh + f + c);
+  const uint4 dv = *reinterpret_cast<const uint4*>(da + r * ldda + c);
+  const uint32_t g[4] = {gv.x, gv.y, gv.z, gv.w}, u[4] = {uv.x, uv.y, uv.z, uv.w}, d[4] = {dv.x, dv.y, dv.z, dv.w};
+  uint32_t dg[4], du[4];
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      const long long i = min(i0 + k * stride, total - 1);   // past the end: the last word again, not stored
-      row[k] = i / words;
-      col[k] = static_cast<int>(i - row[k] * words) * 8;
-      gv[k] = *reinterpret_cast<const uint4*>(h + row[k] * ldh + col[k]);
-      uv[k] = *reinterpret_cast<const uint4*>(h + row[k] * ldh + f + col[k]);
-      dv[k] = *reinterpret_cast<const uint4*>(da + row[k] * ldda + col[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < kWords; ++k) {
-      if (i0 + k * stride >= total) break;
-      const uint32_t g[4] = {gv[k].x, gv[k].y, gv[k].z, gv[k].w}, u[4] = {uv[k].x, uv[k].y, uv[k].z, uv[k].w};
-      const uint32_t d[4] = {dv[k].x, dv[k].y, dv[k].z, dv[k].w};
-      uint32_t dg[4], du[4];
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 gg = to_floats<kBf16>(g[w]), uu = to_floats<kBf16>(u[w]), dd = to_floats<kBf16>(d[w]);
-        const float2 a = gelu_and_slope<kGelu>(gg.x), b = gelu_and_slope<kGelu>(gg.y);
-        dg[w] = to_pair<kBf16>(dd.x * uu.x * a.y, dd.y * uu.y * b.y);
-        du[w] = to_pair<kBf16>(dd.x * a.x, dd.y * b.x);
-      }
-      *reinterpret_cast<uint4*>(dh + row[k] * lddh + col[k]) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-      *reinterpret_cast<uint4*>(dh + row[k] * lddh + f + col[k]) = make_uint4(du[0], du[1], du[2], du[3]);
-    }
+  for (int w = 0; w < 4; ++w) {
+    const float2 gg = to_floats<kBf16>(g[w]), uu = to_floats<kBf16>(u[w]), dd = to_floats<kBf16>(d[w]);
+    const float2 a = gelu16_and_slope<kGelu>(gg.x), b = gelu16_and_slope<kGelu>(gg.y);
+    dg[w] = to_pair<kBf16>(dd.x * uu.x * a.y, dd.y * uu.y * b.y);
+    du[w] = to_pair<kBf16>(dd.x * a.x, dd.y * b.x);
   }
+  *reinterpret_cast<uint4*>(dh + r * lddh + c) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+  *reinterpret_cast<uint4*>(dh + r * lddh + f + c) = make_uint4(du[0], du[1], du[2], du[3]);
 }
 
 // ------------------------------------------------------------------ adapters: u = s A x
@@ -232,11 +205,10 @@ bool launch_pdl(K kernel, dim3 grid, int threads, cudaStream_t s, A... args) {
 
 bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const void* da, long long ldda, void* dh,
                        long long lddh, int m, int f, const int32_t* n_rows, cudaStream_t s) {
-  constexpr int kWords = 2;
   const long long words = static_cast<long long>(m) * (f / 8);
-  const dim3 grid(static_cast<unsigned>(std::min<long long>((words + 256 * kWords - 1) / (256 * kWords), 1 << 20)));
-  const auto kernel = bf16 ? (gelu == 1 ? k_gated_grad<true, 1, kWords> : k_gated_grad<true, 0, kWords>)
-                           : (gelu == 1 ? k_gated_grad<false, 1, kWords> : k_gated_grad<false, 0, kWords>);
+  const dim3 grid(static_cast<unsigned>((words + 255) / 256));
+  const auto kernel = bf16 ? (gelu == 1 ? k_gated_grad<true, 1> : k_gated_grad<true, 0>)
+                           : (gelu == 1 ? k_gated_grad<false, 1> : k_gated_grad<false, 0>);
   return launch_pdl(kernel, grid, 256, s, static_cast<const uint16_t*>(h), ldh, static_cast<const uint16_t*>(da), ldda,
                     static_cast<uint16_t*>(dh), lddh, m, f, n_rows);
 }

@@ -28,6 +28,7 @@
 #include <atomic>
 #include <type_traits>
 
+#include "gelu16.cuh"
 #include "grouped.h"
 #include "tc16.cuh"
 #include "tensor_map.h"
@@ -112,11 +113,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 // The same by a whole warp, which then agrees on the outcome.
 __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
   return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort));
-}
-
-__device__ __forceinline__ float gelu(float v, int variant) {
-  if (variant == 1) return 0.5f * v * (1.f + tanhf(0.7978845608028654f * (v + 0.044715f * v * v * v)));
-  return 0.5f * v * (1.f + erff(v * 0.7071067811865476f));
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
@@ -643,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             __syncwarp();
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[0][i] = gelu(v[0][i], p.gelu) * v[1][i];
+          for (int i = 0; i < 16; ++i) v[0][i] = gelu16(v[0][i], p.gelu) * v[1][i];
           stage_16x32(buf16, v[0], p.bf16, lane);
           __syncwarp();
           store_16x32(buf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
@@ -1017,8 +1013,8 @@ __global__ void __launch_bounds__(192)
           store_out4(p.h, row * p.ldh + f, v, 0, p.bf16);
           store_out4(p.h, row * p.ldh + p.feat + f, up, 0, p.bf16);
         }
-        v = make_float4(gelu(v.x, p.gelu) * up.x, gelu(v.y, p.gelu) * up.y, gelu(v.z, p.gelu) * up.z,
-                        gelu(v.w, p.gelu) * up.w);
+        v = make_float4(gelu16(v.x, p.gelu) * up.x, gelu16(v.y, p.gelu) * up.y, gelu16(v.z, p.gelu) * up.z,
+                        gelu16(v.w, p.gelu) * up.w);
       }
       if (kEpi == GM_ADAPT) add(v, term);
       store_out4(p.y, row * p.ldy + f, v, p.out_f32, p.bf16);

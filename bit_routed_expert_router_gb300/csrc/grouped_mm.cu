@@ -61,6 +61,7 @@ struct BigCfg {
 };
 
 constexpr int kLists = 4;
+constexpr int kEarlyRows = 65536;   // adapters' rows up to which the down half is done in milliseconds
 struct AdaptSmem {
   int id[kLists][256];     // adapter of each column of a tile, -1 for none (tiles in turn)
   int list[kLists][256];   // its distinct adapters, in order
@@ -384,7 +385,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
-  pdl_wait();
+  // with adapters only the u rows come from the previous kernel, and the products of W start on the SMs it leaves (4096
+  // rows 68 -> 61 us) unless it may take so long that the bounded waits for u would run out
+  if (kEpi != GM_ADAPT || p.m > kEarlyRows) pdl_wait();
   pdl_trigger();
   for (int e = tid; e <= p.E; e += BigCfg<kMode, kEpi>::kThreads)
     S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
@@ -695,6 +698,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     bool alive = true;
     int e = 0;
     Tile T;
+    pdl_wait();   // the u rows
     for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
       const int lb = n_tile % kLists;
       if (!wait_bar_warp(&S.ad.list_full[lb], (n_tile / kLists) & 1, &S.abort)) break;
@@ -1054,7 +1058,7 @@ __global__ void __launch_bounds__(192)
   __shared__ uint64_t full[kDownStages], empty[kDownStages], acc_full;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
-  __shared__ int s_n, s_list[kDownCols], s_nth[kDownCols];   // distinct adapters; which of them a row has, or -1
+  __shared__ int s_n, s_list[64], s_nth[64];   // distinct adapters; which of them a row has, or -1
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cluster_rank()), row0 = blockIdx.y * kDownCols, rows = min(kDownCols, p.m - row0);

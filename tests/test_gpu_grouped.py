@@ -291,7 +291,8 @@ def lora_case(seed, t, n, k, N, rank, dtype, order, top=2):
     (1, 8, 8, 1, 8, "one"), (1, 264, 1000, 3, 16, "runs"), (2, 136, 72, 5, 24, "any"), (7, 72, 328, 2, 64, "wild"),
     (33, 200, 512, 40, 8, "any"), (64, 704, 200, 7, 128, "any"), (64, 136, 136, 64, 40, "none"),
     (65, 264, 136, 9, 16, "any"), (127, 40, 64, 3, 32, "wild"), (300, 328, 520, 4, 64, "runs"),
-    (513, 1000, 264, 100, 8, "any"), (1000, 136, 1000, 1, 128, "one"), (600, 520, 72, 300, 16, "any")])
+    (513, 1000, 264, 100, 8, "any"), (1000, 136, 1000, 1, 128, "one"), (600, 520, 72, 300, 16, "any"),
+    (2100, 520, 328, 12, 64, "runs"), (66000, 72, 64, 5, 8, "runs")])
 def test_adapters(t, n, k, N, rank, order, dtype):
     x, w, ids, a, b, scale = lora_case(t, t, n, k, N, rank, dtype, order)
     whole, y = buffer(dtype, t, n)

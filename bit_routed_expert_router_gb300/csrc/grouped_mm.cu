@@ -50,6 +50,12 @@ constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memor
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kUWarps = 4;           // adapters: warps that stage u
 constexpr int kAccCols = 256;
+// fp32 outputs of long reductions: k64 steps that are summed in one accumulator.  The MMA adds its products to the
+// accumulator with truncation, whose bias grows with the number of steps (relative error of a sum of 2816 products 2.6e-6,
+// of 704 9e-7); pieces of 384 are added with rounding by the warps that read them (3.5e-7).  A 16-bit output's own
+// rounding is far above either.  The sums' registers cost the weight gradient 5% (408 -> 428 us), so the persistent
+// kernel has them from kLongRed on (weight gradients: on average).
+constexpr int kSegSteps = 6, kLongRed = 768;
 
 // The weight gradient's tiles have few stages each and store far more than they
 // load: two buffers a warp for TMA stores, and a stage less.
@@ -307,6 +313,20 @@ __device__ __forceinline__ void store_32x32(uint32_t buf, const float (&v)[2][16
   }
 }
 
+// One feature a lane of 32 fp32 columns: each store of the warp is 128 contiguous bytes of a column.
+__device__ __forceinline__ void store_f32(const float (&v)[32], float* out, long long ld, int cols, int feats, int lane) {
+  if (lane >= feats) return;
+  float* y = out + lane;
+  if (cols >= 32) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) y[c * ld] = v[c];
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c < cols) y[c * ld] = v[c];
+  }
+}
+
 // The weight gradient's stores: swizzled rows of 32 features in one of two
 // buffers, which the TMA engine writes out while the other is filled.  A
 // 64-byte segment of each column per warp and ordinary store kept the LSU's
@@ -517,10 +537,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       Tile T;
       for (int t = first; ok && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
         if (T.steps == 0) continue;
-        const int buf = count & 1;
+        int buf = count & 1;
         ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort);
         fence_after();
-        const uint32_t d = tmem + buf * kAccCols, idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb);
+        uint32_t d = tmem + buf * kAccCols;
+        const uint32_t idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb);
         const int red = kMode == GM_WGRAD ? T.rows : p.red;
         const auto multiply = [&](int s, int k, bool first_step) {   // k of the stage's 64
           fence_after();
@@ -550,10 +571,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             if (!ok) break;
             if (ks >= T.steps) continue;
           }
+          if (kEpi == GM_F32 && ks > 0 && ks % kSegSteps == 0) {   // the next piece in the other accumulator
+            commit_pair(&S.acc_full[buf], 3);
+            ++count;
+            buf = count & 1;
+            d = tmem + buf * kAccCols;
+            if (!(ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort))) break;
+            fence_after();
+          }
           const int s = it % kStages;
           if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort))) break;
           fulls ^= 1u << s;
-          multiply(s, red - 64 * ks, ks == 0);
+          multiply(s, red - 64 * ks, ks == 0 || (kEpi == GM_F32 && ks % kSegSteps == 0));
           ++it;
         }
         if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
@@ -577,11 +606,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       // first feature of this warp's 32 lanes (GM_GATED: 16 gate and 16 up lanes of 16 features)
       const int f0 = T.f0 + (kEpi == GM_GATED ? 64 * rank + 16 * q : 128 * rank + 32 * q);
       const int feats = p.feat - f0;   // none or less: the output ends before this warp's features do
-      const int buf = count & 1, c_first = 32 * ((warp - 2) >> 2);
-      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
-      fence_after();
+      const int c_first = 32 * ((warp - 2) >> 2);
       const long long out0 =
           (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
+      if constexpr (kEpi == GM_F32) {
+        // a lane holds one feature of up to 128 columns, summed over the pieces; each store of the warp is 128 contiguous
+        // bytes of a column
+        float sum[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
+        bool ok = true;
+        for (int ks = 0; ok && ks < T.steps; ks += kSegSteps, ++count) {
+          const int buf = count & 1;
+          if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort))) break;
+          fence_after();
+          const uint32_t at = tmem + buf * kAccCols + c_first + (static_cast<uint32_t>(32 * q) << 16);
+          if (ks == 0) {
+            if (c_first < T.cols) ld_cols32x2(at, at + 64, sum[0], sum[1]);
+            if (c_first + 128 < T.cols) ld_cols32x2(at + 128, at + 192, sum[2], sum[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (c_first + 64 * i < T.cols) {
+                float w[32];
+                ld_cols32(at + 64 * i, w);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sum[i][c] += w[c];
+              }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          store_f32(sum[i], static_cast<float*>(p.y) + out0 + (c_first + 64 * i) * p.ldy, p.ldy, T.cols - c_first - 64 * i,
+                    feats, lane);
+        continue;
+      }
+      const int buf = count & 1;
+      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
+      fence_after();
       // the accumulator goes back as soon as this warp has read its last columns, before they are stored
       const auto release = [&](int c0) {
         if (!T.steps || c0 + 64 < T.cols) return;
@@ -592,8 +660,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       if (c_first >= T.cols) release(c_first);
       for (int c0 = c_first; c0 < T.cols; c0 += 64) {
         if (kEpi == GM_PLAIN && p.out_f32) {
-          // a lane holds one feature of 32 columns: each store of the warp is 128 contiguous bytes of a column,
-          // straight from the accumulator
           float w[32];
           if (T.steps) {
             ld_cols32(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), w);
@@ -602,18 +668,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             for (int i = 0; i < 32; ++i) w[i] = 0.f;
           }
           release(c0);
-          float* y = static_cast<float*>(p.y) + out0 + c0 * p.ldy + lane;
-          const int cols = T.cols - c0;
-          if (lane < feats) {
-            if (cols >= 32) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) y[i * p.ldy] = w[i];
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i < cols) y[i * p.ldy] = w[i];
-            }
-          }
+          store_f32(w, static_cast<float*>(p.y) + out0 + c0 * p.ldy, p.ldy, T.cols - c0, feats, lane);
           continue;
         }
         float v[2][16];
@@ -840,7 +895,7 @@ __global__ void __launch_bounds__(192)
   constexpr bool kTa = kMode == GM_DGRAD;
   constexpr int kFeat = kEpi == GM_GATED ? 64 : 128;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[8], empty[8], acc_full;
+  __shared__ uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_tile[4];   // expert, first row, rows
@@ -849,7 +904,7 @@ __global__ void __launch_bounds__(192)
   const int rank = static_cast<int>(cluster_rank()), f0 = blockIdx.x / split * kFeat;
 
   if (warp == 1) {
-    tmem_alloc<false>(&s_tmem, kSmallCols);
+    tmem_alloc<false>(&s_tmem, 2 * kSmallCols);
   } else if (tid == 64) {
     prefetch_map(&maps.a);
     s_abort = 0;
@@ -857,7 +912,11 @@ __global__ void __launch_bounds__(192)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
+    mbar_init(&drain, 1);
     fence_mbar_init();
   }
   if (kEpi != GM_ADAPT) pdl_wait();   // adapters: nothing but the u rows comes from the previous kernel
@@ -904,12 +963,14 @@ __global__ void __launch_bounds__(192)
   const uint32_t tmem = s_tmem;
   const int expert = s_tile[0], row0 = s_tile[1], rows = s_tile[2];
   if (rows <= 0) {   // no such tile: the same for every CTA of the cluster
-    if (warp == 1) tmem_free<false>(tmem, kSmallCols);
+    if (warp == 1) tmem_free<false>(tmem, 2 * kSmallCols);
     return;
   }
   const int n = (rows + 15) & ~15;
   const int bytes = kHalf + n * 128, stages = min(8, kSmallRing / bytes);
   const int all = (p.red + 63) / 64, k0 = all * rank / split, steps = all * (rank + 1) / split - k0;
+  // pieces of the reduction: fp32 outputs in kSegSteps, in two accumulators in turn
+  const int seg = p.out_f32 ? kSegSteps : steps;
 
   if (warp == 0) {
     if (elect_one()) {
@@ -937,18 +998,28 @@ __global__ void __launch_bounds__(192)
   } else if (warp == 1) {
     if (elect_one()) {
       const uint32_t idesc = instr_desc(p.bf16, 128, n, kTa, false);
-      for (int ks = 0; ks < steps; ++ks) {
-        const int s = ks % stages;
-        if (!wait_bar(&full[s], (ks / stages) & 1, &s_abort)) break;
+      bool go = true;
+      for (int ks = 0, piece = 0; go && ks < steps; ++piece) {
+        const int buf = piece & 1, end = min(ks + seg, steps);
+        go = wait_bar(&acc_empty[buf], ((piece >> 1) & 1) ^ 1, &s_abort);
         fence_after();
-        const uint32_t a = smem_u32(ring) + s * bytes;
-        const uint64_t da = tile_desc<kTa>(a), db = tile_desc<false>(a + kHalf);
-        const int nk = (min(64, p.red - 64 * (k0 + ks)) + 15) / 16;
-        for (int kk = 0; kk < nk; ++kk)
-          mma<false>(tmem, da + kk * kStep16<kTa>, db + kk * kStep16<false>, idesc, (ks | kk) != 0);
-        commit(&empty[s]);
+        for (bool first = true; go && ks < end; ++ks) {
+          const int s = ks % stages;
+          if (!(go = wait_bar(&full[s], (ks / stages) & 1, &s_abort))) break;
+          fence_after();
+          const uint32_t a = smem_u32(ring) + s * bytes;
+          const uint64_t da = tile_desc<kTa>(a), db = tile_desc<false>(a + kHalf);
+          const int nk = (min(64, p.red - 64 * (k0 + ks)) + 15) / 16;
+          for (int kk = 0; kk < nk; ++kk, first = false)
+            mma<false>(tmem + buf * kSmallCols, da + kk * kStep16<kTa>, db + kk * kStep16<false>, idesc, !first);
+          commit(&empty[s]);
+        }
+        if (go) commit(&acc_full[buf]);
       }
-      commit(&acc_full);   // after every product above, also when a wait ran out
+      if (!go) {   // the products in flight read shared memory: wait for them
+        commit(&drain);
+        mbar_wait_bounded(&drain, 0, err_word());
+      }
     }
   }
   __syncwarp();
@@ -976,17 +1047,34 @@ __global__ void __launch_bounds__(192)
       for (int i = 0; i < kEarly; ++i)
         if (first + i * step < rows) delta[i] = adapter_values(p, row0 + first + i * step, f);
     }
-    ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full, 0, err_word()) && !s_abort);
-    fence_after();
     const int q = warp & 3;
-    if (ok)
-      for (int c = 0; c < n; c += 16) {
-        float v[16];
-        ld_cols16(tmem + c + (static_cast<uint32_t>(32 * q) << 16), v);
+    float acc[kSmallCols / 16][16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kSmallPitch + 32 * q + lane] = v[i];
-      }
-    fence_before();
+    for (int j = 0; j < kSmallCols / 16; ++j)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
+    for (int ks = 0, piece = 0; ok && ks < steps; ks += seg, ++piece) {
+      const int buf = piece & 1;
+      if (!(ok = wait_bar_warp(&acc_full[buf], (piece >> 1) & 1, &s_abort))) break;
+      fence_after();
+#pragma unroll
+      for (int j = 0; j < kSmallCols / 16; ++j)
+        if (16 * j < n) {
+          float v[16];
+          ld_cols16(tmem + buf * kSmallCols + 16 * j + (static_cast<uint32_t>(32 * q) << 16), v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[j][i] += v[i];
+        }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbarrier_arrive(&acc_empty[buf]);
+    }
+    if (ok)
+#pragma unroll
+      for (int j = 0; j < kSmallCols / 16; ++j)
+        if (16 * j < n)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(16 * j + i) * kSmallPitch + 32 * q + lane] = acc[j][i];
   }
   if (split > 1)
     cluster_sync();
@@ -1038,7 +1126,7 @@ __global__ void __launch_bounds__(192)
     cluster_sync();   // the others may still read this CTA's part
   else
     __syncthreads();
-  if (warp == 1) tmem_free<false>(tmem, kSmallCols);
+  if (warp == 1) tmem_free<false>(tmem, 2 * kSmallCols);
 }
 
 // ------------------------------------------------------------------ adapters' down half for many rows
@@ -1355,7 +1443,8 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
     const cuuint64_t stride[2] = {row, row * o.n};
     if (!p.out_f32 && !encode_store(&maps.c, p.y, dim, stride, p.bf16)) return false;
-    return launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
+    return p.out_f32 && p.m / p.E > kLongRed ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s)
+                                             : launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);
   // a tile has at most all of the rows, and at most kSmallCols or 256 (half of them a CTA)
@@ -1366,13 +1455,18 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
                       : !map_weights(&maps.a, o.w, p.E, o.n, o.k, mode == GM_FWD ? 128 : 64, p.bf16))
     return false;
   if (epi == GM_ADAPT && !small && !map_weights(&maps.c, p.b, p.n_adapters, p.feat, p.rank, 128, p.bf16)) return false;
+  const bool long_f32 = p.out_f32 && p.red > kLongRed;
   if (mode == GM_DGRAD)
-    return small ? launch_small<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s) : launch_big<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s);
+    return small      ? launch_small<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s)
+           : long_f32 ? launch_big<GM_DGRAD, GM_F32>(maps, p, d.sms, s)
+                      : launch_big<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s);
   if (epi == GM_GATED)
     return small ? launch_small<GM_FWD, GM_GATED>(maps, p, d.sms, s) : launch_big<GM_FWD, GM_GATED>(maps, p, d.sms, s);
   if (epi == GM_ADAPT)
     return small ? launch_small<GM_FWD, GM_ADAPT>(maps, p, d.sms, s) : launch_big<GM_FWD, GM_ADAPT>(maps, p, d.sms, s);
-  return small ? launch_small<GM_FWD, GM_PLAIN>(maps, p, d.sms, s) : launch_big<GM_FWD, GM_PLAIN>(maps, p, d.sms, s);
+  return small      ? launch_small<GM_FWD, GM_PLAIN>(maps, p, d.sms, s)
+         : long_f32 ? launch_big<GM_FWD, GM_F32>(maps, p, d.sms, s)
+                    : launch_big<GM_FWD, GM_PLAIN>(maps, p, d.sms, s);
 }
 
 bool grouped_error(cudaStream_t s, uint32_t* err) {

@@ -98,6 +98,18 @@ def test_weight_gradients(i, counts, dtype, out):
     assert (dw[E] == SENTINEL).all()
 
 
+def test_long_weight_gradients():
+    """Groups of more than 768 rows on average: the reduction goes in pieces."""
+    g, counts, n, k = gen(4), [1000, 385, 0, 384, 2600], 264, 328
+    x, dy, off = ints(g, BF16, sum(counts), k), ints(g, BF16, sum(counts), n), offsets_of(counts)
+    dw = torch.full((5, n, k), SENTINEL, dtype=F32, device="cuda")
+    ok(moe.moe_grouped_wgrad(dy, x, off, dw))
+    lo = 0
+    for e, c in enumerate(counts):
+        assert torch.equal(dw[e], (dy[lo:lo + c].double().T @ x[lo:lo + c].double()).float()), e
+        lo += c
+
+
 def test_full_shape_products():
     """The repository's full layer: 128 experts, 32,768 rows, whole-number inputs."""
     g, E, n, k = gen(3), 128, 1408, 2816
@@ -120,19 +132,20 @@ def test_full_shape_products():
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
-@pytest.mark.parametrize("counts", [[2, 0, 3], [150, 31, 0, 300]])
-def test_products_of_real_values(dtype, counts):
-    """Normal inputs.  A k16 step adds 16 products to the accumulator with at most 17 roundings or truncations of
-    2^-23 of the largest magnitude that occurs, which sum |x w| bounds: k / 16 steps give 17 k / 16 * 2^-23 of it
-    (the inputs' products are exact in fp32); the 32-bit output is not rounded further."""
-    g, n, k = gen(5), 264, 1000
+@pytest.mark.parametrize("k", [200, 1000, 2816])
+@pytest.mark.parametrize("counts", [[2, 0, 3], [50, 31, 0, 64], [150, 31, 0, 300]])
+def test_products_of_real_values(dtype, counts, k):
+    """Normal inputs, 32-bit outputs.  A k16 step adds 16 products to the accumulator with at most 17 roundings or
+    truncations of 2^-23 of the largest magnitude that occurs, which sum |x w| bounds; an accumulator takes at most 24
+    steps (48 where the reduction is no longer than 768), and the pieces are added with one rounding each."""
+    g, n = gen(5), 264
     m = sum(counts)
     x = torch.randn(m, k, generator=g, device="cuda").to(dtype)
     w = (torch.randn(len(counts), n, k, generator=g, device="cuda") / k ** 0.5).to(dtype)
     y = torch.empty(m, n, dtype=F32, device="cuda")
     ok(moe.moe_grouped_mm(x, offsets_of(counts), w, y))
     ref, mag = products(x, counts, w), products(x.abs(), counts, w.abs())
-    assert ((y - ref).abs() <= (k / 16 + 1) * 17 * 2 ** -23 * mag).all()
+    assert ((y - ref).abs() <= ((min(k / 16 + 1, 24) if k > 768 else k / 16 + 1) * 17 + k / 384 + 8) * 2 ** -23 * mag).all()
 
 
 def test_a_group_keeps_its_nan():

@@ -54,8 +54,9 @@ constexpr int kAccCols = 256;
 // accumulator with truncation, whose bias grows with the number of steps (relative error of a sum of 2816 products 2.6e-6,
 // of 704 9e-7); pieces of 384 are added with rounding by the warps that read them (3.5e-7).  A 16-bit output's own
 // rounding is far above either.  The sums' registers cost the weight gradient 5% (408 -> 428 us), so the persistent
-// kernel has them from kLongRed on (weight gradients: on average).
-constexpr int kSegSteps = 6, kLongRed = 768;
+// kernel has them past kLongRed (weight gradients: on average past half of it, as the largest groups have a few times the
+// average).
+constexpr int kSegSteps = 6, kLongRed = 512;
 
 // The weight gradient's tiles have few stages each and store far more than they
 // load: two buffers a warp for TMA stores, and a stage less.
@@ -1443,7 +1444,7 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
     const cuuint64_t stride[2] = {row, row * o.n};
     if (!p.out_f32 && !encode_store(&maps.c, p.y, dim, stride, p.bf16)) return false;
-    return p.out_f32 && p.m / p.E > kLongRed ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s)
+    return p.out_f32 && p.m / p.E > kLongRed / 2 ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s)
                                              : launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);

@@ -99,7 +99,7 @@ def test_weight_gradients(i, counts, dtype, out):
 
 
 def test_long_weight_gradients():
-    """Groups of more than 768 rows on average: the reduction goes in pieces."""
+    """Groups of hundreds of rows: the reduction goes in pieces."""
     g, counts, n, k = gen(4), [1000, 385, 0, 384, 2600], 264, 328
     x, dy, off = ints(g, BF16, sum(counts), k), ints(g, BF16, sum(counts), n), offsets_of(counts)
     dw = torch.full((5, n, k), SENTINEL, dtype=F32, device="cuda")
@@ -137,7 +137,7 @@ def test_full_shape_products():
 def test_products_of_real_values(dtype, counts, k):
     """Normal inputs, 32-bit outputs.  A k16 step adds 16 products to the accumulator with at most 17 roundings or
     truncations of 2^-23 of the largest magnitude that occurs, which sum |x w| bounds; an accumulator takes at most 24
-    steps (48 where the reduction is no longer than 768), and the pieces are added with one rounding each."""
+    steps (32 where the reduction is no longer than 512), and the pieces are added with one rounding each."""
     g, n = gen(5), 264
     m = sum(counts)
     x = torch.randn(m, k, generator=g, device="cuda").to(dtype)
@@ -145,7 +145,7 @@ def test_products_of_real_values(dtype, counts, k):
     y = torch.empty(m, n, dtype=F32, device="cuda")
     ok(moe.moe_grouped_mm(x, offsets_of(counts), w, y))
     ref, mag = products(x, counts, w), products(x.abs(), counts, w.abs())
-    assert ((y - ref).abs() <= ((min(k / 16 + 1, 24) if k > 768 else k / 16 + 1) * 17 + k / 384 + 8) * 2 ** -23 * mag).all()
+    assert ((y - ref).abs() <= ((min(k / 16 + 1, 24) if k > 512 else k / 16 + 1) * 17 + k / 384 + 8) * 2 ** -23 * mag).all()
 
 
 def test_a_group_keeps_its_nan():

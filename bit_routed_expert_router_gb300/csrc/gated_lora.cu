@@ -106,33 +106,31 @@ __device__ __forceinline__ void down_products(float (&acc)[4][4], const uint16_t
         }
       }
   };
-  Piece cur, next;
-  load(cur, k0);
+  Piece a, b;   // three in flight were no faster
+  load(a, k0);
   for (; k0 < k; k0 += 2 * step) {
-    load(next, k0 + step);
-    multiply(cur);
-    load(cur, k0 + 2 * step);
-    multiply(next);
+    load(b, k0 + step);
+    multiply(a);
+    load(a, k0 + 2 * step);
+    multiply(b);
   }
 }
 
-// A CTA: 16 kMt rank rows x 32 rows of x, for the distinct adapters number z,
+// A CTA: 16 rank rows x 32 rows of x, for the distinct adapters number z,
 // z + gridDim.z, ... of those rows.  An adapter's rows are gathered, so that
-// its products cost 8 rows at a time whatever their order.  Warps: kMt tiles
-// of 16 ranks, the others split the reduction and are added in order through
-// shared memory.
-template <bool kBf16, int kMt>
+// its products cost 8 rows at a time whatever their order.  The warps split
+// the reduction and are added in order through shared memory.
+template <bool kBf16>
 __global__ void __launch_bounds__(32 * kDownWarps)
     k_adapter_down(const uint16_t* __restrict__ x, long long ldx, int t, const uint16_t* __restrict__ a,
                    const float* __restrict__ scale, const int32_t* __restrict__ ids, int n_adapters, int rank, int k,
                    float* u) {
-  constexpr int kSplit = kDownWarps / kMt;
-  __shared__ float red[kSplit][16 * kMt][kDownRows + 1];
+  __shared__ float red[kDownWarps][16][kDownRows + 1];
   __shared__ uint8_t list[kDownWarps][kDownRows];   // a warp's own copy: the adapter's rows in order
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int row0 = blockIdx.x * kDownRows, r0 = blockIdx.y * 16 * kMt, r1 = r0 + 16 * (warp % kMt), part = warp / kMt;
+  const int row0 = blockIdx.x * kDownRows, r0 = blockIdx.y * 16;
   int id = -1;
   if (row0 + lane < t) {
     id = ids[row0 + lane];
@@ -149,7 +147,7 @@ __global__ void __launch_bounds__(32 * kDownWarps)
     if (id == ad) list[warp][__popc(same & ((1u << lane) - 1u))] = static_cast<uint8_t>(lane);
     __syncwarp();
     const float sc = scale[ad];
-    const uint16_t* arow = a + (static_cast<size_t>(ad) * rank + r1 + g) * k;
+    const uint16_t* arow = a + (static_cast<size_t>(ad) * rank + r0 + g) * k;
     const uint16_t* xrow[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)   // the last group repeats its last row
@@ -159,28 +157,25 @@ __global__ void __launch_bounds__(32 * kDownWarps)
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    if (r1 < rank) {
-      const bool has0 = r1 + g < rank, has1 = r1 + 8 + g < rank;
-      const int k0 = 64 * part, step = 64 * kSplit;
-      if (groups == 1)
-        down_products<kBf16, 1>(acc, arow, has0, has1, xrow, k, k0, step, t4);
-      else if (groups == 2)
-        down_products<kBf16, 2>(acc, arow, has0, has1, xrow, k, k0, step, t4);
-      else
-        down_products<kBf16, 4>(acc, arow, has0, has1, xrow, k, k0, step, t4);
-    }
+    const bool has0 = r0 + g < rank, has1 = r0 + 8 + g < rank;
+    const int k0 = 64 * warp, step = 64 * kDownWarps;
+    if (groups == 1)
+      down_products<kBf16, 1>(acc, arow, has0, has1, xrow, k, k0, step, t4);
+    else if (groups == 2)
+      down_products<kBf16, 2>(acc, arow, has0, has1, xrow, k, k0, step, t4);
+    else
+      down_products<kBf16, 4>(acc, arow, has0, has1, xrow, k, k0, step, t4);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[part][16 * (warp % kMt) + g + 8 * (i >> 1)][8 * j + 2 * t4 + (i & 1)] = acc[j][i];
+      for (int i = 0; i < 4; ++i) red[warp][g + 8 * (i >> 1)][8 * j + 2 * t4 + (i & 1)] = acc[j][i];
     __syncthreads();
-    for (int i = tid; i < 16 * kMt * rows; i += 32 * kDownWarps) {
-      const int r = i % (16 * kMt), c = i / (16 * kMt);
+    for (int i = tid; i < 16 * rows; i += 32 * kDownWarps) {
+      const int r = i & 15, c = i >> 4;
       if (r0 + r >= rank) continue;
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kSplit; ++w) v += red[w][r][c];
+      for (int w = 0; w < kDownWarps; ++w) v += red[w][r][c];
       u[static_cast<size_t>(row0 + list[warp][c]) * rank + r0 + r] = v * sc;
     }
     __syncthreads();
@@ -215,14 +210,10 @@ bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const 
 
 bool launch_adapter_down(bool bf16, const void* x, long long ldx, int t, const void* a, const float* scale,
                          const int32_t* ids, int n_adapters, int rank, int k, float* u, cudaStream_t s) {
-  // Few rows: a CTA for every 16 rank rows, and up to one for each distinct adapter of its 32 rows.  Many: all of the
-  // rank rows in one CTA, which then reads the rows of x once.
-  const int blocks = (t + kDownRows - 1) / kDownRows;
-  const bool many = blocks >= 64;
-  const int mt = (rank + 15) / 16, parts = many ? (mt + 3) / 4 : mt;
+  // a CTA for every 16 rank rows, and up to one for each distinct adapter of its 32 rows
+  const int blocks = (t + kDownRows - 1) / kDownRows, parts = (rank + 15) / 16;
   const int shares = std::max(1, std::min({std::min(t, kDownRows), n_adapters, 512 / (blocks * parts)}));
-  const auto kernel = bf16 ? (many ? k_adapter_down<true, 4> : k_adapter_down<true, 1>)
-                           : (many ? k_adapter_down<false, 4> : k_adapter_down<false, 1>);
+  const auto kernel = bf16 ? k_adapter_down<true> : k_adapter_down<false>;
   return launch_pdl(kernel, dim3(blocks, parts, shares), 32 * kDownWarps, s, static_cast<const uint16_t*>(x), ldx, t,
                     static_cast<const uint16_t*>(a), scale, ids, n_adapters, rank, k, u);
 }

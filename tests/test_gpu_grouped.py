@@ -98,6 +98,21 @@ def test_weight_gradients(i, counts, dtype, out):
     assert (dw[E] == SENTINEL).all()
 
 
+@pytest.mark.parametrize("rows", [3000, 20000])
+def test_as_many_experts_as_allowed(rows):
+    g, E = gen(15), 1024
+    counts = torch.bincount(torch.randint(0, E, (rows,), generator=g, device="cuda") ** 2 // E, minlength=E).tolist()
+    x, dy, w, off = ints(g, F16, rows, 72), ints(g, F16, rows, 40), ints(g, F16, E, 40, 72), offsets_of(counts)
+    y, dw = torch.empty(rows, 40, dtype=F16, device="cuda"), torch.empty(E, 40, 72, dtype=F16, device="cuda")
+    ok(moe.moe_grouped_mm(x, off, w, y))
+    ok(moe.moe_grouped_wgrad(dy, x, off, dw))
+    e_of = torch.repeat_interleave(torch.arange(E, device="cuda"), torch.tensor(counts, device="cuda"))
+    assert torch.equal(y, torch.bmm(w[e_of].double(), x[:, :, None].double())[:, :, 0].to(F16))
+    outer = torch.zeros(E, 40, 72, dtype=torch.float64, device="cuda")
+    outer.index_add_(0, e_of, dy[:, :, None].double() * x[:, None, :].double())
+    assert torch.equal(dw, outer.to(F16))
+
+
 def test_long_weight_gradients():
     """Groups of hundreds of rows: the reduction goes in pieces."""
     g, counts, n, k = gen(4), [1000, 385, 0, 384, 2600], 264, 328
@@ -335,17 +350,35 @@ def test_adapters_of_real_values(t, dtype):
     assert (err <= torch.finfo(dtype).eps / 2 * ref.abs() + 1.01 * ((k / 16 + rank + 8) * 17 * 2 ** -23 + 2 ** -17) * mag).all()
 
 
-@pytest.mark.parametrize("t", [30, 150])
+@pytest.mark.parametrize("t", [30, 150, 700])
 @pytest.mark.parametrize("dtype", [BF16, F16])
 def test_a_broken_adapter_stays_with_its_requests(t, dtype):
-    x, w, ids, a, b, scale = lora_case(9, t, 136, 200, 4, 16, dtype, "any")
-    a[1], b[2] = math.nan, math.inf
+    x, w, ids, a, b, scale = lora_case(9, t, 136, 200, 5, 16, dtype, "any")
+    ws = torch.empty(4 * t * 16, dtype=torch.uint8, device="cuda")
     y = torch.empty(t, 136, dtype=dtype, device="cuda")
-    ok(moe.moe_lora_mm(x, w, ids, a, b, scale, y, torch.empty(4 * t * 16, dtype=torch.uint8, device="cuda")))
-    fine = (ids != 1) & (ids != 2)
-    a[1], b[2] = 0, 0
-    assert torch.equal(y[fine], lora_reference(x, w, ids, a, b, scale)[fine].to(dtype))
-    assert not y[ids == 1].isfinite().any()
+    a[1], b[2], b[3, 17, 5] = math.nan, math.inf, -math.inf   # all of A, all of B, one value of B
+    ok(moe.moe_lora_mm(x, w, ids, a, b, scale, y, ws))
+    a[1], b[2], b[3, 17, 5] = 0, 0, 0
+    want = lora_reference(x, w, ids, a, b, scale).to(dtype)
+    fine = (ids != 1) & (ids != 2) & (ids != 3)
+    assert torch.equal(y[fine], want[fine])
+    assert not y[(ids == 1) | (ids == 2)].isfinite().any()
+    third = ids == 3
+    assert not y[third, 17].isfinite().any()
+    others = torch.arange(136, device="cuda") != 17
+    assert torch.equal(y[third][:, others], want[third][:, others])
+
+
+@pytest.mark.parametrize("t", [40, 900])
+def test_rows_that_are_not_finite_stay_alone(t):
+    x, w, ids, a, b, scale = lora_case(10, t, 264, 200, 3, 24, BF16, "any")
+    x[3], x[t - 1, 7] = math.nan, math.inf
+    y = torch.empty(t, 264, dtype=BF16, device="cuda")
+    ok(moe.moe_lora_mm(x, w, ids, a, b, scale, y, torch.empty(4 * t * 24, dtype=torch.uint8, device="cuda")))
+    fine = torch.ones(t, dtype=torch.bool, device="cuda")
+    fine[3] = fine[t - 1] = False
+    assert torch.equal(y[fine], lora_reference(x, w, ids, a, b, scale).to(BF16)[fine])
+    assert y[3].isnan().all()
 
 
 # ---------------------------------------------------------------- streams, graphs, devices

@@ -312,12 +312,13 @@ def moe_route_noalloc(cfg: MoeConfig, router_w, h, B: int, logit_bias, ids, gate
 # dimension that is not contiguous) return MOE_EINVAL like the library's own checks.  The call runs on the tensors'
 # device, on `stream` or that device's current stream.
 
-_DTYPE = _INT32 = _FLOAT32 = _current_device = _raw_stream = None   # from torch, on the first call
+_DTYPE = _INT32 = _FLOAT32 = _current_device = _raw_stream = _fn = None   # from torch and the library, on the first call
 
 
 def _from_torch() -> None:
-    global _DTYPE, _INT32, _FLOAT32, _current_device, _raw_stream
+    global _DTYPE, _INT32, _FLOAT32, _current_device, _raw_stream, _fn
     import torch
+    _fn = lib()
     _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
     _INT32, _FLOAT32, _current_device = torch.int32, torch.float32, torch.cuda.current_device
     # the stream's handle without the 3 us of a torch.cuda.Stream object: these calls start kernels of 10 us
@@ -325,16 +326,11 @@ def _from_torch() -> None:
                           lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _rows(t, rows: int, cols: int, dev: int) -> bool:
-    """A [rows, cols] matrix on device `dev` whose rows are contiguous."""
-    return t.shape == (rows, cols) and t.stride(1) == 1 and t.get_device() == dev
+# The checks are written out in each function and ask a tensor as little as they can: a call of a few microseconds on the
+# GPU waits for the host (with helper functions for the checks they took 1 us longer).
 
 
-def _ld(t, rows: int, cols: int) -> int:
-    return t.stride(0) if rows > 1 else cols   # the row stride of a single row says nothing
-
-
-def _whole(t, dtype, dev: int, *shape) -> bool:
+def _whole(t, shape, dtype, dev: int) -> bool:
     """A contiguous tensor of this shape and type on device `dev`."""
     return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
 
@@ -357,65 +353,91 @@ def moe_grouped_mm(x, offsets, w, y, transpose: bool = False, stream=None) -> in
     """y[r] = w[e] x[r] (or w[e]^T x[r]) for the rows of each expert; w [E, n, k], offsets int32 [E + 1]."""
     if _DTYPE is None:
         _from_torch()
-    if w.dim() != 3 or x.dim() != 2:
+    sw, sx = w.shape, x.shape
+    if len(sw) != 3 or len(sx) != 2:
         return MOE_EINVAL
-    (E, n, k), m, dev, dt = w.shape, x.shape[0], w.get_device(), w.dtype
+    (E, n, k), m, dev, dt = sw, sx[0], w.get_device(), w.dtype
     into, out = (n, k) if transpose else (k, n)
-    if not (_rows(x, m, into, dev) and _rows(y, m, out, dev) and x.dtype is dt and w.is_contiguous() and
-            _whole(offsets, _INT32, dev, E + 1)):
+    if sx[1] != into or y.shape != (m, out):
         return MOE_EINVAL
-    return _call(lib().moe_grouped_mm, dev, stream, _DTYPE.get(dt, -1), 1 if transpose else 0, x.data_ptr(),
-                 _ld(x, m, into), m, offsets.data_ptr(), E, w.data_ptr(), n, k, y.data_ptr(), _ld(y, m, out),
-                 _DTYPE.get(y.dtype, -1))
+    # a row's values are contiguous; the row stride of a single row says nothing
+    tx, ty = x.stride(), y.stride()
+    if not (tx[1] == 1 and ty[1] == 1 and x.dtype is dt and w.is_contiguous() and x.get_device() == dev and
+            y.get_device() == dev and _whole(offsets, (E + 1,), _INT32, dev)):
+        return MOE_EINVAL
+    return _call(_fn.moe_grouped_mm, dev, stream, _DTYPE.get(dt, -1), 1 if transpose else 0, x.data_ptr(),
+                 tx[0] if m > 1 else into, m, offsets.data_ptr(), E, w.data_ptr(), n, k, y.data_ptr(),
+                 ty[0] if m > 1 else out, _DTYPE.get(y.dtype, -1))
 
 
 def moe_grouped_wgrad(dy, x, offsets, dw, stream=None) -> int:
     """dw[e] = sum over the rows of each expert of dy[r] x[r]^T; dw [E, n, k], all of it written."""
     if _DTYPE is None:
         _from_torch()
-    if dw.dim() != 3 or x.dim() != 2:
+    sw, sx = dw.shape, x.shape
+    if len(sw) != 3 or len(sx) != 2:
         return MOE_EINVAL
-    (E, n, k), m, dev, dt = dw.shape, x.shape[0], dw.get_device(), x.dtype
-    if not (_rows(x, m, k, dev) and _rows(dy, m, n, dev) and dy.dtype is dt and dw.is_contiguous() and
-            _whole(offsets, _INT32, dev, E + 1)):
+    (E, n, k), m, dev, dt = sw, sx[0], dw.get_device(), x.dtype
+    if sx[1] != k or dy.shape != (m, n):
         return MOE_EINVAL
-    return _call(lib().moe_grouped_wgrad, dev, stream, _DTYPE.get(dt, -1), dy.data_ptr(), _ld(dy, m, n), x.data_ptr(),
-                 _ld(x, m, k), m, offsets.data_ptr(), E, n, k, dw.data_ptr(), _DTYPE.get(dw.dtype, -1))
+    tx, ty = x.stride(), dy.stride()
+    if not (tx[1] == 1 and ty[1] == 1 and dy.dtype is dt and dw.is_contiguous() and x.get_device() == dev and
+            dy.get_device() == dev and _whole(offsets, (E + 1,), _INT32, dev)):
+        return MOE_EINVAL
+    return _call(_fn.moe_grouped_wgrad, dev, stream, _DTYPE.get(dt, -1), dy.data_ptr(), ty[0] if m > 1 else n,
+                 x.data_ptr(), tx[0] if m > 1 else k, m, offsets.data_ptr(), E, n, k, dw.data_ptr(),
+                 _DTYPE.get(dw.dtype, -1))
 
 
 def moe_grouped_geglu(x, offsets, w, a, h=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
     """a[r] = GELU(g) u, [g, u] = w[e] x[r]; w [E, 2 f, k]; h [m, 2 f] (optional) receives [g, u]."""
     if _DTYPE is None:
         _from_torch()
-    if w.dim() != 3 or x.dim() != 2 or w.shape[1] % 2:
+    sw, sx = w.shape, x.shape
+    if len(sw) != 3 or len(sx) != 2 or sw[1] % 2:
         return MOE_EINVAL
-    (E, n, k), m, dev, dt = w.shape, x.shape[0], w.get_device(), w.dtype
+    (E, n, k), m, dev, dt = sw, sx[0], w.get_device(), w.dtype
     f = n // 2
-    if not (_rows(x, m, k, dev) and _rows(a, m, f, dev) and x.dtype is dt and a.dtype is dt and w.is_contiguous() and
-            _whole(offsets, _INT32, dev, E + 1)):
+    if sx[1] != k or a.shape != (m, f):
         return MOE_EINVAL
-    if h is not None and not (_rows(h, m, n, dev) and h.dtype is dt):
+    tx, ta = x.stride(), a.stride()
+    if not (tx[1] == 1 and ta[1] == 1 and x.dtype is dt and a.dtype is dt and w.is_contiguous() and
+            x.get_device() == dev and a.get_device() == dev and _whole(offsets, (E + 1,), _INT32, dev)):
         return MOE_EINVAL
-    return _call(lib().moe_grouped_geglu, dev, stream, _DTYPE.get(dt, -1), gelu_variant, x.data_ptr(), _ld(x, m, k), m,
-                 offsets.data_ptr(), E, w.data_ptr(), f, k, a.data_ptr(), _ld(a, m, f),
-                 None if h is None else h.data_ptr(), 0 if h is None else _ld(h, m, n))
+    ph = ldh = None
+    if h is not None:
+        if not (h.shape == (m, n) and h.stride(1) == 1 and h.dtype is dt and h.get_device() == dev):
+            return MOE_EINVAL
+        ph, ldh = h.data_ptr(), h.stride(0) if m > 1 else n
+    return _call(_fn.moe_grouped_geglu, dev, stream, _DTYPE.get(dt, -1), gelu_variant, x.data_ptr(),
+                 tx[0] if m > 1 else k, m, offsets.data_ptr(), E, w.data_ptr(), f, k, a.data_ptr(),
+                 ta[0] if m > 1 else f, ph, ldh or 0)
 
 
 def moe_geglu_grad(h, da, dh, n_rows=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
     """dh = [da u GELU'(g), da GELU(g)] for h = [g, u]; n_rows: int32 tensor of one value, the rows to do."""
     if _DTYPE is None:
         _from_torch()
-    if da.dim() != 2:
+    sa = da.shape
+    if len(sa) != 2:
         return MOE_EINVAL
-    (m, f), dev, dt = da.shape, da.get_device(), da.dtype
-    if not (_rows(h, m, 2 * f, dev) and _rows(da, m, f, dev) and _rows(dh, m, 2 * f, dev) and h.dtype is dt and
-            dh.dtype is dt):
+    (m, f), dev, dt = sa, da.get_device(), da.dtype
+    n = 2 * f
+    if h.shape != (m, n) or dh.shape != (m, n):
         return MOE_EINVAL
-    if n_rows is not None and not (n_rows.numel() == 1 and n_rows.dtype is _INT32 and n_rows.get_device() == dev):
+    th, ta, td = h.stride(), da.stride(), dh.stride()
+    if not (th[1] == 1 and ta[1] == 1 and td[1] == 1 and h.dtype is dt and dh.dtype is dt and h.get_device() == dev and
+            dh.get_device() == dev):
         return MOE_EINVAL
-    return _call(lib().moe_geglu_grad, dev, stream, _DTYPE.get(dt, -1), gelu_variant, h.data_ptr(), _ld(h, m, 2 * f),
-                 da.data_ptr(), _ld(da, m, f), m, f, None if n_rows is None else n_rows.data_ptr(), dh.data_ptr(),
-                 _ld(dh, m, 2 * f))
+    rows = None
+    if n_rows is not None:
+        if n_rows.numel() != 1 or n_rows.dtype is not _INT32 or n_rows.get_device() != dev:
+            return MOE_EINVAL
+        rows = n_rows.data_ptr()
+    if m <= 1:
+        th, ta, td = (n,), (f,), (n,)
+    return _call(_fn.moe_geglu_grad, dev, stream, _DTYPE.get(dt, -1), gelu_variant, h.data_ptr(), th[0], da.data_ptr(),
+                 ta[0], m, f, rows, dh.data_ptr(), td[0])
 
 
 def moe_lora_mm(x, w, ids, a, b, scale, y, workspace, stream=None) -> int:
@@ -423,16 +445,21 @@ def moe_lora_mm(x, w, ids, a, b, scale, y, workspace, stream=None) -> int:
     [N], ids int32 [t] (-1: no adapter), workspace: a tensor of at least 4 * t * rank bytes."""
     if _DTYPE is None:
         _from_torch()
-    if w.dim() != 2 or x.dim() != 2 or a.dim() != 3:
+    sw, sx, sa = w.shape, x.shape, a.shape
+    if len(sw) != 2 or len(sx) != 2 or len(sa) != 3:
         return MOE_EINVAL
-    (n, k), (N, rank, _), t, dev, dt = w.shape, a.shape, x.shape[0], w.get_device(), w.dtype
-    if not (_rows(x, t, k, dev) and _rows(y, t, n, dev) and x.dtype is dt and y.dtype is dt and w.is_contiguous() and
-            _whole(a, dt, dev, N, rank, k) and _whole(b, dt, dev, N, n, rank) and _whole(scale, _FLOAT32, dev, N) and
-            _whole(ids, _INT32, dev, t) and workspace.is_contiguous() and workspace.get_device() == dev):
+    (n, k), (N, rank, _), t, dev, dt = sw, sa, sx[0], w.get_device(), w.dtype
+    if sx[1] != k or y.shape != (t, n):
         return MOE_EINVAL
-    return _call(lib().moe_lora_mm, dev, stream, _DTYPE.get(dt, -1), x.data_ptr(), _ld(x, t, k), t, w.data_ptr(), n, k,
-                 ids.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), N, rank, y.data_ptr(), _ld(y, t, n),
-                 workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    tx, ty = x.stride(), y.stride()
+    if not (tx[1] == 1 and ty[1] == 1 and x.dtype is dt and y.dtype is dt and w.is_contiguous() and
+            x.get_device() == dev and y.get_device() == dev and _whole(a, (N, rank, k), dt, dev) and
+            _whole(b, (N, n, rank), dt, dev) and _whole(scale, (N,), _FLOAT32, dev) and
+            _whole(ids, (t,), _INT32, dev) and workspace.is_contiguous() and workspace.get_device() == dev):
+        return MOE_EINVAL
+    return _call(_fn.moe_lora_mm, dev, stream, _DTYPE.get(dt, -1), x.data_ptr(), tx[0] if t > 1 else k, t, w.data_ptr(),
+                 n, k, ids.data_ptr(), a.data_ptr(), b.data_ptr(), scale.data_ptr(), N, rank, y.data_ptr(),
+                 ty[0] if t > 1 else n, workspace.data_ptr(), workspace.nbytes)
 
 
 def moe_grouped_sync(stream=None) -> int:

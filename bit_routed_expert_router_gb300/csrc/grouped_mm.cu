@@ -73,8 +73,9 @@ struct AdaptSmem {
   int id[kLists][256];     // adapter of each column of a tile, -1 for none (tiles in turn)
   int list[kLists][256];   // its distinct adapters, in order
   int n_list[kLists];
-  // a value of the tile's B rows is not finite.  Sixteen tiles in turn: the listing warps follow the loading one, which
-  // is at most kStages steps, so as many tiles, ahead of the products, those two tiles ahead of the stores, and the lists one ahead of the loads
+  // A value of the tile's B rows is not finite.  Sixteen tiles in turn: a tile is listed (and its mark cleared) at most
+  // kLists tiles ahead of the loads, those run at most kStages steps, so as many tiles, ahead of the products, and those
+  // two tiles ahead of the stores.
   volatile int broken[16];
   uint64_t u_full[8], list_full[kLists], list_empty[kLists];
 };
@@ -414,6 +415,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;
   __syncthreads();
   if (kMode != GM_WGRAD && warp == 0) {
+    // offsets that go down would count rows twice: a group starts no earlier than the one before it ends
+    for (int e0 = 0, before = 0; e0 <= p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int v = e <= p.E ? S.off[e] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+        if (lane >= d) v = max(v, o);
+      }
+      v = max(v, before);
+      if (e <= p.E) S.off[e] = v;
+      before = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    __syncwarp();
     // Parts of at most 256 rows; of 128 or 64 where the tiles then still are one round of the pairs, which few tiles of
     // 256 would leave idle (256 rows and 2816 features: 11 tiles for 76 pairs).
     int n128 = 0, n64 = 0, width = 256;

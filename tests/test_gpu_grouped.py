@@ -179,11 +179,13 @@ def test_a_group_keeps_its_nan():
         assert torch.equal(dw[e], (dy[s].double().T @ x[s].double()).float())
 
 
-def test_offsets_out_of_range_stay_inside_the_tensors():
+@pytest.mark.parametrize("m", [40, 300])
+def test_offsets_out_of_range_stay_inside_the_tensors(m):
     """Undefined outputs, but nothing outside the given rows is touched (the kernels clamp every offset)."""
-    g, n, k, m = gen(7), 72, 136, 40
+    g, n, k = gen(7), 72, 136
     x, dy, w = ints(g, BF16, m, k), ints(g, BF16, m, n), ints(g, BF16, 3, n, k)
-    for bad in ([-5, 10, 900, 2000], [30, 10, 35, 0], [50, 60, 70, 80]):
+    for bad in ([-5, 10, 900, 2000], [30, 10, 35, 0], [m + 10, m + 20, m + 30, m + 40], [0, m, 0, m], [m, 0, m, 0],
+                [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1]):
         off = torch.tensor(bad, dtype=torch.int32, device="cuda")
         whole = torch.full((m + 600, n), SENTINEL, dtype=BF16, device="cuda")
         ok(moe.moe_grouped_mm(x, off, w, whole[300:300 + m]))

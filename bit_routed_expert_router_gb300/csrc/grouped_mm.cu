@@ -219,8 +219,8 @@ __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
 // y = W x + B_i u is a longer reduction: behind the k64 steps of W and x come
 // steps whose features' operand is B_i and whose columns' operand is u, zero in
 // the rows of other adapters; one pair of steps (u as a value of the operands'
-// type and its remainder, 16 bits of bf16 or 22 of fp16) for each distinct
-// adapter of the tile's rows and 64 ranks.  Four warps of each CTA list the
+// type and its remainder, 16 bits of bf16 or 22 of fp16; B_i is loaded once) for
+// each distinct adapter of the tile's rows and 64 ranks.  Four warps of each CTA list the
 // tile's adapters, write u's steps and look through the B rows that TMA loaded
 // for them: a value that is not finite would reach every column (0 times
 // infinity), so it is cleared and the tile marked, and the storing warps put
@@ -390,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&S.full[i], kMode == GM_WGRAD ? 2 : 1);
       mbar_init(&S.empty[i], 1);
-      mbar_init(&S.tail[i], 1);
+      mbar_init(&S.tail[i], kEpi == GM_ADAPT ? 2 : 1);
       if constexpr (kEpi == GM_ADAPT) mbar_init(&S.ad.u_full[i], 2 * kUWarps);
     }
     for (int i = 0; i < 2; ++i) {
@@ -468,7 +468,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     if (elect_one()) {
       const uint32_t lead_full = map_rank(smem_u32(S.full), 0);
       uint32_t it = 0, n_tile = 0;
-      uint32_t extra = 0, fulls = 0, tails = 0;   // by stage: last loaded for an adapter's step; phases issued
+      // by stage: last loaded for an adapter's pair, last given to its second step (no load); phases issued
+      uint32_t extra = 0, unused = 0, fulls = 0, tails = 0;
       int e = 0;
       Tile T;
       for (int t = first; !S.abort && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
@@ -482,18 +483,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         }
         for (int ks = 0; ks < T.steps || pair < pairs; ++ks) {
           if constexpr (kEpi == GM_ADAPT) {
-            for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair)
-#pragma unroll
-              for (int h = 0; h < 2; ++h, ++it) {
-                const int s = it % kStages;
-                if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
-                const int block = pair / S.ad.n_list[lb];
-                mbar_arrive_expect_tx(&S.tail[s], kHalf);
-                load_3d<true>(smem_u32(S.stage[s]), &maps.c, 64 * block, T.f0 + 128 * rank,
-                              S.ad.list[lb][pair - block * S.ad.n_list[lb]], smem_u32(&S.tail[s]));
-                extra |= 1u << s;
-                tails ^= 1u << s;
-              }
+            for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair, it += 2) {
+              // one load of B for both stages; the writing warps go on when it has landed and both are free
+              const int s = it % kStages, s2 = (it + 1) % kStages, block = pair / S.ad.n_list[lb];
+              if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
+              mbar_arrive_expect_tx(&S.tail[s], kHalf);
+              load_3d<true>(smem_u32(S.stage[s]), &maps.c, 64 * block, T.f0 + 128 * rank,
+                            S.ad.list[lb][pair - block * S.ad.n_list[lb]], smem_u32(&S.tail[s]));
+              extra |= 1u << s;
+              unused &= ~(1u << s);
+              tails ^= 1u << s;
+              const bool go = wait_bar(&S.empty[s2], (((it + 1) / kStages) & 1) ^ 1, &S.abort);
+              mbarrier_arrive(&S.tail[s]);
+              unused |= 1u << s2;
+              if (!go) break;
+            }
             if (S.abort) break;
             if (ks >= T.steps) continue;
           }
@@ -531,6 +535,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             load_2d<true>(b, &maps.b[half / 16 - 1], 64 * ks, T.c0 + rank * half, bar);
           }
           extra &= ~(1u << s);
+          unused &= ~(1u << s);
           fulls ^= 1u << s;
           ++it;
         }
@@ -539,6 +544,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       if (S.abort)   // copies already issued land before the pair leaves
         for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
           const int s = i % kStages;
+          if ((unused >> s) & 1u) continue;
           if ((extra >> s) & 1u)
             mbar_wait_bounded(&S.tail[s], ((tails >> s) & 1) ^ 1, err_word());
           else if (rank == 0)
@@ -559,14 +565,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         uint32_t d = tmem + buf * kAccCols;
         const uint32_t idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb);
         const int red = kMode == GM_WGRAD ? T.rows : p.red;
-        const auto multiply = [&](int s, int k, bool first_step) {   // k of the stage's 64
-          fence_after();
-          const uint32_t a = smem_u32(S.stage[s]);
-          const uint64_t da = tile_desc<kTa>(a), db = tile_desc<kTb>(a + kHalf);
+        const auto multiply = [&](int sa, int sb, int k, bool first_step) {   // stages of the operands, k of their 64
+          const uint64_t da = tile_desc<kTa>(smem_u32(S.stage[sa])), db = tile_desc<kTb>(smem_u32(S.stage[sb]) + kHalf);
           const int nk = (min(64, k) + 15) / 16;
           for (int kk = 0; kk < nk; ++kk)
             mma<true>(d, da + kk * kStep16<kTa>, db + kk * kStep16<kTb>, idesc, !first_step || kk != 0);
-          commit_pair(&S.empty[s], 3);
         };
         int pairs = 0, pair = 0;
         [[maybe_unused]] const int lb = count % kLists;
@@ -576,14 +579,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         }
         for (int ks = 0; ok && (ks < T.steps || pair < pairs); ++ks) {
           if constexpr (kEpi == GM_ADAPT) {
-            for (; ok && pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair)
-#pragma unroll
-              for (int h = 0; h < 2; ++h, ++it) {
-                const int s = it % kStages;
-                if (!(ok = wait_bar(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
-                us ^= 1u << s;
-                multiply(s, p.rank - 64 * (pair / S.ad.n_list[lb]), false);
-              }
+            for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair, it += 2) {
+              const int s = it % kStages, s2 = (it + 1) % kStages, k = p.rank - 64 * (pair / S.ad.n_list[lb]);
+              if (!(ok = wait_bar(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
+              us ^= 1u << s;
+              fence_after();
+              multiply(s, s, k, false);
+              multiply(s, s2, k, false);
+              commit_pair(&S.empty[s], 3);
+              commit_pair(&S.empty[s2], 3);
+            }
             if (!ok) break;
             if (ks >= T.steps) continue;
           }
@@ -598,7 +603,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           const int s = it % kStages;
           if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort))) break;
           fulls ^= 1u << s;
-          multiply(s, red - 64 * ks, ks == 0 || (kEpi == GM_F32 && ks % kSegSteps == 0));
+          fence_after();
+          multiply(s, s, red - 64 * ks, ks == 0 || (kEpi == GM_F32 && ks % kSegSteps == 0));
+          commit_pair(&S.empty[s], 3);
           ++it;
         }
         if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
@@ -794,40 +801,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           it += at - at0;
           at0 = at;
           const bool use = mine == S.ad.list[lb][j];
-          bool scan = true;
+          const int s = it % kStages, s2 = (it + 1) % kStages;
+          it += 2;
+          // B has landed and both stages are free (their own barriers' phases would be ambiguous here: these warps do
+          // not see the steps in between)
+          alive = alive && wait_bar_warp(&S.tail[s], (tails >> s) & 1, &S.abort);
+          tails ^= 1u << s;
+          if (i0 < half) {
+            uint8_t *row = S.stage[s] + kHalf + 128 * i0, *row2 = S.stage[s2] + kHalf + 128 * i0;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int h = 0; h < 2; ++h, ++it) {
-            const int s = it % kStages;
-            // the B rows have landed, so the stage was free (its own barrier's phase would be ambiguous here: these
-            // warps do not see the steps in between)
-            alive = alive && wait_bar_warp(&S.tail[s], (tails >> s) & 1, &S.abort);
-            tails ^= 1u << s;
-            if (i0 < half) {
-              uint8_t* row = S.stage[s] + kHalf + 128 * i0;
-#pragma unroll
-              for (int w = 0; w < 8; ++w) {
-                const uint4 v = h ? lo[w] : hi[w];
-                *reinterpret_cast<uint4*>(row + 16 * (w ^ (i0 & 7))) = use ? v : make_uint4(0, 0, 0, 0);
-              }
+            for (int w = 0; w < 8; ++w) {
+              *reinterpret_cast<uint4*>(row + 16 * (w ^ (i0 & 7))) = use ? hi[w] : zero;
+              *reinterpret_cast<uint4*>(row2 + 16 * (w ^ (i0 & 7))) = use ? lo[w] : zero;
             }
-            if (scan) {   // the second step's rows are the first's
-              uint4* words = reinterpret_cast<uint4*>(S.stage[s]) + i0;
-              uint32_t any = 0;
-#pragma unroll
-              for (int w = 0; w < 8; ++w) {
-                const uint4 v = words[128 * w];
-                const uint32_t bad =
-                    not_finite(v.x, p.bf16) | not_finite(v.y, p.bf16) | not_finite(v.z, p.bf16) | not_finite(v.w, p.bf16);
-                if (bad) words[128 * w] = make_uint4(0, 0, 0, 0);
-                any |= bad;
-              }
-              if (any) S.ad.broken[n_tile & 15] = 1;
-              scan = any != 0;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(lead_u + 8 * s);
           }
+          uint4* words = reinterpret_cast<uint4*>(S.stage[s]) + i0;
+          uint32_t any = 0;
+#pragma unroll
+          for (int w = 0; w < 8; ++w) {
+            const uint4 v = words[128 * w];
+            const uint32_t bad =
+                not_finite(v.x, p.bf16) | not_finite(v.y, p.bf16) | not_finite(v.z, p.bf16) | not_finite(v.w, p.bf16);
+            if (bad) words[128 * w] = make_uint4(0, 0, 0, 0);
+            any |= bad;
+          }
+          if (any) S.ad.broken[n_tile & 15] = 1;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(lead_u + 8 * s);
         }
       }
       it += T.steps - at0;

@@ -1167,7 +1167,8 @@ __global__ void __launch_bounds__(192)
   __shared__ int s_n, s_list[64], s_nth[64];   // distinct adapters; which of them a row has, or -1
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = static_cast<int>(cluster_rank()), row0 = blockIdx.y * kDownCols, rows = min(kDownCols, p.m - row0);
+  const int rank = static_cast<int>(cluster_rank()), row0 = blockIdx.x / split * kDownCols,
+            rows = min(kDownCols, p.m - row0);
   if (warp == 1) {
     tmem_alloc<false>(&s_tmem, kDownCols);
   } else if (tid == 64) {
@@ -1217,7 +1218,7 @@ __global__ void __launch_bounds__(192)
 #pragma unroll
   for (int r = 0; r < kMaxSplit; ++r) from[r] = map_rank(smem_u32(part) + 16 * lane, min(r, split - 1));
   uint32_t it = 0, pass = 0;
-  for (int a0 = each * blockIdx.z; a0 < n; a0 += each * gridDim.z, ++pass) {
+  for (int a0 = each * blockIdx.y; a0 < n; a0 += each * gridDim.y, ++pass) {
     const int na = min(each, n - a0);
     const uint32_t bytes = na * slot * 128 + kDownCols * 128;
     if (warp == 0) {
@@ -1420,7 +1421,7 @@ bool launch_adapter_down_many(const GmOperands& o, const GmParams& p, const floa
   const size_t smem = kDownStages * kDownStage + 1024;
   if (!allow_smem(k_adapter_down_many, smem)) return false;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(split, blocks, shares);
+  cfg.gridDim = dim3(split * blocks, shares);   // x: more than 65535 blocks of rows are possible
   cfg.blockDim = dim3(192);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

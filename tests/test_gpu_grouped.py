@@ -476,3 +476,44 @@ def test_no_rows():
     ok(moe.moe_grouped_mm(x, off, w, y))
     ok(moe.moe_grouped_wgrad(dy, x, off, dw))
     assert (dw == 0).all() and (y == SENTINEL).all()
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_as_many_rows_as_allowed(transpose):
+    m = 2 ** 24
+    g = gen(20)
+    counts = [5, 2 ** 23 - 3, 2 ** 23 - 4]   # two rows behind them
+    x, w = ints(g, BF16, m, 8), ints(g, BF16, 3, 8, 8)
+    y = torch.full((m, 8), SENTINEL, dtype=F32, device="cuda")
+    ok(moe.moe_grouped_mm(x, offsets_of(counts), w, y, transpose=transpose))
+    assert torch.equal(y, products(x, counts, w.transpose(1, 2) if transpose else w).float())
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_weight_gradients_of_as_many_rows_as_allowed(out):
+    m = 2 ** 24
+    g = gen(21)
+    x, dy = ints(g, BF16, m, 8, top=1), ints(g, BF16, m, 16, top=1)   # every partial sum is below 2^24
+    dw = torch.full((2, 16, 8), SENTINEL, dtype=out, device="cuda")
+    ok(moe.moe_grouped_wgrad(dy, x, offsets_of([2 ** 23 - 5, 2 ** 23]), dw))
+    want = [dy[lo:hi].double().T @ x[lo:hi].double() for lo, hi in ((0, 2 ** 23 - 5), (2 ** 23 - 5, m - 5))]
+    assert torch.equal(dw, torch.stack(want).to(out))
+
+
+def test_adapters_of_many_rows():
+    """More blocks of rows than a launch has in any dimension but its first."""
+    t = 64 * 65535 + 7
+    x, w, ids, a, b, scale = lora_case(22, t, 8, 8, 3, 8, BF16, "any")
+    y = torch.full((t, 8), SENTINEL, dtype=BF16, device="cuda")
+    ok(moe.moe_lora_mm(x, w, ids, a, b, scale, y, torch.empty(4 * t * 8, dtype=torch.uint8, device="cuda")))
+    assert torch.equal(y, lora_reference(x, w, ids, a, b, scale).to(BF16))
+
+
+@pytest.mark.parametrize("m", [1, 2])
+def test_a_row_of_a_wider_tensor(m):
+    """The distance of a lone row to the next means nothing: it need not be a multiple of 8."""
+    g = gen(23)
+    x, w = ints(g, BF16, m, 75 if m == 1 else 80)[:, :72], ints(g, BF16, 1, 40, 72)
+    y = torch.full((m, 45 if m == 1 else 48), SENTINEL, dtype=BF16, device="cuda")
+    ok(moe.moe_grouped_mm(x, offsets_of([m]), w, y[:, :40]))
+    assert torch.equal(y[:, :40], products(x, [m], w).to(BF16)) and (y[:, 40:] == SENTINEL).all()

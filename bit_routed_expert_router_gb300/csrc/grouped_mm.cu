@@ -495,8 +495,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
               tails ^= 1u << s;
               const bool go = wait_bar(&S.empty[s2], (((it + 1) / kStages) & 1) ^ 1, &S.abort);
               mbarrier_arrive(&S.tail[s]);
+              if (!go) break;   // s2's earlier load may still be in flight
               unused |= 1u << s2;
-              if (!go) break;
             }
             if (S.abort) break;
             if (ks >= T.steps) continue;

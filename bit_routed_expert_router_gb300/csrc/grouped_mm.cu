@@ -10,7 +10,8 @@
 // kernel) instead of to a tile of 128 or 256: an expert's rows are cut into
 // equal parts of at most 256 and each part's N is set per instruction.
 //
-// k_grouped: persistent, pairs of CTAs (one CTA per SM).  A pair computes 256
+// k_grouped: persistent, pairs of CTAs (one CTA per SM), each with tiles in turn or taken as
+// it gets done (Walk).  A pair computes 256
 // features x up to 256 rows with cta_group::2 MMAs; each CTA stages its 128
 // features and half of the rows, so a staged byte feeds twice the products
 // that it would in a lone CTA.  Two accumulators of 256 columns: the epilogue
@@ -53,9 +54,9 @@ constexpr int kAccCols = 256;
 // fp32 outputs of long reductions: k64 steps that are summed in one accumulator.  The MMA adds its products to the
 // accumulator with truncation, whose bias grows with the number of steps (relative error of a sum of 2816 products 2.6e-6,
 // of 704 9e-7); pieces of 384 are added with rounding by the warps that read them (3.5e-7).  A 16-bit output's own
-// rounding is far above either.  The sums' registers cost the weight gradient 5% (408 -> 428 us), so the persistent
-// kernel has them past kLongRed (weight gradients: on average past half of it, as the largest groups have a few times the
-// average).
+// rounding is far above either.  The sums' registers cost the weight gradient 13% (128 experts of 1408 x 2816 at 512 rows each
+// 480 -> 544 us), so the persistent kernel has them past kLongRed (weight gradients: on average past half of it, as the
+// largest groups have a few times the average).
 constexpr int kSegSteps = 6, kLongRed = 512;
 
 // The weight gradient's tiles have few stages each and store far more than they
@@ -81,6 +82,16 @@ struct AdaptSmem {
 };
 struct NoSmem {};
 
+// fp32 weight gradients: the answers to a pair's requests for the next tile, in turn.
+// kAhead at a time: the tile at hand and as many more are the pair's (one: 381 us, two 375, five 377).
+constexpr int kAnswers = 8, kAhead = 2;
+template <int kMode, int kEpi>
+constexpr bool kTakes = kMode == GM_WGRAD && kEpi != GM_PLAIN;   // (see Walk)
+struct TakeSmem {
+  alignas(16) uint8_t answer[kAnswers][16];
+  uint64_t full[kAnswers], empty[kAnswers];
+};
+
 template <int kMode, int kEpi>
 struct BigSmem {
   static constexpr int kStages = BigCfg<kMode, kEpi>::kStages;
@@ -90,6 +101,7 @@ struct BigSmem {
   uint64_t acc_full[2], acc_empty[2], drain;
   uint32_t tmem;
   volatile int abort;
+  std::conditional_t<kTakes<kMode, kEpi>, TakeSmem, NoSmem> take;
   std::conditional_t<kEpi == GM_ADAPT, AdaptSmem, NoSmem> ad;
   int off[(kEpi == GM_ADAPT ? 1 : kMaxE) + 1];    // clamped to [0, m]
   int tiles[(kEpi == GM_ADAPT ? 1 : kMaxE) + 1];  // column tiles before each expert
@@ -186,6 +198,50 @@ __device__ __forceinline__ bool tile_at(const Smem& S, const GmParams& p, int t,
     T.n = max((T.cols + 31) & ~31, 32);   // an MMA has columns whatever the parts are
     T.row0 = T.rows = 0;
     T.steps = (p.red + 63) / 64;
+    return true;
+  }
+}
+
+// The tiles of a pair: its share in turn, or (fp32 weight gradients) the launch
+// has a cluster for each tile and a pair that is done takes over the next one
+// that has not started.  Ordinary stores are not equally fast on every SM, and
+// experts differ in rows: 128 experts of 1408 x 2816 at 4 rows each 339 us in
+// turn against 283, at 64 387 / 321, at 256 421 / 361, at 512 528 / 544.  TMA
+// stores of 16 bits gain nothing (4 rows 164 / 181, 256 rows 243 / 245: the
+// answer is read in the storing warps' chain), nor do the rows' products
+// (32,768 rows: down 125 / 128, input gradient 221 / 224).  Taking several
+// tiles at once writes pages that lie apart (two: 358 -> 367).
+struct Walk {
+  int t;        // tile
+  uint32_t n;   // answers read
+};
+
+// The next tile.  kWarp: called by a whole warp.  `ask` runs before an answer
+// is waited for; a reader gives the answer's place back at `lead_empty` (0: it
+// is the asking thread itself).
+template <bool kTake, bool kWarp, typename Smem, typename Ask>
+__device__ __forceinline__ bool next_tile(Smem& S, Walk& w, uint32_t lead_empty, Ask ask) {
+  if constexpr (kTake) {
+    ask();
+    if (w.t < 0) {
+      w.t = blockIdx.x >> 1;
+      return true;
+    }
+    const int s = w.n % kAnswers;
+    const uint32_t parity = (w.n / kAnswers) & 1;
+    if (!(kWarp ? wait_bar_warp(&S.take.full[s], parity, &S.abort) : wait_bar(&S.take.full[s], parity, &S.abort)))
+      return false;
+    ++w.n;
+    const int block = taken_block(smem_u32(S.take.answer[s]));
+    if (lead_empty) {
+      fence_proxy_async_smem();
+      if (kWarp) __syncwarp();
+      if (!kWarp || (threadIdx.x & 31) == 0) arrive_cluster(lead_empty + 8 * s);
+    }
+    w.t = block >> 1;
+    return block >= 0;
+  } else {
+    w.t += gridDim.x >> 1;
     return true;
   }
 }
@@ -377,13 +433,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     k_grouped(const __grid_constant__ GmMaps maps, GmParams p) {
   constexpr bool kTa = kMode != GM_FWD, kTb = kMode == GM_WGRAD;
   constexpr int kFeat = kEpi == GM_GATED ? 128 : 256;   // features of a pair's tile
+  constexpr bool kTake = kTakes<kMode, kEpi>;
   extern __shared__ uint8_t smem_raw[];
   using Smem = BigSmem<kMode, kEpi>;
   constexpr int kStages = Smem::kStages;
   Smem& S = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
-  const int first = blockIdx.x >> 1, stride = gridDim.x >> 1;
 
   if (tid == 0) {
     prefetch_map(&maps.a);
@@ -402,8 +458,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         mbar_init(&S.ad.list_full[i], 1);
         mbar_init(&S.ad.list_empty[i], kUWarps + (rank == 0 ? 2 : 1));   // and the loading and the issuing warp
       }
+    if constexpr (kTake)
+      for (int i = 0; i < kAnswers; ++i) {
+        mbar_init(&S.take.full[i], 1);
+        mbar_init(&S.take.empty[i], 2 * (BigCfg<kMode, kEpi>::kThreads / 32 - 1));   // all but one loading, one idle warp
+      }
     mbar_init(&S.drain, 1);
-    S.abort = 0;
+    // a pair that gave up leaves its launch's other tiles to clusters that start after it: those do nothing
+    S.abort = kTake && *static_cast<volatile uint32_t*>(err_word()) != 0;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
@@ -439,10 +501,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     }
     n128 = __reduce_add_sync(0xFFFFFFFFu, n128);
     n64 = __reduce_add_sync(0xFFFFFFFFu, n64);
-    const int ft = (p.feat + kFeat - 1) / kFeat;
-    if (n64 * ft <= stride)
+    const int ft = (p.feat + kFeat - 1) / kFeat, pairs = gridDim.x >> 1;
+    if (n64 * ft <= pairs)
       width = 64;
-    else if (n128 * ft <= stride)
+    else if (n128 * ft <= pairs)
       width = 128;
     int base = 0;
     if (lane == 0) S.tiles[0] = 0;
@@ -463,6 +525,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
   cluster_sync();   // both CTAs' barriers are initialised
   fence_after();
   const uint32_t tmem = S.tmem;
+  uint32_t lead_take = 0;
+  if constexpr (kTake) lead_take = map_rank(smem_u32(S.take.empty), 0);
+  const auto no_ask = [] {};
+  Walk walk{kTake ? -1 : static_cast<int>(blockIdx.x >> 1) - static_cast<int>(gridDim.x >> 1), 0};
 
   if (warp == 0) {
     if (elect_one()) {
@@ -472,7 +538,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       uint32_t extra = 0, unused = 0, fulls = 0, tails = 0;
       int e = 0;
       Tile T;
-      for (int t = first; !S.abort && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+      uint32_t asked = 0;
+      const auto ask = [&] {
+        if constexpr (kTake) {
+          for (; rank == 0 && asked < walk.n + kAhead; ++asked) {
+            const int s = asked % kAnswers;
+            if (!wait_bar(&S.take.empty[s], ((asked / kAnswers) & 1) ^ 1, &S.abort)) return;
+            mbar_arrive_expect_tx(&S.take.full[s], 16);
+            arrive_expect_cluster(map_rank(smem_u32(&S.take.full[s]), 1), 16);
+            try_take_cluster(smem_u32(S.take.answer[s]), smem_u32(&S.take.full[s]));
+          }
+        }
+      };
+      while (!S.abort && next_tile<kTake, false>(S, walk, rank == 0 ? 0 : lead_take, ask) &&
+             tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
         const int half = T.n / 2;
         const uint32_t bytes = kHalf + half * 128;
         int pairs = 0, pair = 0;
@@ -541,6 +620,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         }
         if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
       }
+      if (kTake && !S.abort) asked = walk.n + kAhead - 1;   // as many when a refusal is read
+      if constexpr (kTake)   // answers come before the pair leaves
+        for (uint32_t i = walk.n; i < asked; ++i)
+          mbar_wait_bounded(&S.take.full[i % kAnswers], (i / kAnswers) & 1, err_word());
       if (S.abort)   // copies already issued land before the pair leaves
         for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
           const int s = i % kStages;
@@ -557,7 +640,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       int e = 0;
       bool ok = true;
       Tile T;
-      for (int t = first; ok && tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+      while (ok && next_tile<kTake, false>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
         if (T.steps == 0) continue;
         int buf = count & 1;
         ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort);
@@ -621,11 +704,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     const int q = warp & 3;   // the tensor-memory lanes this warp may read
     const uint32_t buf16 = smem_u32(S.epi[warp - 2]);
     const uint32_t lead_empty = map_rank(smem_u32(S.acc_empty), 0);
-    const bool lead = kMode == GM_WGRAD && elect_one();
+    const bool lead = kMode == GM_WGRAD && kEpi == GM_PLAIN && elect_one();
     uint32_t count = 0, n_stores = 0;
     int e = 0;
     Tile T;
-    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+    while (next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
       // first feature of this warp's 32 lanes (GM_GATED: 16 gate and 16 up lanes of 16 features)
       const int f0 = T.f0 + (kEpi == GM_GATED ? 64 * rank + 16 * q : 128 * rank + 32 * q);
       const int feats = p.feat - f0;   // none or less: the output ends before this warp's features do
@@ -682,7 +765,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       };
       if (c_first >= T.cols) release(c_first);
       for (int c0 = c_first; c0 < T.cols; c0 += 64) {
-        if (kEpi == GM_PLAIN && p.out_f32) {
+        if (kEpi == GM_F32_SHORT || (kEpi == GM_PLAIN && kMode != GM_WGRAD && p.out_f32)) {
           float w[32];
           if (T.steps) {
             ld_cols32(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), w);
@@ -706,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           if (S.ad.broken[count & 15] && feats > 0) mark_broken(v, p, T.c0 + c0, cols, f0, lane);
         release(c0);
         if (feats <= 0) continue;
-        if (kMode == GM_WGRAD) {
+        if (kMode == GM_WGRAD && kEpi == GM_PLAIN) {
           tma_store_32x32(buf16, v, p, &maps.c, f0, T.c0 + c0, T.e, lane, lead, n_stores);
         } else if (kEpi == GM_GATED) {
           __syncwarp();
@@ -737,7 +820,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       uint32_t n_tile = 0;
       int e = 0;
       Tile T;
-      for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
+      for (; next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T); ++n_tile) {
         const int lb = n_tile % kLists;
         if (!wait_bar_warp(&S.ad.list_empty[lb], ((n_tile / kLists) & 1) ^ 1, &S.abort)) break;
         int id[8];
@@ -777,7 +860,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     int e = 0;
     Tile T;
     pdl_wait();   // the u rows
-    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride, ++n_tile) {
+    for (; next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T); ++n_tile) {
       const int lb = n_tile % kLists;
       if (!wait_bar_warp(&S.ad.list_full[lb], (n_tile / kLists) & 1, &S.abort)) break;
       const int n = S.ad.n_list[lb], blocks = (p.rank + 63) / 64, pairs = n * blocks;
@@ -843,7 +926,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     uint32_t it = 0, phases = 0;
     int e = 0;
     Tile T;
-    for (int t = first; tile_at<kMode, kFeat>(S, p, t, e, T); t += stride) {
+    while (next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
       it += T.steps;
       if (!(T.rows & 15)) continue;
       const int s = (it - 1) % kStages, lo = ((T.rows - 1) & 63) + 1, hi = (lo + 15) & ~15;
@@ -1382,8 +1465,8 @@ bool launch_big(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s) 
   const long long ft = (p.feat + kFeat - 1) / kFeat;
   const long long ct = kMode == GM_WGRAD ? static_cast<long long>(p.E) * ((p.cols + 255) / 256)
                                          : std::min(p.E, p.m) + static_cast<long long>(p.m) / 64;   // most parts, of 64
-  const int pairs = static_cast<int>(std::min<long long>(sms / 2, ft * ct));
-  return launch(k_grouped<kMode, kEpi>, dim3(2 * pairs), BigCfg<kMode, kEpi>::kThreads,
+  const long long pairs = kTakes<kMode, kEpi> ? ft * ct : std::min<long long>(sms / 2, ft * ct);
+  return launch(k_grouped<kMode, kEpi>, dim3(static_cast<unsigned>(2 * pairs)), BigCfg<kMode, kEpi>::kThreads,
                 sizeof(BigSmem<kMode, kEpi>) + 1024, 2, s, maps, p, 0);
 }
 
@@ -1462,8 +1545,9 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
     const cuuint64_t stride[2] = {row, row * o.n};
     if (!p.out_f32 && !encode_store(&maps.c, p.y, dim, stride, p.bf16)) return false;
-    return p.out_f32 && p.m / p.E > kLongRed / 2 ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s)
-                                             : launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
+    return !p.out_f32                 ? launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s)
+           : p.m / p.E > kLongRed / 2 ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s)
+                                      : launch_big<GM_WGRAD, GM_F32_SHORT>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);
   // a tile has at most all of the rows, and at most kSmallCols or 256 (half of them a CTA)

@@ -63,6 +63,33 @@ __device__ __forceinline__ void arrive_expect_cluster(uint32_t bar, uint32_t byt
                : "memory");
 }
 
+// ------------------------------------------------------------------ taking over clusters that have not started
+
+// Asks for a cluster of this launch that has not started; the answer (16
+// bytes) comes to `answer` and `bar`, at these offsets in every CTA of the
+// cluster.  Not to be asked again after a refusal.
+__device__ __forceinline__ void try_take_cluster(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], "
+      "[%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+
+// blockIdx.x of the taken cluster's first CTA, -1 if none was left.
+__device__ __forceinline__ int taken_block(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\tld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=&r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
+
 // ------------------------------------------------------------------ TMA loads
 
 __device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {

@@ -517,3 +517,44 @@ def test_a_row_of_a_wider_tensor(m):
     y = torch.full((m, 45 if m == 1 else 48), SENTINEL, dtype=BF16, device="cuda")
     ok(moe.moe_grouped_mm(x, offsets_of([m]), w, y[:, :40]))
     assert torch.equal(y[:, :40], products(x, [m], w).to(BF16)) and (y[:, 40:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_many_weight_gradients_on_two_streams_at_once(captured):
+    """More tiles than run at once, in launches that share the device: every tile is done, and done once."""
+    g, n, k, E = gen(24), 520, 264, 60
+    counts = [(7 * e) % 90 for e in range(E)]
+    off, m = offsets_of(counts), sum(counts)
+    x, dy = ints(g, BF16, m, k), ints(g, BF16, m, n)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [[torch.full((E, n, k), SENTINEL, dtype=out, device="cuda") for out in (F32, BF16, F32)] for _ in streams]
+    graphs = []
+    torch.cuda.synchronize()
+
+    def calls(i):
+        for dw in outs[i]:
+            moe.check(moe.moe_grouped_wgrad(dy, x, off, dw))
+
+    for i, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            calls(i)
+        if captured:
+            s.synchronize()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[i]):
+                calls(i)
+    torch.cuda.synchronize()
+    for repeat in range(4):
+        x.copy_(ints(g, BF16, m, k))
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                graphs[i].replay() if captured else calls(i)
+        for s in streams:
+            moe.check(moe.moe_grouped_sync(s))
+        lo, want = 0, []
+        for c in counts:
+            want.append(dy[lo:lo + c].double().T @ x[lo:lo + c].double())
+            lo += c
+        for dw in outs[0] + outs[1]:
+            assert torch.equal(dw, torch.stack(want).to(dw.dtype))

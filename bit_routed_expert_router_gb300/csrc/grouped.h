@@ -9,9 +9,7 @@
 namespace moe {
 
 enum GmMode { GM_FWD = 0, GM_DGRAD = 1, GM_WGRAD = 2 };
-// GM_F32: GM_PLAIN with fp32 outputs of long reductions; GM_F32_SHORT: of short
-// ones, in weight gradients
-enum GmEpi { GM_PLAIN = 0, GM_GATED = 1, GM_ADAPT = 2, GM_F32 = 3, GM_F32_SHORT = 4 };
+enum GmEpi { GM_PLAIN = 0, GM_GATED = 1, GM_ADAPT = 2, GM_F32 = 3 };   // GM_F32: GM_PLAIN with fp32 outputs
 
 // One grouped product.  "Features" are the output's contiguous dimension,
 // "columns" its rows: the grouped rows themselves (GM_FWD, GM_DGRAD), or the n

@@ -10,16 +10,17 @@
 // kernel) instead of to a tile of 128 or 256: an expert's rows are cut into
 // equal parts of at most 256 and each part's N is set per instruction.
 //
-// k_grouped: persistent, pairs of CTAs (one CTA per SM), each with tiles in turn or taken as
-// it gets done (Walk).  A pair computes 256
-// features x up to 256 rows with cta_group::2 MMAs; each CTA stages its 128
-// features and half of the rows, so a staged byte feeds twice the products
-// that it would in a lone CTA.  Two accumulators of 256 columns: the epilogue
-// of one tile overlaps the next tile's products.  Roles: warp 0 loads, warp 1
-// of the even CTA issues, warps 2-9 store, warp 10 (weights only) clears the
-// rows behind a group's end in the last stage.  The loading and issuing
-// threads are elected (elect.sync): with lane == 0 in its place an MMA took
-// 170 cycles whatever its N, against 135 for N = 256 and 87 for N = 160.
+// k_grouped: persistent, pairs of CTAs (one CTA per SM), each with tiles in
+// turn or taken as it gets done (Walk).  A pair computes 256 features x up to
+// 256 rows with cta_group::2 MMAs; each CTA stages its 128 features and half of
+// the rows, so a staged byte feeds twice the products that it would in a lone
+// CTA.  Two accumulators of 256 columns: the epilogue of one tile overlaps the
+// next tile's products.  Roles: warp 0 loads, warp 1 of the even CTA issues,
+// warps 2-9 store; in weight gradients warp 10 clears the rows behind a group's
+// end in the last stage, with adapters warps 10-13 write u and warp 14 lists
+// the adapters.  The loading and issuing threads are elected (elect.sync): with
+// lane == 0 in its place an MMA took 170 cycles whatever its N, against 135 for
+// N = 256 and 87 for N = 160.
 //
 // k_grouped_small: few rows per expert (decode).  The weights are read once
 // and nothing else matters, so a CTA takes 128 features x up to 64 rows, the
@@ -51,13 +52,11 @@ constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memor
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kUWarps = 4;           // adapters: warps that stage u
 constexpr int kAccCols = 256;
-// fp32 outputs of long reductions: k64 steps that are summed in one accumulator.  The MMA adds its products to the
-// accumulator with truncation, whose bias grows with the number of steps (relative error of a sum of 2816 products 2.6e-6,
-// of 704 9e-7); pieces of 384 are added with rounding by the warps that read them (3.5e-7).  A 16-bit output's own
-// rounding is far above either.  The sums' registers cost the weight gradient 13% (128 experts of 1408 x 2816 at 512 rows each
-// 480 -> 544 us), so the persistent kernel has them past kLongRed (weight gradients: on average past half of it, as the
-// largest groups have a few times the average).
-constexpr int kSegSteps = 6, kLongRed = 512;
+// fp32 outputs: k64 steps that are summed in one accumulator.  The MMA adds its products to the accumulator with
+// truncation, whose bias grows with the number of steps (relative error of a sum of 2816 products 2.6e-6, of 704 9e-7);
+// pieces of 384 are added with rounding by the warps that read them (3.5e-7).  A 16-bit output's own rounding is far above
+// either.
+constexpr int kSegSteps = 6;
 
 // The weight gradient's tiles have few stages each and store far more than they
 // load: two buffers a warp for TMA stores, and a stage less.
@@ -75,8 +74,8 @@ struct AdaptSmem {
   int list[kLists][256];   // its distinct adapters, in order
   int n_list[kLists];
   // A value of the tile's B rows is not finite.  Sixteen tiles in turn: a tile is listed (and its mark cleared) at most
-  // kLists tiles ahead of the loads, those run at most kStages steps, so as many tiles, ahead of the products, and those
-  // two tiles ahead of the stores.
+  // kLists tiles ahead of the loads, which run at most kStages steps, so as many tiles, ahead of the products, and these
+  // two ahead of the stores.
   volatile int broken[16];
   uint64_t u_full[8], list_full[kLists], list_empty[kLists];
 };
@@ -86,7 +85,7 @@ struct NoSmem {};
 // kAhead at a time: the tile at hand and as many more are the pair's (one: 381 us, two 375, five 377).
 constexpr int kAnswers = 8, kAhead = 2;
 template <int kMode, int kEpi>
-constexpr bool kTakes = kMode == GM_WGRAD && kEpi != GM_PLAIN;   // (see Walk)
+constexpr bool kTakes = kMode == GM_WGRAD && kEpi == GM_F32;   // (see Walk)
 struct TakeSmem {
   alignas(16) uint8_t answer[kAnswers][16];
   uint64_t full[kAnswers], empty[kAnswers];
@@ -206,7 +205,7 @@ __device__ __forceinline__ bool tile_at(const Smem& S, const GmParams& p, int t,
 // has a cluster for each tile and a pair that is done takes over the next one
 // that has not started.  Ordinary stores are not equally fast on every SM, and
 // experts differ in rows: 128 experts of 1408 x 2816 at 4 rows each 339 us in
-// turn against 283, at 64 387 / 321, at 256 421 / 361, at 512 528 / 544.  TMA
+// turn against 283, at 64 387 / 321, at 256 421 / 361.  TMA
 // stores of 16 bits gain nothing (4 rows 164 / 181, 256 rows 243 / 245: the
 // answer is read in the storing warps' chain), nor do the rows' products
 // (32,768 rows: down 125 / 128, input gradient 221 / 224).  Taking several
@@ -272,17 +271,18 @@ __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
 
 // ---- the adapters' term in the persistent kernel
 //
-// y = W x + B_i u is a longer reduction: behind the k64 steps of W and x come
+// y = W x + B_i u is a longer reduction: among the k64 steps of W and x come
 // steps whose features' operand is B_i and whose columns' operand is u, zero in
 // the rows of other adapters; one pair of steps (u as a value of the operands'
-// type and its remainder, 16 bits of bf16 or 22 of fp16; B_i is loaded once) for
-// each distinct adapter of the tile's rows and 64 ranks.  Four warps of each CTA list the
-// tile's adapters, write u's steps and look through the B rows that TMA loaded
-// for them: a value that is not finite would reach every column (0 times
-// infinity), so it is cleared and the tile marked, and the storing warps put
-// NaN where it belongs.  (As mma.sync products in the epilogue the term took
-// the kernel from 45 to 115 us at 4096 rows and rank 64, since they wait for the
-// tcgen05 products; on the ordinary pipes 145, bound by broadcast loads.)
+// type and its remainder, 16 bits of bf16 or 22 of fp16; B_i is loaded once, one
+// handshake for both) for each distinct adapter of the tile's rows and 64 ranks.
+// One warp of each CTA lists the tiles' adapters; four write u's steps and look
+// through the B rows that TMA loaded for them: a value that is not finite would
+// reach every column (0 times infinity), so it is cleared and the tile marked,
+// and the storing warps put NaN where it belongs.  (As mma.sync products in the
+// epilogue the term took the kernel from 45 to 115 us at 4096 rows and rank 64,
+// since they wait for the tcgen05 products; on the ordinary pipes 145, bound by
+// broadcast loads.)
 
 // The pairs are spread over the tile's reduction, so that the warps that write
 // them have the steps between for it: pair i of n comes before base step
@@ -717,31 +717,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           (kMode == GM_WGRAD ? (static_cast<long long>(T.e) * p.cols + T.c0) : static_cast<long long>(T.c0)) * p.ldy + f0;
       if constexpr (kEpi == GM_F32) {
         // a lane holds one feature of up to 128 columns, summed over the pieces; each store of the warp is 128 contiguous
-        // bytes of a column
+        // bytes of a column.  Read 16 columns at a time: with 32 the sums spilled, and a spilled value's way back queues
+        // behind the stores (weight gradient, 512 rows an expert, 544 us against 492; sixteen storing warps 508)
         float sum[4][32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
+        for (int c = 0; c < 32; ++c) sum[0][c] = sum[1][c] = sum[2][c] = sum[3][c] = 0.f;
         bool ok = true;
         for (int ks = 0; ok && ks < T.steps; ks += kSegSteps, ++count) {
           const int buf = count & 1;
           if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort))) break;
           fence_after();
           const uint32_t at = tmem + buf * kAccCols + c_first + (static_cast<uint32_t>(32 * q) << 16);
-          if (ks == 0) {
-            if (c_first < T.cols) ld_cols32x2(at, at + 64, sum[0], sum[1]);
-            if (c_first + 128 < T.cols) ld_cols32x2(at + 128, at + 192, sum[2], sum[3]);
-          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (c_first + 64 * i < T.cols) {
-                float w[32];
-                ld_cols32(at + 64 * i, w);
+          for (int i = 0; i < 4; ++i)
+            if (c_first + 64 * i < T.cols) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) sum[i][c] += w[c];
+              for (int c0 = 0; c0 < 32; c0 += 16) {
+                float w[16];
+                ld_cols16(at + 64 * i + c0, w);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) sum[i][c0 + c] += w[c];
               }
-          }
+            }
           fence_before();
           __syncwarp();
           if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
@@ -765,18 +762,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       };
       if (c_first >= T.cols) release(c_first);
       for (int c0 = c_first; c0 < T.cols; c0 += 64) {
-        if (kEpi == GM_F32_SHORT || (kEpi == GM_PLAIN && kMode != GM_WGRAD && p.out_f32)) {
-          float w[32];
-          if (T.steps) {
-            ld_cols32(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), w);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = 0.f;
-          }
-          release(c0);
-          store_f32(w, static_cast<float*>(p.y) + out0 + c0 * p.ldy, p.ldy, T.cols - c0, feats, lane);
-          continue;
-        }
         float v[2][16];
         if (T.steps) {
           ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
@@ -1545,9 +1530,7 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
     const cuuint64_t dim[3] = {static_cast<cuuint64_t>(o.k), static_cast<cuuint64_t>(o.n), static_cast<cuuint64_t>(p.E)};
     const cuuint64_t stride[2] = {row, row * o.n};
     if (!p.out_f32 && !encode_store(&maps.c, p.y, dim, stride, p.bf16)) return false;
-    return !p.out_f32                 ? launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s)
-           : p.m / p.E > kLongRed / 2 ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s)
-                                      : launch_big<GM_WGRAD, GM_F32_SHORT>(maps, p, d.sms, s);
+    return p.out_f32 ? launch_big<GM_WGRAD, GM_F32>(maps, p, d.sms, s) : launch_big<GM_WGRAD, GM_PLAIN>(maps, p, d.sms, s);
   }
   const bool small = few_rows(p);
   // a tile has at most all of the rows, and at most kSmallCols or 256 (half of them a CTA)
@@ -1558,18 +1541,17 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
                       : !map_weights(&maps.a, o.w, p.E, o.n, o.k, mode == GM_FWD ? 128 : 64, p.bf16))
     return false;
   if (epi == GM_ADAPT && !small && !map_weights(&maps.c, p.b, p.n_adapters, p.feat, p.rank, 128, p.bf16)) return false;
-  const bool long_f32 = p.out_f32 && p.red > kLongRed;
   if (mode == GM_DGRAD)
-    return small      ? launch_small<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s)
-           : long_f32 ? launch_big<GM_DGRAD, GM_F32>(maps, p, d.sms, s)
-                      : launch_big<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s);
+    return small       ? launch_small<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s)
+           : p.out_f32 ? launch_big<GM_DGRAD, GM_F32>(maps, p, d.sms, s)
+                       : launch_big<GM_DGRAD, GM_PLAIN>(maps, p, d.sms, s);
   if (epi == GM_GATED)
     return small ? launch_small<GM_FWD, GM_GATED>(maps, p, d.sms, s) : launch_big<GM_FWD, GM_GATED>(maps, p, d.sms, s);
   if (epi == GM_ADAPT)
     return small ? launch_small<GM_FWD, GM_ADAPT>(maps, p, d.sms, s) : launch_big<GM_FWD, GM_ADAPT>(maps, p, d.sms, s);
-  return small      ? launch_small<GM_FWD, GM_PLAIN>(maps, p, d.sms, s)
-         : long_f32 ? launch_big<GM_FWD, GM_F32>(maps, p, d.sms, s)
-                    : launch_big<GM_FWD, GM_PLAIN>(maps, p, d.sms, s);
+  return small       ? launch_small<GM_FWD, GM_PLAIN>(maps, p, d.sms, s)
+         : p.out_f32 ? launch_big<GM_FWD, GM_F32>(maps, p, d.sms, s)
+                     : launch_big<GM_FWD, GM_PLAIN>(maps, p, d.sms, s);
 }
 
 bool grouped_error(cudaStream_t s, uint32_t* err) {

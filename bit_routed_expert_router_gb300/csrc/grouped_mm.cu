@@ -1461,11 +1461,13 @@ bool launch_small(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s
   const int ft = (p.feat + kFeat - 1) / kFeat, tiles = std::min(p.E, p.m) + p.m / kSmallCols;
   const int steps = (p.red + 63) / 64;
   // CTAs that share a tile's reduction: up to three on every SM (two with adapters, whose many columns make the sum over
-  // the cluster dearer: 48 rows 17.7 us against 18.8), at least two k64 steps each
+  // the cluster dearer: 48 rows 17.7 us against 18.8), at least two k64 steps each, and eleven once every SM has one
+  // (eight experts of 704 -> 2816, 176 tiles of 11 steps: 7.9 us whole against 8.8 halved; 32 of 512 -> 704 5.9 / 6.3; of
+  // 22 steps 12.4 / 12.2).
   constexpr int kPerSm = kEpi == GM_ADAPT ? 2 : 3;
+  const long long ctas = ft * static_cast<long long>(tiles);
   int split = 1;
-  while (split < kMaxSplit && 2 * split * ft * static_cast<long long>(tiles) <= kPerSm * sms && 4 * split <= steps)
-    split *= 2;
+  while (split < kMaxSplit && 2 * split * ctas <= kPerSm * sms && (split * ctas < sms ? 4 : 22) * split <= steps) split *= 2;
   return launch(k_grouped_small<kMode, kEpi>, dim3(ft * split, tiles), 192, kSmallRing + 1024, split, s, maps, p, split);
 }
 

@@ -52,11 +52,12 @@ constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memor
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kUWarps = 4;           // adapters: warps that stage u
 constexpr int kAccCols = 256;
-// fp32 outputs: k64 steps that are summed in one accumulator.  The MMA adds its products to the accumulator with
-// truncation, whose bias grows with the number of steps (relative error of a sum of 2816 products 2.6e-6, of 704 9e-7);
-// pieces of 384 are added with rounding by the warps that read them (3.5e-7).  A 16-bit output's own rounding is far above
-// either.
-constexpr int kSegSteps = 6;
+// k64 steps that are summed in one accumulator.  The MMA adds its products to the accumulator with truncation, so a sum of
+// products of one sign falls short by about 6e-9 of itself a product (measured: 4e-4 at 65,536 products, 10 % at 2^24);
+// longer reductions go in pieces, which the warps that read them add with rounding.  fp32 outputs in pieces of 384 products
+// (2816 products of either sign: relative error 2.6e-6 in one accumulator, 3.5e-7 in pieces); 16-bit outputs in pieces of
+// 4096, short by at most 2.5e-5 where their own rounding is half a step of 4.9e-4 (fp16) or 3.9e-3 (bf16).
+constexpr int kSegSteps = 6, kLongSteps = 64;
 
 // The weight gradient's tiles have few stages each and store far more than they
 // load: two buffers a warp for TMA stores, and a stage less.
@@ -636,7 +637,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
-      uint32_t it = 0, count = 0, fulls = 0, us = 0;   // fulls, us: phases seen, by stage
+      constexpr int kPiece = kEpi == GM_F32 ? kSegSteps : kLongSteps;
+      uint32_t it = 0, count = 0, fulls = 0, us = 0;   // count: accumulators; fulls, us: phases seen, by stage
+      [[maybe_unused]] uint32_t n_tile = 0;
       int e = 0;
       bool ok = true;
       Tile T;
@@ -655,9 +658,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             mma<true>(d, da + kk * kStep16<kTa>, db + kk * kStep16<kTb>, idesc, !first_step || kk != 0);
         };
         int pairs = 0, pair = 0;
-        [[maybe_unused]] const int lb = count % kLists;
+        [[maybe_unused]] const int lb = n_tile % kLists;
         if constexpr (kEpi == GM_ADAPT) {
-          ok = ok && wait_bar(&S.ad.list_full[lb], (count / kLists) & 1, &S.abort);
+          ok = ok && wait_bar(&S.ad.list_full[lb], (n_tile++ / kLists) & 1, &S.abort);
           pairs = ok ? S.ad.n_list[lb] * ((p.rank + 63) / 64) : 0;
         }
         for (int ks = 0; ok && (ks < T.steps || pair < pairs); ++ks) {
@@ -675,7 +678,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             if (!ok) break;
             if (ks >= T.steps) continue;
           }
-          if (kEpi == GM_F32 && ks > 0 && ks % kSegSteps == 0) {   // the next piece in the other accumulator
+          if (ks > 0 && ks % kPiece == 0) {   // the next piece in the other accumulator
             commit_pair(&S.acc_full[buf], 3);
             ++count;
             buf = count & 1;
@@ -687,7 +690,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort))) break;
           fulls ^= 1u << s;
           fence_after();
-          multiply(s, s, red - 64 * ks, ks == 0 || (kEpi == GM_F32 && ks % kSegSteps == 0));
+          multiply(s, s, red - 64 * ks, ks % kPiece == 0);
           commit_pair(&S.empty[s], 3);
           ++it;
         }
@@ -706,9 +709,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     const uint32_t lead_empty = map_rank(smem_u32(S.acc_empty), 0);
     const bool lead = kMode == GM_WGRAD && kEpi == GM_PLAIN && elect_one();
     uint32_t count = 0, n_stores = 0;
+    [[maybe_unused]] uint32_t n_tile = 0;
     int e = 0;
     Tile T;
-    while (next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
+    for (; next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T); ++n_tile) {
       // first feature of this warp's 32 lanes (GM_GATED: 16 gate and 16 up lanes of 16 features)
       const int f0 = T.f0 + (kEpi == GM_GATED ? 64 * rank + 16 * q : 128 * rank + 32 * q);
       const int feats = p.feat - f0;   // none or less: the output ends before this warp's features do
@@ -750,30 +754,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
                     feats, lane);
         continue;
       }
-      const int buf = count & 1;
-      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
-      fence_after();
-      // the accumulator goes back as soon as this warp has read its last columns, before they are stored
-      const auto release = [&](int c0) {
-        if (!T.steps || c0 + 64 < T.cols) return;
-        fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
-      };
-      if (c_first >= T.cols) release(c_first);
-      for (int c0 = c_first; c0 < T.cols; c0 += 64) {
-        float v[2][16];
-        if (T.steps) {
-          ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
-        }
+      // 32 columns of this warp's features, rounded and stored
+      const auto store = [&](float (&v)[2][16], int c0) {
         const int cols = T.cols - c0;
-        if constexpr (kEpi == GM_ADAPT)
-          if (S.ad.broken[count & 15] && feats > 0) mark_broken(v, p, T.c0 + c0, cols, f0, lane);
-        release(c0);
-        if (feats <= 0) continue;
         if (kMode == GM_WGRAD && kEpi == GM_PLAIN) {
           tma_store_32x32(buf16, v, p, &maps.c, f0, T.c0 + c0, T.e, lane, lead, n_stores);
         } else if (kEpi == GM_GATED) {
@@ -795,6 +778,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         } else {
           store_32x32(buf16, v, p.bf16, static_cast<uint16_t*>(p.y) + out0 + c0 * p.ldy, p.ldy, cols, feats, lane);
         }
+      };
+      if (T.steps > kLongSteps) {
+        // summed over the pieces in local memory (a piece's products take ten times as long), in loops of its own: the other
+        // tiles keep their registers (one loop for both: weight gradient of short samples 81 -> 90 us)
+        float sums[4][2][16];
+        bool ok = true;
+        for (int ks = 0; ok && ks < T.steps; ks += kLongSteps, ++count) {
+          const int buf = count & 1;
+          if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort))) break;
+          fence_after();
+#pragma unroll 1
+          for (int c0 = c_first; c0 < T.cols; c0 += 64) {
+            float v[2][16], (&sum)[2][16] = sums[c0 >> 6];
+            ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              sum[0][i] = ks ? sum[0][i] + v[0][i] : v[0][i];
+              sum[1][i] = ks ? sum[1][i] + v[1][i] : v[1][i];
+            }
+          }
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int c0 = c_first; c0 < T.cols && feats > 0; c0 += 64) {
+          float v[2][16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[0][i] = sums[c0 >> 6][0][i], v[1][i] = sums[c0 >> 6][1][i];
+          if constexpr (kEpi == GM_ADAPT)
+            if (S.ad.broken[n_tile & 15]) mark_broken(v, p, T.c0 + c0, T.cols - c0, f0, lane);
+          store(v, c0);
+        }
+        continue;
+      }
+      const int buf = count & 1;
+      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
+      fence_after();
+      // the accumulator goes back as soon as this warp has read its last columns, before they are stored
+      const auto release = [&](int c0) {
+        if (!T.steps || c0 + 64 < T.cols) return;
+        fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_cluster(lead_empty + 8 * buf);
+      };
+      if (c_first >= T.cols) release(c_first);
+      for (int c0 = c_first; c0 < T.cols; c0 += 64) {
+        float v[2][16];
+        if (T.steps) {
+          ld_frags(tmem + buf * kAccCols + c0 + (static_cast<uint32_t>(32 * q) << 16), v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
+        }
+        if constexpr (kEpi == GM_ADAPT)
+          if (S.ad.broken[n_tile & 15] && feats > 0) mark_broken(v, p, T.c0 + c0, T.cols - c0, f0, lane);
+        release(c0);
+        if (feats > 0) store(v, c0);
       }
       if (T.steps) ++count;
     }
@@ -1055,8 +1097,7 @@ __global__ void __launch_bounds__(192)
   const int n = (rows + 15) & ~15;
   const int bytes = kHalf + n * 128, stages = min(8, kSmallRing / bytes);
   const int all = (p.red + 63) / 64, k0 = all * rank / split, steps = all * (rank + 1) / split - k0;
-  // pieces of the reduction: fp32 outputs in kSegSteps, in two accumulators in turn
-  const int seg = p.out_f32 ? kSegSteps : steps;
+  const int seg = p.out_f32 ? kSegSteps : kLongSteps;   // pieces of the reduction, in two accumulators in turn
 
   if (warp == 0) {
     if (elect_one()) {
@@ -1229,7 +1270,7 @@ static_assert(kDownCols * kSmallPitch * 4 <= kDownStages * kDownStage, "the redu
 __global__ void __launch_bounds__(192)
     k_adapter_down_many(const __grid_constant__ GmMaps maps, GmParams p, const float* scale, float* u, int slot, int split) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[kDownStages], empty[kDownStages], acc_full;
+  __shared__ uint64_t full[kDownStages], empty[kDownStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_abort;
   __shared__ int s_n, s_list[64], s_nth[64];   // distinct adapters; which of them a row has, or -1
@@ -1238,7 +1279,7 @@ __global__ void __launch_bounds__(192)
   const int rank = static_cast<int>(cluster_rank()), row0 = blockIdx.x / split * kDownCols,
             rows = min(kDownCols, p.m - row0);
   if (warp == 1) {
-    tmem_alloc<false>(&s_tmem, kDownCols);
+    tmem_alloc<false>(&s_tmem, 2 * kDownCols);
   } else if (tid == 64) {
     prefetch_map(&maps.a);
     prefetch_map(&maps.b[0]);
@@ -1247,7 +1288,10 @@ __global__ void __launch_bounds__(192)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(&acc_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 4);
+    }
     fence_mbar_init();
   }
   pdl_wait();
@@ -1285,8 +1329,8 @@ __global__ void __launch_bounds__(192)
   uint32_t from[kMaxSplit];
 #pragma unroll
   for (int r = 0; r < kMaxSplit; ++r) from[r] = map_rank(smem_u32(part) + 16 * lane, min(r, split - 1));
-  uint32_t it = 0, pass = 0;
-  for (int a0 = each * blockIdx.y; a0 < n; a0 += each * gridDim.y, ++pass) {
+  uint32_t it = 0, piece = 0;   // pieces of the reductions, in two accumulators in turn
+  for (int a0 = each * blockIdx.y; a0 < n; a0 += each * gridDim.y) {
     const int na = min(each, n - a0);
     const uint32_t bytes = na * slot * 128 + kDownCols * 128;
     if (warp == 0) {
@@ -1308,35 +1352,53 @@ __global__ void __launch_bounds__(192)
       if (elect_one()) {
         const uint32_t idesc = instr_desc(p.bf16, 128, kDownCols, false, false);
         for (int ks = 0; ks < steps; ++ks) {
-          const uint32_t i = it + ks, s = i % kDownStages;
+          const uint32_t i = it + ks, s = i % kDownStages, at = piece + ks / kLongSteps, buf = at & 1;
+          if (ks % kLongSteps == 0 && !wait_bar(&acc_empty[buf], ((at >> 1) & 1) ^ 1, &s_abort)) break;
           if (!wait_bar(&full[s], (i / kDownStages) & 1, &s_abort)) break;
           fence_after();
           const uint32_t a = smem_u32(ring) + s * kDownStage;
           const uint64_t da = tile_desc<false>(a), db = tile_desc<false>(a + kHalf);
           const int nk = (min(64, p.red - 64 * (k0 + ks)) + 15) / 16;
           for (int kk = 0; kk < nk; ++kk)
-            mma<false>(tmem, da + kk * kStep16<false>, db + kk * kStep16<false>, idesc, (ks | kk) != 0);
+            mma<false>(tmem + buf * kDownCols, da + kk * kStep16<false>, db + kk * kStep16<false>, idesc,
+                       (ks % kLongSteps | kk) != 0);
           commit(&empty[s]);
+          if ((ks + 1) % kLongSteps == 0 || ks + 1 == steps) commit(&acc_full[buf]);
         }
-        commit(&acc_full);
       }
     }
     __syncwarp();
     it += steps;
     bool ok = true;
     if (warp >= 2) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&acc_full, pass & 1, err_word()) && !s_abort);
-      fence_after();
       const int q = warp & 3;
-      if (ok)
-        for (int c = 0; c < kDownCols; c += 16) {
-          float v[16];
-          ld_cols16(tmem + c + (static_cast<uint32_t>(32 * q) << 16), v);
+      float acc[kDownCols / 16][16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) part[(c + i) * kSmallPitch + 32 * q + lane] = v[i];
+      for (int j = 0; j < kDownCols / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
+      for (int ks = 0, at = piece; ok && ks < steps; ks += kLongSteps, ++at) {
+        const int buf = at & 1;
+        if (!(ok = wait_bar_warp(&acc_full[buf], (at >> 1) & 1, &s_abort))) break;
+        fence_after();
+#pragma unroll
+        for (int j = 0; j < kDownCols / 16; ++j) {
+          float v[16];
+          ld_cols16(tmem + buf * kDownCols + 16 * j + (static_cast<uint32_t>(32 * q) << 16), v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[j][i] += v[i];
         }
-      fence_before();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbarrier_arrive(&acc_empty[buf]);
+      }
+      if (ok)
+#pragma unroll
+        for (int j = 0; j < kDownCols / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) part[(16 * j + i) * kSmallPitch + 32 * q + lane] = acc[j][i];
     }
+    piece += (steps + kLongSteps - 1) / kLongSteps;
     cluster_sync();
     fence_after();
     if (warp >= 2 && ok)
@@ -1356,7 +1418,7 @@ __global__ void __launch_bounds__(192)
     cluster_sync();             // the others may still read this CTA's part
   }
   __syncthreads();
-  if (warp == 1) tmem_free<false>(tmem, kDownCols);
+  if (warp == 1) tmem_free<false>(tmem, 2 * kDownCols);
 }
 
 // ------------------------------------------------------------------ launches

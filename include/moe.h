@@ -449,7 +449,9 @@ moe_status moe_route_noalloc(const moe_config *cfg, const uint16_t *router_w, co
  *                not non-decreasing or reach past m give undefined outputs, but
  *                every access stays inside the given tensors.
  * Products are accumulated in fp32 and rounded once, to the output's type; a
- * result past the type's range is infinite.  No output may overlap an input.
+ * result past the type's range is infinite.  The tensor cores' additions
+ * truncate: of the sum of the products' magnitudes up to 2.5e-5 can be missing
+ * before a 16-bit output's rounding, 2.5e-6 from a 32-bit output.  No output may overlap an input.
  * Results do not depend on timing: no atomics are used.
  * MOE_EINVAL for an argument outside these rules (checked before anything is
  * enqueued), MOE_ECUDA for a failed CUDA call (there is no context to poison). */

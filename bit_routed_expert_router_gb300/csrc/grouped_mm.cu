@@ -274,9 +274,14 @@ __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
 //
 // y = W x + B_i u is a longer reduction: among the k64 steps of W and x come
 // steps whose features' operand is B_i and whose columns' operand is u, zero in
-// the rows of other adapters; one pair of steps (u as a value of the operands'
-// type and its remainder, 16 bits of bf16 or 22 of fp16; B_i is loaded once, one
-// handshake for both) for each distinct adapter of the tile's rows and 64 ranks.
+// the rows of other adapters; one pair of steps (B_i is loaded once, one handshake
+// for both) for each distinct adapter of the tile's rows and 64 ranks.  These
+// products are of bf16 values whatever the call's type, so that u keeps fp32's
+// range (as fp16 it lost bits below 2^-9 and everything past 65504): u is a value
+// and its remainder, good to 2^-17, and so is fp16's B, whose eleven bits they
+// hold; the product of the two remainders, 2^-15 at most, is left out.  The split
+// and the third product take fp16 calls from 89 to 107 us (4096 rows in runs of 41,
+// rank 64; bf16 89) and from 57 to 58 (one adapter).
 // One warp of each CTA lists the tiles' adapters; four write u's steps and look
 // through the B rows that TMA loaded for them: a value that is not finite would
 // reach every column (0 times infinity), so it is cleared and the tile marked,
@@ -323,21 +328,45 @@ __device__ __forceinline__ void mark_broken(float (&v)[2][16], const GmParams& p
     }
 }
 
-// Eight values of u as the operands' type (kLo: what that leaves).
-template <bool kLo>
-__device__ __forceinline__ uint4 u_words(const float4& a, const float4& b, int bf16) {
+// The upper halves of two fp32 values: them as bf16, cut off.
+__device__ __forceinline__ uint32_t upper_halves(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+
+// Eight values of u as bf16, and what that leaves.  `odd` turns NaN if a remainder is (that of an infinity).
+__device__ __forceinline__ void split_u(const float4& a, const float4& b, uint4& hi, uint4& lo, float& odd) {
   const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  uint32_t w[4];
+  uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[i] = pack16(v[2 * i], v[2 * i + 1], bf16);
-    if (kLo) {
-      const float h0 = bf16 ? __uint_as_float(w[i] << 16) : half_lo(w[i]);
-      const float h1 = bf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : half_hi(w[i]);
-      w[i] = pack16(isfinite(h0) ? v[2 * i] - h0 : 0.f, isfinite(h1) ? v[2 * i + 1] - h1 : 0.f, bf16);
-    }
+    h[i] = pack16(v[2 * i], v[2 * i + 1], 1);
+    const float l0 = v[2 * i] - __uint_as_float(h[i] << 16), l1 = v[2 * i + 1] - __uint_as_float(h[i] & 0xFFFF0000u);
+    l[i] = pack16(l0, l1, 1);
+    odd = fmaf(l0, 0.f, fmaf(l1, 0.f, odd));
   }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+// lo without the halves whose hi is not finite.
+__device__ __forceinline__ uint32_t drop_odd(uint32_t hi, uint32_t lo) { return lo & ~((not_finite(hi, 1) >> 15) * 0xFFFFu); }
+
+// Eight fp16 values as bf16: their first eight bits, and the three that these leave.  False if one is not finite.
+__device__ __forceinline__ bool split_f16(const uint4& v, uint4& hi, uint4& lo) {
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  uint32_t h[4], l[4];
+  __half2 odd = __half2half2(__ushort_as_half(0));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t top = in[i] & 0xFFF8FFF8u;
+    const __half2 left = __hsub2(*reinterpret_cast<const __half2*>(&in[i]), *reinterpret_cast<const __half2*>(&top));
+    odd = __hfma2(left, __half2half2(__ushort_as_half(0)), odd);   // NaN if a remainder is
+    h[i] = upper_halves(half_lo(top), half_hi(top));
+    l[i] = upper_halves(__low2float(left), __high2float(left));
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+  return (*reinterpret_cast<const uint32_t*>(&odd) & 0x7FFF7FFFu) == 0;
 }
 
 // ------------------------------------------------------------------ the persistent kernel
@@ -649,9 +678,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort);
         fence_after();
         uint32_t d = tmem + buf * kAccCols;
-        const uint32_t idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb);
+        const uint32_t idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb), idesc_u = instr_desc(true, 256, T.n, kTa, kTb);
         const int red = kMode == GM_WGRAD ? T.rows : p.red;
-        const auto multiply = [&](int sa, int sb, int k, bool first_step) {   // stages of the operands, k of their 64
+        // stages of the operands, k of their 64
+        const auto multiply = [&](int sa, int sb, int k, uint32_t idesc, bool first_step) {
           const uint64_t da = tile_desc<kTa>(smem_u32(S.stage[sa])), db = tile_desc<kTb>(smem_u32(S.stage[sb]) + kHalf);
           const int nk = (min(64, k) + 15) / 16;
           for (int kk = 0; kk < nk; ++kk)
@@ -670,8 +700,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
               if (!(ok = wait_bar(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
               us ^= 1u << s;
               fence_after();
-              multiply(s, s, k, false);
-              multiply(s, s2, k, false);
+              multiply(s, s, k, idesc_u, false);
+              multiply(s, s2, k, idesc_u, false);
+              if (!p.bf16) multiply(s2, s, k, idesc_u, false);
               commit_pair(&S.empty[s], 3);
               commit_pair(&S.empty[s2], 3);
             }
@@ -690,7 +721,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort))) break;
           fulls ^= 1u << s;
           fence_after();
-          multiply(s, s, red - 64 * ks, ks % kPiece == 0);
+          multiply(s, s, red - 64 * ks, idesc, ks % kPiece == 0);
           commit_pair(&S.empty[s], 3);
           ++it;
         }
@@ -896,6 +927,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       int at0 = 0;
       for (int block = 0; block < blocks; ++block) {
         uint4 hi[8], lo[8];
+        float odd = 0.f;
         const float* src = p.u + static_cast<size_t>(T.c0 + c) * p.rank + 64 * block;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
@@ -903,9 +935,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
           const float4 u0 = in ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * w) : zero;
           const float4 u1 = in ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * w + 1) : zero;
-          hi[w] = u_words<false>(u0, u1, p.bf16);
-          lo[w] = u_words<true>(u0, u1, p.bf16);
+          split_u(u0, u1, hi[w], lo[w], odd);
         }
+        if (odd != 0.f)   // NaN
+#pragma unroll
+          for (int w = 0; w < 8; ++w)
+            lo[w] = make_uint4(drop_odd(hi[w].x, lo[w].x), drop_odd(hi[w].y, lo[w].y), drop_odd(hi[w].z, lo[w].z),
+                               drop_odd(hi[w].w, lo[w].w));
         for (int j = 0; j < n; ++j) {
           const int at = pair_at(block * n + j, pairs, T.steps);   // base steps before this pair
           it += at - at0;
@@ -928,13 +964,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           }
           uint4* words = reinterpret_cast<uint4*>(S.stage[s]) + i0;
           uint32_t any = 0;
+          if (p.bf16) {
 #pragma unroll
-          for (int w = 0; w < 8; ++w) {
-            const uint4 v = words[128 * w];
-            const uint32_t bad =
-                not_finite(v.x, p.bf16) | not_finite(v.y, p.bf16) | not_finite(v.z, p.bf16) | not_finite(v.w, p.bf16);
-            if (bad) words[128 * w] = make_uint4(0, 0, 0, 0);
-            any |= bad;
+            for (int w = 0; w < 8; ++w) {
+              const uint4 v = words[128 * w];
+              const uint32_t bad = not_finite(v.x, 1) | not_finite(v.y, 1) | not_finite(v.z, 1) | not_finite(v.w, 1);
+              if (bad) words[128 * w] = make_uint4(0, 0, 0, 0);
+              any |= bad;
+            }
+          } else {
+            uint4* words2 = reinterpret_cast<uint4*>(S.stage[s2]) + i0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+              uint4 b_hi, b_lo;
+              if (!split_f16(words[128 * w], b_hi, b_lo)) {
+                b_hi = b_lo = make_uint4(0, 0, 0, 0);
+                any = 1;
+              }
+              words[128 * w] = b_hi;
+              words2[128 * w] = b_lo;
+            }
           }
           if (any) S.ad.broken[n_tile & 15] = 1;
           fence_proxy_async_smem();

@@ -490,9 +490,8 @@ moe_status moe_geglu_grad(int dtype, int gelu_variant, const void *h, int64_t ld
  * W [n][k], A [n_adapters][rank][k], B [n_adapters][n][rank], scale fp32
  * [n_adapters], ids int32 [t]; a row whose id is outside [0, n_adapters) (-1)
  * has no adapter.  Rows are in any order; 8 <= rank <= 128, a multiple of 8
- * (an adapter of a smaller rank ends in zeros).  A x is summed in fp32 and
- * handed on with 16 bits or more (MOE_F16: past +-65504 it counts as
- * infinite).
+ * (an adapter of a smaller rank ends in zeros).  s A x is summed in fp32 and
+ * keeps its range; its products with B are good to 2^-14.
  * Non-finite values in an adapter reach the rows of its own requests only.
  * workspace: at least 4 t rank bytes of device memory, 32-byte aligned,
  * contents undefined before and after; calls that may run at the same time

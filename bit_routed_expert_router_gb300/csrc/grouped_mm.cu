@@ -285,7 +285,7 @@ __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
 // One warp of each CTA lists the tiles' adapters; four write u's steps and look
 // through the B rows that TMA loaded for them: a value that is not finite would
 // reach every column (0 times infinity), so it is cleared and the tile marked,
-// and the storing warps put NaN where it belongs.  (As mma.sync products in the
+// and the storing warps add its rows' terms where they belong.  (As mma.sync products in the
 // epilogue the term took the kernel from 45 to 115 us at 4096 rows and rank 64,
 // since they wait for the tcgen05 products; on the ordinary pipes 145, bound by
 // broadcast loads.)
@@ -301,17 +301,23 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t v, int bf16) {
   return ((v & mask) + one) & 0x80008000u;
 }
 
-__device__ __noinline__ bool row_broken(const uint16_t* b, int rank, int bf16) {
+// B's row times u in fp32 if the row has a value that is not finite (an infinity or NaN then), else 0.
+__device__ __noinline__ float broken_value(const uint16_t* b, const float* u, int rank, int bf16) {
   uint32_t bad = 0;
-  for (int k = 0; k < rank; k += 8) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(b + k));
-    bad |= not_finite(w.x, bf16) | not_finite(w.y, bf16) | not_finite(w.z, bf16) | not_finite(w.w, bf16);
+  float sum = 0.f;
+  for (int k = 0; k < rank; k += 2) {
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(b + k));
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(u + k));
+    bad |= not_finite(w, bf16);
+    sum = fmaf(bf16 ? __uint_as_float(w << 16) : half_lo(w), v.x, sum);
+    sum = fmaf(bf16 ? __uint_as_float(w & 0xFFFF0000u) : half_hi(w), v.y, sum);
   }
-  return bad != 0;
+  return bad ? sum : 0.f;
 }
 
-// Columns row0 .. and this warp's 32 features: NaN where the row's adapter has a value that is not finite.
-__device__ __forceinline__ void mark_broken(float (&v)[2][16], const GmParams& p, int row0, int cols, int f0, int lane) {
+// Columns row0 .. and this warp's 32 features of a marked tile: the terms that are not finite.
+__device__ __forceinline__ void add_broken(float (&v)[2][16], const GmParams& p, int row0, int cols, int f0, int lane) {
+  pdl_wait();   // u
 #pragma unroll
   for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -322,8 +328,9 @@ __device__ __forceinline__ void mark_broken(float (&v)[2][16], const GmParams& p
 #pragma unroll
       for (int mb = 0; mb < 2; ++mb) {
         const int f = f0 + 16 * mb + 8 * (i >> 1) + (lane >> 2);
-        if (f < p.feat && row_broken(p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank, p.rank, p.bf16))
-          v[mb][4 * j + i] = __uint_as_float(0x7FC00000u);
+        if (f < p.feat)
+          v[mb][4 * j + i] += broken_value(p.b + (static_cast<size_t>(id) * p.feat + f) * p.rank,
+                                           p.u + static_cast<size_t>(row0 + c) * p.rank, p.rank, p.bf16);
       }
     }
 }
@@ -840,7 +847,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[0][i] = sums[c0 >> 6][0][i], v[1][i] = sums[c0 >> 6][1][i];
           if constexpr (kEpi == GM_ADAPT)
-            if (S.ad.broken[n_tile & 15]) mark_broken(v, p, T.c0 + c0, T.cols - c0, f0, lane);
+            if (S.ad.broken[n_tile & 15]) add_broken(v, p, T.c0 + c0, T.cols - c0, f0, lane);
           store(v, c0);
         }
         continue;
@@ -865,7 +872,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           for (int i = 0; i < 16; ++i) v[0][i] = v[1][i] = 0.f;
         }
         if constexpr (kEpi == GM_ADAPT)
-          if (S.ad.broken[n_tile & 15] && feats > 0) mark_broken(v, p, T.c0 + c0, T.cols - c0, f0, lane);
+          if (S.ad.broken[n_tile & 15] && feats > 0) add_broken(v, p, T.c0 + c0, T.cols - c0, f0, lane);
         release(c0);
         if (feats > 0) store(v, c0);
       }

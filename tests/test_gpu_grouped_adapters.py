@@ -43,3 +43,20 @@ def test_every_bit_of_b_counts(t, rank):
     scale = torch.full_like(scale, 2.0 ** -6)
     assert max(float((x.double() @ a[i].double().T).abs().max()) for i in range(4)) < 2 ** 8
     assert torch.equal(run(x, w, ids, a, b, scale), lora_reference(x, w, ids, a, b, scale).to(F16))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("t,rank", ROWS)
+def test_infinities_of_b_are_infinite(t, rank, dtype):
+    """What 64-bit arithmetic makes of them: an infinity with the sign of its value of A x, NaN where that is 0 or where
+    both signs meet; on every kernel, and nothing in other rows and features."""
+    x, w, ids, a, b, scale = lora_case(t + 2, t, 136, 200, 4, rank, dtype, "any")
+    b[3, 17, 5], b[3, 100, rank - 1], b[1, 30], b[2, 7, 3] = float("inf"), float("-inf"), float("-inf"), float("nan")
+    y = run(x, w, ids, a, b, scale)
+    u = torch.einsum("tk,trk->tr", x.double(), a[ids.clamp(min=0).long()].double()) * scale[ids.clamp(min=0).long(), None]
+    term = (u[:, None, :] * b[ids.clamp(min=0).long()].double()).sum(2)
+    want = (x.double() @ w.double().T + torch.where((ids < 0)[:, None], 0, term)).to(dtype)
+    assert want.isinf().any() and want.isnan().any()
+    assert torch.equal(y.isnan(), want.isnan())
+    assert torch.equal(y.nan_to_num(nan=0.0, posinf=float("inf"), neginf=float("-inf")),
+                       want.nan_to_num(nan=0.0, posinf=float("inf"), neginf=float("-inf")))

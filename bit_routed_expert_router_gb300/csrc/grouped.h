@@ -31,6 +31,7 @@ struct GmParams {
   const uint16_t* b = nullptr;        // [n_adapters][feat][rank]
   const float* u = nullptr;           // [m][rank]: s A x, 32-byte aligned
   int rank = 0, n_adapters = 0;
+  int limit = 0, stall = 0;           // set by the launches, see grouped_test_cycles
 };
 
 // x: rows [m][ldx]; w: [E][n][k] contiguous (GM_FWD: n features, k reduction;
@@ -45,6 +46,11 @@ struct GmOperands {
 
 // false: a CUDA call failed.
 bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, cudaStream_t s);
+// Tests: the bounded waits of launches from now on give up after `cycles`, and
+// their loading threads stop after `loads` (0 or less: the default of either,
+// about two seconds and never).
+void grouped_test_cycles(int64_t cycles);
+void grouped_test_loads(int64_t loads);
 // Reads and clears the current device's error word of these kernels after
 // synchronising the stream.
 bool grouped_error(cudaStream_t s, uint32_t* err);

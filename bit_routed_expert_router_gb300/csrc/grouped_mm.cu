@@ -28,6 +28,7 @@
 // distributed shared memory in rank order (no atomics, no workspace).
 #include <algorithm>
 #include <atomic>
+#include <limits>
 #include <type_traits>
 
 #include "gelu16.cuh"
@@ -92,15 +93,21 @@ struct TakeSmem {
   uint64_t full[kAnswers], empty[kAnswers];
 };
 
+// A CTA's bounded waits.
+struct Waits {
+  volatile int abort;   // 1: one ran out; 2: the launch had given up before this CTA started
+  int limit;            // of each, in 1024 cycles
+};
+
 template <int kMode, int kEpi>
 struct BigSmem {
   static constexpr int kStages = BigCfg<kMode, kEpi>::kStages;
   uint8_t stage[kStages][kStageBytes];
   alignas(1024) uint8_t epi[kEpiWarps][BigCfg<kMode, kEpi>::kEpiBytes];
   uint64_t full[kStages], empty[kStages], tail[kStages];
-  uint64_t acc_full[2], acc_empty[2], drain;
+  uint64_t acc_full[2], acc_empty[2];
   uint32_t tmem;
-  volatile int abort;
+  Waits waits;
   std::conditional_t<kTakes<kMode, kEpi>, TakeSmem, NoSmem> take;
   std::conditional_t<kEpi == GM_ADAPT, AdaptSmem, NoSmem> ad;
   int off[(kEpi == GM_ADAPT ? 1 : kMaxE) + 1];    // clamped to [0, m]
@@ -116,15 +123,17 @@ static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
 
 __device__ __forceinline__ uint32_t* err_word() { return &g_grouped_err; }
 
+constexpr long long kSettleCycles = 20000000;
+
 // Bounded wait that also ends when another role of the CTA gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Waits* w) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
     if (mbar_try_wait(bar, parity)) return true;
-    if (*abort) return false;
-    if (clock64() - t0 > kSpinLimitCycles) {
-      *abort = 1;
+    if (w->abort) return false;
+    if (clock64() - t0 > 1024LL * w->limit) {
+      w->abort = 1;
       atomicOr(err_word(), ERR_WAIT_TIMEOUT);
       return false;
     }
@@ -132,8 +141,17 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
 }
 
 // The same by a whole warp, which then agrees on the outcome.
-__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, volatile int* abort) {
-  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort));
+__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, Waits* w) {
+  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, w));
+}
+
+// The end of a CTA that gave up.  Copies, products and arrivals may be on their
+// way, and no barrier tells which: those of a pair's odd CTA count on the even
+// one's barriers, of which the phases that miss a share stay open.  All of them
+// take microseconds; the CTA keeps its memories for another 10 ms.
+__device__ __forceinline__ void settle() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kSettleCycles) __nanosleep(1000);
 }
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
@@ -229,7 +247,7 @@ __device__ __forceinline__ bool next_tile(Smem& S, Walk& w, uint32_t lead_empty,
     }
     const int s = w.n % kAnswers;
     const uint32_t parity = (w.n / kAnswers) & 1;
-    if (!(kWarp ? wait_bar_warp(&S.take.full[s], parity, &S.abort) : wait_bar(&S.take.full[s], parity, &S.abort)))
+    if (!(kWarp ? wait_bar_warp(&S.take.full[s], parity, &S.waits) : wait_bar(&S.take.full[s], parity, &S.waits)))
       return false;
     ++w.n;
     const int block = taken_block(smem_u32(S.take.answer[s]));
@@ -500,9 +518,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         mbar_init(&S.take.full[i], 1);
         mbar_init(&S.take.empty[i], 2 * (BigCfg<kMode, kEpi>::kThreads / 32 - 1));   // all but one loading, one idle warp
       }
-    mbar_init(&S.drain, 1);
     // a pair that gave up leaves its launch's other tiles to clusters that start after it: those do nothing
-    S.abort = kTake && *static_cast<volatile uint32_t*>(err_word()) != 0;
+    S.waits.abort = kTake && *static_cast<volatile uint32_t*>(err_word()) != 0 ? 2 : 0;
+    S.waits.limit = p.limit;
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
@@ -571,8 +589,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     if (elect_one()) {
       const uint32_t lead_full = map_rank(smem_u32(S.full), 0);
       uint32_t it = 0, n_tile = 0;
-      // by stage: last loaded for an adapter's pair, last given to its second step (no load); phases issued
-      uint32_t extra = 0, unused = 0, fulls = 0, tails = 0;
       int e = 0;
       Tile T;
       uint32_t asked = 0;
@@ -580,45 +596,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         if constexpr (kTake) {
           for (; rank == 0 && asked < walk.n + kAhead; ++asked) {
             const int s = asked % kAnswers;
-            if (!wait_bar(&S.take.empty[s], ((asked / kAnswers) & 1) ^ 1, &S.abort)) return;
+            if (!wait_bar(&S.take.empty[s], ((asked / kAnswers) & 1) ^ 1, &S.waits)) return;
             mbar_arrive_expect_tx(&S.take.full[s], 16);
             arrive_expect_cluster(map_rank(smem_u32(&S.take.full[s]), 1), 16);
             try_take_cluster(smem_u32(S.take.answer[s]), smem_u32(&S.take.full[s]));
           }
         }
       };
-      while (!S.abort && next_tile<kTake, false>(S, walk, rank == 0 ? 0 : lead_take, ask) &&
+      while (!S.waits.abort && it < static_cast<uint32_t>(p.stall) && next_tile<kTake, false>(S, walk, rank == 0 ? 0 : lead_take, ask) &&
              tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
         const int half = T.n / 2;
         const uint32_t bytes = kHalf + half * 128;
         int pairs = 0, pair = 0;
         [[maybe_unused]] const int lb = n_tile++ % kLists;
         if constexpr (kEpi == GM_ADAPT) {
-          if (!wait_bar(&S.ad.list_full[lb], ((n_tile - 1) / kLists) & 1, &S.abort)) break;
+          if (!wait_bar(&S.ad.list_full[lb], ((n_tile - 1) / kLists) & 1, &S.waits)) break;
           pairs = S.ad.n_list[lb] * ((p.rank + 63) / 64);
         }
-        for (int ks = 0; ks < T.steps || pair < pairs; ++ks) {
+        for (int ks = 0; it < static_cast<uint32_t>(p.stall) && (ks < T.steps || pair < pairs); ++ks) {
           if constexpr (kEpi == GM_ADAPT) {
             for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair, it += 2) {
               // one load of B for both stages; the writing warps go on when it has landed and both are free
               const int s = it % kStages, s2 = (it + 1) % kStages, block = pair / S.ad.n_list[lb];
-              if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
+              if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.waits)) break;
               mbar_arrive_expect_tx(&S.tail[s], kHalf);
               load_3d<true>(smem_u32(S.stage[s]), &maps.c, 64 * block, T.f0 + 128 * rank,
                             S.ad.list[lb][pair - block * S.ad.n_list[lb]], smem_u32(&S.tail[s]));
-              extra |= 1u << s;
-              unused &= ~(1u << s);
-              tails ^= 1u << s;
-              const bool go = wait_bar(&S.empty[s2], (((it + 1) / kStages) & 1) ^ 1, &S.abort);
+              if (!wait_bar(&S.empty[s2], (((it + 1) / kStages) & 1) ^ 1, &S.waits)) break;
               mbarrier_arrive(&S.tail[s]);
-              if (!go) break;   // s2's earlier load may still be in flight
-              unused |= 1u << s2;
             }
-            if (S.abort) break;
+            if (S.waits.abort) break;
             if (ks >= T.steps) continue;
           }
           const int s = it % kStages;
-          if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.abort)) break;
+          if (!wait_bar(&S.empty[s], ((it / kStages) & 1) ^ 1, &S.waits)) break;
           uint32_t bar = lead_full + 8 * s;
           if (kMode == GM_WGRAD) {
             if (ks == T.steps - 1 && (T.rows & 15)) {   // warp 10 sees these bytes first
@@ -650,26 +661,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             }
             load_2d<true>(b, &maps.b[half / 16 - 1], 64 * ks, T.c0 + rank * half, bar);
           }
-          extra &= ~(1u << s);
-          unused &= ~(1u << s);
-          fulls ^= 1u << s;
           ++it;
         }
         if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
       }
-      if (kTake && !S.abort) asked = walk.n + kAhead - 1;   // as many when a refusal is read
-      if constexpr (kTake)   // answers come before the pair leaves
-        for (uint32_t i = walk.n; i < asked; ++i)
-          mbar_wait_bounded(&S.take.full[i % kAnswers], (i / kAnswers) & 1, err_word());
-      if (S.abort)   // copies already issued land before the pair leaves
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) {
-          const int s = i % kStages;
-          if ((unused >> s) & 1u) continue;
-          if ((extra >> s) & 1u)
-            mbar_wait_bounded(&S.tail[s], ((tails >> s) & 1) ^ 1, err_word());
-          else if (rank == 0)
-            mbar_wait_bounded(&S.full[s], ((fulls >> s) & 1) ^ 1, err_word());
-        }
+      if constexpr (kTake)   // the answers asked for ahead of the refusal come before the pair leaves
+        for (uint32_t i = walk.n; i < walk.n + kAhead - 1; ++i)
+          if (!wait_bar(&S.take.full[i % kAnswers], (i / kAnswers) & 1, &S.waits)) break;
     }
   } else if (warp == 1) {
     if (rank == 0 && elect_one()) {
@@ -682,7 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       while (ok && next_tile<kTake, false>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
         if (T.steps == 0) continue;
         int buf = count & 1;
-        ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort);
+        ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.waits);
         fence_after();
         uint32_t d = tmem + buf * kAccCols;
         const uint32_t idesc = instr_desc(p.bf16, 256, T.n, kTa, kTb), idesc_u = instr_desc(true, 256, T.n, kTa, kTb);
@@ -697,14 +695,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         int pairs = 0, pair = 0;
         [[maybe_unused]] const int lb = n_tile % kLists;
         if constexpr (kEpi == GM_ADAPT) {
-          ok = ok && wait_bar(&S.ad.list_full[lb], (n_tile++ / kLists) & 1, &S.abort);
+          ok = ok && wait_bar(&S.ad.list_full[lb], (n_tile++ / kLists) & 1, &S.waits);
           pairs = ok ? S.ad.n_list[lb] * ((p.rank + 63) / 64) : 0;
         }
         for (int ks = 0; ok && (ks < T.steps || pair < pairs); ++ks) {
           if constexpr (kEpi == GM_ADAPT) {
             for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair, it += 2) {
               const int s = it % kStages, s2 = (it + 1) % kStages, k = p.rank - 64 * (pair / S.ad.n_list[lb]);
-              if (!(ok = wait_bar(&S.ad.u_full[s], (us >> s) & 1, &S.abort))) break;
+              if (!(ok = wait_bar(&S.ad.u_full[s], (us >> s) & 1, &S.waits))) break;
               us ^= 1u << s;
               fence_after();
               multiply(s, s, k, idesc_u, false);
@@ -721,11 +719,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
             ++count;
             buf = count & 1;
             d = tmem + buf * kAccCols;
-            if (!(ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.abort))) break;
+            if (!(ok = wait_bar(&S.acc_empty[buf], ((count >> 1) & 1) ^ 1, &S.waits))) break;
             fence_after();
           }
           const int s = it % kStages;
-          if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.abort))) break;
+          if (!(ok = wait_bar(&S.full[s], (fulls >> s) & 1, &S.waits))) break;
           fulls ^= 1u << s;
           fence_after();
           multiply(s, s, red - 64 * ks, idesc, ks % kPiece == 0);
@@ -735,10 +733,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         if constexpr (kEpi == GM_ADAPT) mbarrier_arrive(&S.ad.list_empty[lb]);
         if (ok) commit_pair(&S.acc_full[buf], 3);
         ++count;
-      }
-      if (!ok) {   // the products in flight read shared memory: wait for them
-        commit_pair(&S.drain, 1);
-        mbar_wait_bounded(&S.drain, 0, err_word());
       }
     }
   } else if (warp < 2 + kEpiWarps) {
@@ -767,7 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         bool ok = true;
         for (int ks = 0; ok && ks < T.steps; ks += kSegSteps, ++count) {
           const int buf = count & 1;
-          if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort))) break;
+          if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.waits))) break;
           fence_after();
           const uint32_t at = tmem + buf * kAccCols + c_first + (static_cast<uint32_t>(32 * q) << 16);
 #pragma unroll
@@ -824,7 +818,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         bool ok = true;
         for (int ks = 0; ok && ks < T.steps; ks += kLongSteps, ++count) {
           const int buf = count & 1;
-          if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort))) break;
+          if (!(ok = wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.waits))) break;
           fence_after();
 #pragma unroll 1
           for (int c0 = c_first; c0 < T.cols; c0 += 64) {
@@ -853,7 +847,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         continue;
       }
       const int buf = count & 1;
-      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.abort)) break;
+      if (T.steps && !wait_bar_warp(&S.acc_full[buf], (count >> 1) & 1, &S.waits)) break;
       fence_after();
       // the accumulator goes back as soon as this warp has read its last columns, before they are stored
       const auto release = [&](int c0) {
@@ -887,7 +881,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       Tile T;
       for (; next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T); ++n_tile) {
         const int lb = n_tile % kLists;
-        if (!wait_bar_warp(&S.ad.list_empty[lb], ((n_tile / kLists) & 1) ^ 1, &S.abort)) break;
+        if (!wait_bar_warp(&S.ad.list_empty[lb], ((n_tile / kLists) & 1) ^ 1, &S.waits)) break;
         int id[8];
         uint32_t open[8];   // columns whose adapter is not listed yet, 32 at a time
 #pragma unroll
@@ -927,7 +921,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
     pdl_wait();   // the u rows
     for (; next_tile<kTake, true>(S, walk, lead_take, no_ask) && tile_at<kMode, kFeat>(S, p, walk.t, e, T); ++n_tile) {
       const int lb = n_tile % kLists;
-      if (!wait_bar_warp(&S.ad.list_full[lb], (n_tile / kLists) & 1, &S.abort)) break;
+      if (!wait_bar_warp(&S.ad.list_full[lb], (n_tile / kLists) & 1, &S.waits)) break;
       const int n = S.ad.n_list[lb], blocks = (p.rank + 63) / 64, pairs = n * blocks;
       const int half = T.n / 2, c = rank * half + i0;   // this thread's column, one of this CTA's half
       const int mine = i0 < half ? S.ad.id[lb][c] : -1;
@@ -958,7 +952,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           it += 2;
           // B has landed and both stages are free (their own barriers' phases would be ambiguous here: these warps do
           // not see the steps in between)
-          alive = alive && wait_bar_warp(&S.tail[s], (tails >> s) & 1, &S.abort);
+          alive = alive && wait_bar_warp(&S.tail[s], (tails >> s) & 1, &S.waits);
           tails ^= 1u << s;
           if (i0 < half) {
             uint8_t *row = S.stage[s] + kHalf + 128 * i0, *row2 = S.stage[s2] + kHalf + 128 * i0;
@@ -1013,7 +1007,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       it += T.steps;
       if (!(T.rows & 15)) continue;
       const int s = (it - 1) % kStages, lo = ((T.rows - 1) & 63) + 1, hi = (lo + 15) & ~15;
-      if (!wait_bar_warp(&S.tail[s], (phases >> s) & 1, &S.abort)) break;
+      if (!wait_bar_warp(&S.tail[s], (phases >> s) & 1, &S.waits)) break;
       phases ^= 1u << s;
       for (int i = lane; i < (hi - lo) * 32; i += 32) {   // four blocks of 64 x 128 bytes, eight 16-byte words a row
         const int blk = (i & 31) >> 3, word = i & 7, row = lo + (i >> 5);
@@ -1026,6 +1020,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
   }
   fence_before();
   __syncthreads();
+  if (S.waits.abort == 1) settle();
   cluster_sync();   // no CTA leaves while the other may still arrive on its barriers or read its stages
   fence_after();
   if (warp == 1) tmem_free<true>(tmem, 2 * kAccCols);
@@ -1079,9 +1074,9 @@ __global__ void __launch_bounds__(192)
   constexpr bool kTa = kMode == GM_DGRAD;
   constexpr int kFeat = kEpi == GM_GATED ? 64 : 128;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
+  __shared__ uint64_t full[8], empty[8], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
+  __shared__ Waits s_waits;
   __shared__ int s_tile[4];   // expert, first row, rows
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1091,7 +1086,8 @@ __global__ void __launch_bounds__(192)
     tmem_alloc<false>(&s_tmem, 2 * kSmallCols);
   } else if (tid == 64) {
     prefetch_map(&maps.a);
-    s_abort = 0;
+    s_waits.abort = 0;
+    s_waits.limit = p.limit;
     for (int i = 0; i < 8; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -1100,7 +1096,6 @@ __global__ void __launch_bounds__(192)
       mbar_init(&acc_full[i], 1);
       mbar_init(&acc_empty[i], 4);
     }
-    mbar_init(&drain, 1);
     fence_mbar_init();
   }
   if (kEpi != GM_ADAPT) pdl_wait();   // adapters: nothing but the u rows comes from the previous kernel
@@ -1157,10 +1152,9 @@ __global__ void __launch_bounds__(192)
 
   if (warp == 0) {
     if (elect_one()) {
-      int ks = 0;
-      for (; ks < steps; ++ks) {
+      for (int ks = 0; ks < min(steps, p.stall); ++ks) {
         const int s = ks % stages;
-        if (!wait_bar(&empty[s], ((ks / stages) & 1) ^ 1, &s_abort)) break;
+        if (!wait_bar(&empty[s], ((ks / stages) & 1) ^ 1, &s_waits)) break;
         const uint32_t a = smem_u32(ring) + s * bytes, bar = smem_u32(&full[s]);
         mbar_arrive_expect_tx(&full[s], bytes);
         const int k = 64 * (k0 + ks);
@@ -1174,9 +1168,6 @@ __global__ void __launch_bounds__(192)
         }
         load_2d<false>(a + kHalf, &maps.b[n / 16 - 1], k, row0, bar);
       }
-      if (s_abort)
-        for (int i = max(0, ks - stages); i < ks; ++i)
-          mbar_wait_bounded(&full[i % stages], (i / stages) & 1, err_word());
     }
   } else if (warp == 1) {
     if (elect_one()) {
@@ -1184,11 +1175,11 @@ __global__ void __launch_bounds__(192)
       bool go = true;
       for (int ks = 0, piece = 0; go && ks < steps; ++piece) {
         const int buf = piece & 1, end = min(ks + seg, steps);
-        go = wait_bar(&acc_empty[buf], ((piece >> 1) & 1) ^ 1, &s_abort);
+        go = wait_bar(&acc_empty[buf], ((piece >> 1) & 1) ^ 1, &s_waits);
         fence_after();
         for (bool first = true; go && ks < end; ++ks) {
           const int s = ks % stages;
-          if (!(go = wait_bar(&full[s], (ks / stages) & 1, &s_abort))) break;
+          if (!(go = wait_bar(&full[s], (ks / stages) & 1, &s_waits))) break;
           fence_after();
           const uint32_t a = smem_u32(ring) + s * bytes;
           const uint64_t da = tile_desc<kTa>(a), db = tile_desc<false>(a + kHalf);
@@ -1198,10 +1189,6 @@ __global__ void __launch_bounds__(192)
           commit(&empty[s]);
         }
         if (go) commit(&acc_full[buf]);
-      }
-      if (!go) {   // the products in flight read shared memory: wait for them
-        commit(&drain);
-        mbar_wait_bounded(&drain, 0, err_word());
       }
     }
   }
@@ -1238,7 +1225,7 @@ __global__ void __launch_bounds__(192)
       for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
     for (int ks = 0, piece = 0; ok && ks < steps; ks += seg, ++piece) {
       const int buf = piece & 1;
-      if (!(ok = wait_bar_warp(&acc_full[buf], (piece >> 1) & 1, &s_abort))) break;
+      if (!(ok = wait_bar_warp(&acc_full[buf], (piece >> 1) & 1, &s_waits))) break;
       fence_after();
 #pragma unroll
       for (int j = 0; j < kSmallCols / 16; ++j)
@@ -1305,6 +1292,7 @@ __global__ void __launch_bounds__(192)
         finish(c, kEpi == GM_ADAPT ? adapter_values(p, row0 + c, f) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
+  if (s_waits.abort) settle();
   if (split > 1)
     cluster_sync();   // the others may still read this CTA's part
   else
@@ -1328,7 +1316,7 @@ __global__ void __launch_bounds__(192)
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[kDownStages], empty[kDownStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_abort;
+  __shared__ Waits s_waits;
   __shared__ int s_n, s_list[64], s_nth[64];   // distinct adapters; which of them a row has, or -1
   uint8_t* ring = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1339,7 +1327,8 @@ __global__ void __launch_bounds__(192)
   } else if (tid == 64) {
     prefetch_map(&maps.a);
     prefetch_map(&maps.b[0]);
-    s_abort = 0;
+    s_waits.abort = 0;
+    s_waits.limit = p.limit;
     for (int i = 0; i < kDownStages; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
@@ -1389,28 +1378,25 @@ __global__ void __launch_bounds__(192)
   for (int a0 = each * blockIdx.y; a0 < n; a0 += each * gridDim.y) {
     const int na = min(each, n - a0);
     const uint32_t bytes = na * slot * 128 + kDownCols * 128;
+    // after a wait that ran out the passes that are left are only met
     if (warp == 0) {
-      if (elect_one()) {
-        int ks = 0;
-        for (; ks < steps; ++ks) {
+      if (elect_one() && !s_waits.abort) {
+        for (int ks = 0; ks < steps && it + ks < static_cast<uint32_t>(p.stall); ++ks) {
           const uint32_t i = it + ks, s = i % kDownStages;
-          if (!wait_bar(&empty[s], ((i / kDownStages) & 1) ^ 1, &s_abort)) break;
+          if (!wait_bar(&empty[s], ((i / kDownStages) & 1) ^ 1, &s_waits)) break;
           const uint32_t a = smem_u32(ring) + s * kDownStage, bar = smem_u32(&full[s]);
           mbar_arrive_expect_tx(&full[s], bytes);
           for (int j = 0; j < na; ++j) load_3d<false>(a + j * slot * 128, &maps.a, 64 * (k0 + ks), 0, s_list[a0 + j], bar);
           load_2d<false>(a + kHalf, &maps.b[0], 64 * (k0 + ks), row0, bar);
         }
-        if (s_abort)
-          for (uint32_t i = it + ks - min(ks, kDownStages); i < it + ks; ++i)
-            mbar_wait_bounded(&full[i % kDownStages], (i / kDownStages) & 1, err_word());
       }
     } else if (warp == 1) {
-      if (elect_one()) {
+      if (elect_one() && !s_waits.abort) {
         const uint32_t idesc = instr_desc(p.bf16, 128, kDownCols, false, false);
         for (int ks = 0; ks < steps; ++ks) {
           const uint32_t i = it + ks, s = i % kDownStages, at = piece + ks / kLongSteps, buf = at & 1;
-          if (ks % kLongSteps == 0 && !wait_bar(&acc_empty[buf], ((at >> 1) & 1) ^ 1, &s_abort)) break;
-          if (!wait_bar(&full[s], (i / kDownStages) & 1, &s_abort)) break;
+          if (ks % kLongSteps == 0 && !wait_bar(&acc_empty[buf], ((at >> 1) & 1) ^ 1, &s_waits)) break;
+          if (!wait_bar(&full[s], (i / kDownStages) & 1, &s_waits)) break;
           fence_after();
           const uint32_t a = smem_u32(ring) + s * kDownStage;
           const uint64_t da = tile_desc<false>(a), db = tile_desc<false>(a + kHalf);
@@ -1427,6 +1413,7 @@ __global__ void __launch_bounds__(192)
     it += steps;
     bool ok = true;
     if (warp >= 2) {
+      ok = __all_sync(0xFFFFFFFFu, !s_waits.abort);
       const int q = warp & 3;
       float acc[kDownCols / 16][16];
 #pragma unroll
@@ -1435,7 +1422,7 @@ __global__ void __launch_bounds__(192)
         for (int i = 0; i < 16; ++i) acc[j][i] = 0.f;
       for (int ks = 0, at = piece; ok && ks < steps; ks += kLongSteps, ++at) {
         const int buf = at & 1;
-        if (!(ok = wait_bar_warp(&acc_full[buf], (at >> 1) & 1, &s_abort))) break;
+        if (!(ok = wait_bar_warp(&acc_full[buf], (at >> 1) & 1, &s_waits))) break;
         fence_after();
 #pragma unroll
         for (int j = 0; j < kDownCols / 16; ++j) {
@@ -1474,12 +1461,23 @@ __global__ void __launch_bounds__(192)
     cluster_sync();             // the others may still read this CTA's part
   }
   __syncthreads();
+  if (s_waits.abort) settle();
   if (warp == 1) tmem_free<false>(tmem, 2 * kDownCols);
 }
 
 // ------------------------------------------------------------------ launches
 
 constexpr int kMaxKernels = 16;
+
+// A wait's limit in 1024 cycles, and the loads after which a CTA's loading thread stops.
+constexpr int kDefaultLimit = static_cast<int>(kSpinLimitCycles / 1024), kNever = std::numeric_limits<int>::max();
+std::atomic<int> g_limit{kDefaultLimit}, g_stall{kNever};
+
+GmParams with_limits(GmParams p) {
+  p.limit = g_limit.load(std::memory_order_relaxed);
+  p.stall = g_stall.load(std::memory_order_relaxed);
+  return p;
+}
 
 struct DeviceInfo {
   int sms = 0;
@@ -1591,7 +1589,14 @@ bool launch_small(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s
 
 }  // namespace
 
-bool launch_adapter_down_many(const GmOperands& o, const GmParams& p, const float* scale, float* u, cudaStream_t s) {
+void grouped_test_cycles(int64_t cycles) {
+  g_limit = cycles > 0 ? static_cast<int>(std::min<int64_t>(cycles / 1024, kDefaultLimit)) : kDefaultLimit;
+}
+
+void grouped_test_loads(int64_t loads) { g_stall = loads > 0 && loads < kNever ? static_cast<int>(loads) : kNever; }
+
+bool launch_adapter_down_many(const GmOperands& o, const GmParams& params, const float* scale, float* u, cudaStream_t s) {
+  const GmParams p = with_limits(params);
   int slot = 8;
   while (slot < p.rank) slot *= 2;
   GmMaps maps;
@@ -1639,7 +1644,8 @@ bool few_rows(const GmParams& p) {
 
 }  // namespace
 
-bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, cudaStream_t s) {
+bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& params, cudaStream_t s) {
+  const GmParams p = with_limits(params);
   DeviceInfo d;
   if (!device_info(&d)) return false;
   GmMaps maps;

@@ -572,6 +572,12 @@ moe_status moe_get_profile(moe_ctx *ctx, moe_kernel_time *out, int n);
  * hook 14: resident decode steps of 2 to 4 tokens run one clustered-kernel
  * launch per token (value != 0, the default, where that kernel can run) or
  * take the batched paths of hook 13 (0).
+ * ctx NULL: the 16-bit operators' calls from now on, in every thread.  hook 10:
+ * their bounded device waits give up after `value` SM cycles (<= 0: the
+ * default).  hook 15: the threads that load operands stop after `value` loads a
+ * CTA (<= 0: never), so that every wait for what they would have loaded runs
+ * out; the kernels leave their outputs undefined and moe_grouped_sync returns
+ * MOE_ETIMEOUT.
  * Other hooks: MOE_EINVAL. */
 moe_status moe_test_hook(moe_ctx *ctx, int hook, int64_t value);
 

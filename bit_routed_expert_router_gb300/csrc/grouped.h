@@ -51,9 +51,9 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
 // about two seconds and never).
 void grouped_test_cycles(int64_t cycles);
 void grouped_test_loads(int64_t loads);
-// Reads and clears the current device's error word of these kernels after
-// synchronising the stream.
-bool grouped_error(cudaStream_t s, uint32_t* err);
+// Synchronises the stream; news: a wait ran out on the current device since the
+// last call with this stream.
+bool grouped_gave_up(cudaStream_t s, bool* news);
 
 bool launch_gated_grad(bool bf16, int gelu, const void* h, long long ldh, const void* da, long long ldda, void* dh,
                        long long lddh, int m, int f, const int32_t* n_rows, cudaStream_t s);

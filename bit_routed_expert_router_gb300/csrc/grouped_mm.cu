@@ -29,6 +29,8 @@
 #include <algorithm>
 #include <atomic>
 #include <limits>
+#include <map>
+#include <mutex>
 #include <type_traits>
 
 #include "gelu16.cuh"
@@ -42,7 +44,11 @@ namespace {
 
 using namespace tc16;
 
-__device__ uint32_t g_grouped_err;
+// CTAs that gave up on this device, and the number of the last one's grid (plus
+// one; the replays of a graph's node share theirs).  The count is never
+// taken back: each stream that asks compares it with what it was told before.
+__device__ uint32_t g_gave_up;
+__device__ unsigned long long g_gave_up_grid;
 
 constexpr int kMaxE = 1024;
 constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
@@ -121,7 +127,11 @@ static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
                   kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0,
               "staged rows");
 
-__device__ __forceinline__ uint32_t* err_word() { return &g_grouped_err; }
+__device__ __forceinline__ unsigned long long this_grid() {
+  unsigned long long g;
+  asm volatile("mov.u64 %0, %%gridid;" : "=l"(g));
+  return g + 1;
+}
 
 constexpr long long kSettleCycles = 20000000;
 
@@ -134,7 +144,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Waits* 
     if (w->abort) return false;
     if (clock64() - t0 > 1024LL * w->limit) {
       w->abort = 1;
-      atomicOr(err_word(), ERR_WAIT_TIMEOUT);
       return false;
     }
   }
@@ -145,11 +154,16 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, Wa
   return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, w));
 }
 
-// The end of a CTA that gave up.  Copies, products and arrivals may be on their
-// way, and no barrier tells which: those of a pair's odd CTA count on the even
-// one's barriers, of which the phases that miss a share stay open.  All of them
-// take microseconds; the CTA keeps its memories for another 10 ms.
-__device__ __forceinline__ void settle() {
+// The end of a CTA that gave up, by all of its threads.  Copies, products and
+// arrivals may be on their way, and no barrier tells which: those of a pair's odd
+// CTA count on the even one's barriers, of which the phases that miss a share
+// stay open.  All of them take microseconds; the CTA keeps its memories for
+// another 10 ms.
+__device__ __forceinline__ void report_and_settle() {
+  if (threadIdx.x == 0) {
+    *static_cast<volatile unsigned long long*>(&g_gave_up_grid) = this_grid();
+    atomicAdd(&g_gave_up, 1u);
+  }
   const long long t0 = clock64();
   while (clock64() - t0 < kSettleCycles) __nanosleep(1000);
 }
@@ -518,8 +532,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
         mbar_init(&S.take.full[i], 1);
         mbar_init(&S.take.empty[i], 2 * (BigCfg<kMode, kEpi>::kThreads / 32 - 1));   // all but one loading, one idle warp
       }
-    // a pair that gave up leaves its launch's other tiles to clusters that start after it: those do nothing
-    S.waits.abort = kTake && *static_cast<volatile uint32_t*>(err_word()) != 0 ? 2 : 0;
+    // a pair that gave up leaves its launch's other tiles to clusters that start after it: those do nothing, or each would
+    // wait as long
+    S.waits.abort = kTake && *static_cast<volatile unsigned long long*>(&g_gave_up_grid) == this_grid() ? 2 : 0;
+    if (S.waits.abort) atomicAdd(&g_gave_up, 1u);
     S.waits.limit = p.limit;
     fence_mbar_init();
   }
@@ -1020,7 +1036,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
   }
   fence_before();
   __syncthreads();
-  if (S.waits.abort == 1) settle();
+  if (S.waits.abort == 1) report_and_settle();
   cluster_sync();   // no CTA leaves while the other may still arrive on its barriers or read its stages
   fence_after();
   if (warp == 1) tmem_free<true>(tmem, 2 * kAccCols);
@@ -1292,7 +1308,7 @@ __global__ void __launch_bounds__(192)
         finish(c, kEpi == GM_ADAPT ? adapter_values(p, row0 + c, f) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
-  if (s_waits.abort) settle();
+  if (s_waits.abort) report_and_settle();
   if (split > 1)
     cluster_sync();   // the others may still read this CTA's part
   else
@@ -1461,7 +1477,7 @@ __global__ void __launch_bounds__(192)
     cluster_sync();             // the others may still read this CTA's part
   }
   __syncthreads();
-  if (s_waits.abort) settle();
+  if (s_waits.abort) report_and_settle();
   if (warp == 1) tmem_free<false>(tmem, 2 * kDownCols);
 }
 
@@ -1680,11 +1696,28 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& para
                      : launch_big<GM_FWD, GM_PLAIN>(maps, p, d.sms, s);
 }
 
-bool grouped_error(cudaStream_t s, uint32_t* err) {
-  const uint32_t zero = 0;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return false;
-  if (cudaMemcpyFromSymbol(err, g_grouped_err, sizeof(*err)) != cudaSuccess) return false;
-  return *err == 0 || cudaMemcpyToSymbol(g_grouped_err, &zero, sizeof(zero)) == cudaSuccess;
+bool grouped_gave_up(cudaStream_t s, bool* news) try {
+  static std::mutex lock;
+  static std::map<std::pair<int, cudaStream_t>, uint32_t> told;   // counts by device and stream
+  int dev = 0;
+  uint32_t count = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&count, g_gave_up, sizeof(count), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return false;
+  {
+    const std::lock_guard<std::mutex> hold(lock);
+    const auto known = told.find({dev, s});
+    *news = count != (known == told.end() ? 0u : known->second);
+    if (*news) told[{dev, s}] = count;
+  }
+  if (!*news) return true;
+  // the next replay of a graph that gave up does all of its work
+  void* grid = nullptr;
+  return cudaGetSymbolAddress(&grid, g_gave_up_grid) == cudaSuccess &&
+         cudaMemsetAsync(grid, 0, sizeof(g_gave_up_grid), s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+} catch (...) {   // no memory for another stream's count
+  return false;
 }
 
 }  // namespace moe

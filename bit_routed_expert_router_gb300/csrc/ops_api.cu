@@ -1,6 +1,6 @@
 // C entry points of the 16-bit operators: argument checks, then the launches
 // (grouped_mm.cu, gated_lora.cu).  No context, no allocation, no state but the
-// error word that moe_grouped_sync reads.
+// count of waits that ran out, which moe_grouped_sync reads.
 #include <cstdint>
 
 #include "grouped.h"
@@ -129,7 +129,11 @@ extern "C" moe_status moe_lora_mm(int dtype, const void* x, int64_t ldx, int t, 
 }
 
 extern "C" moe_status moe_grouped_sync(void* stream) {
-  uint32_t err = 0;
-  if (!moe::grouped_error(static_cast<cudaStream_t>(stream), &err)) return MOE_ECUDA;
-  return err & moe::ERR_WAIT_TIMEOUT ? MOE_ETIMEOUT : MOE_OK;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return MOE_ECUDA;
+  if (capture != cudaStreamCaptureStatusNone) return MOE_EINVAL;
+  bool news = false;
+  if (!moe::grouped_gave_up(s, &news)) return MOE_ECUDA;
+  return news ? MOE_ETIMEOUT : MOE_OK;
 }

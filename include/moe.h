@@ -433,7 +433,7 @@ moe_status moe_route_noalloc(const moe_config *cfg, const uint16_t *router_w, co
  * For experts kept in bf16 or fp16 (before quantisation, or in layers left
  * unquantised) and for training them.  They take no context: every buffer is
  * the caller's device memory on the current CUDA device, nothing is allocated
- * or kept between calls, and the calls return without synchronising (they can
+ * or kept between calls (but a count of waits that ran out), and the calls return without synchronising (they can
  * be captured).  Common rules:
  *   dtype        MOE_BF16 or MOE_F16, the type of every 16-bit tensor of the
  *                call; out_dtype is the same or MOE_F32
@@ -501,8 +501,11 @@ moe_status moe_lora_mm(int dtype, const void *x, int64_t ldx, int t, const void 
                        void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, then report whether a bounded device wait of these
- * operators ran out on the current device since the last call (MOE_ETIMEOUT:
- * outputs since then are undefined), as moe_sync does for a context. */
+ * operators ran out on the current device since the last call with this stream
+ * (MOE_ETIMEOUT: outputs since then are undefined), as moe_sync does for a
+ * context.  Whichever stream's call it was, every stream that asks is told (one
+ * that has never asked, of all since the library was loaded).  MOE_EINVAL while
+ * the stream is being captured. */
 moe_status moe_grouped_sync(void *stream);
 
 /* Per-kernel timing.  While enabled, decode and prefill calls launch their

@@ -14,6 +14,14 @@ from test_gpu_grouped import BF16, F16, F32, SENTINEL, gen, ints, lora_case, lor
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(scope="module", autouse=True)
+def told():
+    """Every stream that asks is told of a timeout: after these tests all that others may be given have been."""
+    yield
+    for s in [None] + [torch.cuda.Stream() for _ in range(64)]:
+        moe.moe_grouped_sync(s)
+
+
 class Stalled:
     """Calls inside load one stage a CTA and wait 0.1 ms."""
 
@@ -87,3 +95,66 @@ def test_adapters(t, rank):
     ws = torch.empty(4 * t * rank, dtype=torch.uint8, device="cuda")
     run_out(lambda: moe.moe_lora_mm(x, w, ids, a, b, scale, y, ws), whole)
     assert torch.equal(y, lora_reference(x, w, ids, a, b, scale).to(BF16))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_one_callers_timeout_is_not_anothers(captured):
+    """A launch that gave up on one stream: calls of another stream that follow do all of their work, and both streams
+    are told of it."""
+    g, n, k, E = gen(5), 520, 264, 100
+    counts = [129 + e % 7 for e in range(E)]
+    x, dy, off = ints(g, BF16, sum(counts), k), ints(g, BF16, sum(counts), n), offsets_of(counts)
+    dws = [torch.full((E, n, k), SENTINEL, dtype=F32, device="cuda") for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    want, lo = [], 0
+    for c in counts:
+        want.append(dy[lo:lo + c].double().T @ x[lo:lo + c].double())
+        lo += c
+    want = torch.stack(want).float()
+
+    def call(i):
+        moe.check(moe.moe_grouped_wgrad(dy, x, off, dws[i], stream=streams[i]))
+
+    call(1)
+    for s in streams:
+        moe.moe_grouped_sync(s)   # whatever earlier launches left
+    graph = torch.cuda.CUDAGraph()
+    if captured:
+        with torch.cuda.graph(graph, stream=streams[1]):
+            call(1)
+    for repeat in range(2):
+        dws[1].fill_(SENTINEL)
+        torch.cuda.synchronize()
+        with Stalled():
+            call(0)
+        streams[0].synchronize()
+        if captured:
+            with torch.cuda.stream(streams[1]):
+                graph.replay()
+        else:
+            call(1)
+        assert moe.moe_grouped_sync(streams[1]) == moe.MOE_ETIMEOUT
+        assert torch.equal(dws[1], want)
+        assert moe.moe_grouped_sync(streams[0]) == moe.MOE_ETIMEOUT
+        assert [moe.moe_grouped_sync(s) for s in streams] == [moe.MOE_OK] * 2
+        call(0)
+        moe.check(moe.moe_grouped_sync(streams[0]))
+        assert torch.equal(dws[0], want)
+    assert moe.moe_grouped_sync() == moe.MOE_ETIMEOUT   # and this one
+    assert moe.moe_grouped_sync() == moe.MOE_OK
+
+
+def test_no_sync_in_a_capture():
+    """Refused, and the capture goes on."""
+    g = gen(6)
+    x, w, y = ints(g, BF16, 40, 64), ints(g, BF16, 1, 72, 64), torch.empty(40, 72, dtype=BF16, device="cuda")
+    off = offsets_of([40])
+    ok(moe.moe_grouped_mm(x, off, w, y))
+    y.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.check(moe.moe_grouped_mm(x, off, w, y))
+        assert moe.moe_grouped_sync() == moe.MOE_EINVAL
+    graph.replay()
+    ok(moe.MOE_OK)
+    assert torch.equal(y, products(x, [40], w).to(BF16))

@@ -90,3 +90,32 @@ def test_long_products_with_adapters(t, dtype):
         r = (ids == i).nonzero()[:, 0]
         ref[r] += (x[r].double() @ a[i].double().T) @ b[i].double().T
     check(y, ref, k, more=PIECE / 16 * 4 * UNIT / 2 + 2 ** -15)
+
+
+def check32(y, ref, length):
+    """32-bit outputs: pieces of 24 k16 steps, and no further rounding."""
+    s = min(length, 384) / 16 * 4 * UNIT / 2 + -(-length // 384) * 2 ** -24
+    assert ((y.double() - ref).abs() <= s * ref).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m", [9, 300])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("red", [200, 2816, 65536])
+def test_products_in_32_bits(red, transpose, m, dtype):
+    g, out = gen(5), 264
+    x = positive(g, dtype, m, red, red)
+    w = positive(g, dtype, *((red, out) if transpose else (out, red)), red)[None]
+    y = torch.empty(m, out, device="cuda")
+    ok(moe.moe_grouped_mm(x, offsets_of([m]), w, y, transpose=transpose))
+    check32(y, x.double() @ (w[0].double() if transpose else w[0].double().T), red)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("m", [400, 3001, 2 ** 20])
+def test_weight_gradients_in_32_bits(m, dtype):
+    g, n, k = gen(6), 72, 40
+    dy, x = positive(g, dtype, m, n, m), positive(g, dtype, m, k, m)
+    dw = torch.empty(1, n, k, device="cuda")
+    ok(moe.moe_grouped_wgrad(dy, x, offsets_of([m]), dw))
+    check32(dw[0], dy.double().T @ x.double(), m)

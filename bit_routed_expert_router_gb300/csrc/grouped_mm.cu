@@ -76,7 +76,6 @@ struct BigCfg {
 };
 
 constexpr int kLists = 4;
-constexpr int kEarlyRows = 65536;   // adapters' rows up to which the down half is done in milliseconds
 struct AdaptSmem {
   int id[kLists][256];     // adapter of each column of a tile, -1 for none (tiles in turn)
   int list[kLists][256];   // its distinct adapters, in order
@@ -541,8 +540,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
   }
   if (warp == 1) tmem_alloc<true>(&S.tmem, 2 * kAccCols);
   // with adapters only the u rows come from the previous kernel, and the products of W start on the SMs it leaves (4096
-  // rows 68 -> 61 us) unless it may take so long that the bounded waits for u would run out
-  if (kEpi != GM_ADAPT || p.m > kEarlyRows) pdl_wait();
+  // rows 68 -> 61 us): when this kernel may start, all CTAs of the previous one run, so the bounded waits for u last as long
+  // as one of those at most (64 passes of 1024 steps with the largest sizes, tens of milliseconds)
+  if (kEpi != GM_ADAPT) pdl_wait();
   pdl_trigger();
   for (int e = tid; e <= p.E; e += BigCfg<kMode, kEpi>::kThreads)
     S.off[e] = p.offsets ? clamp_off(p.offsets[e], p.m) : e * p.m;

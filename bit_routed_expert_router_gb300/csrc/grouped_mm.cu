@@ -296,7 +296,7 @@ __device__ __forceinline__ void widen8(uint64_t (&o)[4], uint4 v, int bf16) {
                 : pack_f32x2(half_lo(w[i]), half_hi(w[i]));
 }
 
-// Eight floats of u, the same address in every lane.
+// Eight floats of u.
 __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
   asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];" : "=l"(o[0]), "=l"(o[1]), "=l"(o[2]), "=l"(o[3]) : "l"(u));
 }
@@ -311,8 +311,8 @@ __device__ __forceinline__ void load_u8(uint64_t (&o)[4], const float* u) {
 // range (as fp16 it lost bits below 2^-9 and everything past 65504): u is a value
 // and its remainder, good to 2^-17, and so is fp16's B, whose eleven bits they
 // hold; the product of the two remainders, 2^-15 at most, is left out.  The split
-// and the third product take fp16 calls from 89 to 107 us (4096 rows in runs of 41,
-// rank 64; bf16 89) and from 57 to 58 (one adapter).
+// and the third product take fp16 calls from 89 to 104 us (4096 rows in runs of 41,
+// rank 64; bf16 86) and from 57 to 58 (one adapter).
 // One warp of each CTA lists the tiles' adapters; four write u's steps and look
 // through the B rows that TMA loaded for them: a value that is not finite would
 // reach every column (0 times infinity), so it is cleared and the tile marked,
@@ -372,8 +372,11 @@ __device__ __forceinline__ uint32_t upper_halves(float a, float b) {
 }
 
 // Eight values of u as bf16, and what that leaves.  `odd` turns NaN if a remainder is (that of an infinity).
-__device__ __forceinline__ void split_u(const float4& a, const float4& b, uint4& hi, uint4& lo, float& odd) {
-  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+__device__ __forceinline__ void split_u(const uint64_t (&u)[4], uint4& hi, uint4& lo, float& odd) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[2 * i] = __uint_as_float(static_cast<uint32_t>(u[i])), v[2 * i + 1] = __uint_as_float(static_cast<uint32_t>(u[i] >> 32));
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -949,10 +952,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
           const bool in = mine >= 0 && 64 * block + 8 * w < p.rank;
-          const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-          const float4 u0 = in ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * w) : zero;
-          const float4 u1 = in ? __ldcg(reinterpret_cast<const float4*>(src) + 2 * w + 1) : zero;
-          split_u(u0, u1, hi[w], lo[w], odd);
+          // a sector of 32 bytes a load: as two of 16 it was fetched twice (70,000 rows 1,020 us against 970)
+          uint64_t v[4] = {0, 0, 0, 0};
+          if (in) load_u8(v, src + 8 * w);
+          split_u(v, hi[w], lo[w], odd);
         }
         if (odd != 0.f)   // NaN
 #pragma unroll

@@ -45,8 +45,8 @@ namespace {
 using namespace tc16;
 
 // CTAs that gave up on this device, and the number of the last one's grid (plus
-// one; the replays of a graph's node share theirs).  The count is never
-// taken back: each stream that asks compares it with what it was told before.
+// one; the replays of a graph's node share theirs).  The count is never taken
+// back: each stream that asks compares it with what it was told before.
 __device__ uint32_t g_gave_up;
 __device__ unsigned long long g_gave_up_grid;
 
@@ -622,7 +622,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           }
         }
       };
-      while (!S.waits.abort && it < static_cast<uint32_t>(p.stall) && next_tile<kTake, false>(S, walk, rank == 0 ? 0 : lead_take, ask) &&
+      const uint32_t stall = p.stall;
+      while (!S.waits.abort && it < stall && next_tile<kTake, false>(S, walk, rank == 0 ? 0 : lead_take, ask) &&
              tile_at<kMode, kFeat>(S, p, walk.t, e, T)) {
         const int half = T.n / 2;
         const uint32_t bytes = kHalf + half * 128;
@@ -632,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
           if (!wait_bar(&S.ad.list_full[lb], ((n_tile - 1) / kLists) & 1, &S.waits)) break;
           pairs = S.ad.n_list[lb] * ((p.rank + 63) / 64);
         }
-        for (int ks = 0; it < static_cast<uint32_t>(p.stall) && (ks < T.steps || pair < pairs); ++ks) {
+        for (int ks = 0; it < stall && (ks < T.steps || pair < pairs); ++ks) {
           if constexpr (kEpi == GM_ADAPT) {
             for (; pair < pairs && pair_at(pair, pairs, T.steps) <= ks; ++pair, it += 2) {
               // one load of B for both stages; the writing warps go on when it has landed and both are free

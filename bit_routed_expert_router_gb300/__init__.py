@@ -45,6 +45,10 @@ class MoeExpertWeights(C.Structure):
                 ("up_sb", C.c_void_p), ("down_q", C.c_void_p), ("down_sb", C.c_void_p)]
 
 
+class MoeFfnWeights(C.Structure):
+    _fields_ = [("gate_up", C.c_void_p), ("down", C.c_void_p), ("gate_up_scale", C.c_void_p), ("down_scale", C.c_void_p)]
+
+
 class MoeTraceRec(C.Structure):
     _fields_ = [("token", C.c_int32), ("layer", C.c_int32), ("k_pos", C.c_int32), ("expert", C.c_int32),
                 ("hit", C.c_int32), ("slot", C.c_int32), ("evicted", C.c_int32)]
@@ -113,6 +117,19 @@ _SIGS = {
     "moe_lora_mm": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_int, C.c_int, C.c_void_p,
                               C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p,
                               C.c_uint64, C.c_void_p]),
+    "moe_rmsnorm": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_float,
+                              C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
+                              C.c_void_p, C.c_void_p]),
+    "moe_rmsnorm_grad": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64, C.c_void_p, C.c_int64,
+                                   C.c_void_p, C.c_float, C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                   C.c_uint64, C.c_void_p]),
+    "moe_grouped_mm8": (C.c_int, [C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_void_p, C.c_void_p,
+                                  C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p]),
+    "moe_grouped_geglu8": (C.c_int, [C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_void_p, C.c_int, C.c_void_p,
+                                     C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p]),
+    "moe_token_layer": (C.c_int, [C.c_int, C.c_int, C.c_void_p, C.c_int64, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int,
+                                  C.POINTER(MoeFfnWeights), C.POINTER(MoeFfnWeights), C.c_int, C.c_int, C.c_int, C.c_void_p,
+                                  C.c_int64, C.c_int, C.c_void_p, C.c_uint64, C.c_void_p]),
     "moe_grouped_sync": (C.c_int, [C.c_void_p]),
     "moe_profile": (C.c_int, [C.c_void_p, C.c_int]),
     "moe_get_profile": (C.c_int, [C.c_void_p, C.POINTER(MoeKernelTime), C.c_int]),
@@ -313,15 +330,16 @@ def moe_route_noalloc(cfg: MoeConfig, router_w, h, B: int, logit_bias, ids, gate
 # dimension that is not contiguous) return MOE_EINVAL like the library's own checks.  The call runs on the tensors'
 # device, on `stream` or that device's current stream.
 
-_DTYPE = _INT32 = _FLOAT32 = _current_device = _raw_stream = _fn = None   # from torch and the library, on the first call
+_DTYPE = _INT32 = _FLOAT32 = _E4M3 = _current_device = _raw_stream = _fn = None   # from torch and the library, on the first call
 
 
 def _from_torch() -> None:
-    global _DTYPE, _INT32, _FLOAT32, _current_device, _raw_stream, _fn
+    global _DTYPE, _INT32, _FLOAT32, _E4M3, _current_device, _raw_stream, _fn
     import torch
     _fn = lib()
     _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
     _INT32, _FLOAT32, _current_device = torch.int32, torch.float32, torch.cuda.current_device
+    _E4M3 = torch.float8_e4m3fn
     # the stream's handle without the 3 us of a torch.cuda.Stream object: these calls start kernels of 10 us
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -334,6 +352,10 @@ def _from_torch() -> None:
 def _whole(t, shape, dtype, dev: int) -> bool:
     """A contiguous tensor of this shape and type on device `dev`."""
     return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _call(fn, dev: int, stream, *args) -> int:
@@ -465,6 +487,159 @@ def moe_lora_mm(x, w, ids, a, b, scale, y, workspace, stream=None) -> int:
 
 def moe_grouped_sync(stream=None) -> int:
     return lib().moe_grouped_sync(_stream(stream))
+
+
+# ---------------------------------------------------------------- norm and 8-bit operators (no context)
+#
+# As above; 8-bit tensors are torch.float8_e4m3fn, their scales contiguous float32.
+
+
+def moe_rmsnorm(h, y=None, y8=None, scale=None, delta=None, h_out=None, weight=None, eps: float = 1e-6, stream=None) -> int:
+    """h_out = h + delta, y = RMS norm of it times weight, in h's type; y8, scale: the same in e4m3 with a scale for each
+    128 values ([m, ceil(d / 128)]).  delta comes with h_out; y or y8 (with scale), or both."""
+    if _DTYPE is None:
+        _from_torch()
+    sh = h.shape
+    if len(sh) != 2:
+        return MOE_EINVAL
+    (m, d), dev, dt = sh, h.get_device(), h.dtype
+    lds = []
+    for t, of in ((h, dt), (delta, None), (h_out, dt), (y, dt), (y8, _E4M3)):
+        if t is None:
+            lds.append(0)
+            continue
+        if t.shape != sh or (of is not None and t.dtype is not of) or t.get_device() != dev:
+            return MOE_EINVAL
+        st = t.stride()
+        if st[1] != 1:
+            return MOE_EINVAL
+        # a row's values are contiguous; the row stride of a single row says nothing
+        lds.append(st[0] if m > 1 else d)
+    if (delta is None) != (h_out is None) or (y8 is None) != (scale is None):
+        return MOE_EINVAL
+    if weight is not None and not _whole(weight, (d,), dt, dev):
+        return MOE_EINVAL
+    if scale is not None and not _whole(scale, (m, (d + 127) // 128), _FLOAT32, dev):
+        return MOE_EINVAL
+    return _call(_fn.moe_rmsnorm, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), lds[0], _at(delta), lds[1],
+                 0 if delta is None else _DTYPE.get(delta.dtype, -1), _at(weight), eps, m, d, _at(h_out), lds[2], _at(y),
+                 lds[3], _at(y8), lds[4], _at(scale))
+
+
+def moe_rmsnorm_grad(h, dy, dh, dres=None, weight=None, dweight=None, workspace=None, eps: float = 1e-6, stream=None) -> int:
+    """dh (dres added to it) and dweight (float32 [d]) of y = RMS norm of h times weight for the gradient dy; workspace: a
+    tensor of at least 4 * d * min(m, 512) bytes, with dweight."""
+    if _DTYPE is None:
+        _from_torch()
+    sh = h.shape
+    if len(sh) != 2:
+        return MOE_EINVAL
+    (m, d), dev, dt = sh, h.get_device(), h.dtype
+    lds = []
+    for t in (h, dy, dh, dres):
+        if t is None:
+            lds.append(0)
+            continue
+        if t.shape != sh or t.dtype is not dt or t.get_device() != dev:
+            return MOE_EINVAL
+        st = t.stride()
+        if st[1] != 1:
+            return MOE_EINVAL
+        lds.append(st[0] if m > 1 else d)
+    if weight is not None and not _whole(weight, (d,), dt, dev):
+        return MOE_EINVAL
+    if dweight is not None and not _whole(dweight, (d,), _FLOAT32, dev):
+        return MOE_EINVAL
+    if workspace is not None and not (workspace.is_contiguous() and workspace.get_device() == dev):
+        return MOE_EINVAL
+    return _call(_fn.moe_rmsnorm_grad, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), lds[0], dy.data_ptr(), lds[1],
+                 _at(dres), lds[3], _at(weight), eps, m, d, dh.data_ptr(), lds[2], _at(dweight), _at(workspace),
+                 0 if workspace is None else workspace.nbytes)
+
+
+def moe_grouped_mm8(x, sx, offsets, w, sw, y, stream=None) -> int:
+    """y[r] = w[e] x[r] for the rows of each expert, x [m, k] and w [E, n, k] in e4m3 with the scales sx [m, ceil(k / 128)]
+    and sw [E, ceil(n / 128), ceil(k / 128)]; y in 16 or 32 bits."""
+    if _DTYPE is None:
+        _from_torch()
+    sh, sm = w.shape, x.shape
+    if len(sh) != 3 or len(sm) != 2:
+        return MOE_EINVAL
+    (E, n, k), m, dev = sh, sm[0], w.get_device()
+    if sm[1] != k or y.shape != (m, n):
+        return MOE_EINVAL
+    tx, ty, kb = x.stride(), y.stride(), (k + 127) // 128
+    if not (tx[1] == 1 and ty[1] == 1 and x.dtype is _E4M3 and x.get_device() == dev and y.get_device() == dev and
+            _whole(w, sh, _E4M3, dev) and _whole(sx, (m, kb), _FLOAT32, dev) and
+            _whole(sw, (E, (n + 127) // 128, kb), _FLOAT32, dev) and _whole(offsets, (E + 1,), _INT32, dev)):
+        return MOE_EINVAL
+    return _call(_fn.moe_grouped_mm8, dev, stream, x.data_ptr(), tx[0] if m > 1 else k, sx.data_ptr(), m,
+                 offsets.data_ptr(), E, w.data_ptr(), sw.data_ptr(), n, k, y.data_ptr(), ty[0] if m > 1 else n,
+                 _DTYPE.get(y.dtype, -1))
+
+
+def moe_grouped_geglu8(x, sx, offsets, w, sw, a, sa, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
+    """a[r] = GELU(g) u, [g, u] = w[e] x[r] in e4m3 as in moe_grouped_mm8, w [E, 2 f, k]; a [m, f] in e4m3 with the scales
+    sa [m, ceil(f / 128)]."""
+    if _DTYPE is None:
+        _from_torch()
+    sh, sm = w.shape, x.shape
+    if len(sh) != 3 or len(sm) != 2 or sh[1] % 2:
+        return MOE_EINVAL
+    (E, n, k), m, dev = sh, sm[0], w.get_device()
+    f = n // 2
+    if sm[1] != k or a.shape != (m, f):
+        return MOE_EINVAL
+    tx, ta, kb = x.stride(), a.stride(), (k + 127) // 128
+    if not (tx[1] == 1 and ta[1] == 1 and x.dtype is _E4M3 and a.dtype is _E4M3 and x.get_device() == dev and
+            a.get_device() == dev and _whole(w, sh, _E4M3, dev) and _whole(sx, (m, kb), _FLOAT32, dev) and
+            _whole(sw, (E, (n + 127) // 128, kb), _FLOAT32, dev) and _whole(sa, (m, (f + 127) // 128), _FLOAT32, dev) and
+            _whole(offsets, (E + 1,), _INT32, dev)):
+        return MOE_EINVAL
+    return _call(_fn.moe_grouped_geglu8, dev, stream, gelu_variant, x.data_ptr(), tx[0] if m > 1 else k, sx.data_ptr(), m,
+                 offsets.data_ptr(), E, w.data_ptr(), sw.data_ptr(), f, k, a.data_ptr(), ta[0] if m > 1 else f,
+                 sa.data_ptr())
+
+
+def _ffn(weights, lead, d: int, dt, dev: int):
+    """(f, MoeFfnWeights) of (gate_up [*lead, 2 f, d], down [*lead, d, f], and for e4m3 their scales), or None."""
+    gate_up, down, *scales = weights
+    f = down.shape[-1]
+    eight = len(scales) == 2 and scales[0] is not None
+    if eight:
+        dt, db, fb = _E4M3, (d + 127) // 128, (f + 127) // 128
+        if scales[1] is None or not (_whole(scales[0], (*lead, (2 * f + 127) // 128, db), _FLOAT32, dev) and
+                                     _whole(scales[1], (*lead, db, fb), _FLOAT32, dev)):
+            return None
+    elif any(s is not None for s in scales):
+        return None
+    if not (_whole(gate_up, (*lead, 2 * f, d), dt, dev) and _whole(down, (*lead, d, f), dt, dev)):
+        return None
+    return f, MoeFfnWeights(gate_up.data_ptr(), down.data_ptr(), scales[0].data_ptr() if eight else None,
+                            scales[1].data_ptr() if eight else None)
+
+
+def moe_token_layer(x, ids, gates, routed, y, workspace, shared=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
+    """y[t] = sum_j gates[t, j] FFN(routed[ids[t, j]], x[t]) + FFN(shared, x[t]) for up to 32 tokens.  routed: (gate_up
+    [E, 2 f, d], down [E, d, f]) of x's type, or with their scales (gate_up, down, gate_up_scale, down_scale) in e4m3;
+    shared: the same without E, or None; workspace: a tensor of at least 2 * t * (top_k * f + f_shared) bytes."""
+    if _DTYPE is None:
+        _from_torch()
+    sx, si = x.shape, ids.shape
+    if len(sx) != 2 or len(si) != 2 or routed[0].dim() != 3:
+        return MOE_EINVAL
+    (t, d), k, dev, dt, E = sx, si[1], x.get_device(), x.dtype, routed[0].shape[0]
+    tx, ty = x.stride(), y.stride()
+    if not (si[0] == t and y.shape == sx and tx[1] == 1 and ty[1] == 1 and y.get_device() == dev and
+            _whole(ids, (t, k), _INT32, dev) and _whole(gates, (t, k), _FLOAT32, dev) and workspace.is_contiguous() and
+            workspace.get_device() == dev):
+        return MOE_EINVAL
+    r, s = _ffn(routed, (E,), d, dt, dev), (0, None) if shared is None else _ffn(shared, (), d, dt, dev)
+    if r is None or s is None:
+        return MOE_EINVAL
+    return _call(_fn.moe_token_layer, dev, stream, _DTYPE.get(dt, -1), gelu_variant, x.data_ptr(), tx[0] if t > 1 else d, t,
+                 ids.data_ptr(), gates.data_ptr(), k, E, C.byref(r[1]), None if s[1] is None else C.byref(s[1]), d, r[0], s[0],
+                 y.data_ptr(), ty[0] if t > 1 else d, _DTYPE.get(y.dtype, -1), workspace.data_ptr(), workspace.nbytes)
 
 
 def moe_profile(ctx, enable: bool) -> int:

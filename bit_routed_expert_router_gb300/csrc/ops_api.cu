@@ -1,23 +1,16 @@
 // C entry points of the 16-bit operators: argument checks, then the launches
 // (grouped_mm.cu, gated_lora.cu).  No context, no allocation, no state but the
 // count of waits that ran out, which moe_grouped_sync reads.
-#include <cstdint>
-
 #include "grouped.h"
 #include "internal.h"
-#include "moe.h"
+#include "op_checks.h"
 
 namespace {
 
-constexpr int kMaxExperts = 1024, kMaxSide = 65536, kMaxRows = 1 << 24, kMaxRank = 128;
+using namespace moe;
+
+constexpr int kMaxRank = 128;
 constexpr int kManyRows = 256;   // adapters: from here on their down half runs on tcgen05
-
-bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
-
-// m rows of values that the TMA engine or 16-byte accesses can take (no rows need no memory)
-bool rows_ok(const void* p, int m, int64_t ld, int64_t cols) {
-  return (p || m == 0) && aligned(p, 16) && ld >= cols && ld % 8 == 0 && ld < (int64_t{1} << 36);
-}
 
 bool side_ok(int v) { return v >= 8 && v <= kMaxSide && v % 8 == 0; }
 
@@ -25,10 +18,6 @@ bool groups_ok(int dtype, const int32_t* offsets, int n_experts, int m) {
   return (dtype == MOE_BF16 || dtype == MOE_F16) && offsets && aligned(offsets, 4) && n_experts >= 1 &&
          n_experts <= kMaxExperts && m >= 0 && m <= kMaxRows;
 }
-
-bool gelu_ok(int v) { return v == MOE_GELU_ERF || v == MOE_GELU_TANH; }
-
-moe_status status(bool ok) { return ok ? MOE_OK : MOE_ECUDA; }
 
 }  // namespace
 

@@ -508,6 +508,108 @@ moe_status moe_lora_mm(int dtype, const void *x, int64_t ldx, int t, const void 
  * the stream is being captured. */
 moe_status moe_grouped_sync(void *stream);
 
+/* ---- norm, 8-bit operators over rows grouped by expert, and the layer for a few tokens ----
+ *
+ * Beside the 16-bit operators, under the same rules: no context, the caller's
+ * buffers on the current device, nothing allocated, no synchronisation (the
+ * calls can be captured), results that do not depend on timing, MOE_EINVAL
+ * before anything is enqueued, MOE_ECUDA for a failed CUDA call.
+ *
+ * 8-bit values are e4m3 (no infinities, largest 448) with an fp32 scale for each
+ * block: a value stands for e4m3 * scale.  Rows [m][ld] of e4m3, ld a multiple of
+ * 16, 16-byte aligned, have scales [m][ceil(d / 128)], contiguous: one for each
+ * 128 values, the last for what is left.  Where the library writes such rows,
+ *   scale = max(max |v|, 2^-100) / 448,   value = e4m3(v / scale),
+ * computed in fp32 and rounded to the nearest, ties to even (v / scale as v times
+ * 448 / max |v|, which can pass a tie that lies within 2^-22 of it).  Non-finite
+ * values stay in their block: one with a NaN gets a NaN scale and NaN values, one
+ * with an infinity an infinite scale, NaN where v is infinite and 0 elsewhere. */
+
+/* r = h + delta, rounded to dtype and stored in h_out; then from the stored r
+ *   v = r / sqrt(mean(r^2) + eps) * weight
+ * rounded to dtype in y, or to e4m3 in y8 with its scales, or both (one of them at
+ * least).  The step between two layers of moe_decode_step, with a weight.
+ *   dtype       MOE_BF16 or MOE_F16: of h, weight, h_out and y
+ *   delta       [m][ldd] of delta_dtype (dtype or MOE_F32), or NULL: r = h, and
+ *               h_out is NULL
+ *   weight      [d], 16-byte aligned, or NULL (ones)
+ *   m, d        0 <= m <= 2^24, d a multiple of 8 from 8 to 16384
+ *   rows        16-byte aligned, strides multiples of 16 bytes; y8: of 8 (the
+ *               products below want 16)
+ * h_out may be h, and y may be h or delta of its type; nothing else may overlap.
+ * The mean is summed in fp32: a row whose squares pass fp32's range gives 0 and,
+ * for an infinity, NaN; a row of zeros with eps = 0 gives NaN. */
+moe_status moe_rmsnorm(int dtype, const void *h, int64_t ldh, const void *delta, int64_t ldd, int delta_dtype,
+                       const void *weight, float eps, int m, int d, void *h_out, int64_t ldo, void *y, int64_t ldy,
+                       void *y8, int64_t ldy8, float *scale, void *stream);
+
+/* The gradients of y: with x = h / sqrt(mean(h^2) + eps) (h: the stored r), for
+ * the gradient dy of y
+ *   dh = dres + (dy weight - x mean(dy weight x)) / sqrt(mean(h^2) + eps)
+ *   dweight = sum over the rows of dy x         (fp32 [d], 16-byte aligned, or NULL)
+ * dres is the gradient that reaches r past the norm, or NULL; dh is the gradient
+ * of h and of delta.  dh may be h, dy or dres.  All rows are of dtype.
+ * workspace (with dweight): at least 4 d min(m, 512) bytes, 16-byte aligned,
+ * contents undefined before and after; calls that may run at the same time need
+ * one each.  dweight needs a weight. */
+moe_status moe_rmsnorm_grad(int dtype, const void *h, int64_t ldh, const void *dy, int64_t lddy, const void *dres,
+                            int64_t lddres, const void *weight, float eps, int m, int d, void *dh, int64_t lddh,
+                            float *dweight, void *workspace, uint64_t workspace_bytes, void *stream);
+
+/* y[r] = W[e] x[r] for the rows r of each expert e, x [m][k] and W [n_experts][n][k]
+ * in e4m3: sx [m][ceil(k / 128)] and sw [n_experts][ceil(n / 128)][ceil(k / 128)] are
+ * the scales (fp32) of 128 values of a row and of blocks of 128 x 128 weights.
+ *   y[r][n] = sum over the blocks b of sx[r][b] sw[e][n / 128][b] sum over k in b of x[r][k] W[e][n][k]
+ * offsets as in moe_grouped_mm (one group: offsets {0, m}); n a multiple of 8 from 8
+ * to 65536, k a multiple of 16 from 16 to 65536, weights contiguous and 16-byte
+ * aligned; y [m][ldy] of out_dtype (MOE_BF16, MOE_F16, MOE_F32).  Rows before
+ * offsets[0] and from offsets[n_experts] on are not written.  Each block's products
+ * are summed by themselves, the blocks in fp32 with rounding.  No output may overlap
+ * an input.  moe_grouped_sync reports a bounded wait that ran out. */
+moe_status moe_grouped_mm8(const void *x, int64_t ldx, const float *sx, int m, const int32_t *offsets, int n_experts,
+                           const void *w, const float *sw, int n, int k, void *y, int64_t ldy, int out_dtype,
+                           void *stream);
+
+/* a[r] = GELU(g) u with [g, u] = W[e] x[r] as in moe_grouped_mm8, W [n_experts][2 f][k]
+ * (sw [n_experts][ceil(2 f / 128)][ceil(k / 128)]), written in e4m3 with its scales sa
+ * [m][ceil(f / 128)]: the rows that the down product reads.  f a multiple of 16 up
+ * to 32768.  a is computed from the fp32 g and u. */
+moe_status moe_grouped_geglu8(int gelu_variant, const void *x, int64_t ldx, const float *sx, int m,
+                              const int32_t *offsets, int n_experts, const void *w, const float *sw, int f, int k,
+                              void *a, int64_t lda, float *sa, void *stream);
+
+/* The weights of a feed-forward network: gate_up [2 f][d] and down [d][f],
+ * contiguous and 16-byte aligned (the routed ones: of each expert, one after the
+ * other).  Without scales they are of the call's dtype; with both scales (for
+ * blocks of 128 x 128 of each expert's matrices, as in moe_grouped_mm8) e4m3. */
+typedef struct {
+    const void *gate_up;
+    const void *down;
+    const float *gate_up_scale;
+    const float *down_scale;
+} moe_ffn_weights;
+
+/* A routed layer and its shared expert for a few tokens, after the router:
+ *   y[t] = sum over j of gates[t][j] FFN(routed[ids[t][j]], x[t]) + FFN(shared, x[t])
+ *   FFN(w, x) = w.down (GELU(g) u),  [g, u] = w.gate_up x
+ *   x, y        [t][ldx], [t][ldy] of dtype (y: or MOE_F32), 0 <= t <= 32
+ *   ids, gates  int32 and fp32 [t][top_k], as moe_route_noalloc leaves them; 1 <= top_k
+ *               <= 32.  An id outside [0, n_experts) adds nothing; an expert that a
+ *               token names twice counts twice.
+ *   shared      NULL (f_shared = 0): no shared expert; else of the same type as
+ *               routed
+ *   d, f, f_shared   multiples of 16; d up to 65536, f and f_shared up to 32768
+ *   workspace   at least 2 t (top_k f + f_shared) bytes, 16-byte aligned, contents
+ *               undefined before and after; calls that may run at the same time need
+ *               one each
+ * Sums are fp32; gates * GELU(g) u is rounded to dtype once before the down
+ * product, y once at the end.  Non-finite weights of an expert reach the tokens that
+ * name it only. */
+moe_status moe_token_layer(int dtype, int gelu_variant, const void *x, int64_t ldx, int t, const int32_t *ids,
+                           const float *gates, int top_k, int n_experts, const moe_ffn_weights *routed,
+                           const moe_ffn_weights *shared, int d, int f, int f_shared, void *y, int64_t ldy,
+                           int out_dtype, void *workspace, uint64_t workspace_bytes, void *stream);
+
 /* Per-kernel timing.  While enabled, decode and prefill calls launch their
  * kernels one by one (no graph replay), record a CUDA event pair around every
  * launch on the call's stream, and synchronise that stream before returning

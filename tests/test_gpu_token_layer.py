@@ -1,0 +1,195 @@
+"""The layer for a few tokens against the formula in 64 bits."""
+
+import pytest
+import torch
+
+import bit_routed_expert_router_gb300 as moe
+from ops8_reference import BF16, E4M3, F16, F32, blocks, gelu, gen, rand8, rand_scale, wide_weights
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(g, dtype, eight, lead, d, f):
+    if not eight:
+        r = lambda *s: (torch.randn(*s, generator=g, device="cuda") * s[-1] ** -0.5).to(dtype)  # noqa: E731
+        return r(*lead, 2 * f, d), r(*lead, d, f)
+    gu, down = rand8(g, *lead, 2 * f, d), rand8(g, *lead, d, f)
+    # values of about 60 times 2^-10: weights of about the size that the fan-in wants
+    su, sd = rand_scale(g, *lead, blocks(2 * f), blocks(d)) / d ** 0.5, rand_scale(g, *lead, blocks(d), blocks(f)) / f ** 0.5
+    return gu, down, 8 * su, 8 * sd
+
+
+def wide(w):
+    return [t.double() for t in w[:2]] if len(w) == 2 else [wide_weights(w[0], w[2]), wide_weights(w[1], w[3])]
+
+
+def case(t, k, E, d, f, fs, dtype=BF16, eight=False, seed=0):
+    g = gen(seed + 1000 * t + d)
+    x = torch.randn(t, d, generator=g, device="cuda").to(dtype)
+    top = torch.randn(t, E, generator=g, device="cuda").topk(k)
+    ids, gates = top.indices.int(), torch.softmax(top.values, 1)
+    return x, ids, gates, weights(g, dtype, eight, (E,), d, f), weights(g, dtype, eight, (), d, fs) if fs else None
+
+
+def call(x, ids, gates, routed, shared, variant=moe.MOE_GELU_ERF, out=None, y=None, stream=None):
+    f, fs = routed[1].shape[-1], shared[1].shape[-1] if shared else 0
+    ws = torch.empty(2 * x.shape[0] * (ids.shape[1] * f + fs), dtype=torch.uint8, device="cuda")
+    y = torch.full(x.shape, 7.0, dtype=out or x.dtype, device="cuda") if y is None else y
+    moe.check(moe.moe_token_layer(x, ids, gates, routed, y, ws, shared=shared, gelu_variant=variant, stream=stream))
+    return y
+
+
+def check(y, x, ids, gates, routed, shared, variant):
+    """Error: the rounding of each a to 16 bits and the fp32 sums before it, carried through the down product's magnitudes,
+    then the output's rounding."""
+    half = torch.finfo(x.dtype).eps / 2
+    tiny = torch.finfo(x.dtype).smallest_normal * half
+    d = x.shape[1]
+    want, bound = torch.zeros(x.shape, dtype=torch.float64, device="cuda"), torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+    E = routed[0].shape[0]
+
+    def add(t, gate, gu, down):
+        f = down.shape[1]
+        xt = x[t].double()
+        h, size = gu @ xt, gu.abs() @ xt.abs()
+        # the tensor cores truncate, the partial sums round: at most 2^-23 of the magnitudes a product, in fp32
+        e32 = (d + 64) * 2.0 ** -23
+        g, u, eg, eu = h[:f], h[f:], e32 * size[:f], e32 * size[f:]
+        a = gate * gelu(g, variant) * u
+        ea = abs(gate) * (1.13 * eg * (u.abs() + eu) + gelu(g, variant).abs() * eu) + 2.0 ** -18 * a.abs()
+        ea = ea + half * (a.abs() + ea) + tiny
+        want[t] += down @ a
+        bound[t] += down.abs() @ (ea + (f + 64) * 2.0 ** -23 * (a.abs() + ea))
+
+    rw, sw = wide(routed), wide(shared) if shared else None
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if 0 <= e < E:
+                add(t, float(gates[t, j]), rw[0][e], rw[1][e])
+        if shared:
+            add(t, 1.0, *sw)
+    # the sums over the experts take a rounding for each of them
+    bound += (ids.shape[1] + 2) * 2.0 ** -23 * (want.abs() + bound)
+    if y.dtype != F32:
+        out = torch.finfo(y.dtype).eps / 2
+        bound += out * (want.abs() + bound) + torch.finfo(y.dtype).smallest_normal * out
+    err = (y.double() - want).abs()
+    assert torch.all(err <= bound), float((err / bound).max())
+    # and as a whole: independent roundings do not add up as their bound does
+    assert (y.double() - want).norm() <= 4 * half * want.norm()
+
+
+@pytest.mark.parametrize("t,k,E,d,f,fs", [(1, 1, 1, 16, 16, 0), (1, 2, 8, 256, 128, 128), (3, 2, 5, 144, 176, 48), (7, 8, 16, 272, 80, 0),
+                                          (8, 4, 12, 528, 144, 272), (9, 3, 9, 400, 304, 16), (17, 5, 40, 656, 96, 128),
+                                          (32, 8, 32, 1040, 208, 512), (31, 32, 64, 128, 64, 64), (1, 8, 128, 2816, 704, 2816)])
+@pytest.mark.parametrize("dtype,eight,variant", [(BF16, False, moe.MOE_GELU_ERF), (F16, False, moe.MOE_GELU_TANH),
+                                                 (BF16, True, moe.MOE_GELU_TANH), (F16, True, moe.MOE_GELU_ERF)])
+def test_layer(t, k, E, d, f, fs, dtype, eight, variant):
+    args = case(t, k, E, d, f, fs, dtype, eight)
+    for out in (dtype, F32):
+        check(call(*args, variant=variant, out=out), *args, variant)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_every_token_at_one_expert_and_repeated_ids(eight):
+    x, ids, gates, routed, shared = case(32, 4, 6, 320, 112, 64, BF16, eight)
+    ids[:] = 5
+    gates = torch.rand(32, 4, generator=gen(3), device="cuda")
+    check(call(x, ids, gates, routed, shared), x, ids, gates, routed, shared, moe.MOE_GELU_ERF)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_ids_outside_add_nothing(eight):
+    x, ids, gates, routed, shared = case(5, 3, 6, 320, 112, 64, F16, eight)
+    ids[0] = -1
+    ids[1, 1], ids[2, 0], ids[3, 2] = 6, 1 << 30, -(1 << 31)
+    check(call(x, ids, gates, routed, shared), x, ids, gates, routed, shared, moe.MOE_GELU_ERF)
+    ids[:] = -1
+    check(call(x, ids, gates, routed, shared), x, ids, gates, routed, shared, moe.MOE_GELU_ERF)
+    assert torch.all(call(x, ids, gates, routed, None) == 0)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("t", [4, 20])
+def test_non_finite_weights_reach_their_own_tokens(eight, t):
+    x, ids, gates, routed, shared = case(t, 2, 8, 320, 112, 64, BF16, eight)
+    ids[:, 0], ids[:, 1] = 1, 2
+    ids[1, 0], ids[3, 1] = 7, 7
+    clean = call(x, ids, gates, routed, shared)
+    for which, spot in ((0, (7, 5, 9)), (1, (7, 300, 100))):
+        bad = [w.clone() for w in routed]
+        if eight:
+            bad[which].view(torch.uint8)[spot] = 0x7F   # NaN
+        else:
+            bad[which][spot] = float("inf")
+        y = call(x, ids, gates, tuple(bad), shared)
+        hit = torch.zeros(t, dtype=torch.bool, device="cuda")
+        hit[1] = hit[3] = True
+        assert torch.equal(y[~hit], clean[~hit])
+        if which == 0:      # a feature of a: every output that weighs it
+            assert torch.all(~torch.isfinite(y[hit]))
+        else:
+            assert torch.all(~torch.isfinite(y[hit, 300]))
+            y[:, 300] = clean[:, 300]
+            assert torch.equal(y, clean)
+
+
+def test_non_finite_tokens_stay_tokens():
+    args = case(12, 3, 8, 272, 96, 80, BF16)
+    clean = call(*args)
+    x = args[0].clone()
+    x[4, 7] = float("nan")
+    y = call(x, *args[1:])
+    assert torch.all(torch.isnan(y[4]))
+    y[4] = clean[4]
+    assert torch.equal(y, clean)
+
+
+def test_strided_rows_leave_the_rest():
+    x, ids, gates, routed, shared = case(6, 2, 4, 256, 64, 64, BF16)
+    wide_x = torch.randn(6, 512, device="cuda").to(BF16)
+    wide_x[:, 64:320] = x
+    y = torch.full((6, 400), 7.0, dtype=F32, device="cuda")
+    call(wide_x[:, 64:320], ids, gates, routed, shared, y=y[:, 8:264])
+    check(y[:, 8:264], x, ids, gates, routed, shared, moe.MOE_GELU_ERF)
+    assert torch.all(y[:, :8] == 7) and torch.all(y[:, 264:] == 7)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_in_a_graph_with_new_tokens(eight):
+    x, ids, gates, routed, shared = case(3, 4, 16, 512, 256, 384, F16, eight)
+    y, ws = torch.empty_like(x), torch.empty(2 * 3 * (4 * 256 + 384), dtype=torch.uint8, device="cuda")
+
+    def step():
+        moe.check(moe.moe_token_layer(x, ids, gates, routed, y, ws, shared=shared))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+        step()
+    for seed in (1, 2):
+        other = case(3, 4, 16, 512, 256, 384, F16, False, seed=seed)
+        x.copy_(other[0]), ids.copy_(other[1]), gates.copy_(other[2])
+        graph.replay()
+        got = y.clone()
+        step()
+        assert torch.equal(got, y)
+        check(y, x, ids, gates, routed, shared, moe.MOE_GELU_ERF)
+
+
+def test_two_streams_at_once():
+    """A workspace each."""
+    args = [case(5, 4, 16, 512, 256, 384, BF16, seed=s) for s in (1, 2)]
+    streams = [torch.cuda.Stream() for _ in args]
+    torch.cuda.synchronize()
+    ys = [torch.empty_like(a[0]) for a in args]
+    ws = [torch.empty(2 * 5 * (4 * 256 + 384), dtype=torch.uint8, device="cuda") for _ in args]
+    for _ in range(10):
+        for a, y, w, s in zip(args, ys, ws, streams):
+            moe.check(moe.moe_token_layer(*a[:4], y, w, shared=a[4], stream=s))
+    torch.cuda.synchronize()
+    for a, y in zip(args, ys):
+        check(y, *a, moe.MOE_GELU_ERF)

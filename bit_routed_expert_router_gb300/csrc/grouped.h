@@ -51,6 +51,11 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& p, c
 // about two seconds and never).
 void grouped_test_cycles(int64_t cycles);
 void grouped_test_loads(int64_t loads);
+// What they are now: of each wait, in 1024 cycles; loads.
+struct WaitLimits {
+  int cycles1024, loads;
+};
+WaitLimits wait_limits();
 // Synchronises the stream; news: a wait ran out on the current device since the
 // last call with this stream.
 bool grouped_gave_up(cudaStream_t s, bool* news);

@@ -35,20 +35,16 @@
 
 #include "gelu16.cuh"
 #include "grouped.h"
+#include "ops8.h"
 #include "tc16.cuh"
 #include "tensor_map.h"
+#include "waits.cuh"
 
 namespace moe {
 
 namespace {
 
 using namespace tc16;
-
-// CTAs that gave up on this device, and the number of the last one's grid (plus
-// one; the replays of a graph's node share theirs).  The count is never taken
-// back: each stream that asks compares it with what it was told before.
-__device__ uint32_t g_gave_up;
-__device__ unsigned long long g_gave_up_grid;
 
 constexpr int kMaxE = 1024;
 constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
@@ -98,12 +94,6 @@ struct TakeSmem {
   uint64_t full[kAnswers], empty[kAnswers];
 };
 
-// A CTA's bounded waits.
-struct Waits {
-  volatile int abort;   // 1: one ran out; 2: the launch had given up before this CTA started
-  int limit;            // of each, in 1024 cycles
-};
-
 template <int kMode, int kEpi>
 struct BigSmem {
   static constexpr int kStages = BigCfg<kMode, kEpi>::kStages;
@@ -125,47 +115,6 @@ static_assert(sizeof(BigSmem<GM_FWD, GM_PLAIN>) + 1024 <= 227 * 1024 &&
 static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
                   kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0,
               "staged rows");
-
-__device__ __forceinline__ unsigned long long this_grid() {
-  unsigned long long g;
-  asm volatile("mov.u64 %0, %%gridid;" : "=l"(g));
-  return g + 1;
-}
-
-constexpr long long kSettleCycles = 20000000;
-
-// Bounded wait that also ends when another role of the CTA gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, Waits* w) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
-    if (w->abort) return false;
-    if (clock64() - t0 > 1024LL * w->limit) {
-      w->abort = 1;
-      return false;
-    }
-  }
-}
-
-// The same by a whole warp, which then agrees on the outcome.
-__device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, Waits* w) {
-  return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, w));
-}
-
-// The end of a CTA that gave up, by all of its threads.  Copies, products and
-// arrivals may be on their way, and no barrier tells which: those of a pair's odd
-// CTA count on the even one's barriers, of which the phases that miss a share
-// stay open.  All of them take microseconds; the CTA keeps its memories for
-// another 10 ms.
-__device__ __forceinline__ void report_and_settle() {
-  if (threadIdx.x == 0) {
-    *static_cast<volatile unsigned long long*>(&g_gave_up_grid) = this_grid();
-    atomicAdd(&g_gave_up, 1u);
-  }
-  const long long t0 = clock64();
-  while (clock64() - t0 < kSettleCycles) __nanosleep(1000);
-}
 
 __device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
   if (bf16) {
@@ -1494,8 +1443,8 @@ constexpr int kDefaultLimit = static_cast<int>(kSpinLimitCycles / 1024), kNever 
 std::atomic<int> g_limit{kDefaultLimit}, g_stall{kNever};
 
 GmParams with_limits(GmParams p) {
-  p.limit = g_limit.load(std::memory_order_relaxed);
-  p.stall = g_stall.load(std::memory_order_relaxed);
+  const WaitLimits l = wait_limits();
+  p.limit = l.cycles1024, p.stall = l.loads;
   return p;
 }
 
@@ -1609,6 +1558,8 @@ bool launch_small(const GmMaps& maps, const GmParams& p, int sms, cudaStream_t s
 
 }  // namespace
 
+WaitLimits wait_limits() { return {g_limit.load(std::memory_order_relaxed), g_stall.load(std::memory_order_relaxed)}; }
+
 void grouped_test_cycles(int64_t cycles) {
   g_limit = cycles > 0 ? static_cast<int>(std::min<int64_t>(cycles / 1024, kDefaultLimit)) : kDefaultLimit;
 }
@@ -1704,11 +1655,12 @@ bool grouped_gave_up(cudaStream_t s, bool* news) try {
   static std::mutex lock;
   static std::map<std::pair<int, cudaStream_t>, uint32_t> told;   // counts by device and stream
   int dev = 0;
-  uint32_t count = 0;
+  uint32_t own = 0, layer = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaMemcpyFromSymbolAsync(&count, g_gave_up, sizeof(count), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
+      cudaMemcpyFromSymbolAsync(&own, g_gave_up, sizeof(own), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      !layer_gave_up(s, &layer) || cudaStreamSynchronize(s) != cudaSuccess)
     return false;
+  const uint32_t count = own + layer;
   {
     const std::lock_guard<std::mutex> hold(lock);
     const auto known = told.find({dev, s});

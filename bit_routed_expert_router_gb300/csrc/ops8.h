@@ -83,9 +83,12 @@ struct LayerParams {
   void* y = nullptr;
   long long ldy = 0;
   int bf16 = 0, out_f32 = 0, gelu = 0;
+  int limit = 0, stall = 0;         // set by the launches: bounded waits, in 1024 cycles; loads after which they stop
 };
 
 // false: a CUDA call failed.
 bool launch_layer(bool weights8, const LayerParams& p, cudaStream_t s);
+// Enqueues a copy of the count of its CTAs in which a wait ran out.
+bool layer_gave_up(cudaStream_t s, uint32_t* count);
 
 }  // namespace moe

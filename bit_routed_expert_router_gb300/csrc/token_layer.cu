@@ -4,13 +4,15 @@
 //   down   y[t] = sum_e Wd[e] a[e, t]                       over the experts that t names, and the shared one
 //
 // The weights of the picked experts are read once and nothing else is of any
-// size, so both kernels stream them: one warp copies chunks of 16 weight rows,
-// and of the token rows that go with them, into a ring of stages (cp.async.bulk,
-// one copy a row), eight warps share the 32- or 64-value steps of a chunk and
-// multiply them as m16n8k16 fragments, weights on the M side.  A lane reads 16
-// bytes of a row at a time: the order of k within a step is the same in both
-// operands, which is all that a product needs.  e4m3 weights become 16-bit ones
-// in registers (exact); each block of 128 is summed by itself, then scaled.
+// size, so both kernels stream them: one thread copies chunks of 16 weight rows
+// (one TMA load: a bulk copy a row took about 85 cycles each, 52 us for one token
+// where the weights take 21), and of the token rows that go with them, into a ring
+// of stages; eight warps share a chunk's steps of 64 bytes and multiply them as
+// m16n8k16 fragments, weights on the M side.  A lane reads 16 bytes of a row at a
+// time: the order of k within a step is the same in both operands, which is all
+// that a product needs, and chunks of an odd number of steps keep the rows of eight
+// lanes in different banks.  e4m3 weights become 16-bit ones in registers (exact);
+// each step's sums are scaled by themselves.
 //
 // up: a unit is 8 features: their 8 gate and 8 up rows are the 16 rows, so that a
 // lane ends with both factors of its values.  Columns: the expert's tokens.
@@ -25,6 +27,7 @@
 #include "grouped.h"
 #include "ops8.h"
 #include "quant8.cuh"
+#include "tensor_map.h"
 #include "waits.cuh"
 
 namespace moe {
@@ -32,7 +35,7 @@ namespace moe {
 namespace {
 
 constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);
-constexpr int kChunkBytes = 1024;   // of a weight row, at most
+constexpr int kStep = 64, kChunkBytes = 15 * kStep;   // of a weight row; a chunk at most
 constexpr int kMaxStages = 8;
 constexpr int kBudget = 72 * 1024;  // shared memory of a CTA: three fit an SM, so that the down kernel's ring fills early
 
@@ -45,7 +48,7 @@ struct Slot {
 // Host and device: what a launch's CTA keeps, and where.
 struct Plan {
   int kc_d, kc_f, kc_fs;      // values of a chunk: along d, f and f_shared
-  int pitch_w, pitch_x;       // bytes between staged rows: weights, tokens
+  int pitch_x;                // bytes between staged token rows
   int stage, stages;
   int slots;                  // most picked experts
   int at_red, at_mask, at_ids, at_gates, at_slots, bytes;
@@ -53,10 +56,11 @@ struct Plan {
 
 __host__ __device__ __forceinline__ int divide_up(int a, int b) { return (a + b - 1) / b; }
 
-// Equal chunks of at most kChunkBytes, whole steps each.
-int chunk_of(int k, bool w8) {
-  const int most = w8 ? kChunkBytes : kChunkBytes / 2, unit = w8 ? 128 : 32;
-  return k == 0 ? 0 : divide_up(divide_up(k, divide_up(k, most)), unit) * unit;
+// Equal chunks of an odd number of steps, in values.
+int chunk_of(int k, int size) {
+  if (k == 0) return 0;
+  const int chunks = divide_up(k * size, kChunkBytes), steps = divide_up(divide_up(k * size, chunks), kStep);
+  return (steps | 1) * kStep / size;
 }
 
 struct Chunk {
@@ -94,52 +98,102 @@ __device__ __forceinline__ uint32_t widen8(uint32_t v) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// c += 16 weight rows times up to 8 kNt token rows over this warp's steps of a staged chunk.  w: the stage; xr[j]: this
-// lane's token row of columns 8 j .., 0 for none.  With e4m3 weights the chunk is one block a warp, and c is scaled later.
+// c += 16 weight rows times up to 8 kNt token rows over one step of a staged chunk, which ends (k values) in it or behind it.
+// xr[j]: this lane's token row of columns 8 j .., 0 for none.
 template <bool kBf16, bool kW8, int kNt>
-__device__ __forceinline__ void multiply(float (&c)[kNt][4], uint32_t w, const uint32_t (&xr)[kNt], int n_cols, int pitch_w,
-                                         int k, int warp, int lane) {
+__device__ __forceinline__ void multiply(float (&c)[kNt][4], uint32_t w, int pitch_w, const uint32_t (&xr)[kNt], int n_cols, int at,
+                                         int k, int lane) {
   const int g = lane >> 2, t = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
+  const uint32_t from = w + g * pitch_w + (kW8 ? at : 2 * at) + 16 * t;
+  const uint4 w0 = lds16(from), w1 = lds16(from + 8 * pitch_w);   // zeros past k
   if (kW8) {
+    const bool in = at + 16 * t < k;
+    const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+    uint32_t a[4][4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int at = 128 * warp + 64 * h;
-      if (at >= k) return;
-      const bool in = at + 16 * t < k;
-      const uint4 w0 = in ? lds16(w + g * pitch_w + at + 16 * t) : zero, w1 = in ? lds16(w + (g + 8) * pitch_w + at + 16 * t) : zero;
-      const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
-      uint32_t a[4][4];
+    for (int i = 0; i < 4; ++i)
+      a[i][0] = widen8<kBf16>(lo[i]), a[i][1] = widen8<kBf16>(hi[i]), a[i][2] = widen8<kBf16>(lo[i] >> 16),
+      a[i][3] = widen8<kBf16>(hi[i] >> 16);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        a[i][0] = widen8<kBf16>(lo[i]), a[i][1] = widen8<kBf16>(hi[i]), a[i][2] = widen8<kBf16>(lo[i] >> 16),
-        a[i][3] = widen8<kBf16>(hi[i] >> 16);
-#pragma unroll
-      for (int j = 0; j < kNt; ++j) {
-        if (8 * j >= n_cols) break;
-        const bool on = in && xr[j];
-        const uint4 x0 = on ? lds16(xr[j] + 2 * at + 32 * t) : zero, x1 = on ? lds16(xr[j] + 2 * at + 32 * t + 16) : zero;
-        mma16<kBf16>(c[j], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
-        mma16<kBf16>(c[j], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
-        mma16<kBf16>(c[j], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
-        mma16<kBf16>(c[j], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
-      }
+    for (int j = 0; j < kNt; ++j) {
+      if (8 * j >= n_cols) break;
+      const bool on = in && xr[j];
+      const uint4 x0 = on ? lds16(xr[j] + 2 * at + 32 * t) : zero, x1 = on ? lds16(xr[j] + 2 * at + 32 * t + 16) : zero;
+      mma16<kBf16>(c[j], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
+      mma16<kBf16>(c[j], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
+      mma16<kBf16>(c[j], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
+      mma16<kBf16>(c[j], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
     }
   } else {
-    for (int at = 32 * warp; at < k; at += 32 * kWarps) {
-      const bool in = at + 8 * t < k;
-      const uint32_t off = 2 * at + 16 * t;
-      const uint4 w0 = in ? lds16(w + g * pitch_w + off) : zero, w1 = in ? lds16(w + (g + 8) * pitch_w + off) : zero;
+    const bool in = at + 8 * t < k;
 #pragma unroll
-      for (int j = 0; j < kNt; ++j) {
-        if (8 * j >= n_cols) break;
-        const uint4 x = in && xr[j] ? lds16(xr[j] + off) : zero;
-        mma16<kBf16>(c[j], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
-        mma16<kBf16>(c[j], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
-      }
+    for (int j = 0; j < kNt; ++j) {
+      if (8 * j >= n_cols) break;
+      const uint4 x = in && xr[j] ? lds16(xr[j] + 2 * at + 16 * t) : zero;
+      mma16<kBf16>(c[j], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
+      mma16<kBf16>(c[j], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
     }
   }
 }
+
+// This warp's steps of a staged chunk of kc values, of which k are there; with e4m3 weights scaled by lo[block of 128] (rows
+// 0 .. 7) and hi[block] (8 .. 15), blocks counted from k0.
+template <bool kBf16, bool kW8, int kNt>
+__device__ __forceinline__ void chunk_products(float (&acc)[kNt][4], uint32_t w, const uint32_t (&xr)[kNt], int n_cols, int kc,
+                                               int k, int k0, const float* lo, const float* hi, int warp, int lane) {
+  constexpr int kValues = kW8 ? kStep : kStep / 2;
+  if (kW8) {
+    float s[2][2] = {};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = kValues * (warp + kWarps * i);
+      if (at < k) s[i][0] = __ldg(lo + (k0 + at) / 128), s[i][1] = __ldg(hi + (k0 + at) / 128);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = kValues * (warp + kWarps * i);
+      if (at >= k) break;
+      float part[kNt][4] = {};
+      multiply<kBf16, kW8, kNt>(part, w, kc, xr, n_cols, at, k, lane);
+#pragma unroll
+      for (int j = 0; j < kNt; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(part[j][v], s[i][v >> 1], acc[j][v]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = kValues * (warp + kWarps * i);
+      if (at < k) multiply<kBf16, kW8, kNt>(acc, w, 2 * kc, xr, n_cols, at, k, lane);
+    }
+  }
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
+// 16 weight rows: [gate, up] x 8 features of an expert, or 16 outputs.
+__device__ __forceinline__ void load_up(uint8_t* to, const CUtensorMap* map, int word, int f0, int e, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
+          "r"(smem_u32(to)), "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(f0), "r"(0), "r"(e), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void load_down(uint8_t* to, const CUtensorMap* map, int word, int d0, int e, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(smem_u32(to)), "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(d0), "r"(e), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// The weights of the routed and of the shared expert, as 32-bit words.
+struct Maps {
+  CUtensorMap routed, shared;
+};
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -209,7 +263,7 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
 // ------------------------------------------------------------------ up
 
 template <bool kBf16, bool kW8, int kNt>
-__global__ void __launch_bounds__(kThreads) k_layer_up(const __grid_constant__ LayerParams p, const __grid_constant__ Plan P) {
+__global__ void __launch_bounds__(kThreads) k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p, const __grid_constant__ Plan P) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared S;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -223,30 +277,23 @@ __global__ void __launch_bounds__(kThreads) k_layer_up(const __grid_constant__ L
   constexpr int kSize = kW8 ? 1 : 2;   // bytes of a weight
 
   if (warp == kWarps) {
-    int it = 0;
-    bool go = true;
-    for (int unit = blockIdx.x; go && unit < units; unit += gridDim.x) {
-      const bool shared = unit >= routed;
-      const Slot sl = slots[shared ? n_slots : unit / per];
-      const int f = shared ? p.fs : p.f, f0 = 8 * (shared ? unit - routed : unit % per), rows = __popc(sl.mask);
-      const uint8_t* w = static_cast<const uint8_t*>(shared ? p.shared.gate_up : p.routed.gate_up) +
-                         ((shared ? 0LL : 2LL * f * sl.expert) + f0) * p.d * kSize;
-      // lane l copies weight row l (gate, then up) or token row l - 16, and l + 16
-      const uint8_t* from_w = w + (lane < 8 ? lane : lane - 8 + static_cast<long long>(f)) * p.d * kSize;
-      const int t0 = lane >= 16 && lane - 16 < rows ? nth_bit(sl.mask, lane - 16) : -1;
-      const int t1 = lane >= 16 && lane < rows ? nth_bit(sl.mask, lane) : -1;
-      for (int c = 0; c < chunks; ++c, ++it) {
-        const int s = it % P.stages, k0 = c * P.kc_d, k = min(P.kc_d, p.d - k0);
-        if (!(go = it < p.stall && wait_bar_warp(&S.empty[s], ((it / P.stages) & 1) ^ 1, &S.waits))) break;
-        uint8_t* at = smem + s * P.stage;
-        if (lane == 0) mbar_arrive_expect_tx(&S.full[s], 16 * k * kSize + rows * k * 2);
-        __syncwarp();
-        if (lane < 16) {
-          bulk_g2s(at + lane * P.pitch_w, from_w + static_cast<long long>(k0) * kSize, k * kSize, &S.full[s]);
-        } else {
-          uint8_t* x = at + 16 * P.pitch_w;
-          if (t0 >= 0) bulk_g2s(x + (lane - 16) * P.pitch_x, p.x + t0 * p.ldx + k0, 2 * k, &S.full[s]);
-          if (t1 >= 0) bulk_g2s(x + lane * P.pitch_x, p.x + t1 * p.ldx + k0, 2 * k, &S.full[s]);
+    if (elect_one()) {
+      int it = 0;
+      bool go = true;
+      for (int unit = blockIdx.x; go && unit < units; unit += gridDim.x) {
+        const bool shared = unit >= routed;
+        const Slot sl = slots[shared ? n_slots : unit / per];
+        const int f0 = 8 * (shared ? unit - routed : unit % per), rows = __popc(sl.mask);
+        for (int c = 0; c < chunks; ++c, ++it) {
+          const int s = it % P.stages, k0 = c * P.kc_d, k = min(P.kc_d, p.d - k0);
+          if (!(go = it < p.stall && wait_bar(&S.empty[s], ((it / P.stages) & 1) ^ 1, &S.waits))) break;
+          uint8_t* at = smem + s * P.stage;
+          mbar_arrive_expect_tx(&S.full[s], 16 * P.kc_d * kSize + rows * k * 2);
+          load_up(at, shared ? &maps.shared : &maps.routed, k0 * kSize / 4, f0, max(sl.expert, 0), &S.full[s]);
+          uint32_t left = sl.mask;
+          at += 16 * P.kc_d * kSize;
+          for (int i = 0; i < rows; ++i, left &= left - 1, at += P.pitch_x)
+            bulk_g2s(at, p.x + (__ffs(left) - 1) * p.ldx + k0, 2 * k, &S.full[s]);
         }
       }
     }
@@ -269,25 +316,13 @@ __global__ void __launch_bounds__(kThreads) k_layer_up(const __grid_constant__ L
       float acc[kNt][4] = {};
       for (int c = 0; c < chunks; ++c, ++it) {
         const int s = it % P.stages, k0 = c * P.kc_d, k = min(P.kc_d, p.d - k0);
-        float sg = 0.f, su = 0.f;
-        if (kW8 && 128 * warp < k) sg = __ldg(scale + k0 / 128 + warp), su = __ldg(scale + up_scale + k0 / 128 + warp);
         ok = ok && wait_bar_warp(&S.full[s], (it / P.stages) & 1, &S.waits);
         if (ok) {
-          const uint32_t w = smem_u32(smem + s * P.stage), x = w + 16 * P.pitch_w;
+          const uint32_t w = smem_u32(smem + s * P.stage), x = w + 16 * P.kc_d * kSize;
           uint32_t xr[kNt];
 #pragma unroll
           for (int j = 0; j < kNt; ++j) xr[j] = 8 * j + g < rows ? x + (8 * j + g) * P.pitch_x : 0;
-          if (kW8) {
-            float block[kNt][4] = {};
-            multiply<kBf16, kW8, kNt>(block, w, xr, rows, P.pitch_w, k, warp, lane);
-#pragma unroll
-            for (int j = 0; j < kNt; ++j)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (128 * warp < k) acc[j][i] = fmaf(block[j][i], i < 2 ? sg : su, acc[j][i]);
-          } else {
-            multiply<kBf16, kW8, kNt>(acc, w, xr, rows, P.pitch_w, k, warp, lane);
-          }
+          chunk_products<kBf16, kW8, kNt>(acc, w, xr, rows, P.kc_d, k, k0, scale, scale + up_scale, warp, lane);
         }
         __syncwarp();
         if (lane == 0) mbarrier_arrive(&S.empty[s]);
@@ -356,8 +391,8 @@ struct DownChunks {
 };
 
 template <bool kBf16, bool kW8, int kNt>
-__global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__ LayerParams p, const __grid_constant__ Plan P,
-                                                         int split) {
+__global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
+                                                         const __grid_constant__ Plan P, int split) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Shared S;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -374,34 +409,35 @@ __global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__
   const int n = static_cast<int>(static_cast<long long>(C.all) * (rank + 1) / split) - first;
 
   if (warp == kWarps) {
-    const auto rows_of = [&](const Chunk& c) { return __popc(slots[c.slot].mask); };
-    const auto load_w = [&](int i, const Chunk& c, int s) {
-      const bool shared = c.slot == C.n_slots;
-      const int f = shared ? p.fs : p.f;
-      if (lane == 0) mbar_arrive_expect_tx(&S.full[s], 16 * c.k * kSize + rows_of(c) * c.k * 2);
-      __syncwarp();
-      const uint8_t* w = static_cast<const uint8_t*>(shared ? p.shared.down : p.routed.down) +
-                         (((shared ? 0LL : static_cast<long long>(slots[c.slot].expert) * p.d) + d0 + lane) * f + c.k0) * kSize;
-      if (lane < 16) bulk_g2s(smem + s * P.stage + lane * P.pitch_w, w, c.k * kSize, &S.full[s]);
-    };
-    const auto load_a = [&](const Chunk& c, int s) {
-      const bool shared = c.slot == C.n_slots;
-      const int f = shared ? p.fs : p.f;
-      const uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
-                          static_cast<long long>(slots[c.slot].base + lane) * f + c.k0;
-      if (lane < rows_of(c)) bulk_g2s(smem + s * P.stage + 16 * P.pitch_w + lane * P.pitch_x, a, 2 * c.k, &S.full[s]);
-    };
-    const int early = min(min(n, P.stages), p.stall);
-    for (int i = 0; i < early; ++i) load_w(i, C.at(first + i), i);
-    pdl_wait();
-    for (int i = 0; i < early; ++i) load_a(C.at(first + i), i);
-    for (int i = early; i < min(n, p.stall); ++i) {
-      const int s = i % P.stages;
-      if (!wait_bar_warp(&S.empty[s], ((i / P.stages) & 1) ^ 1, &S.waits)) break;
-      const Chunk c = C.at(first + i);
-      load_w(i, c, s);
-      load_a(c, s);
+    if (elect_one()) {
+      const auto load_w = [&](const Chunk& c, int s) {
+        const bool shared = c.slot == C.n_slots;
+        const int kc = shared ? P.kc_fs : P.kc_f;
+        mbar_arrive_expect_tx(&S.full[s], 16 * kc * kSize + __popc(slots[c.slot].mask) * c.k * 2);
+        load_down(smem + s * P.stage, shared ? &maps.shared : &maps.routed, c.k0 * kSize / 4, d0, max(slots[c.slot].expert, 0),
+                  &S.full[s]);
+      };
+      const auto load_a = [&](const Chunk& c, int s) {
+        const bool shared = c.slot == C.n_slots;
+        const int f = shared ? p.fs : p.f, rows = __popc(slots[c.slot].mask);
+        const uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
+                            static_cast<long long>(slots[c.slot].base) * f + c.k0;
+        uint8_t* to = smem + s * P.stage + 16 * (shared ? P.kc_fs : P.kc_f) * kSize;
+        for (int i = 0; i < rows; ++i, a += f, to += P.pitch_x) bulk_g2s(to, a, 2 * c.k, &S.full[s]);
+      };
+      const int early = min(min(n, P.stages), p.stall);
+      for (int i = 0; i < early; ++i) load_w(C.at(first + i), i);
+      pdl_wait();
+      for (int i = 0; i < early; ++i) load_a(C.at(first + i), i);
+      for (int i = early; i < min(n, p.stall); ++i) {
+        const int s = i % P.stages;
+        if (!wait_bar(&S.empty[s], ((i / P.stages) & 1) ^ 1, &S.waits)) break;
+        const Chunk c = C.at(first + i);
+        load_w(c, s);
+        load_a(c, s);
+      }
     }
+    __syncwarp();
   }
   pdl_wait();   // y may be in use until here
   pdl_trigger();
@@ -416,31 +452,21 @@ __global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__
       const int s = i % P.stages;
       const Chunk c = C.at(first + i);
       const uint32_t mask = slots[c.slot].mask;
-      float sc = 0.f;
-      if (kW8 && 128 * warp < c.k)
-        sc = c.slot == C.n_slots
-                 ? __ldg(p.shared.down_scale + d0 / 128 * kbs + c.k0 / 128 + warp)
-                 : __ldg(p.routed.down_scale + (static_cast<long long>(slots[c.slot].expert) * db + d0 / 128) * kb + c.k0 / 128 + warp);
+      const bool shared = c.slot == C.n_slots;
+      const int kc = shared ? P.kc_fs : P.kc_f;
+      const float* scale = !kW8 ? nullptr
+                           : shared ? p.shared.down_scale + d0 / 128 * kbs
+                                    : p.routed.down_scale + (static_cast<long long>(slots[c.slot].expert) * db + d0 / 128) * kb;
       ok = ok && wait_bar_warp(&S.full[s], (i / P.stages) & 1, &S.waits);
       if (ok) {
-        const uint32_t w = smem_u32(smem + s * P.stage), x = w + 16 * P.pitch_w;
+        const uint32_t w = smem_u32(smem + s * P.stage), x = w + 16 * kc * kSize;
         uint32_t xr[kNt];
 #pragma unroll
         for (int j = 0; j < kNt; ++j) {
           const int col = 8 * j + g;
           xr[j] = (mask >> col) & 1 ? x + __popc(mask & ((1u << col) - 1)) * P.pitch_x : 0;
         }
-        if (kW8) {
-          float block[kNt][4] = {};
-          multiply<kBf16, kW8, kNt>(block, w, xr, 32, P.pitch_w, c.k, warp, lane);
-#pragma unroll
-          for (int j = 0; j < kNt; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (128 * warp < c.k) own[j][v] = fmaf(block[j][v], sc, own[j][v]);
-        } else {
-          multiply<kBf16, kW8, kNt>(own, w, xr, 32, P.pitch_w, c.k, warp, lane);
-        }
+        chunk_products<kBf16, kW8, kNt>(own, w, xr, 32, kc, c.k, c.k0, scale, scale, warp, lane);
         if (i + 1 == n || C.at(first + i + 1).slot != c.slot) {
 #pragma unroll
           for (int j = 0; j < kNt; ++j)
@@ -494,21 +520,19 @@ __global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__
 
 // ------------------------------------------------------------------ launches
 
-int padded(int bytes, int to) { return (bytes + 127) / 128 * 128 + to; }
-
 // e4m3 rows have half the bytes of the token rows beside them, which two words a lane of 32 bytes apart read: 16 bytes more
 // than a multiple of 128 keep eight lanes apart there, 64 where a row's four lanes read 64 bytes.
 Plan make_plan(const LayerParams& p, bool w8, bool down) {
   Plan P{};
-  P.kc_d = chunk_of(p.d, w8), P.kc_f = chunk_of(p.f, w8), P.kc_fs = chunk_of(p.fs, w8);
+  const int size = w8 ? 1 : 2;
+  P.kc_d = chunk_of(p.d, size), P.kc_f = chunk_of(p.f, size), P.kc_fs = chunk_of(p.fs, size);
   const int kc = down ? std::max(P.kc_f, P.kc_fs) : P.kc_d, nt = p.t <= 8 ? 1 : 4;
-  P.pitch_w = padded(kc * (w8 ? 1 : 2), 64), P.pitch_x = padded(2 * kc, w8 ? 16 : 64);
-  P.stage = (16 * P.pitch_w + p.t * P.pitch_x + 127) / 128 * 128;
+  P.pitch_x = divide_up(2 * kc, 128) * 128 + (w8 ? 16 : 64);
+  P.stage = divide_up(16 * kc * size + p.t * P.pitch_x, 128) * 128;
   P.slots = std::min(p.t * p.k, p.E);
   const int red = kWarps * nt * 512 * (down ? 1 : 2) + (down ? nt * 512 : 0);
   const int lists = 4 * p.E + 8 * p.t * p.k + static_cast<int>(sizeof(Slot)) * (P.slots + 1) + 64;
-  const int most = down ? kMaxStages : kMaxStages;
-  P.stages = std::clamp((kBudget - red - lists) / P.stage, 2, most);
+  P.stages = std::clamp((kBudget - red - lists) / P.stage, 2, kMaxStages);
   P.at_red = P.stages * P.stage;
   P.at_mask = P.at_red + red;
   P.at_ids = P.at_mask + 4 * p.E;
@@ -516,6 +540,33 @@ Plan make_plan(const LayerParams& p, bool w8, bool down) {
   P.at_slots = P.at_gates + 4 * p.t * p.k;
   P.bytes = P.at_slots + static_cast<int>(sizeof(Slot)) * (P.slots + 1);
   return P;
+}
+
+bool encode_words(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dim, const cuuint64_t* stride,
+                  const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dim, stride,
+                          box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [E][2][f][d] in boxes of kc values x 8 features x both halves.
+bool map_up(CUtensorMap* m, const void* base, int E, int f, int d, int size, int kc) {
+  const cuuint64_t row = static_cast<cuuint64_t>(d) * size;
+  const cuuint64_t dim[4] = {row / 4, static_cast<cuuint64_t>(f), 2, static_cast<cuuint64_t>(E)};
+  const cuuint64_t stride[3] = {row, row * f, row * 2 * f};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kc * size / 4), 8, 2, 1};
+  return encode_words(m, base, 4, dim, stride, box);
+}
+
+// [E][d][f] in boxes of kc values x 16 outputs.
+bool map_down(CUtensorMap* m, const void* base, int E, int d, int f, int size, int kc) {
+  const cuuint64_t row = static_cast<cuuint64_t>(f) * size;
+  const cuuint64_t dim[3] = {row / 4, static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(E)};
+  const cuuint64_t stride[2] = {row, row * d};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kc * size / 4), 16, 1};
+  return encode_words(m, base, 3, dim, stride, box);
 }
 
 template <typename K, typename... A>
@@ -542,14 +593,22 @@ bool launch(K kernel, int grid, const Plan& P, int cluster, cudaStream_t s, cons
 
 template <bool kBf16, bool kW8, int kNt>
 bool launch_both(const LayerParams& p, int sms, cudaStream_t s) {
+  constexpr int kSize = kW8 ? 1 : 2;
   const Plan up = make_plan(p, kW8, false), down = make_plan(p, kW8, true);
+  Maps m_up, m_down;
+  if (!map_up(&m_up.routed, p.routed.gate_up, p.E, p.f, p.d, kSize, up.kc_d) ||
+      !map_down(&m_down.routed, p.routed.down, p.E, p.d, p.f, kSize, down.kc_f))
+    return false;
+  if (p.fs && (!map_up(&m_up.shared, p.shared.gate_up, 1, p.fs, p.d, kSize, up.kc_d) ||
+               !map_down(&m_down.shared, p.shared.down, 1, p.d, p.fs, kSize, down.kc_fs)))
+    return false;
   // every CTA the same number of units, as far as the picked experts are known here: two CTAs an SM
   const int units = up.slots * (p.f / 8) + p.fs / 8, rounds = divide_up(units, 2 * sms);
-  if (!launch(k_layer_up<kBf16, kW8, kNt>, divide_up(units, rounds), up, 1, s, p, up)) return false;
+  if (!launch(k_layer_up<kBf16, kW8, kNt>, divide_up(units, rounds), up, 1, s, m_up, p, up)) return false;
   const int blocks = p.d / 16, chunks = down.slots * divide_up(p.f, down.kc_f) + (p.fs ? divide_up(p.fs, down.kc_fs) : 0);
   int split = 1;
   while (split < 8 && 2 * split * blocks <= 2 * sms && 2 * split <= chunks) split *= 2;
-  return launch(k_layer_down<kBf16, kW8, kNt>, blocks * split, down, split, s, p, down, split);
+  return launch(k_layer_down<kBf16, kW8, kNt>, blocks * split, down, split, s, m_down, p, down, split);
 }
 
 template <bool kBf16, bool kW8>

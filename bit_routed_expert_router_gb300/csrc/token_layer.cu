@@ -4,23 +4,29 @@
 //   down   y[t] = sum_e Wd[e] a[e, t]                       over the experts that t names, and the shared one
 //
 // The weights of the picked experts are read once and nothing else is of any
-// size, so both kernels stream them: one thread copies chunks of 16 weight rows
-// (one TMA load: a bulk copy a row took about 85 cycles each, 52 us for one token
-// where the weights take 21), and of the token rows that go with them, into a ring
-// of stages; eight warps share a chunk's steps of 64 bytes and multiply them as
-// m16n8k16 fragments, weights on the M side.  A lane reads 16 bytes of a row at a
-// time: the order of k within a step is the same in both operands, which is all
-// that a product needs, and chunks of an odd number of steps keep the rows of eight
-// lanes in different banks.  e4m3 weights become 16-bit ones in registers (exact);
-// each step's sums are scaled by themselves.
+// size, so both kernels stream them.  A warp works by itself: one of its lanes
+// loads chunks of 16 weight rows by TMA into the warp's own stages, and the warp
+// multiplies them as m16n8k16 fragments, weights on the M side.  No barrier but a
+// stage's own is waited for on the way (with eight warps that shared the stages and
+// a ninth that loaded, one token took 47 us instead of what stands below).  The
+// token rows come from L2 straight into fragments, before the chunk's weights are
+// waited for (staged beside the weights they took their room: 7 tokens 144 us).
+// A lane reads 16 bytes of a row at a time: the order of k within a step is the
+// same in both operands, which is all that a product needs.  The rows of a fragment
+// are dealt to the lanes so that eight lanes that read at once find the two rows'
+// halves of the 128-byte swizzle in different banks.  e4m3 weights become 16-bit
+// ones in registers (exact); the sums of each block of 128 are scaled by themselves.
 //
-// up: a unit is 8 features: their 8 gate and 8 up rows are the 16 rows, so that a
-// lane ends with both factors of its values.  Columns: the expert's tokens.
-// down: a unit is 16 outputs over all picked experts, its chunks dealt out to a
-// cluster's CTAs, which add their sums through distributed shared memory in rank
-// order.  Columns: all tokens; an expert's sums are added to those that name it
-// only, so that weights that are not finite stay with their own tokens.  The
-// kernel starts while the first one runs and fills its ring with weights.
+// The columns are up to eight tokens of an expert (a slot: an expert with more
+// has several, whose weights come from L2 again), so that weights that are not
+// finite reach the tokens that name their expert only.
+//
+// up: a unit is 8 features of a slot: their 8 gate and 8 up rows are the 16 rows,
+// so that a lane ends with both factors of its values.
+// down: a unit is 16 outputs over all slots, its chunks dealt out to the warps of a
+// cluster's CTAs.  Each adds its slots' sums to its own copy of the tokens'
+// outputs; the copies are added in order, through distributed shared memory.  The
+// kernel starts while the first one runs and fills its stages with weights.
 #include <algorithm>
 
 #include "gelu16.cuh"
@@ -34,55 +40,49 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * (kWarps + 1);
-constexpr int kStep = 64, kChunkBytes = 15 * kStep;   // of a weight row; a chunk at most
-constexpr int kMaxStages = 8;
-constexpr int kBudget = 72 * 1024;  // shared memory of a CTA: three fit an SM, so that the down kernel's ring fills early
+#ifndef SU
+#define SU 2
+#define SD 1
+#define CU 4
+#define CD 4
+#endif
+constexpr int kWarpsUp = 8, kWarpsDown = 8;
+constexpr int kStagesUp = SU, kStagesDown = SD;    // of a warp: three CTAs of the second kernel fit beside one of the first
+constexpr int kCol = 128, kColBytes = 16 * kCol;  // bytes of a weight row that one load takes; of its 16 rows
+constexpr int kColsUp = CU, kColsDown = CD;        // loads of a chunk
+constexpr int kTokens = 8;                       // of a slot
 
 struct Slot {
   int expert;      // -1: the shared expert
-  uint32_t mask;   // its tokens
+  uint32_t mask;   // its tokens, kTokens at most
   int base;        // its rows of a (the shared one's: in its own part)
 };
 
-// Host and device: what a launch's CTA keeps, and where.
+// What a launch's CTA keeps behind the stages, and where.
 struct Plan {
-  int kc_d, kc_f, kc_fs;      // values of a chunk: along d, f and f_shared
-  int pitch_x;                // bytes between staged token rows
-  int stage, stages;
-  int slots;                  // most picked experts
-  int at_red, at_mask, at_ids, at_gates, at_slots, bytes;
+  int at_sums, at_mask, at_ids, at_gates, at_slots, bytes;
 };
 
 __host__ __device__ __forceinline__ int divide_up(int a, int b) { return (a + b - 1) / b; }
 
-// Equal chunks of an odd number of steps, in values.
-int chunk_of(int k, int size) {
-  if (k == 0) return 0;
-  const int chunks = divide_up(k * size, kChunkBytes), steps = divide_up(divide_up(k * size, chunks), kStep);
-  return (steps | 1) * kStep / size;
-}
-
-struct Chunk {
-  int slot;            // index, n_slots for the shared expert
-  int k0, k;           // first value and length
+template <int kWarps, int kStages>
+struct Shared {
+  uint64_t full[kWarps][kStages];
+  Waits waits;
+  int n_routed, n_slots;   // slots of routed experts; and of the shared one
 };
 
-__device__ __forceinline__ uint4 lds16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
+// ------------------------------------------------------------------ pieces
 
 template <bool kBf16>
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   if (kBf16)
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -98,74 +98,63 @@ __device__ __forceinline__ uint32_t widen8(uint32_t v) {
   return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// c += 16 weight rows times up to 8 kNt token rows over one step of a staged chunk, which ends (k values) in it or behind it.
-// xr[j]: this lane's token row of columns 8 j .., 0 for none.
-template <bool kBf16, bool kW8, int kNt>
-__device__ __forceinline__ void multiply(float (&c)[kNt][4], uint32_t w, int pitch_w, const uint32_t (&xr)[kNt], int n_cols, int at,
-                                         int k, int lane) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  const uint32_t from = w + g * pitch_w + (kW8 ? at : 2 * at) + 16 * t;
-  const uint4 w0 = lds16(from), w1 = lds16(from + 8 * pitch_w);   // zeros past k
-  if (kW8) {
-    const bool in = at + 16 * t < k;
-    const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
-    uint32_t a[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      a[i][0] = widen8<kBf16>(lo[i]), a[i][1] = widen8<kBf16>(hi[i]), a[i][2] = widen8<kBf16>(lo[i] >> 16),
-      a[i][3] = widen8<kBf16>(hi[i] >> 16);
-#pragma unroll
-    for (int j = 0; j < kNt; ++j) {
-      if (8 * j >= n_cols) break;
-      const bool on = in && xr[j];
-      const uint4 x0 = on ? lds16(xr[j] + 2 * at + 32 * t) : zero, x1 = on ? lds16(xr[j] + 2 * at + 32 * t + 16) : zero;
-      mma16<kBf16>(c[j], a[0][0], a[0][1], a[0][2], a[0][3], x0.x, x0.y);
-      mma16<kBf16>(c[j], a[1][0], a[1][1], a[1][2], a[1][3], x0.z, x0.w);
-      mma16<kBf16>(c[j], a[2][0], a[2][1], a[2][2], a[2][3], x1.x, x1.y);
-      mma16<kBf16>(c[j], a[3][0], a[3][1], a[3][2], a[3][3], x1.z, x1.w);
-    }
-  } else {
-    const bool in = at + 8 * t < k;
-#pragma unroll
-    for (int j = 0; j < kNt; ++j) {
-      if (8 * j >= n_cols) break;
-      const uint4 x = in && xr[j] ? lds16(xr[j] + 2 * at + 16 * t) : zero;
-      mma16<kBf16>(c[j], w0.x, w1.x, w0.y, w1.y, x.x, x.y);
-      mma16<kBf16>(c[j], w0.z, w1.z, w0.w, w1.w, x.z, x.w);
-    }
-  }
-}
+// The weight row of a fragment's row g (and 8 + it that of row 8 + g).
+__device__ __forceinline__ int row_of(int g) { return g >> 1 | (g & 1) << 2; }
 
-// This warp's steps of a staged chunk of kc values, of which k are there; with e4m3 weights scaled by lo[block of 128] (rows
-// 0 .. 7) and hi[block] (8 .. 15), blocks counted from k0.
-template <bool kBf16, bool kW8, int kNt>
-__device__ __forceinline__ void chunk_products(float (&acc)[kNt][4], uint32_t w, const uint32_t (&xr)[kNt], int n_cols, int kc,
-                                               int k, int k0, const float* lo, const float* hi, int warp, int lane) {
-  constexpr int kValues = kW8 ? kStep : kStep / 2;
-  if (kW8) {
-    float s[2][2] = {};
+// This lane's share of up to 8 token rows over a chunk: 16 bytes a word.
+template <bool kW8, int kCols>
+struct TokenWords {
+  static constexpr int kWords = kW8 ? 2 : 1;   // of a half of a load
+  uint4 v[kCols][2][kWords];
+
+  // row: this lane's token row from the chunk's first value on, of which k are there; null for none
+  __device__ __forceinline__ void load(const uint16_t* row, int k, int lane) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = kValues * (warp + kWarps * i);
-      if (at < k) s[i][0] = __ldg(lo + (k0 + at) / 128), s[i][1] = __ldg(hi + (k0 + at) / 128);
+    for (int i = 0; i < kCols; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          const int at = (kW8 ? kCol : kCol / 2) * i + 32 * kWords * h + 8 * kWords * (lane & 3) + 8 * j;
+          v[i][h][j] = row && at < k ? __ldcg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0, 0, 0, 0);
+        }
+  }
+};
+
+// acc += 16 weight rows of a staged chunk of k values times the token rows.  With e4m3 weights `scale` holds the scales of the
+// chunk's blocks of 128 (its loads): lane i that of rows 0 .. 7, lane 16 + i of rows 8 .. 15.
+template <bool kBf16, bool kW8, int kCols>
+__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const TokenWords<kW8, kCols>& x, int k, float scale,
+                                               int lane) {
+  const int r = row_of(lane >> 2), t = lane & 3;
+  const uint8_t* row = stage + r * kCol;
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) {
+    if ((kW8 ? kCol : kCol / 2) * i >= k) break;
+    float part[2][4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint8_t* from = row + i * kColBytes + (((4 * h + t) ^ r) << 4);   // zeros past the row's end
+      const uint4 w0 = *reinterpret_cast<const uint4*>(from), w1 = *reinterpret_cast<const uint4*>(from + 8 * kCol);
+      const uint4 b0 = x.v[i][h][0];
+      if (kW8) {
+        const uint4 b1 = x.v[i][h][TokenWords<kW8, kCols>::kWords - 1];
+        const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+        const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mma16<kBf16>(part[h], widen8<kBf16>(lo[q]), widen8<kBf16>(hi[q]), widen8<kBf16>(lo[q] >> 16), widen8<kBf16>(hi[q] >> 16),
+                       b[2 * q], b[2 * q + 1]);
+      } else {
+        mma16<kBf16>(part[h], w0.x, w1.x, w0.y, w1.y, b0.x, b0.y);
+        mma16<kBf16>(part[h], w0.z, w1.z, w0.w, w1.w, b0.z, b0.w);
+      }
     }
+    const float lo = kW8 ? __shfl_sync(0xFFFFFFFFu, scale, i) : 1.f, hi = kW8 ? __shfl_sync(0xFFFFFFFFu, scale, 16 + i) : 1.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = kValues * (warp + kWarps * i);
-      if (at >= k) break;
-      float part[kNt][4] = {};
-      multiply<kBf16, kW8, kNt>(part, w, kc, xr, n_cols, at, k, lane);
-#pragma unroll
-      for (int j = 0; j < kNt; ++j)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(part[j][v], s[i][v >> 1], acc[j][v]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int at = kValues * (warp + kWarps * i);
-      if (at < k) multiply<kBf16, kW8, kNt>(acc, w, 2 * kc, xr, n_cols, at, k, lane);
+    for (int v = 0; v < 4; ++v) {
+      const float sum = part[0][v] + part[1][v];
+      acc[v] = kW8 ? fmaf(sum, v < 2 ? lo : hi, acc[v]) : acc[v] + sum;
     }
   }
 }
@@ -176,7 +165,7 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// 16 weight rows: [gate, up] x 8 features of an expert, or 16 outputs.
+// 128 bytes of 16 weight rows: [gate, up] x 8 features of an expert, or 16 outputs.
 __device__ __forceinline__ void load_up(uint8_t* to, const CUtensorMap* map, int word, int f0, int e, uint64_t* bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
@@ -190,166 +179,209 @@ __device__ __forceinline__ void load_down(uint8_t* to, const CUtensorMap* map, i
       : "memory");
 }
 
+__device__ __forceinline__ int loads_of(int k, int size) { return (k * size + kCol - 1) / kCol; }
+
 // The weights of the routed and of the shared expert, as 32-bit words.
 struct Maps {
   CUtensorMap routed, shared;
 };
-
-struct Shared {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  Waits waits;
-  int n_slots;
-};
-
-// The picked experts in order, each with its tokens; every thread of the CTA.
-__device__ void list_slots(const LayerParams& p, const Plan& P, uint8_t* smem, Shared& S) {
-  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + P.at_mask);
-  int* ids = reinterpret_cast<int*>(smem + P.at_ids);
-  float* gates = reinterpret_cast<float*>(smem + P.at_gates);
-  Slot* slots = reinterpret_cast<Slot*>(smem + P.at_slots);
-  for (int i = threadIdx.x; i < p.E; i += kThreads) mask[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.t * p.k; i += kThreads) {
-    const int e = __ldcg(p.ids + i);
-    ids[i] = e;
-    gates[i] = __ldcg(p.gates + i);
-    if (e >= 0 && e < p.E) atomicOr(&mask[e], 1u << (i / p.k));
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int n = 0, rows = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const uint32_t m = e0 + lane < p.E ? mask[e0 + lane] : 0;
-      const uint32_t picked = __ballot_sync(0xFFFFFFFFu, m != 0), before = picked & ((1u << lane) - 1);
-      int sum = __popc(m);
-      const int own = sum;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
-        if (lane >= d) sum += o;
-      }
-      if (m) slots[n + __popc(before)] = {e0 + lane, m, rows + sum - own};
-      n += __popc(picked);
-      rows += __shfl_sync(0xFFFFFFFFu, sum, 31);
-    }
-    if (lane == 0) {
-      S.n_slots = n;
-      slots[n] = {-1, p.t == 32 ? 0xFFFFFFFFu : (1u << p.t) - 1, 0};
-    }
-  }
-  __syncthreads();
-}
-
-__device__ __forceinline__ void init_ring(Shared& S, const LayerParams& p, int stages) {
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) {
-      mbar_init(&S.full[i], 1);
-      mbar_init(&S.empty[i], kWarps);
-    }
-    S.waits.abort = 0;
-    S.waits.limit = p.limit;
-    fence_mbar_init();
-  }
-}
-
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
 
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
   for (; n > 0; --n) m &= m - 1;
   return __ffs(m) - 1;
 }
 
-// ------------------------------------------------------------------ up
+// Slots of up to 32 experts, one a lane with its tokens m (0: none), behind n slots and `rows` rows of a; counts them up.
+__device__ __forceinline__ void add_slots(Slot* slots, int e, uint32_t m, int& n, int& rows, int lane) {
+  const int own = __popc(m), parts = divide_up(own, kTokens);
+  int sum = own << 16 | parts;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+    if (lane >= d) sum += o;
+  }
+  int at = n + (sum & 0xFFFF) - parts, base = rows + (sum >> 16) - own;
+  for (int left = own; left > 0; left -= kTokens, base += kTokens) {
+    const uint32_t all = m;
+    for (int i = 0; i < kTokens; ++i) m &= m - 1;
+    slots[at++] = {e, all ^ m, base};
+  }
+  const int all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+  n += all & 0xFFFF;
+  rows += all >> 16;
+}
 
-template <bool kBf16, bool kW8, int kNt>
-__global__ void __launch_bounds__(kThreads) k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p, const __grid_constant__ Plan P) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared S;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  init_ring(S, p, P.stages);
-  pdl_wait();
-  pdl_trigger();
-  list_slots(p, P, smem, S);
-  const Slot* slots = reinterpret_cast<const Slot*>(smem + P.at_slots);
-  const int n_slots = S.n_slots, per = p.f / 8, routed = n_slots * per, units = routed + p.fs / 8;
-  const int chunks = divide_up(p.d, P.kc_d);
-  constexpr int kSize = kW8 ? 1 : 2;   // bytes of a weight
+// Slot q of the shared expert.
+__device__ __forceinline__ Slot shared_slot(int q, int t) {
+  return {-1, ((1u << min(kTokens, t - kTokens * q)) - 1) << (kTokens * q), kTokens * q};
+}
 
-  if (warp == kWarps) {
-    if (elect_one()) {
-      int it = 0;
-      bool go = true;
-      for (int unit = blockIdx.x; go && unit < units; unit += gridDim.x) {
-        const bool shared = unit >= routed;
-        const Slot sl = slots[shared ? n_slots : unit / per];
-        const int f0 = 8 * (shared ? unit - routed : unit % per), rows = __popc(sl.mask);
-        for (int c = 0; c < chunks; ++c, ++it) {
-          const int s = it % P.stages, k0 = c * P.kc_d, k = min(P.kc_d, p.d - k0);
-          if (!(go = it < p.stall && wait_bar(&S.empty[s], ((it / P.stages) & 1) ^ 1, &S.waits))) break;
-          uint8_t* at = smem + s * P.stage;
-          mbar_arrive_expect_tx(&S.full[s], 16 * P.kc_d * kSize + rows * k * 2);
-          load_up(at, shared ? &maps.shared : &maps.routed, k0 * kSize / 4, f0, max(sl.expert, 0), &S.full[s]);
-          uint32_t left = sl.mask;
-          at += 16 * P.kc_d * kSize;
-          for (int i = 0; i < rows; ++i, left &= left - 1, at += P.pitch_x)
-            bulk_g2s(at, p.x + (__ffs(left) - 1) * p.ldx + k0, 2 * k, &S.full[s]);
-        }
+// The slots of the picked experts, then those of the shared one; every thread of the CTA.
+template <int kWarps, int kStages>
+__device__ __forceinline__ void list_slots(const LayerParams& p, const Plan& P, uint8_t* smem, Shared<kWarps, kStages>& S) {
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + P.at_mask);   // zeros, as prepare() leaves them
+  int* ids = reinterpret_cast<int*>(smem + P.at_ids);
+  float* gates = reinterpret_cast<float*>(smem + P.at_gates);
+  Slot* slots = reinterpret_cast<Slot*>(smem + P.at_slots);
+  const int pairs = p.t * p.k, lane = threadIdx.x & 31;
+  const bool few = pairs <= 32;   // one warp sees all pairs: slots in the order of their first ones (2.0 us -> 1.1 us)
+  if (!few) {
+    for (int i = threadIdx.x; i < pairs; i += 32 * kWarps) {
+      const int e = __ldcg(p.ids + i);
+      ids[i] = e;
+      gates[i] = __ldcg(p.gates + i);
+      if (e >= 0 && e < p.E) atomicOr(&mask[e], 1u << (i / p.k));
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x < 32) {
+    int n = 0, rows = 0;
+    if (few) {
+      const int e = lane < pairs ? __ldcg(p.ids + lane) : -1;
+      if (lane < pairs) ids[lane] = e, gates[lane] = __ldcg(p.gates + lane);
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+      uint32_t m = 0;
+      if (e >= 0 && e < p.E && __ffs(same) - 1 == lane)
+        for (uint32_t left = same; left; left &= left - 1) m |= 1u << ((__ffs(left) - 1) / p.k);
+      add_slots(slots, e, m, n, rows, lane);
+    } else {
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const uint32_t m = e0 + lane < p.E ? mask[e0 + lane] : 0;
+        if (__any_sync(0xFFFFFFFFu, m != 0)) add_slots(slots, e0 + lane, m, n, rows, lane);
       }
     }
-  } else {
-    const int g = lane >> 2;
-    int it = 0, turn = 0;
-    bool ok = true;
-    for (int unit = blockIdx.x; unit < units; unit += gridDim.x, turn ^= 1) {
-      const bool shared = unit >= routed;
-      const Slot sl = slots[shared ? n_slots : unit / per];
-      const int f = shared ? p.fs : p.f, f0 = 8 * (shared ? unit - routed : unit % per), rows = __popc(sl.mask);
-      const float* scale = nullptr;
-      int up_scale = 0;
-      if (kW8) {
-        const int kb = divide_up(p.d, 128);
-        scale = (shared ? p.shared.gate_up_scale : p.routed.gate_up_scale + static_cast<long long>(sl.expert) * divide_up(2 * f, 128) * kb) +
-                f0 / 128 * kb;
-        up_scale = ((f + f0) / 128 - f0 / 128) * kb;
-      }
-      float acc[kNt][4] = {};
-      for (int c = 0; c < chunks; ++c, ++it) {
-        const int s = it % P.stages, k0 = c * P.kc_d, k = min(P.kc_d, p.d - k0);
-        ok = ok && wait_bar_warp(&S.full[s], (it / P.stages) & 1, &S.waits);
-        if (ok) {
-          const uint32_t w = smem_u32(smem + s * P.stage), x = w + 16 * P.kc_d * kSize;
-          uint32_t xr[kNt];
+    const int shared = p.fs ? divide_up(p.t, kTokens) : 0;
+    if (lane < shared) slots[n + lane] = shared_slot(lane, p.t);
+    if (lane == 0) S.n_routed = n, S.n_slots = n + shared;
+  }
+  __syncthreads();
+}
+
+// What needs no input.
+template <int kWarps, int kStages>
+__device__ __forceinline__ void prepare(const LayerParams& p, const Maps& maps, const Plan& P, uint8_t* smem,
+                                        Shared<kWarps, kStages>& S) {
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + P.at_mask);
+  for (int i = threadIdx.x; i < p.E; i += 32 * kWarps) mask[i] = 0;
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < kWarps; ++w)
+      for (int i = 0; i < kStages; ++i) mbar_init(&S.full[w][i], 1);
+    S.waits.abort = 0;
+    S.waits.limit = p.limit;
+    fence_mbar_init();
+  } else if (threadIdx.x < 3) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(threadIdx.x == 1 || !p.fs ? &maps.routed : &maps.shared))
+                 : "memory");
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------------ up
+
+template <bool kBf16, bool kW8>
+__global__ void __launch_bounds__(32 * kWarpsUp) k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
+                                                       const __grid_constant__ Plan P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ Shared<kWarpsUp, kStagesUp> S;
+  constexpr int kWarps = kWarpsUp, kStages = kStagesUp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
+  constexpr int kSize = kW8 ? 1 : 2;   // bytes of a weight
+  constexpr int kCols = kColsUp, kChunk = kCols * kCol / kSize, kStageBytes = kCols * kColBytes;   // values of a chunk
+  prepare(p, maps, P, smem, S);
+  pdl_wait();
+  pdl_trigger();
+  const Slot* slots = reinterpret_cast<const Slot*>(smem + P.at_slots);
+  const int per = p.f / 8, per_shared = p.fs / 8, of_shared = p.fs ? divide_up(p.t, kTokens) * per_shared : 0;
+  const int stride = gridDim.x * kWarps;
+  int units = of_shared;   // and the routed ones, once they are known
+  uint8_t* const stages = smem + warp * kStages * kStageBytes;
+  uint64_t* const full = S.full[warp];
+
+  // A place in this warp's units and their chunks: the shared expert's units first, which are known before the picked experts.
+  struct Place {
+    int unit, k0;
+    Slot slot;
+    int f, f0;
+  };
+  const auto enter = [&](Place& at) {
+    at.k0 = 0;
+    if (at.unit >= units) return;
+    const bool shared = at.unit < of_shared;
+    const int i = shared ? at.unit : at.unit - of_shared, n = shared ? per_shared : per, s = i / n;
+    at.slot = shared ? shared_slot(s, p.t) : slots[s];
+    at.f = shared ? p.fs : p.f;
+    at.f0 = 8 * (i - s * n);
+  };
+  Place next;
+  next.unit = blockIdx.x + warp * gridDim.x;   // as many on every SM as can be
+  enter(next);
+  int loads = 0;
+  const auto load = [&] {   // the next chunk into the next stage, which no lane reads any more
+    if (next.unit >= units) return;
+    if (loads < p.stall && elect_one()) {
+      const int s = loads % kStages, cols = loads_of(min(kChunk, p.d - next.k0), kSize);
+      mbar_arrive_expect_tx(&full[s], cols * kColBytes);
+      for (int i = 0; i < cols; ++i)
+        load_up(stages + s * kStageBytes + i * kColBytes, next.slot.expert < 0 ? &maps.shared : &maps.routed,
+                (next.k0 * kSize + i * kCol) / 4, next.f0, max(next.slot.expert, 0), &full[s]);
+    }
+    ++loads;
+    next.k0 += kChunk;
+    if (next.k0 >= p.d) {
+      next.unit += stride;
+      enter(next);
+    }
+  };
+  for (int i = 0; i < kStages; ++i) load();
+  list_slots(p, P, smem, S);
+  units += S.n_routed * per;
+  if (next.k0 == 0) enter(next);
+  while (loads < kStages && next.unit < units) load();
+
+  int it = 0;
+  bool ok = true;
+  Place at;
+  for (at.unit = blockIdx.x + warp * gridDim.x; ok && at.unit < units; at.unit += stride) {
+    enter(at);
+    const int rows = __popc(at.slot.mask), f = at.f, f0 = at.f0;
+    const float* scale = nullptr;   // lanes 0 .. 15: of the gate rows, 16 .. 31: of the up rows
+    if (kW8) {
+      const int kb = divide_up(p.d, 128);
+      scale = (at.slot.expert < 0 ? p.shared.gate_up_scale
+                                  : p.routed.gate_up_scale + static_cast<long long>(at.slot.expert) * divide_up(2 * f, 128) * kb) +
+              (lane < 16 ? f0 : f + f0) / 128 * kb;
+    }
+    float acc[4] = {};
+    const uint16_t* x = g < rows ? p.x + nth_bit(at.slot.mask, g) * p.ldx : nullptr;
+    for (int k0 = 0; k0 < p.d; k0 += kChunk, ++it) {
+      const int s = it % kStages, k = min(kChunk, p.d - k0);
+      TokenWords<kW8, kCols> tokens;
+      tokens.load(x ? x + k0 : nullptr, k, lane);
+      float sc = 0.f;
+      if (kW8 && kCol * (lane & 15) < k) sc = __ldg(scale + k0 / 128 + (lane & 15));
+      if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
+      chunk_products<kBf16, kW8, kCols>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
+      __syncwarp();
+      load();
+    }
+    // this lane: gate and up of one feature, columns 2 (lane % 4) and the next
+    uint16_t* a = p.a + (at.slot.expert < 0 ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
+                  static_cast<long long>(at.slot.base) * f + f0 + row_of(g);
 #pragma unroll
-          for (int j = 0; j < kNt; ++j) xr[j] = 8 * j + g < rows ? x + (8 * j + g) * P.pitch_x : 0;
-          chunk_products<kBf16, kW8, kNt>(acc, w, xr, rows, P.kc_d, k, k0, scale, scale + up_scale, warp, lane);
-        }
-        __syncwarp();
-        if (lane == 0) mbarrier_arrive(&S.empty[s]);
+    for (int i = 0; i < 2; ++i) {
+      const int col = 2 * (lane & 3) + i;
+      if (!ok || col >= rows) continue;
+      float gate = 1.f;
+      if (at.slot.expert >= 0) {
+        const int* ids = reinterpret_cast<const int*>(smem + P.at_ids);
+        const float* gates = reinterpret_cast<const float*>(smem + P.at_gates);
+        const int t = nth_bit(at.slot.mask, col);
+        gate = 0.f;
+        for (int j = 0; j < p.k; ++j) gate += ids[t * p.k + j] == at.slot.expert ? gates[t * p.k + j] : 0.f;
       }
-      // the warps' sums in turn: 8 features x 8 kNt columns, both factors
-      float4* red = reinterpret_cast<float4*>(smem + P.at_red) + turn * kWarps * kNt * 32;
-#pragma unroll
-      for (int j = 0; j < kNt; ++j) red[(warp * kNt + j) * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-      consumers_sync();
-      const int i = tid & 7, col = tid >> 3;   // feature, column
-      if (ok && col < rows && col < 8 * kNt) {
-        const float* from = reinterpret_cast<const float*>(red + (col >> 3) * 32 + 4 * i + ((col & 7) >> 1)) + (col & 1);
-        float gate = 0.f, up = 0.f;
-#pragma unroll
-        for (int v = 0; v < kWarps; ++v) gate += from[v * kNt * 128], up += from[v * kNt * 128 + 2];
-        float weight = 1.f;
-        if (!shared) {
-          const int* ids = reinterpret_cast<const int*>(smem + P.at_ids);
-          const float* gates = reinterpret_cast<const float*>(smem + P.at_gates);
-          const int t = nth_bit(sl.mask, col);
-          weight = 0.f;
-          for (int j = 0; j < p.k; ++j) weight += ids[t * p.k + j] == sl.expert ? gates[t * p.k + j] : 0.f;
-        }
-        const float v = weight * (gelu16(gate, p.gelu) * up);
-        uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) + static_cast<long long>(sl.base + col) * f + f0 + i;
-        *a = kBf16 ? float_to_bf16_bits(v) : __half_as_ushort(__float2half_rn(v));
-      }
+      const float v = gate * (gelu16(acc[i], p.gelu) * acc[2 + i]);
+      a[static_cast<long long>(col) * f] = kBf16 ? float_to_bf16_bits(v) : __half_as_ushort(__float2half_rn(v));
     }
   }
   __syncthreads();
@@ -376,124 +408,115 @@ __device__ __forceinline__ float ld_rank(const float* at, uint32_t rank) {
   return v;
 }
 
-// The chunks of a unit: each picked expert's along f, then the shared expert's.
-struct DownChunks {
-  int n_slots, per, all, f, fs, kc, kcs;
-  __device__ __forceinline__ Chunk at(int i) const {
-    Chunk c;
-    c.slot = min(i / per, n_slots);
-    const int first = i - c.slot * per;
-    const bool shared = c.slot == n_slots;
-    c.k0 = first * (shared ? kcs : kc);
-    c.k = min(shared ? kcs : kc, (shared ? fs : f) - c.k0);
-    return c;
-  }
-};
-
-template <bool kBf16, bool kW8, int kNt>
-__global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
+template <bool kBf16, bool kW8>
+__global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
                                                          const __grid_constant__ Plan P, int split) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Shared S;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ Shared<kWarpsDown, kStagesDown> S;
+  constexpr int kWarps = kWarpsDown, kStages = kStagesDown, kThreads = 32 * kWarps;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int rank = static_cast<int>(cluster_rank()), d0 = blockIdx.x / split * 16;
   constexpr int kSize = kW8 ? 1 : 2;
-  init_ring(S, p, P.stages);
+  constexpr int kCols = kColsDown, kStageBytes = kCols * kColBytes, kColValues = kCol / kSize;
+  prepare(p, maps, P, smem, S);
   // ids and weights are older than the first kernel, which let this one start after its own wait
   list_slots(p, P, smem, S);
   const Slot* slots = reinterpret_cast<const Slot*>(smem + P.at_slots);
-  DownChunks C;
-  C.n_slots = S.n_slots, C.f = p.f, C.fs = p.fs, C.kc = P.kc_f, C.kcs = P.kc_fs, C.per = divide_up(p.f, P.kc_f);
-  C.all = C.n_slots * C.per + (p.fs ? divide_up(p.fs, P.kc_fs) : 0);
-  const int first = static_cast<int>(static_cast<long long>(C.all) * rank / split);
-  const int n = static_cast<int>(static_cast<long long>(C.all) * (rank + 1) / split) - first;
+  const int n_routed = S.n_routed;
+  // a unit's columns of 128 bytes, slot after slot, in equal parts: a chunk lies in one slot and one part
+  const int per = divide_up(p.f, kColValues), per_shared = divide_up(p.fs, kColValues);
+  const int all = n_routed * per + (S.n_slots - n_routed) * per_shared;
+  const int part = rank * kWarps + warp, parts = split * kWarps;
+  const int first = static_cast<int>(static_cast<long long>(all) * part / parts);
+  const int end = static_cast<int>(static_cast<long long>(all) * (part + 1) / parts);
+  uint8_t* const stages = smem + warp * kStages * kStageBytes;
+  uint64_t* const full = S.full[warp];
+  float* const sums = reinterpret_cast<float*>(smem + P.at_sums);   // [warp][token][16]
+  float* const own = sums + warp * p.t * 16;
+  for (int i = lane; i < p.t * 16; i += 32) own[i] = 0.f;
 
-  if (warp == kWarps) {
-    if (elect_one()) {
-      const auto load_w = [&](const Chunk& c, int s) {
-        const bool shared = c.slot == C.n_slots;
-        const int kc = shared ? P.kc_fs : P.kc_f;
-        mbar_arrive_expect_tx(&S.full[s], 16 * kc * kSize + __popc(slots[c.slot].mask) * c.k * 2);
-        load_down(smem + s * P.stage, shared ? &maps.shared : &maps.routed, c.k0 * kSize / 4, d0, max(slots[c.slot].expert, 0),
-                  &S.full[s]);
-      };
-      const auto load_a = [&](const Chunk& c, int s) {
-        const bool shared = c.slot == C.n_slots;
-        const int f = shared ? p.fs : p.f, rows = __popc(slots[c.slot].mask);
-        const uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
-                            static_cast<long long>(slots[c.slot].base) * f + c.k0;
-        uint8_t* to = smem + s * P.stage + 16 * (shared ? P.kc_fs : P.kc_f) * kSize;
-        for (int i = 0; i < rows; ++i, a += f, to += P.pitch_x) bulk_g2s(to, a, 2 * c.k, &S.full[s]);
-      };
-      const int early = min(min(n, P.stages), p.stall);
-      for (int i = 0; i < early; ++i) load_w(C.at(first + i), i);
-      pdl_wait();
-      for (int i = 0; i < early; ++i) load_a(C.at(first + i), i);
-      for (int i = early; i < min(n, p.stall); ++i) {
-        const int s = i % P.stages;
-        if (!wait_bar(&S.empty[s], ((i / P.stages) & 1) ^ 1, &S.waits)) break;
-        const Chunk c = C.at(first + i);
-        load_w(c, s);
-        load_a(c, s);
-      }
-    }
-    __syncwarp();
+  struct Place {
+    int slot, col, left;   // in the slot; of this part's columns from here on
+    __device__ __forceinline__ int cols(int of_slot) const { return min(min(kCols, left), of_slot - col); }
+  };
+  const auto of_slot = [&](const Place& at) { return at.slot >= n_routed ? per_shared : per; };
+  const auto advance = [&](Place& at) {
+    const int n = at.cols(of_slot(at));
+    at.left -= n;
+    at.col += n;
+    if (at.col == of_slot(at)) at.col = 0, ++at.slot;
+  };
+  const auto load = [&](const Place& at, int s) {
+    const int cols = at.cols(of_slot(at));
+    mbar_arrive_expect_tx(&full[s], cols * kColBytes);
+    for (int i = 0; i < cols; ++i)
+      load_down(stages + s * kStageBytes + i * kColBytes, at.slot >= n_routed ? &maps.shared : &maps.routed, (at.col + i) * (kCol / 4),
+                d0, max(slots[at.slot].expert, 0), &full[s]);
+  };
+  Place at;
+  at.left = end - first;
+  {
+    const bool shared = first >= n_routed * per;
+    const int i = shared ? first - n_routed * per : first, n = max(shared ? per_shared : per, 1), s = i / n;
+    at.slot = shared ? n_routed + s : s;
+    at.col = i - s * n;
   }
-  pdl_wait();   // y may be in use until here
+  Place next = at;
+  int loads = 0;
+  const auto load_next = [&] {
+    if (next.left <= 0 || loads >= p.stall) return;
+    if (elect_one()) load(next, loads % kStages);
+    ++loads;
+    advance(next);
+  };
+  for (int i = 0; i < kStages; ++i) load_next();
+  __syncwarp();
+  pdl_wait();      // a; and y may be in use until here
   pdl_trigger();
-  float* part = reinterpret_cast<float*>(smem + P.at_red);   // [column][16] of this CTA, behind the warps' sums
-  constexpr int kRed = kWarps * kNt * 32 * 4;
+
   bool ok = true;
-  if (warp < kWarps) {
-    const int g = lane >> 2, t = lane & 3;
-    float acc[kNt][4] = {}, own[kNt][4] = {};   // of all experts, of the one at hand
-    const int kb = divide_up(p.f, 128), kbs = divide_up(p.fs, 128), db = divide_up(p.d, 128);
-    for (int i = 0; i < n; ++i) {
-      const int s = i % P.stages;
-      const Chunk c = C.at(first + i);
-      const uint32_t mask = slots[c.slot].mask;
-      const bool shared = c.slot == C.n_slots;
-      const int kc = shared ? P.kc_fs : P.kc_f;
-      const float* scale = !kW8 ? nullptr
-                           : shared ? p.shared.down_scale + d0 / 128 * kbs
-                                    : p.routed.down_scale + (static_cast<long long>(slots[c.slot].expert) * db + d0 / 128) * kb;
-      ok = ok && wait_bar_warp(&S.full[s], (i / P.stages) & 1, &S.waits);
-      if (ok) {
-        const uint32_t w = smem_u32(smem + s * P.stage), x = w + 16 * kc * kSize;
-        uint32_t xr[kNt];
-#pragma unroll
-        for (int j = 0; j < kNt; ++j) {
-          const int col = 8 * j + g;
-          xr[j] = (mask >> col) & 1 ? x + __popc(mask & ((1u << col) - 1)) * P.pitch_x : 0;
-        }
-        chunk_products<kBf16, kW8, kNt>(own, w, xr, 32, kc, c.k, c.k0, scale, scale, warp, lane);
-        if (i + 1 == n || C.at(first + i + 1).slot != c.slot) {
-#pragma unroll
-          for (int j = 0; j < kNt; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              if ((mask >> (8 * j + 2 * t + (v & 1))) & 1) acc[j][v] += own[j][v];
-              own[j][v] = 0.f;
-            }
-        }
-      }
-      __syncwarp();
-      if (lane == 0) mbarrier_arrive(&S.empty[s]);
+  float acc[4] = {};
+  const int db = divide_up(p.d, 128);
+  for (int it = 0; at.left > 0; ++it) {
+    const int s = it % kStages, k0 = at.col * kColValues;
+    const bool shared = at.slot >= n_routed;
+    const Slot slot = slots[at.slot];
+    const int f = shared ? p.fs : p.f, k = min(at.cols(of_slot(at)) * kColValues, f - k0);
+    TokenWords<kW8, kCols> tokens;
+    tokens.load(g < __popc(slot.mask) ? p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
+                                            static_cast<long long>(slot.base + g) * f + k0
+                                      : nullptr,
+                k, lane);
+    float sc = 0.f;
+    if (kW8 && kCol * (lane & 15) < k) {
+      const long long block = (shared ? 0LL : static_cast<long long>(slot.expert) * db) + d0 / 128;
+      sc = __ldg((shared ? p.shared.down_scale : p.routed.down_scale) + block * divide_up(f, 128) + k0 / 128 + (lane & 15));
     }
-    float4* red = reinterpret_cast<float4*>(smem + P.at_red);
+    if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
+    chunk_products<kBf16, kW8, kCols>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
+    __syncwarp();
+    load_next();
+    const int was = at.slot;
+    advance(at);
+    if (at.slot != was || at.left <= 0) {   // two rows of columns 2 (lane % 4) and the next
 #pragma unroll
-    for (int j = 0; j < kNt; ++j) red[(warp * kNt + j) * 32 + lane] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-    consumers_sync();
-    const int row = tid & 15;
-    for (int col = tid >> 4; col < p.t; col += 16) {
-      const float* from = part + ((col >> 3) * 32 + 4 * (row & 7) + ((col & 7) >> 1)) * 4 + (col & 1) + (row >> 3) * 2;
-      float sum = 0.f;
-#pragma unroll
-      for (int v = 0; v < kWarps; ++v) sum += from[v * kNt * 128];
-      part[kRed + col * 16 + row] = sum;
+      for (int v = 0; v < 4; ++v) {
+        const int col = 2 * (lane & 3) + (v & 1);
+        if (col < __popc(slot.mask)) own[nth_bit(slot.mask, col) * 16 + row_of(g) + 8 * (v >> 1)] += acc[v];
+        acc[v] = 0.f;
+      }
     }
   }
-  ok = ok && !S.waits.abort;
+  __syncthreads();
+  // the warps' sums; each CTA's are then in the first warp's place
+  for (int i = tid; i < 16 * p.t; i += kThreads) {
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < kWarps; ++v) sum += sums[v * p.t * 16 + i];
+    sums[i] = sum;
+  }
+  ok = !S.waits.abort;
   if (split > 1)
     cluster_sync();
   else
@@ -504,14 +527,14 @@ __global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__
       if (col % split != rank) continue;
       float sum = 0.f;
       if (split == 1)
-        sum = part[kRed + i];
+        sum = sums[i];
       else
-        for (int r = 0; r < split; ++r) sum += ld_rank(part + kRed + i, r);
-      const long long at = col * p.ldy + d0 + row;
+        for (int r = 0; r < split; ++r) sum += ld_rank(sums + i, r);
+      const long long to = col * p.ldy + d0 + row;
       if (p.out_f32)
-        static_cast<float*>(p.y)[at] = sum;
+        static_cast<float*>(p.y)[to] = sum;
       else
-        static_cast<uint16_t*>(p.y)[at] = kBf16 ? float_to_bf16_bits(sum) : __half_as_ushort(__float2half_rn(sum));
+        static_cast<uint16_t*>(p.y)[to] = kBf16 ? float_to_bf16_bits(sum) : __half_as_ushort(__float2half_rn(sum));
     }
   if (split > 1) cluster_sync();   // the others may still read this CTA's sums
   __syncthreads();
@@ -520,25 +543,18 @@ __global__ void __launch_bounds__(kThreads) k_layer_down(const __grid_constant__
 
 // ------------------------------------------------------------------ launches
 
-// e4m3 rows have half the bytes of the token rows beside them, which two words a lane of 32 bytes apart read: 16 bytes more
-// than a multiple of 128 keep eight lanes apart there, 64 where a row's four lanes read 64 bytes.
-Plan make_plan(const LayerParams& p, bool w8, bool down) {
+// Of the routed experts: each has a token at least, or eight.
+int most_slots(const LayerParams& p) { return std::min(p.t * p.k, p.E + p.t * p.k / kTokens); }
+
+Plan make_plan(const LayerParams& p, bool down) {
   Plan P{};
-  const int size = w8 ? 1 : 2;
-  P.kc_d = chunk_of(p.d, size), P.kc_f = chunk_of(p.f, size), P.kc_fs = chunk_of(p.fs, size);
-  const int kc = down ? std::max(P.kc_f, P.kc_fs) : P.kc_d, nt = p.t <= 8 ? 1 : 4;
-  P.pitch_x = divide_up(2 * kc, 128) * 128 + (w8 ? 16 : 64);
-  P.stage = divide_up(16 * kc * size + p.t * P.pitch_x, 128) * 128;
-  P.slots = std::min(p.t * p.k, p.E);
-  const int red = kWarps * nt * 512 * (down ? 1 : 2) + (down ? nt * 512 : 0);
-  const int lists = 4 * p.E + 8 * p.t * p.k + static_cast<int>(sizeof(Slot)) * (P.slots + 1) + 64;
-  P.stages = std::clamp((kBudget - red - lists) / P.stage, 2, kMaxStages);
-  P.at_red = P.stages * P.stage;
-  P.at_mask = P.at_red + red;
+  const int slots = most_slots(p) + divide_up(p.t, kTokens);
+  P.at_sums = (down ? kWarpsDown * kStagesDown * kColsDown : kWarpsUp * kStagesUp * kColsUp) * kColBytes;
+  P.at_mask = P.at_sums + (down ? kWarpsDown * p.t * 64 : 0);
   P.at_ids = P.at_mask + 4 * p.E;
   P.at_gates = P.at_ids + 4 * p.t * p.k;
   P.at_slots = P.at_gates + 4 * p.t * p.k;
-  P.bytes = P.at_slots + static_cast<int>(sizeof(Slot)) * (P.slots + 1);
+  P.bytes = P.at_slots + static_cast<int>(sizeof(Slot)) * slots + 1024;   // the stages start at a multiple of 1024
   return P;
 }
 
@@ -547,36 +563,36 @@ bool encode_words(CUtensorMap* m, const void* base, int rank, const cuuint64_t* 
   PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
   const cuuint32_t ones[4] = {1, 1, 1, 1};
   return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dim, stride,
-                          box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [E][2][f][d] in boxes of kc values x 8 features x both halves.
-bool map_up(CUtensorMap* m, const void* base, int E, int f, int d, int size, int kc) {
+// [E][2][f][d] in boxes of 128 bytes x 8 features x both halves.
+bool map_up(CUtensorMap* m, const void* base, int E, int f, int d, int size) {
   const cuuint64_t row = static_cast<cuuint64_t>(d) * size;
   const cuuint64_t dim[4] = {row / 4, static_cast<cuuint64_t>(f), 2, static_cast<cuuint64_t>(E)};
   const cuuint64_t stride[3] = {row, row * f, row * 2 * f};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(kc * size / 4), 8, 2, 1};
+  const cuuint32_t box[4] = {kCol / 4, 8, 2, 1};
   return encode_words(m, base, 4, dim, stride, box);
 }
 
-// [E][d][f] in boxes of kc values x 16 outputs.
-bool map_down(CUtensorMap* m, const void* base, int E, int d, int f, int size, int kc) {
+// [E][d][f] in boxes of 128 bytes x 16 outputs.
+bool map_down(CUtensorMap* m, const void* base, int E, int d, int f, int size) {
   const cuuint64_t row = static_cast<cuuint64_t>(f) * size;
   const cuuint64_t dim[3] = {row / 4, static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(E)};
   const cuuint64_t stride[2] = {row, row * d};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kc * size / 4), 16, 1};
+  const cuuint32_t box[3] = {kCol / 4, 16, 1};
   return encode_words(m, base, 3, dim, stride, box);
 }
 
 template <typename K, typename... A>
-bool launch(K kernel, int grid, const Plan& P, int cluster, cudaStream_t s, const A&... args) {
+bool launch(K kernel, int grid, int threads, const Plan& P, int cluster, cudaStream_t s, const A&... args) {
   if (P.bytes > 48 * 1024 - 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P.bytes) != cudaSuccess)
     return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = P.bytes;
   cfg.stream = s;
   cudaLaunchAttribute at[2];
@@ -591,29 +607,26 @@ bool launch(K kernel, int grid, const Plan& P, int cluster, cudaStream_t s, cons
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
-template <bool kBf16, bool kW8, int kNt>
+template <bool kBf16, bool kW8>
 bool launch_both(const LayerParams& p, int sms, cudaStream_t s) {
   constexpr int kSize = kW8 ? 1 : 2;
-  const Plan up = make_plan(p, kW8, false), down = make_plan(p, kW8, true);
+  const Plan up = make_plan(p, false), down = make_plan(p, true);
   Maps m_up, m_down;
-  if (!map_up(&m_up.routed, p.routed.gate_up, p.E, p.f, p.d, kSize, up.kc_d) ||
-      !map_down(&m_down.routed, p.routed.down, p.E, p.d, p.f, kSize, down.kc_f))
+  if (!map_up(&m_up.routed, p.routed.gate_up, p.E, p.f, p.d, kSize) ||
+      !map_down(&m_down.routed, p.routed.down, p.E, p.d, p.f, kSize))
     return false;
-  if (p.fs && (!map_up(&m_up.shared, p.shared.gate_up, 1, p.fs, p.d, kSize, up.kc_d) ||
-               !map_down(&m_down.shared, p.shared.down, 1, p.d, p.fs, kSize, down.kc_fs)))
+  if (p.fs && (!map_up(&m_up.shared, p.shared.gate_up, 1, p.fs, p.d, kSize) ||
+               !map_down(&m_down.shared, p.shared.down, 1, p.d, p.fs, kSize)))
     return false;
-  // every CTA the same number of units, as far as the picked experts are known here: two CTAs an SM
-  const int units = up.slots * (p.f / 8) + p.fs / 8, rounds = divide_up(units, 2 * sms);
-  if (!launch(k_layer_up<kBf16, kW8, kNt>, divide_up(units, rounds), up, 1, s, m_up, p, up)) return false;
-  const int blocks = p.d / 16, chunks = down.slots * divide_up(p.f, down.kc_f) + (p.fs ? divide_up(p.fs, down.kc_fs) : 0);
+  // one CTA an SM, or as many as the units of the most slots need; a CTA's warps share the units evenly
+  const int slots = most_slots(p);
+  const long long units = static_cast<long long>(slots) * (p.f / 8) + divide_up(p.t, kTokens) * (p.fs / 8);
+  const int grid = static_cast<int>(std::min<long long>(sms, units));
+  if (!launch(k_layer_up<kBf16, kW8>, grid, 32 * kWarpsUp, up, 1, s, m_up, p, up)) return false;
+  const int blocks = p.d / 16, cols = slots * divide_up(p.f * kSize, kCol) + divide_up(p.fs * kSize, kCol);
   int split = 1;
-  while (split < 8 && 2 * split * blocks <= 2 * sms && 2 * split <= chunks) split *= 2;
-  return launch(k_layer_down<kBf16, kW8, kNt>, blocks * split, down, split, s, m_down, p, down, split);
-}
-
-template <bool kBf16, bool kW8>
-bool launch_of(const LayerParams& p, int sms, cudaStream_t s) {
-  return p.t <= 8 ? launch_both<kBf16, kW8, 1>(p, sms, s) : launch_both<kBf16, kW8, 4>(p, sms, s);
+  while (split < 8 && 2 * split * blocks <= 2 * sms && 2 * split * kWarpsDown * kColsDown <= cols) split *= 2;
+  return launch(k_layer_down<kBf16, kW8>, blocks * split, 32 * kWarpsDown, down, split, s, m_down, p, down, split);
 }
 
 }  // namespace
@@ -625,8 +638,8 @@ bool launch_layer(bool weights8, const LayerParams& params, cudaStream_t s) {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return false;
-  if (weights8) return p.bf16 ? launch_of<true, true>(p, sms, s) : launch_of<false, true>(p, sms, s);
-  return p.bf16 ? launch_of<true, false>(p, sms, s) : launch_of<false, false>(p, sms, s);
+  if (weights8) return p.bf16 ? launch_both<true, true>(p, sms, s) : launch_both<false, true>(p, sms, s);
+  return p.bf16 ? launch_both<true, false>(p, sms, s) : launch_both<false, false>(p, sms, s);
 }
 
 bool layer_gave_up(cudaStream_t s, uint32_t* count) {
@@ -634,3 +647,4 @@ bool layer_gave_up(cudaStream_t s, uint32_t* count) {
 }
 
 }  // namespace moe
+

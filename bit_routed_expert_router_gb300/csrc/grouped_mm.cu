@@ -38,6 +38,7 @@
 #include "ops8.h"
 #include "tc16.cuh"
 #include "tensor_map.h"
+#include "tile_regs.cuh"
 #include "waits.cuh"
 
 namespace moe {
@@ -49,8 +50,7 @@ using namespace tc16;
 constexpr int kMaxE = 1024;
 constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
 constexpr int kHalf = 16384;
-constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 32 bytes: multiples of 16, and the
-constexpr int kEpiPitch16 = 48;      // 16-byte words of eight rows hit all 32 banks
+constexpr int kEpiPitch16 = 48;      // bytes between staged rows of 32 bytes, as kEpiPitch
 constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memory lanes, 32 columns in turn
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kUWarps = 4;           // adapters: warps that stage u
@@ -115,18 +115,6 @@ static_assert(sizeof(BigSmem<GM_FWD, GM_PLAIN>) + 1024 <= 227 * 1024 &&
 static_assert(kEpiBytes >= 4 * 8 * kEpiPitch && kEpiBytes % 16 == 0 &&
                   kEpiPitch % 16 == 0 && kEpiPitch16 % 16 == 0,
               "staged rows");
-
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, int bf16) {
-  if (bf16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// Row range of expert e: inside [0, m] whatever the offsets hold.
-__device__ __forceinline__ int clamp_off(int v, int m) { return min(max(v, 0), m); }
 
 // The two operands' tensor maps.  The rows' map comes in boxes of 16 (i + 1)
 // rows, so a stage's rows are one load whatever their number: loads of 16 rows
@@ -227,14 +215,6 @@ __device__ __forceinline__ bool next_tile(Smem& S, Walk& w, uint32_t lead_empty,
 }
 
 // ------------------------------------------------------------------ adapter term of the epilogue
-
-// Two fp32 values in one register pair, and d = a b + d on both at once.
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
-}
-__device__ __forceinline__ void fma_f32x2(uint64_t& d, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
-}
 
 // Eight 16-bit values as four pairs of floats.
 __device__ __forceinline__ void widen8(uint64_t (&o)[4], uint4 v, int bf16) {
@@ -360,36 +340,6 @@ __device__ __forceinline__ bool split_f16(const uint4& v, uint4& hi, uint4& lo) 
 }
 
 // ------------------------------------------------------------------ the persistent kernel
-
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 w;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
-  return w;
-}
-
-// The stores of one warp: 32 columns of its accumulator lanes as fragments,
-// turned through the warp's own shared memory so that every lane stores 16
-// bytes.  All of a tensor's fragments are staged before the first is read
-// back: one warp barrier each way, and four independent loads and stores.
-
-// 32 features x 32 columns of 16-bit values: 64 contiguous bytes of a column.
-__device__ __forceinline__ void store_32x32(uint32_t buf, const float (&v)[2][16], int bf16, uint16_t* out, long long ld,
-                                            int cols, int feats, int lane) {
-  __syncwarp();   // earlier reads of this buffer are done
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    stmatrix4_trans(buf + j * 8 * kEpiPitch + (lane & 7) * kEpiPitch + (lane >> 3) * 16,
-                    pack16(v[0][4 * j], v[0][4 * j + 1], bf16), pack16(v[0][4 * j + 2], v[0][4 * j + 3], bf16),
-                    pack16(v[1][4 * j], v[1][4 * j + 1], bf16), pack16(v[1][4 * j + 2], v[1][4 * j + 3], bf16));
-  __syncwarp();
-  const int f = 8 * (lane & 3);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = 8 * j + (lane >> 2);
-    const uint4 w = lds128(buf + c * kEpiPitch + (lane & 3) * 16);
-    if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
-  }
-}
 
 // One feature a lane of 32 fp32 columns: each store of the warp is 128 contiguous bytes of a column.
 __device__ __forceinline__ void store_f32(const float (&v)[32], float* out, long long ld, int cols, int feats, int lane) {
@@ -1655,12 +1605,12 @@ bool grouped_gave_up(cudaStream_t s, bool* news) try {
   static std::mutex lock;
   static std::map<std::pair<int, cudaStream_t>, uint32_t> told;   // counts by device and stream
   int dev = 0;
-  uint32_t own = 0, layer = 0;
+  uint32_t own = 0, layer = 0, mm8 = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaMemcpyFromSymbolAsync(&own, g_gave_up, sizeof(own), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      !layer_gave_up(s, &layer) || cudaStreamSynchronize(s) != cudaSuccess)
+      !layer_gave_up(s, &layer) || !mm8_gave_up(s, &mm8) || cudaStreamSynchronize(s) != cudaSuccess)
     return false;
-  const uint32_t count = own + layer;
+  const uint32_t count = own + layer + mm8;
   {
     const std::lock_guard<std::mutex> hold(lock);
     const auto known = told.find({dev, s});

@@ -56,10 +56,13 @@ struct Mm8Params {
   int out = 0;
   float* sa = nullptr;                // gated: [m][ceil(n / 2 / 128)]
   int gelu = 0;
+  int limit = 0, stall = 0;           // set by the launches: bounded waits, in 1024 cycles; loads after which they stop
 };
 
 // false: a CUDA call failed.
 bool launch_grouped8(bool gated, const Mm8Params& p, cudaStream_t s);
+// Enqueues a copy of the count of its CTAs in which a wait ran out.
+bool mm8_gave_up(cudaStream_t s, uint32_t* count);
 
 constexpr int kLayerTokens = 32, kLayerTopK = 32;
 

@@ -36,6 +36,16 @@ inline bool encode_tiles(CUtensorMap* m, const void* base, int rank, const cuuin
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same over bytes, in rows of 128.
+inline bool encode_byte_tiles(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dim, const cuuint64_t* stride,
+                              const cuuint32_t* box) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return encode && encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dim, stride,
+                          box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // A map over bf16 or fp16 values for stores of 32 x 32: rows of 64 bytes in
 // shared memory, swizzled over their own width.
 inline bool encode_store(CUtensorMap* m, void* base, const cuuint64_t (&dim)[3], const cuuint64_t (&stride)[2], bool bf16) {

@@ -67,10 +67,17 @@ struct Tile {
   int r0, rows;   // first row of x, rows
 };
 
-// Tile t in the order expert, feature tile, row tile.
+// Tile t in the order expert, feature tile, row tile; a whole warp, which looks at 32 experts at a time (one after the other they
+// took longer than some tiles).  e: the last tile's expert.
 __device__ __forceinline__ bool tile_at(const Smem8& S, int E, int ft, int feats, int t, int& e, Tile& T) {
-  while (e < E && S.tiles[e + 1] * ft <= t) ++e;
-  if (e >= E) return false;
+  const int lane = threadIdx.x & 31;
+  uint32_t later = 0;
+  for (; e < E; e += 32) {
+    later = __ballot_sync(0xFFFFFFFFu, e + lane < E && S.tiles[min(e + lane, E - 1) + 1] * ft > t);
+    if (later) break;
+  }
+  if (!later) return false;
+  e += __ffs(later) - 1;
   const int nt = S.tiles[e + 1] - S.tiles[e], rem = t - S.tiles[e] * ft, f = rem / nt, c = rem - f * nt;
   const int lo = S.off[e], rows = S.off[e + 1] - lo, part = (rows + nt - 1) / nt;
   T.e = e;
@@ -161,13 +168,16 @@ struct Cols16 {
   __device__ __forceinline__ uint64_t pair(int i) const { return static_cast<uint64_t>(r[2 * i + 1]) << 32 | r[2 * i]; }
 };
 
-// The weights' scales of 128 weight rows, 32 blocks at a time: lane i holds that of block i.
-struct BlockScales {
-  const float* from;
-  float mine;
-  __device__ __forceinline__ float at(int b, int blocks, int lane) {
-    if ((b & 31) == 0) mine = b + lane < blocks ? __ldg(from + b + lane) : 0.f;
-    return __shfl_sync(0xFFFFFFFFu, mine, b & 31);
+// The scales of a block that an adding thread needs: of its row, and of its columns' blocks of weight rows.
+template <int kOf>
+struct Scales {
+  const float *sx, *sw;
+  int at[kOf];
+  float x, w[kOf];
+  __device__ __forceinline__ void load(int b) {
+    x = sx[b];
+#pragma unroll
+    for (int i = 0; i < kOf; ++i) w[i] = __ldg(sw + at[i] + b);
   }
 };
 
@@ -212,14 +222,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
   if (warp < 4) {
     give_registers<kFewRegs>();
     if (warp == 0) {
-      if (elect_one()) {
-        int it = 0, s = 0;
-        uint32_t phase = 1;
-        bool go = true;
-        for (int t = blockIdx.x; go && tile_at(S, p.E, ft, kFeats, t, e, T); t += gridDim.x) {
-          const int box = box_of(T.rows);
-          for (int b = 0; b < blocks; ++b, ++it) {
-            if (!(go = it < p.stall && wait_bar(&S.empty[s], phase, &S.waits))) break;
+      int it = 0, s = 0;
+      uint32_t phase = 1;
+      bool go = true;
+      for (int t = blockIdx.x; go && tile_at(S, p.E, ft, kFeats, t, e, T); t += gridDim.x) {
+        const int box = box_of(T.rows);
+        if (elect_one())
+          for (int b = 0; b < blocks; ++b) {
+            if (!(go = it + b < p.stall && wait_bar(&S.empty[s], phase, &S.waits))) break;
             mbar_arrive_expect_tx(&S.full[s], kW + (2048 << box));
             const uint32_t w = smem_u32(S.ring) + s * stage_bytes, bar = smem_u32(&S.full[s]);
             load_3d<false>(w, &maps.w, 128 * b, T.f0, T.e, bar);
@@ -227,7 +237,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
             load_2d<false>(w + kW, &maps.x[box], 128 * b, T.r0, bar);
             if (++s == stages) s = 0, phase ^= 1;
           }
-        }
+        it += blocks;
+        go = __all_sync(0xFFFFFFFFu, go);
       }
     } else if (warp == 1) {
       if (elect_one()) {
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
         int it = 0, s = 0;
         uint32_t phase = 0;
         bool go = true;
-        for (int t = blockIdx.x; go && tile_at(S, p.E, ft, kFeats, t, e, T); t += gridDim.x) {
+        for (int t = blockIdx.x; go && t < S.tiles[p.E] * ft; t += gridDim.x) {
           for (int b = 0; b < blocks; ++b, ++it) {
             const int buf = it & 1;
             if (!(go = wait_bar(&S.full[s], phase, &S.waits) && wait_bar(&S.acc_empty[buf], ((it >> 1) & 1) ^ 1, &S.waits))) break;
@@ -255,58 +266,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
     take_registers<kManyRegs>();
     const int q = warp & 3, half = (warp - 4) >> 2;   // this warp's lanes of tensor memory, its half of the columns
     const int rows_w = (p.n + 127) / 128;             // blocks of weight rows
+    const int r = 32 * q + lane;                      // this thread's row of a tile
+    Scales<kGated ? 3 : 1> sc;
+    // gated: of the gate rows, and of the (one or two) blocks of the up rows
+    const auto start = [&](const Tile& T) {
+      const int f0 = T.f0 + (kGated ? 64 : 128) * half;
+      sc.sx = p.sx + static_cast<long long>(max(T.r0 + min(r, T.rows - 1), 0)) * blocks;
+      sc.sw = p.sw + static_cast<long long>(T.e) * rows_w * blocks;
+      sc.at[0] = min(f0 / 128, rows_w - 1) * blocks;
+      if constexpr (kGated) {
+        sc.at[1] = min((feats + f0) / 128, rows_w - 1) * blocks;
+        sc.at[2] = min((feats + f0) / 128 + 1, rows_w - 1) * blocks;
+      }
+      sc.load(0);
+    };
     int it = 0, n_tile = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && tile_at(S, p.E, ft, kFeats, t, e, T); t += gridDim.x, ++n_tile) {
-      const int r = 32 * q + lane;        // this thread's row of the tile
+    bool ok = true, more = tile_at(S, p.E, ft, kFeats, blockIdx.x, e, T);
+    if (more) start(T);
+    for (int t = blockIdx.x; ok && more; t += gridDim.x, ++n_tile) {
       const bool rows_here = 32 * q < T.rows;
       // The sums of 128 columns, two a register pair.  Plain: features f0 ..; gated: 64 gate columns, then their up columns.
       const int f0 = T.f0 + (kGated ? 64 : 128) * half;
       uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0;
-      const float* sw = p.sw + static_cast<long long>(T.e) * rows_w * blocks;
-      // scales of the first rows' block, and gated of the (one or two) blocks of the up rows
-      BlockScales s0{sw + min(f0 / 128, rows_w - 1) * blocks, 0.f}, s1{sw + min((feats + f0) / 128, rows_w - 1) * blocks, 0.f},
-          s2{sw + min((feats + f0) / 128 + 1, rows_w - 1) * blocks, 0.f};
-      const int in_s1 = ((feats + f0) / 128 + 1) * 128 - (feats + f0);   // up rows in the first of them
-      // The row's scales four blocks at a time, the next ones on their way meanwhile.
-      const float* sx = p.sx + static_cast<long long>(max(T.r0 + min(r, T.rows - 1), 0)) * blocks;
-      float x[4], x_next[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x_next[i] = sx[min(i, blocks - 1)];
+      const int in_first = ((feats + f0) / 128 + 1) * 128 - (feats + f0);   // up rows in the first of their blocks
+      const uint32_t at0 = tmem + (static_cast<uint32_t>(32 * q) << 16) + (kGated ? 64 : 128) * half;
       for (int b = 0; b < blocks; ++b, ++it) {
         const int buf = it & 1;
-        if ((b & 3) == 0) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = x_next[i], x_next[i] = sx[min(b + 4 + i, blocks - 1)];
-        }
-        const float mine = (b & 2) ? ((b & 1) ? x[3] : x[2]) : ((b & 1) ? x[1] : x[0]);
-        const float g = mine * s0.at(b, blocks, lane);
-        const float u = kGated ? mine * s1.at(b, blocks, lane) : g, u2 = kGated ? mine * s2.at(b, blocks, lane) : g;
         if (!(ok = wait_bar_warp(&S.acc_full[buf], (it >> 1) & 1, &S.waits))) break;
         fence_after();
-        // 16 columns at a time, the next ones on their way meanwhile; the accumulator is given back once the last have come
+        // this block's factors; the next one's scales are on their way while it is added
+        const float f[3] = {sc.x * sc.w[0], kGated ? sc.x * sc.w[kGated ? 1 : 0] : 0.f, kGated ? sc.x * sc.w[kGated ? 2 : 0] : 0.f};
+        if (b + 1 < blocks) sc.load(b + 1);
         if (rows_here) {
-          const uint32_t at = tmem + buf * kWeightRows + (static_cast<uint32_t>(32 * q) << 16) + (kGated ? 64 : 128) * half;
+          const uint32_t at = at0 + buf * kWeightRows;
           const auto column = [](int i) { return kGated ? 16 * (i & 3) + 128 * (i >> 2) : 16 * i; };
           Cols16 v[2];
           v[0].issue(at);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             v[i & 1].wait();
-            if (i < 7) v[(i + 1) & 1].issue(at + column(i + 1));
-            const float f = !kGated || i < 4 ? g : 16 * (i & 3) < in_s1 ? u : u2;
-            const uint64_t f2 = pack_f32x2(f, f);
+            if (i < 7) {
+              v[(i + 1) & 1].issue(at + column(i + 1));
+            } else {   // the accumulator is given back
+              fence_before();
+              __syncwarp();
+              if (lane == 0) mbarrier_arrive(&S.acc_empty[buf]);
+            }
+            const float now = !kGated || i < 4 ? f[0] : 16 * (i & 3) < in_first ? f[1] : f[2];
+            const uint64_t f2 = pack_f32x2(now, now);
 #pragma unroll
             for (int j = 0; j < 8; ++j) fma_f32x2(acc[8 * i + j], v[i & 1].pair(j), f2);
           }
+        } else {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbarrier_arrive(&S.acc_empty[buf]);
         }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbarrier_arrive(&S.acc_empty[buf]);
       }
       if (!ok) break;
+      const Tile D = T;   // done; the next tile's first scales come while it is stored
+      if ((more = tile_at(S, p.E, ft, kFeats, t + gridDim.x, e, T))) start(T);
       if constexpr (kGated) {
         // a in the gate values' place, and its largest magnitude
         uint32_t top = 0;
@@ -322,10 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
         if (lane == 0) mbarrier_arrive(&S.top_full);
         if (!(ok = wait_bar_warp(&S.top_full, n_tile & 1, &S.waits))) break;
         // (two tiles' maxima in turn: who writes one again knows that all have come to the tile between)
-        const Scale8 sc = scale8(max(top, S.top[n_tile & 1][half ^ 1][r]));
-        if (r < T.rows) {
-          const long long row = T.r0 + r;
-          if (half == 0) p.sa[row * ((feats + 127) / 128) + T.f0 / 128] = sc.scale;
+        const Scale8 s8 = scale8(max(top, S.top[n_tile & 1][half ^ 1][r]));
+        if (r < D.rows) {
+          const long long row = D.r0 + r;
+          if (half == 0) p.sa[row * ((feats + 127) / 128) + D.f0 / 128] = s8.scale;
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + row * p.ldy + f0);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -333,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const uint64_t a = acc[8 * i + 2 * j], c = acc[8 * i + 2 * j + 1];
-              w[j] = to_e4m3x4(lo_f32(a) * sc.inverse, hi_f32(a) * sc.inverse, lo_f32(c) * sc.inverse, hi_f32(c) * sc.inverse);
+              w[j] = to_e4m3x4(lo_f32(a) * s8.inverse, hi_f32(a) * s8.inverse, lo_f32(c) * s8.inverse, hi_f32(c) * s8.inverse);
             }
             if (f0 + 16 * i < feats) out[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -342,7 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
         // 64 bytes of 32 rows at a time through the warp's own shared memory, so that a store takes 64 bytes of eight rows
         uint8_t* const stage = S.out[warp - 4];
         const bool wide = p.out == MOE_F32;
-        const int n_parts = wide ? 8 : 4;
+        const int n_parts = wide ? 8 : 4, each = wide ? 4 : 8;
+        const int row0 = 32 * q + (lane >> 2), first = f0 + each * (lane & 3);   // the first of this lane's four rows
+        uint8_t* out = static_cast<uint8_t*>(p.y) + ((D.r0 + row0) * p.ldy + first) * (wide ? 4 : 2);
+        const long long step = 8 * p.ldy * (wide ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if (i >= n_parts) break;
@@ -363,19 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
             *reinterpret_cast<uint4*>(stage + lane * kOutPitch + 16 * j) = w;
           }
           __syncwarp();
-          const int f = f0 + (wide ? 16 * i + 4 * (lane & 3) : 32 * i + 8 * (lane & 3));
+          if (first + 4 * each * i < feats)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int row = 8 * j + (lane >> 2);
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + row * kOutPitch + 16 * (lane & 3));
-            if (32 * q + row < T.rows && f < feats) {
-              const long long at = (T.r0 + 32 * q + row) * p.ldy + f;
-              if (wide)
-                *reinterpret_cast<uint4*>(static_cast<float*>(p.y) + at) = w;
-              else
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + at) = w;
-            }
-          }
+            for (int j = 0; j < 4; ++j)
+              if (row0 + 8 * j < D.rows)
+                *reinterpret_cast<uint4*>(out + j * step + 64 * i) =
+                    *reinterpret_cast<const uint4*>(stage + (8 * j + (lane >> 2)) * kOutPitch + 16 * (lane & 3));
         }
       }
     }

@@ -53,9 +53,10 @@ struct Smem8 {
   uint8_t ring[kRing];
   alignas(16) uint8_t out[kAddWarps][32 * kOutPitch];
   uint32_t top[2][2][kRows];   // gated: rows' maxima over each half of the features, two tiles in turn
-  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], top_full;
+  uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], top_full, tile_full[4], tile_empty[4];
   uint32_t tmem;
   Waits waits;
+  int4 tile[4];           // of the adding warps: expert, first feature, first row, rows; expert -1: no more
   int box;                // rows that a load takes at most: 16 << box
   int off[kMaxE + 1];     // clamped to [0, m], never going down
   int tiles[kMaxE + 1];   // row tiles before each expert
@@ -202,6 +203,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       mbar_init(&S.acc_empty[i], kAddWarps);
     }
     mbar_init(&S.top_full, kAddWarps);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&S.tile_full[i], 1);
+      mbar_init(&S.tile_empty[i], kAddWarps);
+    }
     S.waits.abort = 0;
     S.waits.limit = p.limit;
     fence_mbar_init();
@@ -261,6 +266,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
           }
         }
       }
+    } else if (warp == 2) {
+      bool go = true, more = true;
+      for (int t = blockIdx.x, n = 0; go && more; t += gridDim.x, ++n) {   // the adding warps' tiles
+        more = tile_at(S, p.E, ft, kFeats, t, e, T);
+        if (!(go = wait_bar_warp(&S.tile_empty[n & 3], ((n >> 2) & 1) ^ 1, &S.waits))) break;
+        if (lane == 0) {
+          S.tile[n & 3] = make_int4(more ? T.e : -1, T.f0, T.r0, T.rows);
+          mbarrier_arrive(&S.tile_full[n & 3]);
+        }
+      }
     }
   } else {
     take_registers<kManyRegs>();
@@ -281,9 +296,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       sc.load(0);
     };
     int it = 0, n_tile = 0;
-    bool ok = true, more = tile_at(S, p.E, ft, kFeats, blockIdx.x, e, T);
-    if (more) start(T);
-    for (int t = blockIdx.x; ok && more; t += gridDim.x, ++n_tile) {
+    bool ok = true, more = false;
+    const auto next_tile = [&](int n) {
+      if (!(ok = wait_bar_warp(&S.tile_full[n & 3], (n >> 2) & 1, &S.waits))) return;
+      const int4 v = S.tile[n & 3];
+      __syncwarp();
+      if (lane == 0) mbarrier_arrive(&S.tile_empty[n & 3]);
+      T.e = v.x, T.f0 = v.y, T.r0 = v.z, T.rows = v.w;
+      if ((more = v.x >= 0)) start(T);
+    };
+    next_tile(0);
+    for (; ok && more; ++n_tile) {
       const bool rows_here = 32 * q < T.rows;
       // The sums of 128 columns, two a register pair.  Plain: features f0 ..; gated: 64 gate columns, then their up columns.
       const int f0 = T.f0 + (kGated ? 64 : 128) * half;
@@ -327,7 +350,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       }
       if (!ok) break;
       const Tile D = T;   // done; the next tile's first scales come while it is stored
-      if ((more = tile_at(S, p.E, ft, kFeats, t + gridDim.x, e, T))) start(T);
+      next_tile(n_tile + 1);
+      if (!ok) break;
       if constexpr (kGated) {
         // a in the gate values' place, and its largest magnitude
         uint32_t top = 0;

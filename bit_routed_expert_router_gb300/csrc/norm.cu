@@ -56,130 +56,169 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 enum { kNoDelta = 0, kDelta16 = 1, kDelta32 = 2 };
 
-// A row is the threads of one threadIdx.y; kV words of eight values a thread.
-template <bool kBf16, int kDelta, int kV>
-__global__ void __launch_bounds__(1024) k_norm(NormParams p) {
-  __shared__ float s_sum[32];
-  const int r = blockIdx.x * blockDim.y + threadIdx.y, n_words = p.d / 8, warps = blockDim.x / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const bool in_row = r < p.m;
+// A row is the threads of one threadIdx.y; kV words of eight values a thread, of kR rows at a time: one barrier for all of them,
+// and more loads on their way (4096 rows of 2816, 8-bit out: one row at a time 18.0 us).
+template <bool kBf16, int kDelta, int kV, int kR>
+__global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 1024) k_norm(NormParams p) {
+  __shared__ float s_sum[kR][32];
+  const int n_words = p.d / 8, warps = blockDim.x / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = (blockIdx.x * blockDim.y + threadIdx.y) * kR;
   pdl_wait();
   pdl_trigger();
-  float v[kV][8], sum = 0.f;
+  float v[kR][kV][8], sum[kR];
   uint4 w[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
-    if (in_row && i < n_words) {
-      const uint4 h = *reinterpret_cast<const uint4*>(row16(p.h, p.ldh, r, c));
-      if (p.weight) w[j] = __ldg(reinterpret_cast<const uint4*>(p.weight) + i);
-      widen<kBf16>(v[j], h);
-      if (kDelta != kNoDelta) {
-        float d[8];
-        if (kDelta == kDelta16) {
-          widen<kBf16>(d, *reinterpret_cast<const uint4*>(row16(p.delta, p.ldd, r, c)));
-        } else {
+    uint4 h[kR], d16[kR];
+    float4 d32[kR][2];
+#pragma unroll
+    for (int q = 0; q < kR; ++q) {
+      const int r = r0 + q;
+      if (r < p.m && i < n_words) {
+        h[q] = *reinterpret_cast<const uint4*>(row16(p.h, p.ldh, r, c));
+        if (kDelta == kDelta16) d16[q] = *reinterpret_cast<const uint4*>(row16(p.delta, p.ldd, r, c));
+        if (kDelta == kDelta32) {
           const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(p.delta) + r * p.ldd + c);
-          const float4 a = at[0], b = at[1];
-          d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+          d32[q][0] = at[0], d32[q][1] = at[1];
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[j][k] += d[k];
-        const uint4 stored = narrow<kBf16>(v[j]);
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h_out) + r * p.ldo + c) = stored;
-        widen<kBf16>(v[j], stored);
       }
+    }
+    if (p.weight && i < n_words) w[j] = __ldg(reinterpret_cast<const uint4*>(p.weight) + i);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum = fmaf(v[j][k], v[j][k], sum);
-    } else {
+    for (int q = 0; q < kR; ++q) {
+      const int r = r0 + q;
+      if (r < p.m && i < n_words) {
+        widen<kBf16>(v[q][j], h[q]);
+        if (kDelta != kNoDelta) {
+          float d[8];
+          if (kDelta == kDelta16) {
+            widen<kBf16>(d, d16[q]);
+          } else {
+            const float4 a = d32[q][0], b = d32[q][1];
+            d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+          }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] = 0.f;
+          for (int k = 0; k < 8; ++k) v[q][j][k] += d[k];
+          const uint4 stored = narrow<kBf16>(v[q][j]);
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h_out) + r * p.ldo + c) = stored;
+          widen<kBf16>(v[q][j], stored);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[q][j][k] = 0.f;
+      }
     }
   }
-  sum = warp_sum(sum);
+#pragma unroll
+  for (int q = 0; q < kR; ++q) {
+    sum[q] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[q] = fmaf(v[q][j][k], v[q][j][k], sum[q]);
+    sum[q] = warp_sum(sum[q]);
+  }
   if (warps > 1) {
-    float* mine = s_sum + threadIdx.y * warps;
-    if (lane == 0) mine[warp] = sum;
+    const int mine = threadIdx.y * warps;
+    if (lane == 0)
+#pragma unroll
+      for (int q = 0; q < kR; ++q) s_sum[q][mine + warp] = sum[q];
     __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < warps; ++i) sum += mine[i];
+#pragma unroll
+    for (int q = 0; q < kR; ++q) sum[q] = 0.f;
+    for (int i = 0; i < warps; ++i)
+#pragma unroll
+      for (int q = 0; q < kR; ++q) sum[q] += s_sum[q][mine + i];
   }
-  const float rstd = 1.f / sqrtf(sum / static_cast<float>(p.d) + p.eps);
 #pragma unroll
-  for (int j = 0; j < kV; ++j) {
-    const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
-    const bool in = in_row && i < n_words;
+  for (int q = 0; q < kR; ++q) {
+    const int r = r0 + q;
+    const float rstd = 1.f / sqrtf(sum[q] / static_cast<float>(p.d) + p.eps);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[j][k] *= rstd;
-    if (p.weight && in) {
-      float f[8];
-      widen<kBf16>(f, w[j]);
+    for (int j = 0; j < kV; ++j) {
+      const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
+      const bool in = r < p.m && i < n_words;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[j][k] *= f[k];
-    }
-    if (in && p.y) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.ldy + c) = narrow<kBf16>(v[j]);
-    if (p.y8) {
-      uint32_t top = 0;   // of the 16 lanes that hold a group; words past the row are 0
+      for (int k = 0; k < 8; ++k) v[q][j][k] *= rstd;
+      if (p.weight && in) {
+        float f[8];
+        widen<kBf16>(f, w[j]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[j][k]));
-      if (!in) top = 0;
+        for (int k = 0; k < 8; ++k) v[q][j][k] *= f[k];
+      }
+      if (in && p.y) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.ldy + c) = narrow<kBf16>(v[q][j]);
+      if (p.y8) {
+        uint32_t top = 0;   // of the 16 lanes that hold a group; words past the row are 0
 #pragma unroll
-      for (int d = 8; d; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-      const Scale8 s = scale8(top);
-      if (in) {
-        const float q = s.inverse;
-        *reinterpret_cast<uint2*>(p.y8 + r * p.ldy8 + c) =
-            make_uint2(to_e4m3x4(v[j][0] * q, v[j][1] * q, v[j][2] * q, v[j][3] * q),
-                       to_e4m3x4(v[j][4] * q, v[j][5] * q, v[j][6] * q, v[j][7] * q));
-        if ((i & 15) == 0) p.scale[static_cast<long long>(r) * ((p.d + 127) / 128) + i / 16] = s.scale;
+        for (int k = 0; k < 8; ++k) top = max(top, abs_bits(v[q][j][k]));
+        if (!in) top = 0;
+#pragma unroll
+        for (int d = 8; d; d >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        const Scale8 s = scale8(top);
+        if (in) {
+          const float x = s.inverse;
+          float(&a)[8] = v[q][j];
+          *reinterpret_cast<uint2*>(p.y8 + r * p.ldy8 + c) =
+              make_uint2(to_e4m3x4(a[0] * x, a[1] * x, a[2] * x, a[3] * x), to_e4m3x4(a[4] * x, a[5] * x, a[6] * x, a[7] * x));
+          if ((i & 15) == 0) p.scale[static_cast<long long>(r) * ((p.d + 127) / 128) + i / 16] = s.scale;
+        }
       }
     }
   }
 }
 
-// CTA b takes the rows b, b + parts, ...: its columns' part of the weight gradient stays in registers and is written once.
-template <bool kBf16, int kV>
-__global__ void __launch_bounds__(1024) k_norm_grad(NormGradParams p) {
+// CTA b takes the rows b, b + parts, ...: its columns' part of the weight gradient stays in registers and is written once.  The
+// next row's loads are on their way while a row is at hand.  (Without that, and with 512 parts, more than fit the GPU at once,
+// 36.0 us for 4096 rows of 2816.)
+template <bool kBf16, int kV, int kThreads>
+__global__ void __launch_bounds__(kThreads, kV == 1 ? 2 : 1) k_norm_grad(NormGradParams p) {
   __shared__ float2 s_sum[2][32];
   const int n_words = p.d / 8, warps = blockDim.x / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  float dw[kV][8];
-  uint4 wt[kV];
+  float dw[kV][8], w[kV][8];
+  uint4 h[kV], dy[kV], dres[kV];   // the next row
+  const auto load = [&](int r) {
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+      const int i = threadIdx.x + j * blockDim.x;
+      if (i >= n_words || r >= p.m) continue;
+      h[j] = *reinterpret_cast<const uint4*>(row16(p.h, p.ldh, r, 8 * i));
+      dy[j] = *reinterpret_cast<const uint4*>(row16(p.dy, p.lddy, r, 8 * i));
+      if (p.dres) dres[j] = *reinterpret_cast<const uint4*>(row16(p.dres, p.lddres, r, 8 * i));
+    }
+  };
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
+    h[j] = dy[j] = dres[j] = make_uint4(0, 0, 0, 0);   // what lies behind a row stays 0
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[j][k] = 0.f;
-    if (p.weight && i < n_words) wt[j] = __ldg(reinterpret_cast<const uint4*>(p.weight) + i);
+    for (int k = 0; k < 8; ++k) dw[j][k] = 0.f, w[j][k] = 1.f;
+    if (p.weight && i < n_words) widen<kBf16>(w[j], __ldg(reinterpret_cast<const uint4*>(p.weight) + i));
   }
+  load(blockIdx.x);
+  const float over_d = 1.f / static_cast<float>(p.d);
   int turn = 0;
   for (int r = blockIdx.x; r < p.m; r += gridDim.x, turn ^= 1) {
-    uint4 h[kV], dy[kV], dres[kV];
-    float ss = 0.f, dot = 0.f;
+    float a[kV][8], b[kV][8], o[kV][8], ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
-      if (i >= n_words) continue;
-      h[j] = *reinterpret_cast<const uint4*>(row16(p.h, p.ldh, r, c));
-      dy[j] = *reinterpret_cast<const uint4*>(row16(p.dy, p.lddy, r, c));
-      if (p.dres) dres[j] = *reinterpret_cast<const uint4*>(row16(p.dres, p.lddres, r, c));
-    }
-#pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      if (threadIdx.x + j * blockDim.x >= n_words) continue;
-      float a[8], b[8], w[8];
-      widen<kBf16>(a, h[j]);
-      widen<kBf16>(b, dy[j]);
-      if (p.weight) widen<kBf16>(w, wt[j]);
+      widen<kBf16>(a[j], h[j]);
+      widen<kBf16>(b[j], dy[j]);
+      widen<kBf16>(o[j], dres[j]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        ss = fmaf(a[k], a[k], ss);
-        dot = fmaf(p.weight ? b[k] * w[k] : b[k], a[k], dot);
+        ss = fmaf(a[j][k], a[j][k], ss);
+        dot = fmaf(b[j][k] * w[j][k], a[j][k], dot);
       }
     }
-    ss = warp_sum(ss);
-    dot = warp_sum(dot);
+    load(r + gridDim.x);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) {
+      ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
+      dot += __shfl_xor_sync(0xFFFFFFFFu, dot, d);
+    }
     if (warps > 1) {
       if (lane == 0) s_sum[turn][warp] = make_float2(ss, dot);
       __syncthreads();
@@ -191,23 +230,16 @@ __global__ void __launch_bounds__(1024) k_norm_grad(NormGradParams p) {
       }
     }
     const float rstd = 1.f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
-    const float mean = dot * rstd / static_cast<float>(p.d);   // of dy w xh
+    const float mean = rstd * (rstd * (dot * rstd * over_d));   // of dy w xh, times rstd^2
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
-      if (i >= n_words) continue;
-      float a[8], b[8], w[8], o[8];
-      widen<kBf16>(a, h[j]);
-      widen<kBf16>(b, dy[j]);
-      if (p.weight) widen<kBf16>(w, wt[j]);
-      if (p.dres) widen<kBf16>(o, dres[j]);
+      const int i = threadIdx.x + j * blockDim.x;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float xh = a[k] * rstd, g = p.weight ? b[k] * w[k] : b[k], dx = rstd * (g - xh * mean);
-        dw[j][k] = fmaf(b[k], xh, dw[j][k]);
-        o[k] = p.dres ? o[k] + dx : dx;
+        dw[j][k] = fmaf(b[j][k], a[j][k] * rstd, dw[j][k]);
+        o[j][k] += fmaf(b[j][k] * w[j][k], rstd, -(a[j][k] * mean));
       }
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dh) + r * p.lddh + c) = narrow<kBf16>(o);
+      if (i < n_words) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dh) + r * p.lddh + 8 * i) = narrow<kBf16>(o[j]);
     }
   }
   if (!p.part) return;
@@ -221,27 +253,28 @@ __global__ void __launch_bounds__(1024) k_norm_grad(NormGradParams p) {
   }
 }
 
-// Sums of the columns of part [parts][d], in a fixed order: 32 columns a CTA, 32 threads for each four of them.
-__global__ void __launch_bounds__(256) k_norm_dweight(const float* part, int parts, int d, float* dweight) {
-  __shared__ float4 s_sum[32][8];
+// Sums of the columns of part [parts][d], in a fixed order: 32 columns a CTA, 64 threads for each four of them.
+__global__ void __launch_bounds__(512) k_norm_dweight(const float* part, int parts, int d, float* dweight) {
+  __shared__ float4 s_sum[64][8];
   const int q = threadIdx.x & 7, g = threadIdx.x >> 3, c = 32 * blockIdx.x + 4 * q;
   pdl_wait();
   pdl_trigger();
   float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < d)
 #pragma unroll 8
-    for (int i = g; i < parts; i += 32) {
+    for (int i = g; i < parts; i += 64) {
       const float4 v = *reinterpret_cast<const float4*>(part + static_cast<long long>(i) * d + c);
       sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
     }
   s_sum[g][q] = sum;
   __syncthreads();
-  if (g != 0 || c >= d) return;
-  for (int i = 1; i < 32; ++i) {
-    const float4 v = s_sum[i][q];
-    sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
-  }
-  *reinterpret_cast<float4*>(dweight + c) = sum;
+  if (threadIdx.x >= 32) return;
+  // 32 columns, one a thread
+  const float* col = reinterpret_cast<const float*>(s_sum) + threadIdx.x;
+  float total = 0.f;
+#pragma unroll 16
+  for (int i = 0; i < 64; ++i) total += col[32 * i];
+  if (32 * blockIdx.x + threadIdx.x < d) dweight[32 * blockIdx.x + threadIdx.x] = total;
 }
 
 template <typename K, typename... A>
@@ -258,34 +291,55 @@ bool launch(K kernel, dim3 grid, dim3 block, cudaStream_t s, const A&... args) {
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
 }
 
+template <bool kBf16, int kDelta, int kV, int kR>
+bool launch_rows(const NormParams& p, int nt, int rows, cudaStream_t s) {
+  return launch(k_norm<kBf16, kDelta, kV, kR>, dim3((p.m + rows * kR - 1) / (rows * kR)), dim3(nt, rows), s, p);
+}
+
 template <bool kBf16, int kDelta>
-bool launch_norm_of(const NormParams& p, cudaStream_t s) {
+bool launch_norm_of(const NormParams& p, int sms, cudaStream_t s) {
   const int words = p.d / 8;
-  if (words > 1024) return launch(k_norm<kBf16, kDelta, 2>, dim3(p.m), dim3(1024), s, p);
+  if (words > 1024) return launch_rows<kBf16, kDelta, 2, 1>(p, 1024, 1, s);
   const int nt = (words + 31) / 32 * 32, rows = std::max(1, 256 / nt);
-  return launch(k_norm<kBf16, kDelta, 1>, dim3((p.m + rows - 1) / rows), dim3(nt, rows), s, p);
+  // two rows a thread once every SM has eight CTAs of them (and the threads have the registers)
+  if (nt <= 512 && p.m >= 16 * rows * sms) return launch_rows<kBf16, kDelta, 1, 2>(p, nt, rows, s);
+  return launch_rows<kBf16, kDelta, 1, 1>(p, nt, rows, s);
 }
 
 template <bool kBf16>
 bool launch_grad_of(const NormGradParams& p, cudaStream_t s) {
-  const int words = p.d / 8;
-  return words > 1024 ? launch(k_norm_grad<kBf16, 2>, dim3(p.parts), dim3(1024), s, p)
-                      : launch(k_norm_grad<kBf16, 1>, dim3(p.parts), dim3((words + 31) / 32 * 32), s, p);
+  const int words = p.d / 8, nt = (words + 31) / 32 * 32;
+  if (nt <= 384) return launch(k_norm_grad<kBf16, 1, 384>, dim3(p.parts), dim3(nt), s, p);
+  if (nt <= 512) return launch(k_norm_grad<kBf16, 1, 512>, dim3(p.parts), dim3(nt), s, p);
+  return launch(k_norm_grad<kBf16, 2, 1024>, dim3(p.parts), dim3((words + 63) / 64 * 32), s, p);
+}
+
+// Multiprocessors of the current device; 0: a CUDA call failed.
+int multiprocessors() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  return sms;
 }
 
 }  // namespace
 
 bool launch_norm(bool bf16, bool delta_f32, const NormParams& p, cudaStream_t s) {
-  if (!p.delta) return bf16 ? launch_norm_of<true, kNoDelta>(p, s) : launch_norm_of<false, kNoDelta>(p, s);
-  if (delta_f32) return bf16 ? launch_norm_of<true, kDelta32>(p, s) : launch_norm_of<false, kDelta32>(p, s);
-  return bf16 ? launch_norm_of<true, kDelta16>(p, s) : launch_norm_of<false, kDelta16>(p, s);
+  const int sms = multiprocessors();
+  if (!sms) return false;
+  if (!p.delta) return bf16 ? launch_norm_of<true, kNoDelta>(p, sms, s) : launch_norm_of<false, kNoDelta>(p, sms, s);
+  if (delta_f32) return bf16 ? launch_norm_of<true, kDelta32>(p, sms, s) : launch_norm_of<false, kDelta32>(p, sms, s);
+  return bf16 ? launch_norm_of<true, kDelta16>(p, sms, s) : launch_norm_of<false, kDelta16>(p, sms, s);
 }
 
 bool launch_norm_grad(bool bf16, const NormGradParams& params, cudaStream_t s) {
   NormGradParams p = params;
-  p.parts = std::min(p.m, kNormParts);
+  const int sms = multiprocessors();
+  if (!sms) return false;
+  // all CTAs at once: two an SM, or one of 1024 threads; more where a row is few warps
+  const int words = p.d / 8, warps = words > 512 ? (words + 63) / 64 : (words + 31) / 32;
+  p.parts = std::min({p.m, kNormParts, sms * std::max(1, 32 / warps)});
   if (!(bf16 ? launch_grad_of<true>(p, s) : launch_grad_of<false>(p, s))) return false;
-  return !p.part || launch(k_norm_dweight, dim3((p.d + 31) / 32), dim3(256), s, static_cast<const float*>(p.part), p.parts,
+  return !p.part || launch(k_norm_dweight, dim3((p.d + 31) / 32), dim3(512), s, static_cast<const float*>(p.part), p.parts,
                            p.d, p.dweight);
 }
 

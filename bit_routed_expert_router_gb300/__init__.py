@@ -354,10 +354,6 @@ def _whole(t, shape, dtype, dev: int) -> bool:
     return t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev
 
 
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
 def _call(fn, dev: int, stream, *args) -> int:
     if dev < 0:
         return MOE_EINVAL
@@ -502,28 +498,36 @@ def moe_rmsnorm(h, y=None, y8=None, scale=None, delta=None, h_out=None, weight=N
     sh = h.shape
     if len(sh) != 2:
         return MOE_EINVAL
-    (m, d), dev, dt = sh, h.get_device(), h.dtype
-    lds = []
-    for t, of in ((h, dt), (delta, None), (h_out, dt), (y, dt), (y8, _E4M3)):
-        if t is None:
-            lds.append(0)
-            continue
-        if t.shape != sh or (of is not None and t.dtype is not of) or t.get_device() != dev:
+    (m, d), dev, dt, th = sh, h.get_device(), h.dtype, h.stride()
+    if th[1] != 1 or (delta is None) != (h_out is None) or (y8 is None) != (scale is None):
+        return MOE_EINVAL
+    # a row's values are contiguous; the row stride of a single row says nothing
+    one = m <= 1
+    pd = po = py = p8 = ps = pw = None
+    ldd = ldo = ldy = ld8 = dd = 0
+    if delta is not None:
+        td, to = delta.stride(), h_out.stride()
+        if not (delta.shape == sh and h_out.shape == sh and td[1] == 1 and to[1] == 1 and h_out.dtype is dt and
+                delta.get_device() == dev and h_out.get_device() == dev):
             return MOE_EINVAL
-        st = t.stride()
-        if st[1] != 1:
+        pd, ldd, dd, po, ldo = delta.data_ptr(), d if one else td[0], _DTYPE.get(delta.dtype, -1), h_out.data_ptr(), d if one else to[0]
+    if y is not None:
+        ty = y.stride()
+        if not (y.shape == sh and ty[1] == 1 and y.dtype is dt and y.get_device() == dev):
             return MOE_EINVAL
-        # a row's values are contiguous; the row stride of a single row says nothing
-        lds.append(st[0] if m > 1 else d)
-    if (delta is None) != (h_out is None) or (y8 is None) != (scale is None):
-        return MOE_EINVAL
-    if weight is not None and not _whole(weight, (d,), dt, dev):
-        return MOE_EINVAL
-    if scale is not None and not _whole(scale, (m, (d + 127) // 128), _FLOAT32, dev):
-        return MOE_EINVAL
-    return _call(_fn.moe_rmsnorm, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), lds[0], _at(delta), lds[1],
-                 0 if delta is None else _DTYPE.get(delta.dtype, -1), _at(weight), eps, m, d, _at(h_out), lds[2], _at(y),
-                 lds[3], _at(y8), lds[4], _at(scale))
+        py, ldy = y.data_ptr(), d if one else ty[0]
+    if y8 is not None:
+        t8 = y8.stride()
+        if not (y8.shape == sh and t8[1] == 1 and y8.dtype is _E4M3 and y8.get_device() == dev and
+                _whole(scale, (m, (d + 127) // 128), _FLOAT32, dev)):
+            return MOE_EINVAL
+        p8, ld8, ps = y8.data_ptr(), d if one else t8[0], scale.data_ptr()
+    if weight is not None:
+        if not _whole(weight, (d,), dt, dev):
+            return MOE_EINVAL
+        pw = weight.data_ptr()
+    return _call(_fn.moe_rmsnorm, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), d if one else th[0], pd, ldd, dd, pw, eps, m, d,
+                 po, ldo, py, ldy, p8, ld8, ps)
 
 
 def moe_rmsnorm_grad(h, dy, dh, dres=None, weight=None, dweight=None, workspace=None, eps: float = 1e-6, stream=None) -> int:
@@ -534,27 +538,29 @@ def moe_rmsnorm_grad(h, dy, dh, dres=None, weight=None, dweight=None, workspace=
     sh = h.shape
     if len(sh) != 2:
         return MOE_EINVAL
-    (m, d), dev, dt = sh, h.get_device(), h.dtype
-    lds = []
-    for t in (h, dy, dh, dres):
-        if t is None:
-            lds.append(0)
-            continue
-        if t.shape != sh or t.dtype is not dt or t.get_device() != dev:
+    (m, d), dev, dt, th, ty, to = sh, h.get_device(), h.dtype, h.stride(), dy.stride(), dh.stride()
+    if not (dy.shape == sh and dh.shape == sh and th[1] == 1 and ty[1] == 1 and to[1] == 1 and dy.dtype is dt and
+            dh.dtype is dt and dy.get_device() == dev and dh.get_device() == dev):
+        return MOE_EINVAL
+    one = m <= 1
+    pr = pw = pdw = ws = None
+    ldr = nws = 0
+    if dres is not None:
+        tr = dres.stride()
+        if not (dres.shape == sh and tr[1] == 1 and dres.dtype is dt and dres.get_device() == dev):
             return MOE_EINVAL
-        st = t.stride()
-        if st[1] != 1:
+        pr, ldr = dres.data_ptr(), d if one else tr[0]
+    if weight is not None:
+        if not _whole(weight, (d,), dt, dev):
             return MOE_EINVAL
-        lds.append(st[0] if m > 1 else d)
-    if weight is not None and not _whole(weight, (d,), dt, dev):
-        return MOE_EINVAL
-    if dweight is not None and not _whole(dweight, (d,), _FLOAT32, dev):
-        return MOE_EINVAL
-    if workspace is not None and not (workspace.is_contiguous() and workspace.get_device() == dev):
-        return MOE_EINVAL
-    return _call(_fn.moe_rmsnorm_grad, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), lds[0], dy.data_ptr(), lds[1],
-                 _at(dres), lds[3], _at(weight), eps, m, d, dh.data_ptr(), lds[2], _at(dweight), _at(workspace),
-                 0 if workspace is None else workspace.nbytes)
+        pw = weight.data_ptr()
+    if dweight is not None:
+        if workspace is None or not (_whole(dweight, (d,), _FLOAT32, dev) and workspace.is_contiguous() and
+                                     workspace.get_device() == dev):
+            return MOE_EINVAL
+        pdw, ws, nws = dweight.data_ptr(), workspace.data_ptr(), workspace.nbytes
+    return _call(_fn.moe_rmsnorm_grad, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), d if one else th[0], dy.data_ptr(),
+                 d if one else ty[0], pr, ldr, pw, eps, m, d, dh.data_ptr(), d if one else to[0], pdw, ws, nws)
 
 
 def moe_grouped_mm8(x, sx, offsets, w, sw, y, stream=None) -> int:

@@ -52,7 +52,7 @@ struct Maps8 {
 struct Smem8 {
   uint8_t ring[kRing];
   alignas(16) uint8_t out[kAddWarps][32 * kOutPitch];
-  uint32_t top[2][2][kRows];   // gated: rows' maxima over each half of the features, two tiles in turn
+  float top[2][2][kRows];     // gated: rows' maxima over each half of the features, two tiles in turn
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], top_full, tile_full[4], tile_empty[4];
   uint32_t tmem;
   Waits waits;
@@ -354,20 +354,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       if (!ok) break;
       if constexpr (kGated) {
         // a in the gate values' place, and its largest magnitude
-        uint32_t top = 0;
+        float top = 0.f;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const float a0 = gelu16(lo_f32(acc[j]), kGelu) * lo_f32(acc[32 + j]);
           const float a1 = gelu16(hi_f32(acc[j]), kGelu) * hi_f32(acc[32 + j]);
           acc[j] = pack_f32x2(a0, a1);
-          if (f0 + 2 * j < feats) top = max(top, max(abs_bits(a0), abs_bits(a1)));
+          if (f0 + 2 * j < feats) top = max_abs(max_abs(top, a0), a1);
         }
         S.top[n_tile & 1][half][r] = top;
         __syncwarp();
         if (lane == 0) mbarrier_arrive(&S.top_full);
         if (!(ok = wait_bar_warp(&S.top_full, n_tile & 1, &S.waits))) break;
         // (two tiles' maxima in turn: who writes one again knows that all have come to the tile between)
-        const Scale8 s8 = scale8(max(top, S.top[n_tile & 1][half ^ 1][r]));
+        const Scale8 s8 = scale8(max_abs(top, S.top[n_tile & 1][half ^ 1][r]));
         if (r < D.rows) {
           const long long row = D.r0 + r;
           if (half == 0) p.sa[row * ((feats + 127) / 128) + D.f0 / 128] = s8.scale;

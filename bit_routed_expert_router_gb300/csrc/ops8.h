@@ -21,7 +21,7 @@ struct NormParams {
   float* scale = nullptr;   // [m][ceil(d / 128)]
   long long ldh = 0, ldd = 0, ldo = 0, ldy = 0, ldy8 = 0;   // elements
   int m = 0, d = 0;
-  float eps = 0.f;
+  float eps = 0.f, over_d = 0.f;   // over_d: 1 / d, set by the launches
 };
 
 struct NormGradParams {
@@ -34,7 +34,7 @@ struct NormGradParams {
   float* dweight = nullptr;
   long long ldh = 0, lddy = 0, lddres = 0, lddh = 0;
   int m = 0, d = 0, parts = 0;
-  float eps = 0.f;
+  float eps = 0.f, over_d = 0.f;   // parts and over_d (1 / d): set by the launches
 };
 
 // false: a CUDA call failed.

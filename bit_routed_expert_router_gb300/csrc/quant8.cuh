@@ -2,9 +2,10 @@
 //
 // The scale is max|v| / 448, so that the largest value lands on e4m3's largest;
 // the maximum is taken as at least 2^-100, so that a group of zeros has a scale
-// too.  v is multiplied by 448 / max|v| (fp32, rounded) before its one rounding
-// to e4m3, to the nearest, ties to even.  Maxima are compared as bit patterns, in
-// which an infinity and then a NaN lie above every number: a group with a NaN
+// too.  v is multiplied by 448 / max|v| before its one rounding to e4m3, to the
+// nearest, ties to even.  Both factors are products with fast reciprocals, within
+// 2^-22 of the quotients (as quotients they were a third of the norm's
+// instructions).  A NaN is the maximum of whatever it is with: a group with a NaN
 // has the scale NaN and only NaN, one with an infinity the scale infinity, its
 // finite values 0 and its infinities NaN.
 #pragma once
@@ -14,17 +15,24 @@
 namespace moe {
 
 constexpr float kMaxE4m3 = 448.f;
-constexpr uint32_t kTinyBits = 0x0D800000u;   // 2^-100
+constexpr float kTiny = 7.888609052210118e-31f;   // 2^-100
 
-__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+// The larger magnitude (top has none yet: 0); NaN if either is.
+__device__ __forceinline__ float max_abs(float top, float v) {
+  float r;
+  asm("{\n\t.reg .f32 a;\n\tabs.f32 a, %2;\n\tmax.NaN.f32 %0, %1, a;\n\t}" : "=f"(r) : "f"(top), "f"(v));
+  return r;
+}
 
 struct Scale8 {
   float scale, inverse;
 };
 
-__device__ __forceinline__ Scale8 scale8(uint32_t max_bits) {
-  const float top = __uint_as_float(max(max_bits, kTinyBits));
-  return {top / kMaxE4m3, kMaxE4m3 / top};
+__device__ __forceinline__ Scale8 scale8(float top) {
+  top = max_abs(kTiny, top);
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(top));   // subnormal results too
+  return {top * (1.f / kMaxE4m3), kMaxE4m3 * r};
 }
 
 // Two values as e4m3, a in the low byte; what is past 448 is 448, NaN stays.

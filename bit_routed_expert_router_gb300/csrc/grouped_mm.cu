@@ -34,6 +34,7 @@
 #include <type_traits>
 
 #include "gelu16.cuh"
+#include "allow_smem.h"
 #include "grouped.h"
 #include "ops8.h"
 #include "tc16.cuh"
@@ -1386,8 +1387,6 @@ __global__ void __launch_bounds__(192)
 
 // ------------------------------------------------------------------ launches
 
-constexpr int kMaxKernels = 16;
-
 // A wait's limit in 1024 cycles, and the loads after which a CTA's loading thread stops.
 constexpr int kDefaultLimit = static_cast<int>(kSpinLimitCycles / 1024), kNever = std::numeric_limits<int>::max();
 std::atomic<int> g_limit{kDefaultLimit}, g_stall{kNever};
@@ -1433,26 +1432,6 @@ bool map_gated(CUtensorMap* m, const void* base, int E, int f, int k, bool bf16)
   const cuuint64_t stride[4] = {row, row * f, row * 16, row * 2 * f};
   const cuuint32_t box[5] = {64, 16, 2, 4, 1};
   return encode_tiles(m, base, 5, dim, stride, box, bf16);
-}
-
-// Dynamic shared memory past 48 KB has to be allowed once for a kernel and device.
-template <typename K>
-bool allow_smem(K kernel, size_t smem) {
-  static std::atomic<uint64_t> done[kMaxKernels];   // devices, by kernel
-  static std::atomic<const void*> known[kMaxKernels];
-  int dev = 0, i = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const void* id = reinterpret_cast<const void*>(kernel);
-  for (; i < kMaxKernels; ++i) {
-    const void* at = known[i].load(std::memory_order_acquire);
-    if (at == id || (!at && known[i].compare_exchange_strong(at, id)) || at == id) break;
-  }
-  const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
-  if (i < kMaxKernels && (done[i].load(std::memory_order_acquire) & bit)) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return false;
-  if (i < kMaxKernels) done[i].fetch_or(bit, std::memory_order_release);
-  return true;
 }
 
 template <typename K>

@@ -24,6 +24,7 @@
 #include <algorithm>
 #include <limits>
 
+#include "allow_smem.h"
 #include "gelu16.cuh"
 #include "grouped.h"
 #include "moe.h"
@@ -450,8 +451,7 @@ bool launch(const Maps8& maps, const Mm8Params& p, int sms, cudaStream_t s) {
   const int per = kGelu >= 0 ? kWeightRows / 2 : kWeightRows;
   const long long most = (feats + per - 1) / per * (std::min(p.E, p.m) + static_cast<long long>(p.m) / kRows);
   const size_t smem = sizeof(Smem8) + 1024;
-  if (cudaFuncSetAttribute(k_grouped8<kGelu>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
-    return false;
+  if (!allow_smem(k_grouped8<kGelu>, smem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, most)));
   cfg.blockDim = dim3(kThreads);

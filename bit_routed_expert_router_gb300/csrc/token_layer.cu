@@ -29,6 +29,7 @@
 // kernel starts while the first one runs and fills its stages with weights.
 #include <algorithm>
 
+#include "allow_smem.h"
 #include "gelu16.cuh"
 #include "grouped.h"
 #include "ops8.h"
@@ -47,6 +48,7 @@ constexpr int kCol = 128, kColBytes = 16 * kCol;  // bytes of a weight row that 
 // seven; of 512 and 640 29.8 and 87.9).  Two CTAs of the second kernel fit an SM, one beside one of the first.
 constexpr int kColsUp = 4, kColsDown = 5;
 constexpr int kTokens = 8;                       // of a slot
+constexpr int kMostSmem = 160 * 1024;            // of either kernel: the stages, and the lists of 1024 pairs and experts
 
 struct Slot {
   int expert;      // -1: the shared expert
@@ -583,9 +585,7 @@ bool map_down(CUtensorMap* m, const void* base, int E, int d, int f, int size) {
 
 template <typename K, typename... A>
 bool launch(K kernel, int grid, int threads, const Plan& P, int cluster, cudaStream_t s, const A&... args) {
-  if (P.bytes > 48 * 1024 - 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P.bytes) != cudaSuccess)
-    return false;
+  if (!allow_smem(kernel, kMostSmem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);

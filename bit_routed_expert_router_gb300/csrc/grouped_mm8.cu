@@ -5,7 +5,7 @@
 //
 // and the gated form, whose output is e4m3 again with a scale for each 128 values.
 //
-// Persistent, one CTA an SM.  A tile is up to 128 rows of one expert (equal parts)
+// Persistent, one CTA an SM.  A tile is up to 128 rows of one expert
 // by 256 weight rows: 256 features, or gated the gate and the up rows of 128.  A
 // block of 128 is one stage of 128-byte rows and four MMAs into one of two
 // accumulators of 256 columns.  The MMA cannot scale by fp32 factors, so eight warps
@@ -22,6 +22,7 @@
 // take: 1,600 cycles a block for what takes 340 alone, with CTA pairs 1,500 (shared
 // expert's gate/up, 4096 rows: 144 and 90 us).
 #include <algorithm>
+#include <cstddef>
 #include <limits>
 
 #include "allow_smem.h"
@@ -43,26 +44,41 @@ constexpr int kRows = 128, kWeightRows = 256;     // of a tile
 constexpr int kMaxStages = 6, kRing = 196608, kW = kWeightRows * 128;
 constexpr int kAddWarps = 8, kThreads = 32 * (4 + kAddWarps);
 constexpr int kRowMaps = 4;
-constexpr int kOutPitch = 80;   // bytes between staged rows of 64: multiples of 16, eight rows' words in different banks
+constexpr int kOutBytes = 32 * 64;   // of an output buffer: 64 bytes of 32 rows, swizzled over their own width
 
 struct Maps8 {
   CUtensorMap w;
   CUtensorMap x[kRowMaps];   // boxes of 16 << i rows
+  CUtensorMap y;             // not gated: 64 bytes of 32 rows
 };
 
 struct Smem8 {
   uint8_t ring[kRing];
-  alignas(16) uint8_t out[kAddWarps][32 * kOutPitch];
   float top[2][2][kRows];     // gated: rows' maxima over each half of the features, two tiles in turn
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], top_full, tile_full[4], tile_empty[4];
   uint32_t tmem;
   Waits waits;
   int4 tile[4];           // of the adding warps: expert, first feature, first row, rows; expert -1: no more
   int box;                // rows that a load takes at most: 16 << box
-  int off[kMaxE + 1];     // clamped to [0, m], never going down
-  int tiles[kMaxE + 1];   // row tiles before each expert
+  // Behind it: the output's buffers (not gated: one or two for each adding warp), then the lists of the experts: their rows'
+  // offsets, clamped to [0, m] and never going down, and the row tiles before each.
+  alignas(1024) uint8_t rest[1];
 };
-static_assert(sizeof(Smem8) + 1024 <= 227 * 1024, "one CTA per SM");
+constexpr int kMostSmem = 227 * 1024 - 1024;   // the struct starts at a multiple of 1024
+
+// Bytes behind Smem8's fixed part; two buffers a warp where the lists leave room.
+__host__ __device__ __forceinline__ int out_buffers(bool gated, int E) {
+  const int fixed = static_cast<int>(offsetof(Smem8, rest)) + 8 * (E + 1);
+  return gated ? 0 : fixed + 2 * kAddWarps * kOutBytes <= kMostSmem ? 2 : 1;
+}
+static_assert(offsetof(Smem8, rest) + kAddWarps * kOutBytes + 8 * (kMaxE + 1) <= kMostSmem, "one CTA per SM");
+
+// The lists behind the buffers.
+struct Lists {
+  int *off, *tiles;
+  __device__ __forceinline__ Lists(Smem8& S, bool gated, int E)
+      : off(reinterpret_cast<int*>(S.rest + out_buffers(gated, E) * kAddWarps * kOutBytes)), tiles(off + E + 1) {}
+};
 
 struct Tile {
   int e, f0;      // expert, first feature
@@ -71,21 +87,21 @@ struct Tile {
 
 // Tile t in the order expert, feature tile, row tile; a whole warp, which looks at 32 experts at a time (one after the other they
 // took longer than some tiles).  e: the last tile's expert.
-__device__ __forceinline__ bool tile_at(const Smem8& S, int E, int ft, int feats, int t, int& e, Tile& T) {
+__device__ __forceinline__ bool tile_at(const Lists& L, int E, int ft, int feats, int t, int& e, Tile& T) {
   const int lane = threadIdx.x & 31;
   uint32_t later = 0;
   for (; e < E; e += 32) {
-    later = __ballot_sync(0xFFFFFFFFu, e + lane < E && S.tiles[min(e + lane, E - 1) + 1] * ft > t);
+    later = __ballot_sync(0xFFFFFFFFu, e + lane < E && L.tiles[min(e + lane, E - 1) + 1] * ft > t);
     if (later) break;
   }
   if (!later) return false;
   e += __ffs(later) - 1;
-  const int nt = S.tiles[e + 1] - S.tiles[e], rem = t - S.tiles[e] * ft, f = rem / nt, c = rem - f * nt;
-  const int lo = S.off[e], rows = S.off[e + 1] - lo, part = (rows + nt - 1) / nt;
+  const int nt = L.tiles[e + 1] - L.tiles[e], rem = t - L.tiles[e] * ft, f = rem / nt, c = rem - f * nt;
+  const int lo = L.off[e];
   T.e = e;
   T.f0 = f * feats;
-  T.r0 = lo + c * part;
-  T.rows = min(part, lo + rows - T.r0);   // the last part may be empty
+  T.r0 = lo + c * kRows;
+  T.rows = min(kRows, L.off[e + 1] - T.r0);
   return true;
 }
 
@@ -93,10 +109,10 @@ __device__ __forceinline__ bool tile_at(const Smem8& S, int E, int ft, int feats
 __device__ __forceinline__ int box_of(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
 // Offsets clamped and made to never go down, and the number of row tiles before each expert; one warp.
-__device__ void list_tiles(Smem8& S, const int32_t* offsets, int E, int m) {
+__device__ void list_tiles(Smem8& S, const Lists& L, const int32_t* offsets, int E, int m) {
   const int lane = threadIdx.x & 31;
   int base = 0, before = 0, most = 0;
-  if (lane == 0) S.tiles[0] = 0;
+  if (lane == 0) L.tiles[0] = 0;
   for (int e0 = 0; e0 <= E; e0 += 32) {
     const int e = e0 + lane;
     int v = e <= E ? clamp_off(offsets[e], m) : 0;
@@ -106,22 +122,30 @@ __device__ void list_tiles(Smem8& S, const int32_t* offsets, int E, int m) {
       if (lane >= d) v = max(v, o);
     }
     v = max(v, before);
-    if (e <= E) S.off[e] = v;
+    if (e <= E) L.off[e] = v;
     const int prev = __shfl_up_sync(0xFFFFFFFFu, v, 1), rows = e > 0 && e <= E ? v - (lane ? prev : before) : 0;
     const int nt = (rows + kRows - 1) / kRows;
-    if (nt) most = max(most, (rows + nt - 1) / nt);
+    most = max(most, min(rows, kRows));
     int c = nt;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int o = __shfl_up_sync(0xFFFFFFFFu, c, d);
       if (lane >= d) c += o;
     }
-    if (e > 0 && e <= E) S.tiles[e] = base + c;
+    if (e > 0 && e <= E) L.tiles[e] = base + c;
     base += __shfl_sync(0xFFFFFFFFu, c, 31);
     before = __shfl_sync(0xFFFFFFFFu, v, 31);
   }
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   if (lane == 0) S.box = box_of(most);
+}
+
+__device__ __forceinline__ void store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(map)),
+      "r"(x), "r"(y), "r"(src)
+      : "memory");
 }
 
 // kind::f8f6f4: fp32 accumulators, e4m3 operands, both K-major, M x N.
@@ -191,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   Smem8& S = *reinterpret_cast<Smem8*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Lists L(S, kGated, p.E);
   const int feats = kGated ? p.n / 2 : p.n, ft = (feats + kFeats - 1) / kFeats, blocks = (p.k + 127) / 128;
 
   if (tid == 0) {
@@ -215,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
   if (warp == 1) tmem_alloc<false>(&S.tmem, 2 * kWeightRows);
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) list_tiles(S, p.offsets, p.E, p.m);
+  if (warp == 0) list_tiles(S, L, p.offsets, p.E, p.m);
   fence_before();
   __syncthreads();
   fence_after();
@@ -231,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       int it = 0, s = 0;
       uint32_t phase = 1;
       bool go = true;
-      for (int t = blockIdx.x; go && tile_at(S, p.E, ft, kFeats, t, e, T); t += gridDim.x) {
+      for (int t = blockIdx.x; go && tile_at(L, p.E, ft, kFeats, t, e, T); t += gridDim.x) {
         const int box = box_of(T.rows);
         if (elect_one())
           for (int b = 0; b < blocks; ++b) {
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
         int it = 0, s = 0;
         uint32_t phase = 0;
         bool go = true;
-        for (int t = blockIdx.x; go && t < S.tiles[p.E] * ft; t += gridDim.x) {
+        for (int t = blockIdx.x; go && t < L.tiles[p.E] * ft; t += gridDim.x) {
           for (int b = 0; b < blocks; ++b, ++it) {
             const int buf = it & 1;
             if (!(go = wait_bar(&S.full[s], phase, &S.waits) && wait_bar(&S.acc_empty[buf], ((it >> 1) & 1) ^ 1, &S.waits))) break;
@@ -270,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
     } else if (warp == 2) {
       bool go = true, more = true;
       for (int t = blockIdx.x, n = 0; go && more; t += gridDim.x, ++n) {   // the adding warps' tiles
-        more = tile_at(S, p.E, ft, kFeats, t, e, T);
+        more = tile_at(L, p.E, ft, kFeats, t, e, T);
         if (!(go = wait_bar_warp(&S.tile_empty[n & 3], ((n >> 2) & 1) ^ 1, &S.waits))) break;
         if (lane == 0) {
           S.tile[n & 3] = make_int4(more ? T.e : -1, T.f0, T.r0, T.rows);
@@ -296,6 +321,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       }
       sc.load(0);
     };
+    [[maybe_unused]] const int n_buf = out_buffers(kGated, p.E);
+    [[maybe_unused]] uint32_t n_part = 0;
     int it = 0, n_tile = 0;
     bool ok = true, more = false;
     const auto next_tile = [&](int n) {
@@ -385,16 +412,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
           }
         }
       } else if (rows_here) {
-        // 64 bytes of 32 rows at a time through the warp's own shared memory, so that a store takes 64 bytes of eight rows
-        uint8_t* const stage = S.out[warp - 4];
-        const bool wide = p.out == MOE_F32;
-        const int n_parts = wide ? 8 : 4, each = wide ? 4 : 8;
-        const int row0 = 32 * q + (lane >> 2), first = f0 + each * (lane & 3);   // the first of this lane's four rows
-        uint8_t* out = static_cast<uint8_t*>(p.y) + ((D.r0 + row0) * p.ldy + first) * (wide ? 4 : 2);
+        // 64 bytes of 32 rows at a time through the warp's own buffers: the TMA engine writes one out while the next is filled,
+        // where all 32 rows are the tile's; of the last ones each row's words go out by themselves.  (Read back and stored by
+        // the warps, 64 bytes of eight rows an instruction, all of them took 2,500 cycles a tile: down, 4096 tokens, 114 us.)
+        const bool wide = p.out == MOE_F32, whole = 32 * q + 32 <= D.rows;
+        const int n_parts = wide ? 8 : 4, each = wide ? 16 : 32;   // features of a part
+        // the first of this lane's rows and words where rows go out by themselves
+        const int row0 = 32 * q + (lane >> 2), first = f0 + each / 4 * (lane & 3);
+        uint8_t* const out = static_cast<uint8_t*>(p.y) + ((D.r0 + row0) * p.ldy + first) * (wide ? 4 : 2);
         const long long step = 8 * p.ldy * (wide ? 4 : 2);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          if (i >= n_parts) break;
+          if (i >= n_parts || f0 + each * i >= feats) break;
+          uint8_t* const buf = S.rest + ((n_buf == 2 ? n_part & 1 : 0) * kAddWarps + warp - 4) * kOutBytes;
+          ++n_part;
+          if (lane == 0) {   // (this lane issues all of the warp's stores)
+            if (n_buf == 2 && whole)   // (parts that are not whole commit nothing that could be counted)
+              store_wait<1>();
+            else
+              store_wait<0>();
+          }
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -409,18 +446,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
               w = make_uint4(pack16(lo_f32(a[0]), hi_f32(a[0]), bf16), pack16(lo_f32(a[1]), hi_f32(a[1]), bf16),
                              pack16(lo_f32(a[2]), hi_f32(a[2]), bf16), pack16(lo_f32(a[3]), hi_f32(a[3]), bf16));
             }
-            *reinterpret_cast<uint4*>(stage + lane * kOutPitch + 16 * j) = w;
+            *reinterpret_cast<uint4*>(buf + 64 * lane + 16 * (j ^ ((lane >> 1) & 3))) = w;
+          }
+          if (whole) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) store_2d(&maps.y, smem_u32(buf), f0 + each * i, D.r0 + 32 * q);
+            continue;
           }
           __syncwarp();
-          if (first + 4 * each * i < feats)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (row0 + 8 * j < D.rows)
-                *reinterpret_cast<uint4*>(out + j * step + 64 * i) =
-                    *reinterpret_cast<const uint4*>(stage + (8 * j + (lane >> 2)) * kOutPitch + 16 * (lane & 3));
+          for (int j = 0; j < 4; ++j) {
+            if (32 * q + 8 * j >= D.rows) break;
+            if (row0 + 8 * j < D.rows && first + each * i < feats)
+              *reinterpret_cast<uint4*>(out + j * step + 64 * i) =
+                  *reinterpret_cast<const uint4*>(buf + 64 * (8 * j + (lane >> 2)) + 16 * ((lane & 3) ^ ((lane >> 3) & 3)));
+          }
         }
       }
     }
+    if (!kGated && lane == 0) store_wait<0>();   // before the buffers go
   }
   fence_before();
   __syncthreads();
@@ -445,13 +490,28 @@ bool map_weights8(CUtensorMap* m, const void* base, int E, int n, int k) {
   return encode_byte_tiles(m, base, 3, dim, stride, box);
 }
 
+// Stores of 64 bytes of 32 rows, swizzled over their own width.
+bool map_out(CUtensorMap* m, const Mm8Params& p) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  const int size = p.out == MOE_F32 ? 4 : 2;
+  const cuuint64_t dim[2] = {static_cast<cuuint64_t>(p.n), static_cast<cuuint64_t>(p.m)};
+  const cuuint64_t stride[1] = {static_cast<cuuint64_t>(p.ldy) * size};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / size), 32}, ones[2] = {1, 1};
+  return encode &&
+         encode(m, p.out == MOE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                   : p.out == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                2, p.y, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kGelu>
 bool launch(const Maps8& maps, const Mm8Params& p, int sms, cudaStream_t s) {
   const int feats = kGelu >= 0 ? p.n / 2 : p.n;
   const int per = kGelu >= 0 ? kWeightRows / 2 : kWeightRows;
   const long long most = (feats + per - 1) / per * (std::min(p.E, p.m) + static_cast<long long>(p.m) / kRows);
-  const size_t smem = sizeof(Smem8) + 1024;
-  if (!allow_smem(k_grouped8<kGelu>, smem)) return false;
+  const size_t smem = offsetof(Smem8, rest) + out_buffers(kGelu >= 0, p.E) * kAddWarps * kOutBytes + 8 * (p.E + 1) + 1024;
+  if (!allow_smem(k_grouped8<kGelu>, kMostSmem + 1024)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(sms, most)));
   cfg.blockDim = dim3(kThreads);
@@ -479,6 +539,7 @@ bool launch_grouped8(bool gated, const Mm8Params& params, cudaStream_t s) {
   for (int i = 0; i < kRowMaps && (i == 0 || 8 << i < most); ++i)
     if (!map_rows8(&maps.x[i], p.x, p.k, p.m, p.ldx, 16 << i)) return false;
   if (!map_weights8(&maps.w, p.w, p.E, p.n, p.k)) return false;
+  if (!gated && !map_out(&maps.y, p)) return false;
   if (!gated) return launch<-1>(maps, p, sms, s);
   return p.gelu == MOE_GELU_TANH ? launch<MOE_GELU_TANH>(maps, p, sms, s) : launch<MOE_GELU_ERF>(maps, p, sms, s);
 }

@@ -169,8 +169,8 @@ template <int kRegs>
 __device__ __forceinline__ void take_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-// 384 threads are launched with 168 registers each: 128 x 72 + 256 x 216 are the same 64,512.
-constexpr int kFewRegs = 72, kManyRegs = 216;
+// 384 threads are launched with 168 registers each: 128 x 40 + 256 x 232 are the same 64,512.
+constexpr int kFewRegs = 40, kManyRegs = 232;
 
 __device__ __forceinline__ float lo_f32(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
 __device__ __forceinline__ float hi_f32(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
@@ -194,16 +194,20 @@ struct Cols16 {
   __device__ __forceinline__ uint64_t pair(int i) const { return static_cast<uint64_t>(r[2 * i + 1]) << 32 | r[2 * i]; }
 };
 
-// The scales of a block that an adding thread needs: of its row, and of its columns' blocks of weight rows.
-template <int kOf>
+// The scales of a block that an adding thread needs: of its row, and of its columns' blocks of weight rows (gated: of the gate
+// rows, of the up rows, and where these are rows of two blocks, of the second one).
+template <bool kGated>
 struct Scales {
-  const float *sx, *sw;
-  int at[kOf];
-  float x, w[kOf];
-  __device__ __forceinline__ void load(int b) {
-    x = sx[b];
-#pragma unroll
-    for (int i = 0; i < kOf; ++i) w[i] = __ldg(sw + at[i] + b);
+  const float *sx, *sg, *su;
+  int second;   // from su's row of scales to the second block's; 0: there is none
+  float x, g, u, u2;
+  __device__ __forceinline__ void load() {
+    x = *sx++;
+    g = __ldg(sg++);
+    if (kGated) {
+      if (second) u2 = __ldg(su + second);
+      u = __ldg(su++);
+    }
   }
 };
 
@@ -308,18 +312,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
     const int q = warp & 3, half = (warp - 4) >> 2;   // this warp's lanes of tensor memory, its half of the columns
     const int rows_w = (p.n + 127) / 128;             // blocks of weight rows
     const int r = 32 * q + lane;                      // this thread's row of a tile
-    Scales<kGated ? 3 : 1> sc;
-    // gated: of the gate rows, and of the (one or two) blocks of the up rows
+    Scales<kGated> sc;
+    sc.u2 = 0.f;
     const auto start = [&](const Tile& T) {
       const int f0 = T.f0 + (kGated ? 64 : 128) * half;
       sc.sx = p.sx + static_cast<long long>(max(T.r0 + min(r, T.rows - 1), 0)) * blocks;
-      sc.sw = p.sw + static_cast<long long>(T.e) * rows_w * blocks;
-      sc.at[0] = min(f0 / 128, rows_w - 1) * blocks;
+      const float* sw = p.sw + static_cast<long long>(T.e) * rows_w * blocks;
+      sc.sg = sw + min(f0 / 128, rows_w - 1) * blocks;
       if constexpr (kGated) {
-        sc.at[1] = min((feats + f0) / 128, rows_w - 1) * blocks;
-        sc.at[2] = min((feats + f0) / 128 + 1, rows_w - 1) * blocks;
+        const int up = feats + f0, block = min(up / 128, rows_w - 1);
+        sc.su = sw + block * blocks;
+        sc.second = up % 128 > 64 && block + 1 < rows_w ? blocks : 0;
       }
-      sc.load(0);
+      sc.load();
     };
     [[maybe_unused]] const int n_buf = out_buffers(kGated, p.E);
     [[maybe_unused]] uint32_t n_part = 0;
@@ -348,8 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
         if (!(ok = wait_bar_warp(&S.acc_full[buf], (it >> 1) & 1, &S.waits))) break;
         fence_after();
         // this block's factors; the next one's scales are on their way while it is added
-        const float f[3] = {sc.x * sc.w[0], kGated ? sc.x * sc.w[kGated ? 1 : 0] : 0.f, kGated ? sc.x * sc.w[kGated ? 2 : 0] : 0.f};
-        if (b + 1 < blocks) sc.load(b + 1);
+        const float f[3] = {sc.x * sc.g, kGated ? sc.x * sc.u : 0.f, kGated ? sc.x * sc.u2 : 0.f};
+        if (b + 1 < blocks) sc.load();
         if (rows_here) {
           const uint32_t at = at0 + buf * kWeightRows;
           const auto column = [](int i) { return kGated ? 16 * (i & 3) + 128 * (i >> 2) : 16 * i; };

@@ -12,7 +12,7 @@
 // read every block's accumulator, multiply it by the factors and add it to sums in
 // registers: 128 a thread, two at a time (fma.f32x2).  As the products of a block are
 // exact and few, the sums are fp32's own.  The adding warps take registers from the
-// others (setmaxnreg): 208 a thread.
+// others (setmaxnreg): 232 a thread.
 //
 // The rows are the MMA's M side, other than in the 16-bit products, although a ragged
 // group then costs its rows rounded up to 128: a thread owns a row, so a block's factor

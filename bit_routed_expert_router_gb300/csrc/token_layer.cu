@@ -164,16 +164,25 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 // 128 bytes of 16 weight rows: [gate, up] x 8 features of an expert, or 16 outputs.
-__device__ __forceinline__ void load_up(uint8_t* to, const CUtensorMap* map, int word, int f0, int e, uint64_t* bar) {
+// Once read, they leave L2 first: what else lies there (the kernels' code, the tokens) stays.
+__device__ __forceinline__ uint64_t read_once() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void load_up(uint8_t* to, const CUtensorMap* map, int word, int f0, int e, uint64_t* bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::
-          "r"(smem_u32(to)), "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(f0), "r"(0), "r"(e), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, "
+      "%5}], [%6], %7;" ::"r"(smem_u32(to)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(f0), "r"(0), "r"(e), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
-__device__ __forceinline__ void load_down(uint8_t* to, const CUtensorMap* map, int word, int d0, int e, uint64_t* bar) {
+__device__ __forceinline__ void load_down(uint8_t* to, const CUtensorMap* map, int word, int d0, int e, uint64_t* bar,
+                                          uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-          "r"(smem_u32(to)), "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(d0), "r"(e), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], "
+      "[%5], %6;" ::"r"(smem_u32(to)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(word), "r"(d0), "r"(e), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 
@@ -295,6 +304,7 @@ __global__ void __launch_bounds__(32 * kWarpsUp) k_layer_up(const __grid_constan
   int units = of_shared;   // and the routed ones, once they are known
   uint8_t* const stages = smem + warp * kStages * kStageBytes;
   uint64_t* const full = S.full[warp];
+  const uint64_t policy = read_once();
 
   // A place in this warp's units and their chunks: the shared expert's units first, which are known before the picked experts.
   struct Place {
@@ -322,7 +332,7 @@ __global__ void __launch_bounds__(32 * kWarpsUp) k_layer_up(const __grid_constan
       mbar_arrive_expect_tx(&full[s], cols * kColBytes);
       for (int i = 0; i < cols; ++i)
         load_up(stages + s * kStageBytes + i * kColBytes, next.slot.expert < 0 ? &maps.shared : &maps.routed,
-                (next.k0 * kSize + i * kCol) / 4, next.f0, max(next.slot.expert, 0), &full[s]);
+                (next.k0 * kSize + i * kCol) / 4, next.f0, max(next.slot.expert, 0), &full[s], policy);
     }
     ++loads;
     next.k0 += kChunk;
@@ -430,6 +440,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_con
   const int end = static_cast<int>(static_cast<long long>(all) * (part + 1) / parts);
   uint8_t* const stages = smem + warp * kStages * kStageBytes;
   uint64_t* const full = S.full[warp];
+  const uint64_t policy = read_once();
   float* const sums = reinterpret_cast<float*>(smem + P.at_sums);   // [warp][token][16]
   float* const own = sums + warp * p.t * 16;
   for (int i = lane; i < p.t * 16; i += 32) own[i] = 0.f;
@@ -450,7 +461,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_con
     mbar_arrive_expect_tx(&full[s], cols * kColBytes);
     for (int i = 0; i < cols; ++i)
       load_down(stages + s * kStageBytes + i * kColBytes, at.slot >= n_routed ? &maps.shared : &maps.routed, (at.col + i) * (kCol / 4),
-                d0, max(slots[at.slot].expert, 0), &full[s]);
+                d0, max(slots[at.slot].expert, 0), &full[s], policy);
   };
   Place at;
   at.left = end - first;

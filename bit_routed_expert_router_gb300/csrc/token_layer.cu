@@ -163,13 +163,14 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
-// 128 bytes of 16 weight rows: [gate, up] x 8 features of an expert, or 16 outputs.
 // Once read, they leave L2 first: what else lies there (the kernels' code, the tokens) stays.
 __device__ __forceinline__ uint64_t read_once() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
   return p;
 }
+
+// 128 bytes of 16 weight rows: [gate, up] x 8 features of an expert, or 16 outputs.
 __device__ __forceinline__ void load_up(uint8_t* to, const CUtensorMap* map, int word, int f0, int e, uint64_t* bar, uint64_t policy) {
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4, "

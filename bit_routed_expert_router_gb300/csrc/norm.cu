@@ -11,6 +11,7 @@
 // eight values (16 bytes) a thread.
 #include <algorithm>
 
+#include "allow_smem.h"
 #include "ops8.h"
 #include "quant8.cuh"
 
@@ -165,51 +166,70 @@ __global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 10
   }
 }
 
+__device__ __forceinline__ void copy16(uint4* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void end_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Rows on their way to a CTA of k_norm_grad (three of them: 20.2 us for 4096 rows of 2816; four: 21.0; two: 20.0).
+constexpr int kGradStages = 2;
+
 // CTA b takes the rows b, b + parts, ...: its columns' part of the weight gradient stays in registers and is written once.  The
-// next row's loads are on their way while a row is at hand.  (Without that, and with 512 parts, more than fit the GPU at once,
-// 36.0 us for 4096 rows of 2816.)
+// next rows are on their way to shared memory, each thread's words to its own place there, which needs no barrier.  (With one
+// row on its way in registers 22.0 us for 4096 rows of 2816, with none 36; with three CTAs an SM 20.5.)
 template <bool kBf16, int kV, int kThreads>
 __global__ void __launch_bounds__(kThreads, kV == 1 ? 2 : 1) k_norm_grad(NormGradParams p) {
+  constexpr int kStages = kGradStages;
+  extern __shared__ uint4 s_rows[];   // [stage][h, dy, dres][word of a thread][thread]
   __shared__ float2 s_sum[2][32];
   const int n_words = p.d / 8, warps = blockDim.x / 32, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  float dw[kV][8], w[kV][8];
-  uint4 h[kV], dy[kV], dres[kV];   // the next row
-  const auto load = [&](int r) {
+  const auto place = [&](int s, int which, int j) { return s_rows + ((s * 3 + which) * kV + j) * blockDim.x + threadIdx.x; };
+  const auto load = [&](int r, int s) {
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       const int i = threadIdx.x + j * blockDim.x;
       if (i >= n_words || r >= p.m) continue;
-      h[j] = *reinterpret_cast<const uint4*>(row16(p.h, p.ldh, r, 8 * i));
-      dy[j] = *reinterpret_cast<const uint4*>(row16(p.dy, p.lddy, r, 8 * i));
-      if (p.dres) dres[j] = *reinterpret_cast<const uint4*>(row16(p.dres, p.lddres, r, 8 * i));
+      copy16(place(s, 0, j), row16(p.h, p.ldh, r, 8 * i));
+      copy16(place(s, 1, j), row16(p.dy, p.lddy, r, 8 * i));
+      if (p.dres) copy16(place(s, 2, j), row16(p.dres, p.lddres, r, 8 * i));
     }
+    end_copies();
   };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) load(blockIdx.x + s * gridDim.x, s);
+  float dw[kV][8], w[kV][8];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
-    h[j] = dy[j] = dres[j] = make_uint4(0, 0, 0, 0);   // what lies behind a row stays 0
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[j][k] = 0.f, w[j][k] = 1.f;
     if (p.weight && i < n_words) widen<kBf16>(w[j], __ldg(reinterpret_cast<const uint4*>(p.weight) + i));
   }
-  load(blockIdx.x);
-  int turn = 0;
+  int turn = 0, s = 0;
   for (int r = blockIdx.x; r < p.m; r += gridDim.x, turn ^= 1) {
     float a[kV][8], b[kV][8], o[kV][8], ss = 0.f, dot = 0.f;
+    wait_copies<kStages - 1>();
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      widen<kBf16>(a[j], h[j]);
-      widen<kBf16>(b[j], dy[j]);
-      widen<kBf16>(o[j], dres[j]);
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      const bool in = static_cast<int>(threadIdx.x + j * blockDim.x) < n_words;
+      widen<kBf16>(a[j], in ? *place(s, 0, j) : none);
+      widen<kBf16>(b[j], in ? *place(s, 1, j) : none);
+      widen<kBf16>(o[j], in && p.dres ? *place(s, 2, j) : none);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         ss = fmaf(a[j][k], a[j][k], ss);
         dot = fmaf(b[j][k] * w[j][k], a[j][k], dot);
       }
     }
-    load(r + gridDim.x);
+    load(r + kStages * gridDim.x, s);
+    s = (s + 1) % kStages;
     ss = warp_sum(ss);
     dot = warp_sum(dot);
     if (warps > 1) {
@@ -268,11 +288,12 @@ __global__ void __launch_bounds__(512) k_norm_dweight(const float* part, int par
 }
 
 template <typename K, typename... A>
-bool launch(K kernel, dim3 grid, dim3 block, cudaStream_t s, const A&... args) {
+bool launch(K kernel, dim3 grid, dim3 block, cudaStream_t s, int smem, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.stream = s;
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
@@ -283,7 +304,7 @@ bool launch(K kernel, dim3 grid, dim3 block, cudaStream_t s, const A&... args) {
 
 template <bool kBf16, int kDelta, int kV, int kR>
 bool launch_rows(const NormParams& p, int nt, int rows, cudaStream_t s) {
-  return launch(k_norm<kBf16, kDelta, kV, kR>, dim3((p.m + rows * kR - 1) / (rows * kR)), dim3(nt, rows), s, p);
+  return launch(k_norm<kBf16, kDelta, kV, kR>, dim3((p.m + rows * kR - 1) / (rows * kR)), dim3(nt, rows), s, 0, p);
 }
 
 template <bool kBf16, int kDelta>
@@ -296,14 +317,20 @@ bool launch_norm_of(const NormParams& p, int sms, cudaStream_t s) {
   return launch_rows<kBf16, kDelta, 1, 1>(p, nt, rows, s);
 }
 
+template <bool kBf16, int kV, int kThreads>
+bool launch_grad_rows(const NormGradParams& p, int nt, cudaStream_t s) {
+  constexpr int kMost = kGradStages * 3 * kV * kThreads * 16;
+  return allow_smem(k_norm_grad<kBf16, kV, kThreads>, kMost) &&
+         launch(k_norm_grad<kBf16, kV, kThreads>, dim3(p.parts), dim3(nt), s, kGradStages * 3 * kV * nt * 16, p);
+}
+
 template <bool kBf16>
 bool launch_grad_of(const NormGradParams& p, cudaStream_t s) {
   const int words = p.d / 8, nt = (words + 31) / 32 * 32;
-  if (nt <= 384) return launch(k_norm_grad<kBf16, 1, 384>, dim3(p.parts), dim3(nt), s, p);
-  if (nt <= 512) return launch(k_norm_grad<kBf16, 1, 512>, dim3(p.parts), dim3(nt), s, p);
+  if (nt <= 384) return launch_grad_rows<kBf16, 1, 384>(p, nt, s);
+  if (nt <= 512) return launch_grad_rows<kBf16, 1, 512>(p, nt, s);
   const int half = (words + 63) / 64 * 32;   // two words a thread
-  return half <= 512 ? launch(k_norm_grad<kBf16, 2, 512>, dim3(p.parts), dim3(half), s, p)
-                     : launch(k_norm_grad<kBf16, 2, 1024>, dim3(p.parts), dim3(half), s, p);
+  return half <= 512 ? launch_grad_rows<kBf16, 2, 512>(p, half, s) : launch_grad_rows<kBf16, 2, 1024>(p, half, s);
 }
 
 // Multiprocessors of the current device; 0: a CUDA call failed.
@@ -334,7 +361,7 @@ bool launch_norm_grad(bool bf16, const NormGradParams& params, cudaStream_t s) {
   const int words = p.d / 8, warps = words > 512 ? (words + 63) / 64 : (words + 31) / 32;
   p.parts = std::min({p.m, kNormParts, sms * std::max(1, 32 / warps)});
   if (!(bf16 ? launch_grad_of<true>(p, s) : launch_grad_of<false>(p, s))) return false;
-  return !p.part || launch(k_norm_dweight, dim3((p.d + 31) / 32), dim3(512), s, static_cast<const float*>(p.part), p.parts,
+  return !p.part || launch(k_norm_dweight, dim3((p.d + 31) / 32), dim3(512), s, 0, static_cast<const float*>(p.part), p.parts,
                            p.d, p.dweight);
 }
 

@@ -194,6 +194,32 @@ struct Cols16 {
   __device__ __forceinline__ uint64_t pair(int i) const { return static_cast<uint64_t>(r[2 * i + 1]) << 32 | r[2 * i]; }
 };
 
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// GELU(g) u of two features.  The tanh form: g / (1 + 2^z) u, z = -2 log2(e) sqrt(2 / pi) (g + 0.044715 g^3); past fp32's range
+// 2^z is infinite and the quotient 0.
+template <int kGelu>
+__device__ __forceinline__ uint64_t gated_pair(uint64_t g, uint64_t u) {
+  if constexpr (kGelu == MOE_GELU_TANH) {
+    constexpr float c = -2.f * 1.4426950408889634f * 0.7978845608028654f;
+    uint64_t s = pack_f32x2(c, c);
+    fma_f32x2(s, mul_f32x2(g, g), pack_f32x2(0.044715f * c, 0.044715f * c));
+    const uint64_t z = mul_f32x2(g, s);
+    float e[2], r[2];
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e[0]) : "f"(lo_f32(z)));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e[1]) : "f"(hi_f32(z)));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r[0]) : "f"(1.f + e[0]));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r[1]) : "f"(1.f + e[1]));
+    return mul_f32x2(mul_f32x2(g, pack_f32x2(r[0], r[1])), u);
+  } else {
+    return pack_f32x2(gelu16(lo_f32(g), kGelu) * lo_f32(u), gelu16(hi_f32(g), kGelu) * hi_f32(u));
+  }
+}
+
 // The scales of a block that an adding thread needs: of its row, and of its columns' blocks of weight rows (gated: of the gate
 // rows, of the up rows, and where these are rows of two blocks, of the second one).
 template <bool kGated>
@@ -388,13 +414,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
       if constexpr (kGated) {
         // a in the gate values' place, and its largest magnitude
         float top = 0.f;
+        if (rows_here)
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float a0 = gelu16(lo_f32(acc[j]), kGelu) * lo_f32(acc[32 + j]);
-          const float a1 = gelu16(hi_f32(acc[j]), kGelu) * hi_f32(acc[32 + j]);
-          acc[j] = pack_f32x2(a0, a1);
-          if (f0 + 2 * j < feats) top = max_abs(max_abs(top, a0), a1);
-        }
+          for (int i = 0; i < 4; ++i) {
+            if (f0 + 16 * i >= feats) break;
+#pragma unroll
+            for (int j = 8 * i; j < 8 * i + 8; ++j) {
+              acc[j] = gated_pair<kGelu>(acc[j], acc[32 + j]);
+              top = max_abs(max_abs(top, lo_f32(acc[j])), hi_f32(acc[j]));
+            }
+          }
         S.top[n_tile & 1][half][r] = top;
         __syncwarp();
         if (lane == 0) mbarrier_arrive(&S.top_full);
@@ -405,13 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
           const long long row = D.r0 + r;
           if (half == 0) p.sa[row * ((feats + 127) / 128) + D.f0 / 128] = s8.scale;
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + row * p.ldy + f0);
+          const uint64_t x2 = pack_f32x2(s8.inverse, s8.inverse);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint64_t a = acc[8 * i + 2 * j], c = acc[8 * i + 2 * j + 1];
-              w[j] = to_e4m3x4(lo_f32(a) * s8.inverse, hi_f32(a) * s8.inverse, lo_f32(c) * s8.inverse, hi_f32(c) * s8.inverse);
+              const uint64_t a = mul_f32x2(acc[8 * i + 2 * j], x2), c = mul_f32x2(acc[8 * i + 2 * j + 1], x2);
+              w[j] = to_e4m3x4(lo_f32(a), hi_f32(a), lo_f32(c), hi_f32(c));
             }
             if (f0 + 16 * i < feats) out[i] = make_uint4(w[0], w[1], w[2], w[3]);
           }

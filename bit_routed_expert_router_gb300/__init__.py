@@ -25,11 +25,11 @@ MOE_BF16, MOE_F16, MOE_F32 = 0, 1, 2
 HOOK_FAIL_NEXT_COPY, HOOK_WAIT_LIMIT_US, HOOK_PDL, HOOK_PERSISTENT, HOOK_TIMELINE, HOOK_FREE_BYTES = 1, 2, 3, 4, 5, 6
 HOOK_PREFILL_TC = 7
 HOOK_CLUSTER = 9
-HOOK_SPIN_LIMIT = 10      # bounded waits of the persistent decode kernels (no context: of the 16-bit operators): cycles
+HOOK_SPIN_LIMIT = 10      # bounded waits of the persistent decode kernels (no context: of the operators): cycles
 HOOK_AT_REST = 11         # MOE_OK when the persistent kernels' launch words are back at rest
 HOOK_WAIT_DIAG = 12       # the clustered kernel's first wait that ran out (site << 16 | CTA) into a host uint32
 HOOK_SMALL_BATCH = 13     # small-batch grouped GEMVs (calls of at most 32 tokens) on / off
-HOOK_STOP_LOADS = 15      # no context: loads after which the 16-bit operators' loading threads stop (<= 0: never)
+HOOK_STOP_LOADS = 15      # no context: loads after which the operators' loading threads stop (<= 0: never)
 HOOK_TOKEN_LOOP = 14      # decode steps of 2 to 4 tokens: one clustered-kernel launch per token on / off
 
 

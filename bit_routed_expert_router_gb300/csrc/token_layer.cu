@@ -45,8 +45,9 @@ constexpr int kWarpsUp = 8, kWarpsDown = 8;
 constexpr int kStagesUp = 2, kStagesDown = 1;      // of a warp
 constexpr int kCol = 128, kColBytes = 16 * kCol;  // bytes of a weight row that one load takes; of its 16 rows
 // Loads of a chunk: neighbours in their rows, which the memory likes (chunks of 256 bytes of a row 34 us for one token, 104 for
-// seven; of 512 and 640 29.8 and 87.9).  Two CTAs of the second kernel fit an SM, one beside one of the first.
-constexpr int kColsUp = 4, kColsDown = 5;
+// seven, when those of 512 took 29.8 and 87.9).  A CTA of the second kernel fits an SM beside one of the first: what it loads
+// before its wait hides its start.
+constexpr int kCols = 4;
 constexpr int kTokens = 8;                       // of a slot
 constexpr int kMostSmem = 160 * 1024;            // of either kernel: the stages, and the lists of 1024 pairs and experts
 
@@ -100,43 +101,52 @@ __device__ __forceinline__ uint32_t widen8(uint32_t v) {
 __device__ __forceinline__ int row_of(int g) { return g >> 1 | (g & 1) << 2; }
 
 // This lane's share of up to 8 token rows over a chunk: 16 bytes a word.
-template <bool kW8, int kCols>
+template <bool kW8>
 struct TokenWords {
   static constexpr int kWords = kW8 ? 2 : 1;   // of a half of a load
   uint4 v[kCols][2][kWords];
 
-  // row: this lane's token row from the chunk's first value on, of which k are there; null for none
+  // row: this lane's token row from the chunk's first value on, of which k are there (a lane without a token of its own takes
+  // another's: its column is not used)
   __device__ __forceinline__ void load(const uint16_t* row, int k, int lane) {
+    const int at = 8 * kWords * (lane & 3);
+    if (k >= (kW8 ? kCol : kCol / 2) * kCols)
+      take<true>(row + at, k - at);
+    else
+      take<false>(row + at, k - at);
+  }
+  template <bool kWhole>
+  __device__ __forceinline__ void take(const uint16_t* row, int k) {
 #pragma unroll
     for (int i = 0; i < kCols; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int j = 0; j < kWords; ++j) {
-          const int at = (kW8 ? kCol : kCol / 2) * i + 32 * kWords * h + 8 * kWords * (lane & 3) + 8 * j;
-          v[i][h][j] = row && at < k ? __ldcg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0, 0, 0, 0);
+          const int at = (kW8 ? kCol : kCol / 2) * i + 32 * kWords * h + 8 * j;
+          v[i][h][j] = kWhole || at < k ? __ldcg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0, 0, 0, 0);
         }
   }
 };
 
 // acc += 16 weight rows of a staged chunk of k values times the token rows.  With e4m3 weights `scale` holds the scales of the
 // chunk's blocks of 128 (its loads): lane i that of rows 0 .. 7, lane 16 + i of rows 8 .. 15.
-template <bool kBf16, bool kW8, int kCols>
-__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const TokenWords<kW8, kCols>& x, int k, float scale,
+template <bool kBf16, bool kW8>
+__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const TokenWords<kW8>& x, int k, float scale,
                                                int lane) {
   const int r = row_of(lane >> 2), t = lane & 3;
   const uint8_t* row = stage + r * kCol;
+  float part[2][4] = {};
 #pragma unroll
   for (int i = 0; i < kCols; ++i) {
     if ((kW8 ? kCol : kCol / 2) * i >= k) break;
-    float part[2][4] = {};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const uint8_t* from = row + i * kColBytes + (((4 * h + t) ^ r) << 4);   // zeros past the row's end
       const uint4 w0 = *reinterpret_cast<const uint4*>(from), w1 = *reinterpret_cast<const uint4*>(from + 8 * kCol);
       const uint4 b0 = x.v[i][h][0];
       if (kW8) {
-        const uint4 b1 = x.v[i][h][TokenWords<kW8, kCols>::kWords - 1];
+        const uint4 b1 = x.v[i][h][TokenWords<kW8>::kWords - 1];
         const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
         const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -148,13 +158,18 @@ __device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* s
         mma16<kBf16>(part[h], w0.z, w1.z, w0.w, w1.w, b0.z, b0.w);
       }
     }
-    const float lo = kW8 ? __shfl_sync(0xFFFFFFFFu, scale, i) : 1.f, hi = kW8 ? __shfl_sync(0xFFFFFFFFu, scale, 16 + i) : 1.f;
+    if (kW8) {
+      const float lo = __shfl_sync(0xFFFFFFFFu, scale, i), hi = __shfl_sync(0xFFFFFFFFu, scale, 16 + i);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float sum = part[0][v] + part[1][v];
-      acc[v] = kW8 ? fmaf(sum, v < 2 ? lo : hi, acc[v]) : acc[v] + sum;
+      for (int v = 0; v < 4; ++v) {
+        acc[v] = fmaf(part[0][v] + part[1][v], v < 2 ? lo : hi, acc[v]);
+        part[0][v] = part[1][v] = 0.f;
+      }
     }
   }
+  if (!kW8)   // tensor cores truncate: their sums go on for a chunk only
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[v] += part[0][v] + part[1][v];
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -286,8 +301,10 @@ __device__ __forceinline__ void prepare(const LayerParams& p, const Maps& maps, 
 
 // ------------------------------------------------------------------ up
 
+// (Registers: one CTA of each kernel an SM.  16-bit weights leave room for more than 128 a thread, which the loads of a chunk's
+// tokens use: 7 tokens 87.7 -> 85.6 us; with more for e4m3 weights the second kernel waits for the first: 23.6 -> 27.6 us.)
 template <bool kBf16, bool kW8>
-__global__ void __launch_bounds__(32 * kWarpsUp) k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
+__global__ void __launch_bounds__(32 * kWarpsUp, kW8 ? 2 : 1) k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
                                                        const __grid_constant__ Plan P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -295,7 +312,7 @@ __global__ void __launch_bounds__(32 * kWarpsUp) k_layer_up(const __grid_constan
   constexpr int kWarps = kWarpsUp, kStages = kStagesUp;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   constexpr int kSize = kW8 ? 1 : 2;   // bytes of a weight
-  constexpr int kCols = kColsUp, kChunk = kCols * kCol / kSize, kStageBytes = kCols * kColBytes;   // values of a chunk
+  constexpr int kChunk = kCols * kCol / kSize, kStageBytes = kCols * kColBytes;   // values of a chunk
   prepare(p, maps, P, smem, S);
   pdl_wait();
   pdl_trigger();
@@ -362,15 +379,15 @@ __global__ void __launch_bounds__(32 * kWarpsUp) k_layer_up(const __grid_constan
               (lane < 16 ? f0 : f + f0) / 128 * kb;
     }
     float acc[4] = {};
-    const uint16_t* x = g < rows ? p.x + nth_bit(at.slot.mask, g) * p.ldx : nullptr;
+    const uint16_t* x = p.x + nth_bit(at.slot.mask, min(g, rows - 1)) * p.ldx;
     for (int k0 = 0; k0 < p.d; k0 += kChunk, ++it) {
       const int s = it % kStages, k = min(kChunk, p.d - k0);
-      TokenWords<kW8, kCols> tokens;
-      tokens.load(x ? x + k0 : nullptr, k, lane);
+      TokenWords<kW8> tokens;
+      tokens.load(x + k0, k, lane);
       float sc = 0.f;
       if (kW8 && kCol * (lane & 15) < k) sc = __ldg(scale + k0 / 128 + (lane & 15));
       if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
-      chunk_products<kBf16, kW8, kCols>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
+      chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
       __syncwarp();
       load();
     }
@@ -418,7 +435,7 @@ __device__ __forceinline__ float ld_rank(const float* at, uint32_t rank) {
 }
 
 template <bool kBf16, bool kW8>
-__global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
+__global__ void __launch_bounds__(32 * kWarpsDown, kW8 ? 2 : 1) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
                                                          const __grid_constant__ Plan P, int split) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -427,7 +444,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int rank = static_cast<int>(cluster_rank()), d0 = blockIdx.x / split * 16;
   constexpr int kSize = kW8 ? 1 : 2;
-  constexpr int kCols = kColsDown, kStageBytes = kCols * kColBytes, kColValues = kCol / kSize;
+  constexpr int kStageBytes = kCols * kColBytes, kColValues = kCol / kSize;
   prepare(p, maps, P, smem, S);
   // ids and weights are older than the first kernel, which let this one start after its own wait
   list_slots(p, P, smem, S);
@@ -493,10 +510,9 @@ __global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_con
     const bool shared = at.slot >= n_routed;
     const Slot slot = slots[at.slot];
     const int f = shared ? p.fs : p.f, k = min(at.cols(of_slot(at)) * kColValues, f - k0);
-    TokenWords<kW8, kCols> tokens;
-    tokens.load(g < __popc(slot.mask) ? p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
-                                            static_cast<long long>(slot.base + g) * f + k0
-                                      : nullptr,
+    TokenWords<kW8> tokens;
+    tokens.load(p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
+                    static_cast<long long>(slot.base + min(g, __popc(slot.mask) - 1)) * f + k0,
                 k, lane);
     float sc = 0.f;
     if (kW8 && kCol * (lane & 15) < k) {
@@ -504,7 +520,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown) k_layer_down(const __grid_con
       sc = __ldg((shared ? p.shared.down_scale : p.routed.down_scale) + block * divide_up(f, 128) + k0 / 128 + (lane & 15));
     }
     if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
-    chunk_products<kBf16, kW8, kCols>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
+    chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
     __syncwarp();
     load_next();
     const int was = at.slot;
@@ -559,7 +575,7 @@ int most_slots(const LayerParams& p) { return std::min(p.t * p.k, p.E + p.t * p.
 Plan make_plan(const LayerParams& p, bool down) {
   Plan P{};
   const int slots = most_slots(p) + divide_up(p.t, kTokens);
-  P.at_sums = (down ? kWarpsDown * kStagesDown * kColsDown : kWarpsUp * kStagesUp * kColsUp) * kColBytes;
+  P.at_sums = (down ? kWarpsDown * kStagesDown * kCols : kWarpsUp * kStagesUp * kCols) * kColBytes;
   P.at_mask = P.at_sums + (down ? kWarpsDown * p.t * 64 : 0);
   P.at_ids = P.at_mask + 4 * p.E;
   P.at_gates = P.at_ids + 4 * p.t * p.k;
@@ -633,7 +649,7 @@ bool launch_both(const LayerParams& p, int sms, cudaStream_t s) {
   if (!launch(k_layer_up<kBf16, kW8>, grid, 32 * kWarpsUp, up, 1, s, m_up, p, up)) return false;
   const int blocks = p.d / 16, cols = slots * divide_up(p.f * kSize, kCol) + divide_up(p.fs * kSize, kCol);
   int split = 1;
-  while (split < 8 && 2 * split * blocks <= 2 * sms && 2 * split * kWarpsDown * kColsDown <= cols) split *= 2;
+  while (split < 8 && 2 * split * blocks <= 2 * sms && 2 * split * kWarpsDown * kCols <= cols) split *= 2;
   return launch(k_layer_down<kBf16, kW8>, blocks * split, 32 * kWarpsDown, down, split, s, m_down, p, down, split);
 }
 

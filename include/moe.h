@@ -501,7 +501,7 @@ moe_status moe_lora_mm(int dtype, const void *x, int64_t ldx, int t, const void 
                        void *workspace, uint64_t workspace_bytes, void *stream);
 
 /* Synchronise `stream`, then report whether a bounded device wait of these
- * operators ran out on the current device since the last call with this stream
+ * operators (and of the 8-bit ones below) ran out on the current device since the last call with this stream
  * (MOE_ETIMEOUT: outputs since then are undefined), as moe_sync does for a
  * context.  Whichever stream's call it was, every stream that asks is told (one
  * that has never asked, of all since the library was loaded).  MOE_EINVAL while
@@ -520,9 +520,9 @@ moe_status moe_grouped_sync(void *stream);
  * 16, 16-byte aligned, have scales [m][ceil(d / 128)], contiguous: one for each
  * 128 values, the last for what is left.  Where the library writes such rows,
  *   scale = max(max |v|, 2^-100) / 448,   value = e4m3(v / scale),
- * computed in fp32 and rounded to the nearest, ties to even (v / scale as v times
- * 448 / max |v|, which can pass a tie that lies within 2^-22 of it).  Non-finite
- * values stay in their block: one with a NaN gets a NaN scale and NaN values, one
+ * in fp32, both quotients within 2^-22 of themselves (v is multiplied by 448 /
+ * max |v|, which can pass a tie that lies as near), then rounded to the nearest,
+ * ties to even.  Non-finite values stay in their block: one with a NaN gets a NaN scale and NaN values, one
  * with an infinity an infinite scale, NaN where v is infinite and 0 elsewhere. */
 
 /* r = h + delta, rounded to dtype and stored in h_out; then from the stored r
@@ -604,7 +604,8 @@ typedef struct {
  *               one each
  * Sums are fp32; gates * GELU(g) u is rounded to dtype once before the down
  * product, y once at the end.  Non-finite weights of an expert reach the tokens that
- * name it only. */
+ * name it only.  y may be x; nothing else may overlap.  moe_grouped_sync reports a
+ * bounded wait that ran out. */
 moe_status moe_token_layer(int dtype, int gelu_variant, const void *x, int64_t ldx, int t, const int32_t *ids,
                            const float *gates, int top_k, int n_experts, const moe_ffn_weights *routed,
                            const moe_ffn_weights *shared, int d, int f, int f_shared, void *y, int64_t ldy,
@@ -677,10 +678,11 @@ moe_status moe_get_profile(moe_ctx *ctx, moe_kernel_time *out, int n);
  * hook 14: resident decode steps of 2 to 4 tokens run one clustered-kernel
  * launch per token (value != 0, the default, where that kernel can run) or
  * take the batched paths of hook 13 (0).
- * ctx NULL: the 16-bit operators' calls from now on, in every thread.  hook 10:
+ * ctx NULL: the 16-bit and 8-bit operators' calls and the layer's for a few
+ * tokens from now on, in every thread.  hook 10:
  * their bounded device waits give up after `value` SM cycles (<= 0: the
  * default).  hook 15: the threads that load operands stop after `value` loads a
- * CTA (<= 0: never), so that every wait for what they would have loaded runs
+ * CTA (the layer's: each warp; <= 0: never), so that every wait for what they would have loaded runs
  * out; the kernels leave their outputs undefined and moe_grouped_sync returns
  * MOE_ETIMEOUT.
  * Other hooks: MOE_EINVAL. */

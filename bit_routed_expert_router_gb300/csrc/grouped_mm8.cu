@@ -21,6 +21,13 @@
 // column to column and came from shared memory, whose bandwidth the MMAs and the loads
 // take: 1,600 cycles a block for what takes 340 alone, with CTA pairs 1,500 (shared
 // expert's gate/up, 4096 rows: 144 and 90 us).
+//
+// What bounds it: few rows an expert, HBM (gated, 33 tokens of 128 experts, 2816 to
+// 704 features: 67 us, 6.66 TB/s).  Many, tensor memory: a block's MMAs take 540
+// cycles, its reads and additions 340, both at once 1,040 (shared expert's gate/up,
+// 4096 rows, 2816 to 5632: 59 us, 2.19 PFLOP/s; gated, 4096 tokens: 169 us, 1.54).
+// Pairs of CTAs on 256 rows, which load a third less, take 58.9 us and, with ragged
+// groups, 209.
 #include <algorithm>
 #include <cstddef>
 #include <limits>

@@ -226,3 +226,49 @@ def test_in_a_graph_and_on_another_stream():
         both()
         for a, b in zip(got, (y8.view(torch.uint8), s, dh, dw)):
             assert torch.equal(a, b)
+
+
+# the forms that the shapes above leave out: two rows a thread (many rows), and two words a thread of 288 to 512 in the gradient
+MORE = [(2501, 2816), (10001, 264), (20001, 8), (2433, 4096), (40, 4104), (301, 5000), (9, 8192)]
+
+
+@pytest.mark.parametrize("m,d", MORE)
+@pytest.mark.parametrize("dtype,delta,out", [(BF16, F32, "both"), (F16, F16, "8"), (BF16, None, "16")])
+def test_norm_of_many_and_of_long_rows(m, d, dtype, delta, out):
+    g = gen(3 * m + d)
+    h, w = rand(g, dtype, m, d, scale=3), rand(g, dtype, d)
+    dl = None if delta is None else rand(g, delta, m, d)
+    before = h.clone()
+    r, y, y8, s = call(h, dl, w, out, inplace=True)
+    if dl is not None:
+        assert torch.equal(r, (before.float() + dl.float()).to(dtype))
+    want = normed(h, w)
+    if y is not None:
+        near16(y, want, dtype)
+    if y8 is not None:
+        near8(y8, s, want)
+
+
+@pytest.mark.parametrize("m,d", MORE)
+@pytest.mark.parametrize("dtype,residual", [(BF16, True), (F16, False)])
+def test_gradients_of_many_and_of_long_rows(m, d, dtype, residual):
+    g = gen(5 * m + d)
+    h, dy, w = rand(g, dtype, m, d, scale=2), rand(g, dtype, m, d), rand(g, dtype, d)
+    dres = rand(g, dtype, m, d) if residual else None
+    near_grads(h, dy, dres, w, *call_grad(h, dy, dres, w))
+
+
+def test_calls_on_two_streams_at_once():
+    """Workspaces of their own; the same inputs."""
+    g = gen(41)
+    h, dy, w = rand(g, BF16, 900, 1032), rand(g, BF16, 900, 1032), rand(g, BF16, 1032)
+    want = call_grad(h, dy, None, w)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append([call_grad(h, dy, None, w) for _ in range(3)])
+    torch.cuda.synchronize()
+    for dh, dw in sum(got, []):
+        assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])

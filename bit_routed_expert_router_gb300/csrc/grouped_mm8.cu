@@ -30,7 +30,6 @@
 // groups, 209.
 #include <algorithm>
 #include <cstddef>
-#include <limits>
 
 #include "allow_smem.h"
 #include "gelu16.cuh"

@@ -46,11 +46,4 @@ __device__ __forceinline__ uint32_t to_e4m3x4(float a, float b, float c, float d
   return to_e4m3x2(a, b) | to_e4m3x2(c, d) << 16;
 }
 
-// Two e4m3 values (exact in fp16) as floats.
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t v) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(v)));
-  return make_float2(half_lo(h), half_hi(h));
-}
-
 }  // namespace moe

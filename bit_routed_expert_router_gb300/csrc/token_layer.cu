@@ -3,6 +3,10 @@
 //   up     a[i] = gate GELU(g) u,  [g, u] = Wgu[e] x[t]     for the tokens of each picked expert, rounded to the call's type
 //   down   y[t] = sum_e Wd[e] a[e, t]                       over the experts that t names, and the shared one
 //
+// a is rounded because it is an operand of 16-bit products: with its remainder as a
+// second operand the output's error would fall from 1.4 roundings of its type to
+// one, for twice the second kernel's products and workspace.
+//
 // The weights of the picked experts are read once and nothing else is of any
 // size, so both kernels stream them.  A warp works by itself: one of its lanes
 // loads chunks of 16 weight rows by TMA into the warp's own stages, and the warp
@@ -38,7 +42,6 @@
 #include "gelu16.cuh"
 #include "grouped.h"
 #include "ops8.h"
-#include "quant8.cuh"
 #include "tensor_map.h"
 #include "waits.cuh"
 

@@ -203,3 +203,39 @@ def test_the_most_experts():
     moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y))
     want, size = products(wide_rows(x, sx), wide_weights(w, sw), off)
     close(y, want, size, 80)
+
+
+def test_no_group_has_rows():
+    x, sx, off, w, sw = case([0, 0, 0], 128, 144, pad=9, first=4)
+    y = torch.full((13, 128), 7.0, device="cuda")
+    a, sa = torch.ones(13, 64, device="cuda").to(E4M3), torch.ones(13, 1, device="cuda")
+    moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y))
+    moe.check(moe.moe_grouped_geglu8(x, sx, off, w, sw, a, sa))
+    moe.check(moe.moe_grouped_sync())
+    assert torch.all(y == 7) and torch.all(a.float() == 1) and torch.all(sa == 1)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+def test_many_experts_with_whole_and_ragged_tiles(out):
+    """1024 experts leave one output buffer a warp; whole blocks of 32 rows and what is left of them in turn."""
+    counts = [0] * 1024
+    for i, c in enumerate((32, 33, 64, 127, 128, 129, 160, 1, 256, 31)):
+        counts[100 * i + 7] = c
+    x, sx, off, w, sw = case(counts, 136, 272, pad=3)
+    y = torch.full((x.shape[0], 144), 7.0, dtype=out, device="cuda")
+    moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y[:, :136]))
+    want, size = products(wide_rows(x, sx), wide_weights(w, sw), off)
+    close(y[:-3, :136], want[:-3], size[:-3], 272)
+    y[:-3, :136] = 7
+    assert torch.all(y == 7)
+
+
+def test_the_same_rows_alone_and_in_a_batch():
+    """A row's sums do not depend on the rows and groups around it: bit for bit."""
+    counts, n, k = [130, 0, 257, 3], 264, 400
+    x, sx, off, w, sw = case(counts, n, k)
+    y, one = torch.empty(390, n, device="cuda"), torch.empty(1, n, device="cuda")
+    moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y))
+    for r, e in ((0, 0), (129, 0), (130, 2), (386, 2), (388, 3)):
+        moe.check(moe.moe_grouped_mm8(x[r:r + 1], sx[r:r + 1], offsets_of([1]), w[e:e + 1], sw[e:e + 1], one))
+        assert torch.equal(one[0], y[r])

@@ -193,3 +193,17 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, y in zip(args, ys):
         check(y, *a, moe.MOE_GELU_ERF)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("t,d,f,fs", [(1, 512, 1024, 2048), (3, 256, 2048, 0), (32, 1024, 512, 1024), (2, 16, 4096, 16)])
+def test_narrow_outputs_and_long_reductions(t, d, f, fs, eight):
+    """Outputs whose reduction is split over a cluster of two to eight CTAs."""
+    args = case(t, 4, 12, d, f, fs, BF16, eight)
+    check(call(*args), *args, moe.MOE_GELU_ERF)
+
+
+def test_the_most_pairs_and_experts():
+    """32 tokens that name 32 experts each, of 1024."""
+    args = case(32, 32, 1024, 64, 32, 48, F16)
+    check(call(*args), *args, moe.MOE_GELU_ERF)

@@ -338,7 +338,9 @@ def _from_torch() -> None:
     import torch
     _fn = lib()
     _DTYPE = {torch.bfloat16: MOE_BF16, torch.float16: MOE_F16, torch.float32: MOE_F32}
-    _INT32, _FLOAT32, _current_device = torch.int32, torch.float32, torch.cuda.current_device
+    _INT32, _FLOAT32 = torch.int32, torch.float32
+    # (without the check that CUDA has been initialised: whoever has tensors there has done so)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _E4M3 = torch.float8_e4m3fn
     # the stream's handle without the 3 us of a torch.cuda.Stream object: these calls start kernels of 10 us
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -519,11 +521,12 @@ def moe_rmsnorm(h, y=None, y8=None, scale=None, delta=None, h_out=None, weight=N
     if y8 is not None:
         t8 = y8.stride()
         if not (y8.shape == sh and t8[1] == 1 and y8.dtype is _E4M3 and y8.get_device() == dev and
-                _whole(scale, (m, (d + 127) // 128), _FLOAT32, dev)):
+                scale.shape == (m, (d + 127) // 128) and scale.dtype is _FLOAT32 and scale.is_contiguous() and
+                scale.get_device() == dev):
             return MOE_EINVAL
         p8, ld8, ps = y8.data_ptr(), d if one else t8[0], scale.data_ptr()
     if weight is not None:
-        if not _whole(weight, (d,), dt, dev):
+        if not (weight.shape == (d,) and weight.dtype is dt and weight.is_contiguous() and weight.get_device() == dev):
             return MOE_EINVAL
         pw = weight.data_ptr()
     return _call(_fn.moe_rmsnorm, dev, stream, _DTYPE.get(dt, -1), h.data_ptr(), d if one else th[0], pd, ldd, dd, pw, eps, m, d,
@@ -551,11 +554,12 @@ def moe_rmsnorm_grad(h, dy, dh, dres=None, weight=None, dweight=None, workspace=
             return MOE_EINVAL
         pr, ldr = dres.data_ptr(), d if one else tr[0]
     if weight is not None:
-        if not _whole(weight, (d,), dt, dev):
+        if not (weight.shape == (d,) and weight.dtype is dt and weight.is_contiguous() and weight.get_device() == dev):
             return MOE_EINVAL
         pw = weight.data_ptr()
     if dweight is not None:
-        if workspace is None or not (_whole(dweight, (d,), _FLOAT32, dev) and workspace.is_contiguous() and
+        if workspace is None or not (dweight.shape == (d,) and dweight.dtype is _FLOAT32 and dweight.is_contiguous() and
+                                     dweight.get_device() == dev and workspace.is_contiguous() and
                                      workspace.get_device() == dev):
             return MOE_EINVAL
         pdw, ws, nws = dweight.data_ptr(), workspace.data_ptr(), workspace.nbytes
@@ -576,8 +580,10 @@ def moe_grouped_mm8(x, sx, offsets, w, sw, y, stream=None) -> int:
         return MOE_EINVAL
     tx, ty, kb = x.stride(), y.stride(), (k + 127) // 128
     if not (tx[1] == 1 and ty[1] == 1 and x.dtype is _E4M3 and x.get_device() == dev and y.get_device() == dev and
-            _whole(w, sh, _E4M3, dev) and _whole(sx, (m, kb), _FLOAT32, dev) and
-            _whole(sw, (E, (n + 127) // 128, kb), _FLOAT32, dev) and _whole(offsets, (E + 1,), _INT32, dev)):
+            w.dtype is _E4M3 and w.is_contiguous() and
+            sx.shape == (m, kb) and sx.dtype is _FLOAT32 and sx.is_contiguous() and sx.get_device() == dev and
+            sw.shape == (E, (n + 127) // 128, kb) and sw.dtype is _FLOAT32 and sw.is_contiguous() and sw.get_device() == dev and
+            offsets.shape == (E + 1,) and offsets.dtype is _INT32 and offsets.is_contiguous() and offsets.get_device() == dev):
         return MOE_EINVAL
     return _call(_fn.moe_grouped_mm8, dev, stream, x.data_ptr(), tx[0] if m > 1 else k, sx.data_ptr(), m,
                  offsets.data_ptr(), E, w.data_ptr(), sw.data_ptr(), n, k, y.data_ptr(), ty[0] if m > 1 else n,
@@ -598,31 +604,40 @@ def moe_grouped_geglu8(x, sx, offsets, w, sw, a, sa, gelu_variant: int = MOE_GEL
         return MOE_EINVAL
     tx, ta, kb = x.stride(), a.stride(), (k + 127) // 128
     if not (tx[1] == 1 and ta[1] == 1 and x.dtype is _E4M3 and a.dtype is _E4M3 and x.get_device() == dev and
-            a.get_device() == dev and _whole(w, sh, _E4M3, dev) and _whole(sx, (m, kb), _FLOAT32, dev) and
-            _whole(sw, (E, (n + 127) // 128, kb), _FLOAT32, dev) and _whole(sa, (m, (f + 127) // 128), _FLOAT32, dev) and
-            _whole(offsets, (E + 1,), _INT32, dev)):
+            a.get_device() == dev and w.dtype is _E4M3 and w.is_contiguous() and
+            sx.shape == (m, kb) and sx.dtype is _FLOAT32 and sx.is_contiguous() and sx.get_device() == dev and
+            sw.shape == (E, (n + 127) // 128, kb) and sw.dtype is _FLOAT32 and sw.is_contiguous() and sw.get_device() == dev and
+            sa.shape == (m, (f + 127) // 128) and sa.dtype is _FLOAT32 and sa.is_contiguous() and sa.get_device() == dev and
+            offsets.shape == (E + 1,) and offsets.dtype is _INT32 and offsets.is_contiguous() and offsets.get_device() == dev):
         return MOE_EINVAL
     return _call(_fn.moe_grouped_geglu8, dev, stream, gelu_variant, x.data_ptr(), tx[0] if m > 1 else k, sx.data_ptr(), m,
                  offsets.data_ptr(), E, w.data_ptr(), sw.data_ptr(), f, k, a.data_ptr(), ta[0] if m > 1 else f,
                  sa.data_ptr())
 
 
-def _ffn(weights, lead, d: int, dt, dev: int):
-    """(f, MoeFfnWeights) of (gate_up [*lead, 2 f, d], down [*lead, d, f], and for e4m3 their scales), or None."""
+def _ffn(weights, E: int, d: int, dt, dev: int):
+    """(f, MoeFfnWeights) of (gate_up [2 f, d], down [d, f], and for e4m3 their scales; E >= 0: each of E experts), or None."""
     gate_up, down, *scales = weights
-    f = down.shape[-1]
-    eight = len(scales) == 2 and scales[0] is not None
-    if eight:
-        dt, db, fb = _E4M3, (d + 127) // 128, (f + 127) // 128
-        if scales[1] is None or not (_whole(scales[0], (*lead, (2 * f + 127) // 128, db), _FLOAT32, dev) and
-                                     _whole(scales[1], (*lead, db, fb), _FLOAT32, dev)):
+    su, f = gate_up.shape, down.shape[-1]
+    pu = pd = None
+    if len(scales) == 2 and scales[0] is not None:
+        up, dn = scales
+        db, hb, fb = (d + 127) // 128, (2 * f + 127) // 128, (f + 127) // 128
+        if dn is None or not (
+                up.shape == ((hb, db) if E < 0 else (E, hb, db)) and up.dtype is _FLOAT32 and up.is_contiguous() and
+                up.get_device() == dev and dn.shape == ((db, fb) if E < 0 else (E, db, fb)) and dn.dtype is _FLOAT32 and
+                dn.is_contiguous() and dn.get_device() == dev):
             return None
-    elif any(s is not None for s in scales):
+        dt, pu, pd = _E4M3, up.data_ptr(), dn.data_ptr()
+    else:
+        for t in scales:
+            if t is not None:
+                return None
+    if not (su == ((2 * f, d) if E < 0 else (E, 2 * f, d)) and gate_up.dtype is dt and gate_up.is_contiguous() and
+            gate_up.get_device() == dev and down.shape == ((d, f) if E < 0 else (E, d, f)) and down.dtype is dt and
+            down.is_contiguous() and down.get_device() == dev):
         return None
-    if not (_whole(gate_up, (*lead, 2 * f, d), dt, dev) and _whole(down, (*lead, d, f), dt, dev)):
-        return None
-    return f, MoeFfnWeights(gate_up.data_ptr(), down.data_ptr(), scales[0].data_ptr() if eight else None,
-                            scales[1].data_ptr() if eight else None)
+    return f, MoeFfnWeights(gate_up.data_ptr(), down.data_ptr(), pu, pd)
 
 
 def moe_token_layer(x, ids, gates, routed, y, workspace, shared=None, gelu_variant: int = MOE_GELU_ERF, stream=None) -> int:
@@ -637,10 +652,11 @@ def moe_token_layer(x, ids, gates, routed, y, workspace, shared=None, gelu_varia
     (t, d), k, dev, dt, E = sx, si[1], x.get_device(), x.dtype, routed[0].shape[0]
     tx, ty = x.stride(), y.stride()
     if not (si[0] == t and y.shape == sx and tx[1] == 1 and ty[1] == 1 and y.get_device() == dev and
-            _whole(ids, (t, k), _INT32, dev) and _whole(gates, (t, k), _FLOAT32, dev) and workspace.is_contiguous() and
-            workspace.get_device() == dev):
+            ids.dtype is _INT32 and ids.is_contiguous() and ids.get_device() == dev and
+            gates.shape == si and gates.dtype is _FLOAT32 and gates.is_contiguous() and gates.get_device() == dev and
+            workspace.is_contiguous() and workspace.get_device() == dev):
         return MOE_EINVAL
-    r, s = _ffn(routed, (E,), d, dt, dev), (0, None) if shared is None else _ffn(shared, (), d, dt, dev)
+    r, s = _ffn(routed, E, d, dt, dev), (0, None) if shared is None else _ffn(shared, -1, d, dt, dev)
     if r is None or s is None:
         return MOE_EINVAL
     return _call(_fn.moe_token_layer, dev, stream, _DTYPE.get(dt, -1), gelu_variant, x.data_ptr(), tx[0] if t > 1 else d, t,

@@ -30,12 +30,16 @@
 // down: a unit is 16 outputs over all slots, its chunks dealt out to the warps of a
 // cluster's CTAs.  Each adds its slots' sums to its own copy of the tokens'
 // outputs; the copies are added in order, through distributed shared memory.  The
-// kernel starts while the first one runs and fills its stages with weights.
+// kernel starts on an SM as the first one leaves it, and fills its stages with
+// weights while others still run.
 //
 // 128 experts of 2816 x 704, 8 of them a token, and a shared one of 2816 x 2816: 7
-// tokens 84.7 us in a graph, HBM; one token 27.8 us (143 MB, 5.1 TB/s), in 8 bits 23.4
-// (71 MB, 3.0 TB/s): the chain from ids over the first bytes to the second kernel's
-// last ones, which nothing hides, is 8 us; in 8 bits the widening to bf16 adds 3.
+// tokens 83.1 us in a graph, HBM; one token 27.1 us (143 MB, 5.3 TB/s), in 8 bits 21.9
+// (71 MB, 3.3 TB/s).  What nothing hides there: 2.3 us from the start to the first
+// weights, 2.7 us from one kernel's last sums to the other's first weights (their
+// shared memory does not fit the SM's share that the first one has set; with all of
+// it set the second starts early, but takes HBM from the first: 28.5 us), 1.5 us of
+// tails; in 8 bits the widening.
 #include <algorithm>
 
 #include "allow_smem.h"
@@ -49,13 +53,18 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarpsUp = 8, kWarpsDown = 8;
-constexpr int kStagesUp = 2, kStagesDown = 1;      // of a warp
+constexpr int kTeams = 8, kWarpsDown = 8;          // units that a CTA of the first kernel has at hand; warps of the second's
+// Warps of a team, which take a unit's chunks in turn.  Widening e4m3 is a chain of four instructions: with one warp a unit, two a
+// scheduler, it held the weights up (8 bits, one token, 23.5 -> 21.9 us; with 88 registers a thread instead of 128 25.5).
+constexpr int team_of(bool w8) { return w8 ? 2 : 1; }
+constexpr int kTeamStages = 2, kStagesDown = 1;    // chunks on their way: of a team, of a warp
 constexpr int kCol = 128, kColBytes = 16 * kCol;  // bytes of a weight row that one load takes; of its 16 rows
 // Loads of a chunk: neighbours in their rows, which the memory likes (chunks of 256 bytes of a row 34 us for one token, 104 for
-// seven, when those of 512 took 29.8 and 87.9).  A CTA of the second kernel fits an SM beside one of the first: what it loads
-// before its wait hides its start.
-constexpr int kCols = 4;
+// seven, when those of 512 took 29.8 and 87.9; in the second kernel 768 bytes instead of 512 27.6 -> 27.1 and 83.5 -> 83.1).
+constexpr int kColsUp = 4, kColsDown = 6;
+// Of these, loads whose token values a lane holds at a time (registers: two CTAs of the second kernel an SM).
+constexpr int kTokensUp = kColsUp;
+constexpr int tokens_down(bool w8) { return w8 ? 3 : kColsDown; }
 constexpr int kTokens = 8;                       // of a slot
 constexpr int kMostSmem = 160 * 1024;            // of either kernel: the stages, and the lists of 1024 pairs and experts
 
@@ -109,7 +118,7 @@ __device__ __forceinline__ uint32_t widen8(uint32_t v) {
 __device__ __forceinline__ int row_of(int g) { return g >> 1 | (g & 1) << 2; }
 
 // This lane's share of up to 8 token rows over a chunk: 16 bytes a word.
-template <bool kW8>
+template <bool kW8, int kCols>
 struct TokenWords {
   static constexpr int kWords = kW8 ? 2 : 1;   // of a half of a load
   uint4 v[kCols][2][kWords];
@@ -137,11 +146,11 @@ struct TokenWords {
   }
 };
 
-// acc += 16 weight rows of a staged chunk of k values times the token rows.  With e4m3 weights `scale` holds the scales of the
-// chunk's blocks of 128 (its loads): lane i that of rows 0 .. 7, lane 16 + i of rows 8 .. 15.
-template <bool kBf16, bool kW8>
-__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const TokenWords<kW8>& x, int k, float scale,
-                                               int lane) {
+// acc += 16 weight rows of staged loads of k values times the token rows.  With e4m3 weights `scale` holds the scales of the
+// chunk's blocks of 128 (its loads, these from `block` on): lane i that of rows 0 .. 7, lane 16 + i of rows 8 .. 15.
+template <bool kBf16, bool kW8, int kCols>
+__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const TokenWords<kW8, kCols>& x, int k, float scale,
+                                               int block, int lane) {
   const int r = row_of(lane >> 2), t = lane & 3;
   const uint8_t* row = stage + r * kCol;
   float part[2][4] = {};
@@ -154,7 +163,7 @@ __device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* s
       const uint4 w0 = *reinterpret_cast<const uint4*>(from), w1 = *reinterpret_cast<const uint4*>(from + 8 * kCol);
       const uint4 b0 = x.v[i][h][0];
       if (kW8) {
-        const uint4 b1 = x.v[i][h][TokenWords<kW8>::kWords - 1];
+        const uint4 b1 = x.v[i][h][TokenWords<kW8, kCols>::kWords - 1];
         const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
         const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -167,7 +176,7 @@ __device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* s
       }
     }
     if (kW8) {
-      const float lo = __shfl_sync(0xFFFFFFFFu, scale, i), hi = __shfl_sync(0xFFFFFFFFu, scale, 16 + i);
+      const float lo = __shfl_sync(0xFFFFFFFFu, scale, block + i), hi = __shfl_sync(0xFFFFFFFFu, scale, 16 + block + i);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         acc[v] = fmaf(part[0][v] + part[1][v], v < 2 ? lo : hi, acc[v]);
@@ -309,37 +318,37 @@ __device__ __forceinline__ void prepare(const LayerParams& p, const Maps& maps, 
 
 // ------------------------------------------------------------------ up
 
-// (Registers: one CTA of each kernel an SM.  16-bit weights leave room for more than 128 a thread, which the loads of a chunk's
-// tokens use: 7 tokens 87.7 -> 85.6 us; with more for e4m3 weights the second kernel waits for the first: 23.6 -> 27.6 us.)
 template <bool kBf16, bool kW8>
-__global__ void __launch_bounds__(32 * kWarpsUp, kW8 ? 2 : 1) k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
-                                                       const __grid_constant__ Plan P) {
+__global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
+    k_layer_up(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p, const __grid_constant__ Plan P) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ Shared<kWarpsUp, kStagesUp> S;
-  constexpr int kWarps = kWarpsUp, kStages = kStagesUp;
+  constexpr int kTeam = team_of(kW8), kWarps = kTeams * kTeam, kStages = kTeamStages / kTeam;
+  __shared__ Shared<kWarps, kStages> S;
+  __shared__ float4 s_acc[2][kTeams][32];   // the second warps' sums, and what became of a team's waits; two units in turn
+  __shared__ int s_ok[2][kTeams][kTeam];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2;
   constexpr int kSize = kW8 ? 1 : 2;   // bytes of a weight
-  constexpr int kChunk = kCols * kCol / kSize, kStageBytes = kCols * kColBytes;   // values of a chunk
+  constexpr int kChunk = kColsUp * kCol / kSize, kStageBytes = kColsUp * kColBytes;   // values of a chunk
   prepare(p, maps, P, smem, S);
   pdl_wait();
   pdl_trigger();
   const Slot* slots = reinterpret_cast<const Slot*>(smem + P.at_slots);
   const int per = p.f / 8, per_shared = p.fs / 8, of_shared = p.fs ? divide_up(p.t, kTokens) * per_shared : 0;
-  const int stride = gridDim.x * kWarps;
+  const int stride = gridDim.x * kTeams, team = warp % kTeams, member = warp / kTeams;
   int units = of_shared;   // and the routed ones, once they are known
   uint8_t* const stages = smem + warp * kStages * kStageBytes;
   uint64_t* const full = S.full[warp];
   const uint64_t policy = read_once();
 
-  // A place in this warp's units and their chunks: the shared expert's units first, which are known before the picked experts.
+  // A place in this team's units and this warp's chunks: the shared expert's units first, which are known before the picked experts.
   struct Place {
     int unit, k0;
     Slot slot;
     int f, f0;
   };
   const auto enter = [&](Place& at) {
-    at.k0 = 0;
+    at.k0 = member * kChunk;
     if (at.unit >= units) return;
     const bool shared = at.unit < of_shared;
     const int i = shared ? at.unit : at.unit - of_shared, n = shared ? per_shared : per, s = i / n;
@@ -348,11 +357,11 @@ __global__ void __launch_bounds__(32 * kWarpsUp, kW8 ? 2 : 1) k_layer_up(const _
     at.f0 = 8 * (i - s * n);
   };
   Place next;
-  next.unit = blockIdx.x + warp * gridDim.x;   // as many on every SM as can be
+  next.unit = blockIdx.x + team * gridDim.x;   // as many on every SM as can be
   enter(next);
   int loads = 0;
   const auto load = [&] {   // the next chunk into the next stage, which no lane reads any more
-    if (next.unit >= units) return;
+    if (next.unit >= units || next.k0 >= p.d) return;   // (rows of one chunk leave the second warp nothing)
     if (loads < p.stall && elect_one()) {
       const int s = loads % kStages, cols = loads_of(min(kChunk, p.d - next.k0), kSize);
       mbar_arrive_expect_tx(&full[s], cols * kColBytes);
@@ -361,7 +370,7 @@ __global__ void __launch_bounds__(32 * kWarpsUp, kW8 ? 2 : 1) k_layer_up(const _
                 (next.k0 * kSize + i * kCol) / 4, next.f0, max(next.slot.expert, 0), &full[s], policy);
     }
     ++loads;
-    next.k0 += kChunk;
+    next.k0 += kTeam * kChunk;
     if (next.k0 >= p.d) {
       next.unit += stride;
       enter(next);
@@ -370,13 +379,13 @@ __global__ void __launch_bounds__(32 * kWarpsUp, kW8 ? 2 : 1) k_layer_up(const _
   for (int i = 0; i < kStages; ++i) load();
   list_slots(p, P, smem, S);
   units += S.n_routed * per;
-  if (next.k0 == 0) enter(next);
-  while (loads < kStages && next.unit < units) load();
+  if (next.unit >= of_shared) enter(next);
+  while (loads < kStages && next.unit < units && next.k0 < p.d) load();
 
-  int it = 0;
+  int it = 0, n_unit = 0;
   bool ok = true;
   Place at;
-  for (at.unit = blockIdx.x + warp * gridDim.x; ok && at.unit < units; at.unit += stride) {
+  for (at.unit = blockIdx.x + team * gridDim.x; ok && at.unit < units; at.unit += stride, ++n_unit) {
     enter(at);
     const int rows = __popc(at.slot.mask), f = at.f, f0 = at.f0;
     const float* scale = nullptr;   // lanes 0 .. 15: of the gate rows, 16 .. 31: of the up rows
@@ -388,16 +397,26 @@ __global__ void __launch_bounds__(32 * kWarpsUp, kW8 ? 2 : 1) k_layer_up(const _
     }
     float acc[4] = {};
     const uint16_t* x = p.x + nth_bit(at.slot.mask, min(g, rows - 1)) * p.ldx;
-    for (int k0 = 0; k0 < p.d; k0 += kChunk, ++it) {
+    for (int k0 = member * kChunk; k0 < p.d; k0 += kTeam * kChunk, ++it) {
       const int s = it % kStages, k = min(kChunk, p.d - k0);
-      TokenWords<kW8> tokens;
+      TokenWords<kW8, kTokensUp> tokens;
       tokens.load(x + k0, k, lane);
       float sc = 0.f;
       if (kW8 && kCol * (lane & 15) < k) sc = __ldg(scale + k0 / 128 + (lane & 15));
       if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
-      chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
+      chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes, tokens, k, sc, 0, lane);
       __syncwarp();
       load();
+    }
+    if constexpr (kTeam > 1) {   // the second warp's sums go to the first (who writes a buffer again knows that the other came to the unit between)
+      const int buf = n_unit & 1;
+      if (member) s_acc[buf][team][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      if (lane == 0) s_ok[buf][team][member] = ok;
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * kTeam) : "memory");
+      ok = s_ok[buf][team][0] && s_ok[buf][team][1];
+      if (member) continue;
+      const float4 v = s_acc[buf][team][lane];
+      acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
     }
     // this lane: gate and up of one feature, columns 2 (lane % 4) and the next
     uint16_t* a = p.a + (at.slot.expert < 0 ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
@@ -443,7 +462,7 @@ __device__ __forceinline__ float ld_rank(const float* at, uint32_t rank) {
 }
 
 template <bool kBf16, bool kW8>
-__global__ void __launch_bounds__(32 * kWarpsDown, kW8 ? 2 : 1) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
+__global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_constant__ Maps maps, const __grid_constant__ LayerParams p,
                                                          const __grid_constant__ Plan P, int split) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -452,7 +471,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, kW8 ? 2 : 1) k_layer_down(con
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2;
   const int rank = static_cast<int>(cluster_rank()), d0 = blockIdx.x / split * 16;
   constexpr int kSize = kW8 ? 1 : 2;
-  constexpr int kStageBytes = kCols * kColBytes, kColValues = kCol / kSize;
+  constexpr int kStageBytes = kColsDown * kColBytes, kColValues = kCol / kSize;
   prepare(p, maps, P, smem, S);
   // ids and weights are older than the first kernel, which let this one start after its own wait
   list_slots(p, P, smem, S);
@@ -473,7 +492,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, kW8 ? 2 : 1) k_layer_down(con
 
   struct Place {
     int slot, col, left;   // in the slot; of this part's columns from here on
-    __device__ __forceinline__ int cols(int of_slot) const { return min(min(kCols, left), of_slot - col); }
+    __device__ __forceinline__ int cols(int of_slot) const { return min(min(kColsDown, left), of_slot - col); }
   };
   const auto of_slot = [&](const Place& at) { return at.slot >= n_routed ? per_shared : per; };
   const auto advance = [&](Place& at) {
@@ -518,17 +537,26 @@ __global__ void __launch_bounds__(32 * kWarpsDown, kW8 ? 2 : 1) k_layer_down(con
     const bool shared = at.slot >= n_routed;
     const Slot slot = slots[at.slot];
     const int f = shared ? p.fs : p.f, k = min(at.cols(of_slot(at)) * kColValues, f - k0);
-    TokenWords<kW8> tokens;
-    tokens.load(p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
-                    static_cast<long long>(slot.base + min(g, __popc(slot.mask) - 1)) * f + k0,
-                k, lane);
+    const uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
+                        static_cast<long long>(slot.base + min(g, __popc(slot.mask) - 1)) * f + k0;
+    constexpr int kTokenCols = tokens_down(kW8);
+    TokenWords<kW8, kTokenCols> tokens;
+    tokens.load(a, k, lane);
     float sc = 0.f;
     if (kW8 && kCol * (lane & 15) < k) {
       const long long block = (shared ? 0LL : static_cast<long long>(slot.expert) * db) + d0 / 128;
       sc = __ldg((shared ? p.shared.down_scale : p.routed.down_scale) + block * divide_up(f, 128) + k0 / 128 + (lane & 15));
     }
     if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
-    chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes, tokens, k, sc, lane);
+#pragma unroll
+    for (int c = 0; c < kColsDown; c += kTokenCols) {
+      const int done = c * kColValues;
+      if (c) {
+        if (done >= k) break;
+        tokens.load(a + done, k - done, lane);
+      }
+      chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes + c * kColBytes, tokens, k - done, sc, c, lane);
+    }
     __syncwarp();
     load_next();
     const int was = at.slot;
@@ -583,7 +611,7 @@ int most_slots(const LayerParams& p) { return std::min(p.t * p.k, p.E + p.t * p.
 Plan make_plan(const LayerParams& p, bool down) {
   Plan P{};
   const int slots = most_slots(p) + divide_up(p.t, kTokens);
-  P.at_sums = (down ? kWarpsDown * kStagesDown * kCols : kWarpsUp * kStagesUp * kCols) * kColBytes;
+  P.at_sums = (down ? kWarpsDown * kStagesDown * kColsDown : kTeams * kTeamStages * kColsUp) * kColBytes;
   P.at_mask = P.at_sums + (down ? kWarpsDown * p.t * 64 : 0);
   P.at_ids = P.at_mask + 4 * p.E;
   P.at_gates = P.at_ids + 4 * p.t * p.k;
@@ -650,16 +678,16 @@ bool launch_both(const LayerParams& p, int sms, cudaStream_t s) {
   if (p.fs && (!map_up(&m_up.shared, p.shared.gate_up, 1, p.fs, p.d, kSize) ||
                !map_down(&m_down.shared, p.shared.down, 1, p.d, p.fs, kSize)))
     return false;
-  // one CTA an SM, or as many as the units of the most slots need; a CTA's warps share the units evenly
+  // one CTA an SM, or as many as the units of the most slots need; a CTA's teams share the units evenly
   const int slots = most_slots(p);
   const long long units = static_cast<long long>(slots) * (p.f / 8) + divide_up(p.t, kTokens) * (p.fs / 8);
   const int grid = static_cast<int>(std::min<long long>(sms, units));
-  if (!launch(k_layer_up<kBf16, kW8>, grid, 32 * kWarpsUp, up, 1, s, m_up, p, up)) return false;
+  if (!launch(k_layer_up<kBf16, kW8>, grid, 32 * kTeams * team_of(kW8), up, 1, s, m_up, p, up)) return false;
   const int blocks = p.d / 16, cols = slots * divide_up(p.f * kSize, kCol) + divide_up(p.fs * kSize, kCol);
   int split = 1;
   // Up to two CTAs an SM (16 experts of f = 2048, 4 tokens: d = 1024 split in 4 31.1 us, in 2 33.8; d = 512 in 4 21.6, in 1 31.8),
   // but of eight only as many as SMs: two an SM do not all start at once (d = 512 in 8 26.3; d = 256 in 8 16.7, in 4 18.3).
-  while (split < 8 && 2 * split * blocks <= (split < 4 ? 2 : 1) * sms && 2 * split * kWarpsDown * kCols <= cols) split *= 2;
+  while (split < 8 && 2 * split * blocks <= (split < 4 ? 2 : 1) * sms && 2 * split * kWarpsDown * kColsDown <= cols) split *= 2;
   return launch(k_layer_down<kBf16, kW8>, blocks * split, 32 * kWarpsDown, down, split, s, m_down, p, down, split);
 }
 

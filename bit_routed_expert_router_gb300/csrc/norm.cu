@@ -10,8 +10,8 @@
 // value is read once, a row stays in registers between its sum and its outputs,
 // eight values (16 bytes) a thread.
 //
-// 4096 rows of 2816, delta in 16 bits, out in 8 bits: 15.0 us, 5.4 TB/s (80 % of a
-// copy's rate).  Their gradient with dres: 20.0 us, of which 16.0 are the rows'
+// 4096 rows of 2816, delta in 16 bits, out in 8 bits: 14.9 us, 5.4 TB/s (80 % of a
+// copy's rate).  Their gradient with dres: 19.6 us, of which 16.0 are the rows'
 // (5.8 TB/s) and the rest the sum of the weight gradient's parts after them.  One
 // row: 1.7 us in a graph, a launch.
 #include <algorithm>
@@ -24,26 +24,56 @@ namespace moe {
 
 namespace {
 
-template <bool kBf16>
-__device__ __forceinline__ void widen(float (&o)[8], uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = kBf16 ? __uint_as_float(w[i] << 16) : half_lo(w[i]);
-    o[2 * i + 1] = kBf16 ? __uint_as_float(w[i] & 0xFFFF0000u) : half_hi(w[i]);
-  }
+// Eight values as four pairs: the arithmetic on them is two values an instruction (f32x2).
+struct Eight {
+  uint64_t p[4];
+  __device__ __forceinline__ float lo(int i) const { return __uint_as_float(static_cast<uint32_t>(p[i])); }
+  __device__ __forceinline__ float hi(int i) const { return __uint_as_float(static_cast<uint32_t>(p[i] >> 32)); }
+};
+
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+  return __uint_as_float(static_cast<uint32_t>(v)) + __uint_as_float(static_cast<uint32_t>(v >> 32));
 }
 
 template <bool kBf16>
-__device__ __forceinline__ uint4 narrow(const float (&v)[8]) {
+__device__ __forceinline__ Eight widen(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  Eight o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    o.p[i] = kBf16 ? pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)) : pair(half_lo(w[i]), half_hi(w[i]));
+  return o;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint4 narrow(const Eight& v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (kBf16) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(v.lo(i), v.hi(i));
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     } else {
-      const __half2 p = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+      const __half2 p = __floats2half2_rn(v.lo(i), v.hi(i));
       w[i] = *reinterpret_cast<const uint32_t*>(&p);
     }
   }
@@ -71,7 +101,8 @@ __global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 10
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = (blockIdx.x * blockDim.y + threadIdx.y) * kR;
   pdl_wait();
   pdl_trigger();
-  float v[kR][kV][8], sum[kR];
+  Eight v[kR][kV];
+  float sum[kR];
   uint4 w[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
@@ -95,35 +126,34 @@ __global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 10
     for (int q = 0; q < kR; ++q) {
       const int r = r0 + q;
       if (r < p.m && i < n_words) {
-        widen<kBf16>(v[q][j], h[q]);
+        v[q][j] = widen<kBf16>(h[q]);
         if (kDelta != kNoDelta) {
-          float d[8];
+          Eight d;
           if (kDelta == kDelta16) {
-            widen<kBf16>(d, d16[q]);
+            d = widen<kBf16>(d16[q]);
           } else {
             const float4 a = d32[q][0], b = d32[q][1];
-            d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
+            d = {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) v[q][j][k] += d[k];
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = add2(v[q][j].p[k], d.p[k]);
           const uint4 stored = narrow<kBf16>(v[q][j]);
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h_out) + r * p.ldo + c) = stored;
-          widen<kBf16>(v[q][j], stored);
+          v[q][j] = widen<kBf16>(stored);
         }
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[q][j][k] = 0.f;
+        v[q][j] = {};
       }
     }
   }
 #pragma unroll
   for (int q = 0; q < kR; ++q) {
-    sum[q] = 0.f;
+    uint64_t two = 0;
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[q] = fmaf(v[q][j][k], v[q][j][k], sum[q]);
-    sum[q] = warp_sum(sum[q]);
+      for (int k = 0; k < 4; ++k) two = fma2(v[q][j].p[k], v[q][j].p[k], two);
+    sum[q] = warp_sum(sum2(two));
   }
   if (warps > 1) {
     const int mine = threadIdx.y * warps;
@@ -143,27 +173,27 @@ __global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 10
       const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
       const bool in = r < p.m && i < n_words;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[q][j][k] *= rstd;
+      for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], both(rstd));
       if (p.weight && in) {
-        float f[8];
-        widen<kBf16>(f, w[j]);
+        const Eight f = widen<kBf16>(w[j]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[q][j][k] *= f[k];
+        for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], f.p[k]);
       }
       if (in && p.y) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.ldy + c) = narrow<kBf16>(v[q][j]);
       if (p.y8) {
         float top = 0.f;   // of the 16 lanes that hold a group; words past the row are 0
 #pragma unroll
-        for (int k = 0; k < 8; ++k) top = max_abs(top, v[q][j][k]);
+        for (int k = 0; k < 4; ++k) top = max_abs(max_abs(top, v[q][j].lo(k)), v[q][j].hi(k));
         if (!in) top = 0.f;
 #pragma unroll
         for (int d = 8; d; d >>= 1) top = max_abs(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         const Scale8 s = scale8(top);
         if (in) {
-          const float x = s.inverse;
-          float(&a)[8] = v[q][j];
+          Eight a;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) a.p[k] = mul2(v[q][j].p[k], both(s.inverse));
           *reinterpret_cast<uint2*>(p.y8 + r * p.ldy8 + c) =
-              make_uint2(to_e4m3x4(a[0] * x, a[1] * x, a[2] * x, a[3] * x), to_e4m3x4(a[4] * x, a[5] * x, a[6] * x, a[7] * x));
+              make_uint2(to_e4m3x4(a.lo(0), a.hi(0), a.lo(1), a.hi(1)), to_e4m3x4(a.lo(2), a.hi(2), a.lo(3), a.hi(3)));
           if ((i & 15) == 0) p.scale[static_cast<long long>(r) * ((p.d + 127) / 128) + i / 16] = s.scale;
         }
       }
@@ -180,14 +210,14 @@ __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Rows on their way to a CTA of k_norm_grad (three of them: 20.2 us for 4096 rows of 2816; four: 21.0; two: 20.0).
+// Rows on their way to a CTA of k_norm_grad (4096 rows of 2816: two 20.0 us, three 20.2, four 21.0).
 constexpr int kGradStages = 2;
 
 // CTA b takes the rows b, b + parts, ...: its columns' part of the weight gradient stays in registers and is written once.  The
 // next rows are on their way to shared memory, each thread's words to its own place there, which needs no barrier.  (With one
 // row on its way in registers 22.0 us for 4096 rows of 2816, with none 36; with three CTAs an SM 20.5.)
 template <bool kBf16, int kV, int kThreads>
-__global__ void __launch_bounds__(kThreads, kV == 1 ? 2 : 1) k_norm_grad(NormGradParams p) {
+__global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 2 : 1) k_norm_grad(NormGradParams p) {
   constexpr int kStages = kGradStages;
   extern __shared__ uint4 s_rows[];   // [stage][h, dy, dres][word of a thread][thread]
   __shared__ float2 s_sum[2][32];
@@ -208,35 +238,45 @@ __global__ void __launch_bounds__(kThreads, kV == 1 ? 2 : 1) k_norm_grad(NormGra
   };
 #pragma unroll
   for (int s = 0; s < kStages; ++s) load(blockIdx.x + s * gridDim.x, s);
-  float dw[kV][8], w[kV][8];
+  // A row's values stay in registers between its sums and its outputs where a thread has one word of them; two would spill
+  // or leave room for one CTA an SM, so they are read again, and the weight is kept as it is (2000 rows of 5632 22.9 -> 21.4 us,
+  // 700 of 16384 40.3 -> 24.0).
+  constexpr bool kAgain = kV > 1;
+  Eight dw[kV], w[kV];
+  uint4 w_raw[kV];
 #pragma unroll
   for (int j = 0; j < kV; ++j) {
     const int i = threadIdx.x + j * blockDim.x;
+    const uint32_t one = kBf16 ? 0x3F803F80u : 0x3C003C00u;
+    w_raw[j] = p.weight && i < n_words ? __ldg(reinterpret_cast<const uint4*>(p.weight) + i) : make_uint4(one, one, one, one);
+    w[j] = widen<kBf16>(w_raw[j]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[j][k] = 0.f, w[j][k] = 1.f;
-    if (p.weight && i < n_words) widen<kBf16>(w[j], __ldg(reinterpret_cast<const uint4*>(p.weight) + i));
+    for (int k = 0; k < 4; ++k) dw[j].p[k] = 0;
   }
   int turn = 0, s = 0;
   for (int r = blockIdx.x; r < p.m; r += gridDim.x, turn ^= 1) {
-    float a[kV][8], b[kV][8], o[kV][8], ss = 0.f, dot = 0.f;
+    Eight a[kV], b[kV], o[kV];
+    uint64_t ss2 = 0, dot2 = 0;
+    const auto fetch = [&](int j) {
+      const uint4 none = make_uint4(0, 0, 0, 0);
+      const bool in = static_cast<int>(threadIdx.x + j * blockDim.x) < n_words;
+      a[j] = widen<kBf16>(in ? *place(s, 0, j) : none);
+      b[j] = widen<kBf16>(in ? *place(s, 1, j) : none);
+      o[j] = widen<kBf16>(in && p.dres ? *place(s, 2, j) : none);
+      if (kAgain) w[j] = widen<kBf16>(w_raw[j]);
+    };
     wait_copies<kStages - 1>();
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-      const uint4 none = make_uint4(0, 0, 0, 0);
-      const bool in = static_cast<int>(threadIdx.x + j * blockDim.x) < n_words;
-      widen<kBf16>(a[j], in ? *place(s, 0, j) : none);
-      widen<kBf16>(b[j], in ? *place(s, 1, j) : none);
-      widen<kBf16>(o[j], in && p.dres ? *place(s, 2, j) : none);
+      fetch(j);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ss = fmaf(a[j][k], a[j][k], ss);
-        dot = fmaf(b[j][k] * w[j][k], a[j][k], dot);
+      for (int k = 0; k < 4; ++k) {
+        ss2 = fma2(a[j].p[k], a[j].p[k], ss2);
+        dot2 = fma2(mul2(b[j].p[k], w[j].p[k]), a[j].p[k], dot2);
       }
     }
-    load(r + kStages * gridDim.x, s);
-    s = (s + 1) % kStages;
-    ss = warp_sum(ss);
-    dot = warp_sum(dot);
+    if (!kAgain) load(r + kStages * gridDim.x, s);
+    float ss = warp_sum(sum2(ss2)), dot = warp_sum(sum2(dot2));
     if (warps > 1) {
       if (lane == 0) s_sum[turn][warp] = make_float2(ss, dot);
       __syncthreads();
@@ -249,13 +289,16 @@ __global__ void __launch_bounds__(kThreads, kV == 1 ? 2 : 1) k_norm_grad(NormGra
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
       const int i = threadIdx.x + j * blockDim.x;
+      if (kAgain) fetch(j);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        dw[j][k] = fmaf(b[j][k], a[j][k] * rstd, dw[j][k]);
-        o[j][k] += fmaf(b[j][k] * w[j][k], rstd, -(a[j][k] * mean));
+      for (int k = 0; k < 4; ++k) {
+        dw[j].p[k] = fma2(b[j].p[k], mul2(a[j].p[k], both(rstd)), dw[j].p[k]);
+        o[j].p[k] = add2(o[j].p[k], fma2(mul2(b[j].p[k], w[j].p[k]), both(rstd), mul2(a[j].p[k], both(-mean))));
       }
       if (i < n_words) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dh) + r * p.lddh + 8 * i) = narrow<kBf16>(o[j]);
     }
+    if (kAgain) load(r + kStages * gridDim.x, s);
+    s = (s + 1) % kStages;
   }
   if (!p.part) return;
 #pragma unroll
@@ -263,8 +306,8 @@ __global__ void __launch_bounds__(kThreads, kV == 1 ? 2 : 1) k_norm_grad(NormGra
     const int i = threadIdx.x + j * blockDim.x;
     if (i >= n_words) continue;
     float4* at = reinterpret_cast<float4*>(p.part + static_cast<long long>(blockIdx.x) * p.d + 8 * i);
-    at[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-    at[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    at[0] = make_float4(dw[j].lo(0), dw[j].hi(0), dw[j].lo(1), dw[j].hi(1));
+    at[1] = make_float4(dw[j].lo(2), dw[j].hi(2), dw[j].lo(3), dw[j].hi(3));
   }
 }
 

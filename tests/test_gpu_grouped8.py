@@ -81,12 +81,13 @@ def test_gated(counts, f, k, variant):
     close_gated(a, sa, x, sx, off, w, sw, f, variant)
 
 
-def test_rows_of_no_group_and_strides():
-    counts, n, k = [40, 0, 9], 264, 272
+@pytest.mark.parametrize("n", [264, 6600])   # few tiles, and many
+def test_rows_of_no_group_and_strides(n):
+    counts, k = [40, 0, 9], 272
     x, sx, off, w, sw = case(counts, n, k, pad=13, first=5)
     wide_x = torch.zeros(x.shape[0], 512, device="cuda").to(E4M3)
     wide_x[:, 32:32 + k] = x
-    y = torch.full((x.shape[0], 400), 7.0, dtype=BF16, device="cuda")
+    y = torch.full((x.shape[0], n + 136), 7.0, dtype=BF16, device="cuda")
     moe.check(moe.moe_grouped_mm8(wide_x[:, 32:32 + k], sx, off, w, sw, y[:, 8:8 + n]))
     want, size = products(wide_rows(x, sx), wide_weights(w, sw), off)
     close(y[5:54, 8:8 + n], want[5:54], size[5:54], k)
@@ -101,8 +102,9 @@ def test_rows_of_no_group_and_strides():
     assert torch.all(a[:5].float() == 1) and torch.all(a[54:].float() == 1) and torch.all(a[:, 16 + f:].float() == 1)
 
 
-def test_non_finite_rows_stay_rows():
-    counts, n, k = [20, 30, 10], 160, 384
+@pytest.mark.parametrize("n", [160, 6504])   # few tiles, and many
+def test_non_finite_rows_stay_rows(n):
+    counts, k = [20, 30, 10], 384
     x, sx, off, w, sw = case(counts, n, k, pad=4)
     clean = torch.empty(x.shape[0], n, device="cuda")
     moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, clean))
@@ -137,10 +139,11 @@ def test_long_reductions_of_one_sign():
     assert torch.all((y.double() - want).abs() <= (512 + 3 + 256) * 2.0 ** -24 * want)
 
 
-def test_offsets_out_of_order_stay_inside():
+@pytest.mark.parametrize("n", [64, 6600])   # few tiles, and many
+def test_offsets_out_of_order_stay_inside(n):
     """Undefined outputs, but only inside the tensors: what surrounds them is as it was."""
-    x, sx, _, w, sw = case([16, 16, 16], 64, 64)
-    buf = torch.full((48 + 200, 64), 3.0, device="cuda")
+    x, sx, _, w, sw = case([16, 16, 16], n, 64)
+    buf = torch.full((48 + 200, n), 3.0, device="cuda")
     for off in ([0, 40, 10, 48], [-5, 16, 100, 1 << 30], [48, 30, 20, 0], [10, 10, 10, 10]):
         buf.fill_(3.0)
         moe.check(moe.moe_grouped_mm8(x, sx, torch.tensor(off, dtype=torch.int32, device="cuda"), w, sw, buf[100:148]))
@@ -239,3 +242,23 @@ def test_the_same_rows_alone_and_in_a_batch():
     for r, e in ((0, 0), (129, 0), (130, 2), (386, 2), (388, 3)):
         moe.check(moe.moe_grouped_mm8(x[r:r + 1], sx[r:r + 1], offsets_of([1]), w[e:e + 1], sw[e:e + 1], one))
         assert torch.equal(one[0], y[r])
+
+
+@pytest.mark.parametrize("out", [BF16, F16, F32])
+@pytest.mark.parametrize("counts,n,k", [([1], 20008, 144), ([300, 0, 1, 257], 2840, 400), ([513, 40], 5000, 272), ([33] * 8, 5384, 128)])
+def test_products_of_many_tiles(counts, n, k, out):
+    """More tiles than multiprocessors, of 256 features, the last ones ragged."""
+    x, sx, off, w, sw = case(counts, n, k, seed=n + k)
+    sx = sx * 2.0 ** -8
+    y = torch.full((x.shape[0], n), 7.0, dtype=out, device="cuda")
+    moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y))
+    close(y, *products(wide_rows(x, sx), wide_weights(w, sw), off), k)
+
+
+def test_few_and_many_tiles_give_the_same_sums():
+    """An expert's first features alone, and among many: bit for bit."""
+    x, sx, off, w, sw = case([100, 60], 6528, 656)
+    y, few = torch.empty(160, 6528, device="cuda"), torch.empty(160, 256, device="cuda")
+    moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y))
+    moe.check(moe.moe_grouped_mm8(x, sx, off, w.view(torch.uint8)[:, :256].contiguous().view(E4M3), sw[:, :2].contiguous(), few))
+    assert torch.equal(few, y[:, :256])

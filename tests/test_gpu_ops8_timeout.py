@@ -41,9 +41,11 @@ def run_out(call, *outs):
     moe.check(moe.moe_grouped_sync())
 
 
-@pytest.mark.parametrize("counts,out", [([9, 0, 14], BF16), ([300, 0, 1100], F16), ([300, 0, 1100], F32)])
-def test_products(counts, out):
-    n, k = 1000, 1040
+@pytest.mark.parametrize("counts,out,n", [([9, 0, 14], BF16, 1000), ([300, 0, 1100], F16, 1000), ([300, 0, 1100], F32, 1000),
+                                          ([9, 0, 14], BF16, 6600), ([300, 0, 1100], F16, 2104), ([300, 0, 1100], F32, 2104)])
+def test_products(counts, out, n):
+    """Few tiles, and many."""
+    k = 1040
     x, sx, off, w, sw = case(counts, n, k)
     sx *= 2.0 ** -8
     whole, y = guarded(out, sum(counts), n)

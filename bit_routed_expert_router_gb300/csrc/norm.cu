@@ -10,7 +10,7 @@
 // value is read once, a row stays in registers between its sum and its outputs,
 // eight values (16 bytes) a thread.
 //
-// 4096 rows of 2816, delta in 16 bits, out in 8 bits: 14.9 us, 5.4 TB/s (80 % of a
+// 4096 rows of 2816, delta in 16 bits, out in 8 bits: 15.0 us, 5.4 TB/s (80 % of a
 // copy's rate).  Their gradient with dres: 19.6 us, of which 16.0 are the rows'
 // (5.8 TB/s) and the rest the sum of the weight gradient's parts after them.  One
 // row: 1.7 us in a graph, a launch.
@@ -90,12 +90,28 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Where the largest |r w| of a group is a top of common size, its quotients come from r w alone: that is exact (two 16-bit
+// values), and rstd is in the largest value too.  With the roundings of 448 / top and of the product only, fewer of them land on the
+// wrong side of a tie (of 78 million values 8,700 instead of 14,300 differ from quotients in 64 bits, which break the exact ties
+// among them as they come; as fp32 quotients of v and its scale 10,500).
+__device__ __forceinline__ bool common(float top) {
+  constexpr uint32_t lo = 0x15000000u, hi = 0x6A000000u;   // 2^-85 and 2^85
+  return __float_as_uint(top) - lo < hi - lo;
+}
+
+// 448 / top: the fast reciprocal after one of Newton's steps.
+__device__ __forceinline__ float inverse_of(float top) {
+  float x;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(x) : "f"(top));
+  return kMaxE4m3 * fmaf(x, fmaf(-top, x, 1.f), x);
+}
+
 enum { kNoDelta = 0, kDelta16 = 1, kDelta32 = 2 };
 
 // A row is the threads of one threadIdx.y; kV words of eight values a thread, of kR rows at a time: one barrier for all of them,
 // and more loads on their way (4096 rows of 2816, 8-bit out: 15.0 us against 16.2).
 template <bool kBf16, int kDelta, int kV, int kR>
-__global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 1024) k_norm(NormParams p) {
+__global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(NormParams p) {   // (with 52 registers 16.2 us)
   __shared__ float s_sum[kR][32];
   const int n_words = p.d / 8, warps = blockDim.x / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r0 = (blockIdx.x * blockDim.y + threadIdx.y) * kR;
@@ -121,7 +137,7 @@ __global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 10
         }
       }
     }
-    if (p.weight && i < n_words) w[j] = __ldg(reinterpret_cast<const uint4*>(p.weight) + i);
+    w[j] = p.weight && i < n_words ? __ldg(reinterpret_cast<const uint4*>(p.weight) + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int q = 0; q < kR; ++q) {
       const int r = r0 + q;
@@ -172,22 +188,35 @@ __global__ void __launch_bounds__(kV == 1 && kR == 1 ? 1024 : kV == 1 ? 512 : 10
     for (int j = 0; j < kV; ++j) {
       const int i = threadIdx.x + j * blockDim.x, c = 8 * i;
       const bool in = r < p.m && i < n_words;
+      const auto f = [&](int k) { return widen<kBf16>(w[j]).p[k]; };
+      if (p.y && in) {
+        Eight y;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], both(rstd));
-      if (p.weight && in) {
-        const Eight f = widen<kBf16>(w[j]);
+        for (int k = 0; k < 4; ++k) y.p[k] = mul2(v[q][j].p[k], both(rstd));
+        if (p.weight)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], f.p[k]);
+          for (int k = 0; k < 4; ++k) y.p[k] = mul2(y.p[k], f(k));
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.ldy + c) = narrow<kBf16>(y);
       }
-      if (in && p.y) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.ldy + c) = narrow<kBf16>(v[q][j]);
       if (p.y8) {
+        if (p.weight)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], f(k));
         float top = 0.f;   // of the 16 lanes that hold a group; words past the row are 0
 #pragma unroll
         for (int k = 0; k < 4; ++k) top = max_abs(max_abs(top, v[q][j].lo(k)), v[q][j].hi(k));
-        if (!in) top = 0.f;
 #pragma unroll
         for (int d = 8; d; d >>= 1) top = max_abs(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-        const Scale8 s = scale8(top);
+        Scale8 s;
+        const float least = max_abs(kTiny, top * rstd);
+        if (common(top) && least > kTiny) {
+          s.scale = least * (1.f / kMaxE4m3);
+          s.inverse = inverse_of(top);
+        } else {   // the least scale, or values that are not finite
+          s = scale8(least);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], both(rstd));
+        }
         if (in) {
           Eight a;
 #pragma unroll

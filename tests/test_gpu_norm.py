@@ -272,3 +272,27 @@ def test_calls_on_two_streams_at_once():
     torch.cuda.synchronize()
     for dh, dw in sum(got, []):
         assert torch.equal(dh, want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("size,weight,eps", [(1e-27, 1.0, 1e-30), (1e-20, 1e-7, 1e-30), (1.0, 1e26, 1e-6), (1e17, 1e-20, 0.0), (0.0, 1.0, 1e-30)])
+def test_quotients_of_very_small_and_large_values(size, weight, eps):
+    """Past where they come from the row and the weight alone."""
+    g = gen(51)
+    h, w = rand(g, BF16, 6, 400, scale=size), (1 + 0.2 * torch.randn(400, generator=g, device="cuda")).mul(weight).to(BF16)
+    _, y, y8, s = call(h, None, w, "both", eps=eps)
+    want = normed(h, w, eps)
+    near16(y, want, BF16)
+    near8(y8, s, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_quotients_are_rounded_to_the_nearest(dtype):
+    """e4m3 values against quotients in 64 bits: off only where these lie next to a tie, by three roundings of fp32 at most
+    (r w is exact, 448 / top takes two, the product one)."""
+    h, w = rand(gen(61), dtype, 3000, 1024), rand(gen(62), dtype, 1024)
+    _, _, y8, _ = call(h, None, w, "8")
+    u = groups(h.double() * w.double())
+    q = (u * 448 / u.abs().amax(-1, keepdim=True)).view(3000, 1024)
+    got = y8.double()
+    nearest = q.float().to(E4M3).double()
+    assert torch.all((got - q).abs() <= (nearest - q).abs() + 3 * 2.0 ** -24 * 2 * q.abs())

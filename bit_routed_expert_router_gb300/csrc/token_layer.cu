@@ -54,8 +54,8 @@ namespace moe {
 namespace {
 
 constexpr int kTeams = 8, kWarpsDown = 8;          // units that a CTA of the first kernel has at hand; warps of the second's
-// Warps of a team, which take a unit's chunks in turn.  Widening e4m3 is a chain of four instructions: with one warp a unit, two a
-// scheduler, it held the weights up (8 bits, one token, 23.5 -> 21.9 us; with 88 registers a thread instead of 128 25.5).
+// Warps of a team, which take a unit's chunks in turn where it has several.  Widening e4m3 is a chain of four instructions: with
+// one warp a unit, two a scheduler, it held the weights up (8 bits, one token, 23.5 -> 21.9 us; with 88 registers a thread instead of 128 25.5).
 constexpr int team_of(bool w8) { return w8 ? 2 : 1; }
 constexpr int kTeamStages = 2, kStagesDown = 1;    // chunks on their way: of a team, of a warp
 constexpr int kCol = 128, kColBytes = 16 * kCol;  // bytes of a weight row that one load takes; of its 16 rows
@@ -66,6 +66,7 @@ constexpr int kColsUp = 4, kColsDown = 6;
 constexpr int kTokensUp = kColsUp;
 constexpr int tokens_down(bool w8) { return w8 ? 3 : kColsDown; }
 constexpr int kTokens = 8;                       // of a slot
+constexpr int kMostSplit = 8;                    // CTAs that share a unit of the second kernel
 constexpr int kMostSmem = 160 * 1024;            // of either kernel: the stages, and the lists of 1024 pairs and experts
 
 struct Slot {
@@ -335,7 +336,8 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
   pdl_trigger();
   const Slot* slots = reinterpret_cast<const Slot*>(smem + P.at_slots);
   const int per = p.f / 8, per_shared = p.fs / 8, of_shared = p.fs ? divide_up(p.t, kTokens) * per_shared : 0;
-  const int stride = gridDim.x * kTeams, team = warp % kTeams, member = warp / kTeams;
+  const int mates = kTeam > 1 && p.d > kChunk ? kTeam : 1;   // units of one chunk: one warp each
+  const int teams = kWarps / mates, stride = gridDim.x * teams, team = warp % teams, member = warp / teams;
   int units = of_shared;   // and the routed ones, once they are known
   uint8_t* const stages = smem + warp * kStages * kStageBytes;
   uint64_t* const full = S.full[warp];
@@ -361,7 +363,7 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
   enter(next);
   int loads = 0;
   const auto load = [&] {   // the next chunk into the next stage, which no lane reads any more
-    if (next.unit >= units || next.k0 >= p.d) return;   // (rows of one chunk leave the second warp nothing)
+    if (next.unit >= units) return;
     if (loads < p.stall && elect_one()) {
       const int s = loads % kStages, cols = loads_of(min(kChunk, p.d - next.k0), kSize);
       mbar_arrive_expect_tx(&full[s], cols * kColBytes);
@@ -370,7 +372,7 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
                 (next.k0 * kSize + i * kCol) / 4, next.f0, max(next.slot.expert, 0), &full[s], policy);
     }
     ++loads;
-    next.k0 += kTeam * kChunk;
+    next.k0 += mates * kChunk;
     if (next.k0 >= p.d) {
       next.unit += stride;
       enter(next);
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
   list_slots(p, P, smem, S);
   units += S.n_routed * per;
   if (next.unit >= of_shared) enter(next);
-  while (loads < kStages && next.unit < units && next.k0 < p.d) load();
+  while (loads < kStages && next.unit < units) load();
 
   int it = 0, n_unit = 0;
   bool ok = true;
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
     }
     float acc[4] = {};
     const uint16_t* x = p.x + nth_bit(at.slot.mask, min(g, rows - 1)) * p.ldx;
-    for (int k0 = member * kChunk; k0 < p.d; k0 += kTeam * kChunk, ++it) {
+    for (int k0 = member * kChunk; k0 < p.d; k0 += mates * kChunk, ++it) {
       const int s = it % kStages, k = min(kChunk, p.d - k0);
       TokenWords<kW8, kTokensUp> tokens;
       tokens.load(x + k0, k, lane);
@@ -408,7 +410,8 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
       __syncwarp();
       load();
     }
-    if constexpr (kTeam > 1) {   // the second warp's sums go to the first (who writes a buffer again knows that the other came to the unit between)
+    if (mates > 1) {   // the second warp's sums go to the first's (who writes a buffer again knows that the other came to the unit
+                       // between)
       const int buf = n_unit & 1;
       if (member) s_acc[buf][team][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
       if (lane == 0) s_ok[buf][team][member] = ok;
@@ -587,11 +590,15 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
     for (int i = tid; i < 16 * p.t; i += kThreads) {
       const int col = i >> 4, row = i & 15;
       if (col % split != rank) continue;
-      float sum = 0.f;
-      if (split == 1)
-        sum = sums[i];
-      else
-        for (int r = 0; r < split; ++r) sum += ld_rank(sums + i, r);
+      float sum = sums[i];
+      if (split > 1) {   // all on their way at once
+        float v[kMostSplit];
+#pragma unroll
+        for (int r = 0; r < kMostSplit; ++r) v[r] = r < split ? ld_rank(sums + i, r) : 0.f;
+        sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMostSplit; ++r) sum += v[r];
+      }
       const long long to = col * p.ldy + d0 + row;
       if (p.out_f32)
         static_cast<float*>(p.y)[to] = sum;
@@ -687,7 +694,7 @@ bool launch_both(const LayerParams& p, int sms, cudaStream_t s) {
   int split = 1;
   // Up to two CTAs an SM (16 experts of f = 2048, 4 tokens: d = 1024 split in 4 31.1 us, in 2 33.8; d = 512 in 4 21.6, in 1 31.8),
   // but of eight only as many as SMs: two an SM do not all start at once (d = 512 in 8 26.3; d = 256 in 8 16.7, in 4 18.3).
-  while (split < 8 && 2 * split * blocks <= (split < 4 ? 2 : 1) * sms && 2 * split * kWarpsDown * kColsDown <= cols) split *= 2;
+  while (split < kMostSplit && 2 * split * blocks <= (split < 4 ? 2 : 1) * sms && 2 * split * kWarpsDown * kColsDown <= cols) split *= 2;
   return launch(k_layer_down<kBf16, kW8>, blocks * split, 32 * kWarpsDown, down, split, s, m_down, p, down, split);
 }
 

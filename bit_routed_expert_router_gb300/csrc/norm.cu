@@ -99,6 +99,8 @@ __device__ __forceinline__ bool common(float top) {
   return __float_as_uint(top) - lo < hi - lo;
 }
 
+constexpr float kLargest = 3.4028234663852886e38f;   // fp32's largest value
+
 // 448 / top: the fast reciprocal after one of Newton's steps.
 __device__ __forceinline__ float inverse_of(float top) {
   float x;
@@ -202,20 +204,25 @@ __global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(
         if (p.weight)
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], f(k));
-        float top = 0.f;   // of the 16 lanes that hold a group; words past the row are 0
+        // the largest magnitude of the 16 lanes that hold a group; words past the row are 0
+        const auto largest = [&](uint32_t lanes) {
+          float top = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = max_abs(max_abs(top, v[q][j].lo(k)), v[q][j].hi(k));
+          for (int k = 0; k < 4; ++k) top = max_abs(max_abs(top, v[q][j].lo(k)), v[q][j].hi(k));
 #pragma unroll
-        for (int d = 8; d; d >>= 1) top = max_abs(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          for (int d = 8; d; d >>= 1) top = max_abs(top, __shfl_xor_sync(lanes, top, d));
+          return top;
+        };
+        const float top = largest(0xFFFFFFFFu);
         Scale8 s;
         const float least = max_abs(kTiny, top * rstd);
-        if (common(top) && least > kTiny) {
+        if (common(top) && least > kTiny && least <= kLargest) {
           s.scale = least * (1.f / kMaxE4m3);
           s.inverse = inverse_of(top);
-        } else {   // the least scale, or values that are not finite
-          s = scale8(least);
+        } else {   // the least scale, or values that are not finite: of r or w, or only once rstd (infinite with eps = 0) is in them
 #pragma unroll
           for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], both(rstd));
+          s = scale8(largest(0xFFFFu << (lane & 16)));
         }
         if (in) {
           Eight a;

@@ -296,3 +296,20 @@ def test_quotients_are_rounded_to_the_nearest(dtype):
     got = y8.double()
     nearest = q.float().to(E4M3).double()
     assert torch.all((got - q).abs() <= (nearest - q).abs() + 3 * 2.0 ** -24 * 2 * q.abs())
+
+
+@pytest.mark.parametrize("m", [5, 2500])   # one row a thread, and two
+def test_rows_that_are_infinite_in_eight_bits(m):
+    """Squares below fp32's range and eps = 0: r times an infinite quotient.  A block with a zero in it has a NaN, one
+    without has infinities only, and the outputs agree."""
+    h = torch.full((m, 2816), 1e-23, dtype=BF16, device="cuda")
+    h[:, 200:210] = 0                  # block 1: infinities and NaN; block 2 none but NaN
+    h[:, 256:384] = 0
+    h[1] = 3.0                         # a row as others are
+    _, y, y8, s = call(h, None, None, "both", eps=0.0)
+    v = h.float() / h.float().square().mean(1, keepdim=True).sqrt()
+    assert torch.equal(torch.isnan(y), torch.isnan(v)) and torch.equal(torch.isinf(y), torch.isinf(v))
+    rest = [i for i in range(m) if i != 1]
+    assert torch.all(torch.isnan(s[rest, 1:3])) and torch.all(torch.isinf(s[rest, :1])) and torch.all(torch.isinf(s[rest, 3:]))
+    assert torch.all(torch.isnan(y8[rest].float()))
+    near8(y8[1:2], s[1:2], normed(h[1:2], None))

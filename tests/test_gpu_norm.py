@@ -313,3 +313,16 @@ def test_rows_that_are_infinite_in_eight_bits(m):
     assert torch.all(torch.isnan(s[rest, 1:3])) and torch.all(torch.isinf(s[rest, :1])) and torch.all(torch.isinf(s[rest, 3:]))
     assert torch.all(torch.isnan(y8[rest].float()))
     near8(y8[1:2], s[1:2], normed(h[1:2], None))
+
+
+@pytest.mark.parametrize("m", [6, 2500])
+@pytest.mark.parametrize("size,weight,eps", [(1e17, 1e25, 1e-6), (1e17, 1e25, 0.0), (5e17, 2e21, 1e-6), (1e-20, 1e-24, 1e-30)])
+def test_products_of_row_and_weight_past_fp32(m, size, weight, eps):
+    """r w is above or below fp32's range, the normed value times the weight is not."""
+    g = gen(71)
+    h = (torch.randn(m, 400, generator=g, device="cuda").clamp(-3, 3) * size).to(BF16)
+    w = (1 + 0.2 * torch.randn(400, generator=g, device="cuda")).mul(weight).to(BF16)
+    _, y, y8, s = call(h, None, w, "both", eps=eps)
+    want = normed(h, w, eps)
+    near16(y, want, BF16)
+    near8(y8, s, want)

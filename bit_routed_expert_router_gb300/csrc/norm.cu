@@ -402,8 +402,10 @@ bool launch_norm_of(const NormParams& p, int sms, cudaStream_t s) {
   const int nt = (words + 31) / 32 * 32, rows = std::max(1, 256 / nt);
   // Two rows a thread where that leaves every SM two CTAs of long rows (2816 values: 600 rows 3.1 us either way, 2400 10.0 against
   // 10.7, 300 2.4 against 2.3) or eight of short ones (264 values: 20,000 rows 10.8 us against 11.5, 9000 5.5 against 5.4, 4000
-  // 4.3 against 3.4), and the threads have the registers.
-  if (nt <= 512 && p.m >= (rows == 1 ? 4 : 16) * rows * sms) return launch_rows<kBf16, kDelta, 1, 2>(p, nt, rows, s);
+  // 4.3 against 3.4).  Not with fp32 delta, whose words take twice the registers (4096 rows of 2816, 16-bit out, 20.9 us, with two
+  // rows that spill 26.1, with two rows and two CTAs an SM 24.4; 20,000 of 264 13.9, 17.0 and 14.9).
+  if constexpr (kDelta != kDelta32)
+    if (nt <= 512 && p.m >= (rows == 1 ? 4 : 16) * rows * sms) return launch_rows<kBf16, kDelta, 1, 2>(p, nt, rows, s);
   return launch_rows<kBf16, kDelta, 1, 1>(p, nt, rows, s);
 }
 

@@ -56,6 +56,14 @@ struct WaitLimits {
   int cycles1024, loads;
 };
 WaitLimits wait_limits();
+// CTAs in which a wait of an operator ran out on a device, and the number of the last one's grid (plus one; the replays of a
+// graph's node share theirs).  The count is never taken back: each stream that asks compares it with what it was told before.
+struct GaveUp {
+  unsigned long long grid;
+  uint32_t count;
+};
+// The current device's, in its memory; null: a CUDA call failed.
+GaveUp* gave_up_here();
 // Synchronises the stream; news: a wait ran out on the current device since the
 // last call with this stream.
 bool grouped_gave_up(cudaStream_t s, bool* news);

@@ -36,7 +36,6 @@
 #include "gelu16.cuh"
 #include "allow_smem.h"
 #include "grouped.h"
-#include "ops8.h"
 #include "tc16.cuh"
 #include "tensor_map.h"
 #include "tile_regs.cuh"
@@ -47,6 +46,8 @@ namespace moe {
 namespace {
 
 using namespace tc16;
+
+__device__ GaveUp g_gave_up;
 
 constexpr int kMaxE = 1024;
 constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
@@ -436,8 +437,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
       }
     // a pair that gave up leaves its launch's other tiles to clusters that start after it: those do nothing, or each would
     // wait as long
-    S.waits.abort = kTake && *static_cast<volatile unsigned long long*>(&g_gave_up_grid) == this_grid() ? 2 : 0;
-    if (S.waits.abort) atomicAdd(&g_gave_up, 1u);
+    S.waits.abort = kTake && *static_cast<volatile unsigned long long*>(&g_gave_up.grid) == this_grid() ? 2 : 0;
+    if (S.waits.abort) atomicAdd(&g_gave_up.count, 1u);
     S.waits.limit = p.limit;
     fence_mbar_init();
   }
@@ -940,7 +941,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(BigCfg<kMode, kEpi>:
   }
   fence_before();
   __syncthreads();
-  if (S.waits.abort == 1) report_and_settle();
+  if (S.waits.abort == 1) report_and_settle(&g_gave_up);
   cluster_sync();   // no CTA leaves while the other may still arrive on its barriers or read its stages
   fence_after();
   if (warp == 1) tmem_free<true>(tmem, 2 * kAccCols);
@@ -1212,7 +1213,7 @@ __global__ void __launch_bounds__(192)
         finish(c, kEpi == GM_ADAPT ? adapter_values(p, row0 + c, f) : make_float4(0.f, 0.f, 0.f, 0.f));
     }
   }
-  if (s_waits.abort) report_and_settle();
+  if (s_waits.abort) report_and_settle(&g_gave_up);
   if (split > 1)
     cluster_sync();   // the others may still read this CTA's part
   else
@@ -1381,7 +1382,7 @@ __global__ void __launch_bounds__(192)
     cluster_sync();             // the others may still read this CTA's part
   }
   __syncthreads();
-  if (s_waits.abort) report_and_settle();
+  if (s_waits.abort) report_and_settle(&g_gave_up);
   if (warp == 1) tmem_free<false>(tmem, 2 * kDownCols);
 }
 
@@ -1580,16 +1581,29 @@ bool launch_grouped(int mode, int epi, const GmOperands& o, const GmParams& para
                      : launch_big<GM_FWD, GM_PLAIN>(maps, p, d.sms, s);
 }
 
+GaveUp* gave_up_here() {
+  static std::atomic<GaveUp*> known[64];   // by device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  GaveUp* at = dev < 64 ? known[dev].load(std::memory_order_acquire) : nullptr;
+  if (at) return at;
+  void* found = nullptr;
+  if (cudaGetSymbolAddress(&found, g_gave_up) != cudaSuccess) return nullptr;
+  at = static_cast<GaveUp*>(found);
+  if (dev < 64) known[dev].store(at, std::memory_order_release);
+  return at;
+}
+
 bool grouped_gave_up(cudaStream_t s, bool* news) try {
   static std::mutex lock;
   static std::map<std::pair<int, cudaStream_t>, uint32_t> told;   // counts by device and stream
   int dev = 0;
-  uint32_t own = 0, layer = 0, mm8 = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaMemcpyFromSymbolAsync(&own, g_gave_up, sizeof(own), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      !layer_gave_up(s, &layer) || !mm8_gave_up(s, &mm8) || cudaStreamSynchronize(s) != cudaSuccess)
+  uint32_t count = 0;
+  GaveUp* const here = gave_up_here();
+  if (!here || cudaGetDevice(&dev) != cudaSuccess ||
+      cudaMemcpyAsync(&count, &here->count, sizeof(count), cudaMemcpyDeviceToHost, s) != cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
     return false;
-  const uint32_t count = own + layer + mm8;
   {
     const std::lock_guard<std::mutex> hold(lock);
     const auto known = told.find({dev, s});
@@ -1598,9 +1612,7 @@ bool grouped_gave_up(cudaStream_t s, bool* news) try {
   }
   if (!*news) return true;
   // the next replay of a graph that gave up does all of its work
-  void* grid = nullptr;
-  return cudaGetSymbolAddress(&grid, g_gave_up_grid) == cudaSuccess &&
-         cudaMemsetAsync(grid, 0, sizeof(g_gave_up_grid), s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  return cudaMemsetAsync(&here->grid, 0, sizeof(here->grid), s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
 } catch (...) {   // no memory for another stream's count
   return false;
 }

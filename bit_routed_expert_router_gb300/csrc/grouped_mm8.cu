@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_grouped8(const __grid_constant_
   }
   fence_before();
   __syncthreads();
-  if (S.waits.abort == 1) report_and_settle();
+  if (S.waits.abort == 1) report_and_settle(p.gave_up);
   fence_after();
   if (warp == 1) tmem_free<false>(tmem, 2 * kWeightRows);
 }
@@ -578,6 +578,7 @@ bool launch_grouped8(bool gated, const Mm8Params& params, cudaStream_t s) {
   Mm8Params p = params;
   const WaitLimits l = wait_limits();
   p.limit = l.cycles1024, p.stall = l.loads;
+  if (!(p.gave_up = gave_up_here())) return false;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return false;
@@ -591,10 +592,6 @@ bool launch_grouped8(bool gated, const Mm8Params& params, cudaStream_t s) {
   // of 4 rows, 2816 to 1408: 13.0 -> 10.0); where they do not, they cost (8 rows of as many experts, 704 to 2816: 8.3 -> 9.3).
   if (!gated) return most_tiles(p, 128) <= sms ? launch<-1, 128>(maps, p, sms, s) : launch<-1, 256>(maps, p, sms, s);
   return p.gelu == MOE_GELU_TANH ? launch<MOE_GELU_TANH, 256>(maps, p, sms, s) : launch<MOE_GELU_ERF, 256>(maps, p, sms, s);
-}
-
-bool mm8_gave_up(cudaStream_t s, uint32_t* count) {
-  return cudaMemcpyFromSymbolAsync(count, g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, s) == cudaSuccess;
 }
 
 }  // namespace moe

@@ -6,6 +6,8 @@
 #include <cstdint>
 #include <cuda_runtime.h>
 
+#include "grouped.h"
+
 namespace moe {
 
 constexpr int kNormMaxD = 16384;
@@ -57,12 +59,11 @@ struct Mm8Params {
   float* sa = nullptr;                // gated: [m][ceil(n / 2 / 128)]
   int gelu = 0;
   int limit = 0, stall = 0;           // set by the launches: bounded waits, in 1024 cycles; loads after which they stop
+  GaveUp* gave_up = nullptr;          // the same
 };
 
 // false: a CUDA call failed.
 bool launch_grouped8(bool gated, const Mm8Params& p, cudaStream_t s);
-// Enqueues a copy of the count of its CTAs in which a wait ran out.
-bool mm8_gave_up(cudaStream_t s, uint32_t* count);
 
 constexpr int kLayerTokens = 32, kLayerTopK = 32;
 
@@ -87,11 +88,10 @@ struct LayerParams {
   long long ldy = 0;
   int bf16 = 0, out_f32 = 0, gelu = 0;
   int limit = 0, stall = 0;         // set by the launches: bounded waits, in 1024 cycles; loads after which they stop
+  GaveUp* gave_up = nullptr;        // the same
 };
 
 // false: a CUDA call failed.
 bool launch_layer(bool weights8, const LayerParams& p, cudaStream_t s);
-// Enqueues a copy of the count of its CTAs in which a wait ran out.
-bool layer_gave_up(cudaStream_t s, uint32_t* count);
 
 }  // namespace moe

@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
     }
   }
   __syncthreads();
-  if (S.waits.abort) report_and_settle();
+  if (S.waits.abort) report_and_settle(p.gave_up);
 }
 
 // ------------------------------------------------------------------ down
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
     }
   if (split > 1) cluster_sync();   // the others may still read this CTA's sums
   __syncthreads();
-  if (S.waits.abort) report_and_settle();
+  if (S.waits.abort) report_and_settle(p.gave_up);
 }
 
 // ------------------------------------------------------------------ launches
@@ -704,15 +704,12 @@ bool launch_layer(bool weights8, const LayerParams& params, cudaStream_t s) {
   LayerParams p = params;
   const WaitLimits l = wait_limits();
   p.limit = l.cycles1024, p.stall = l.loads;
+  if (!(p.gave_up = gave_up_here())) return false;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return false;
   if (weights8) return p.bf16 ? launch_both<true, true>(p, sms, s) : launch_both<false, true>(p, sms, s);
   return p.bf16 ? launch_both<true, false>(p, sms, s) : launch_both<false, false>(p, sms, s);
-}
-
-bool layer_gave_up(cudaStream_t s, uint32_t* count) {
-  return cudaMemcpyFromSymbolAsync(count, g_gave_up, sizeof(*count), 0, cudaMemcpyDeviceToHost, s) == cudaSuccess;
 }
 
 }  // namespace moe

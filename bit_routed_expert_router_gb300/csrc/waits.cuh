@@ -1,17 +1,10 @@
-// Bounded waits on barriers, and what a CTA does in which one ran out.  Each
-// translation unit that includes this has counts of its own, which
-// moe_grouped_sync adds up.
+// Bounded waits on barriers, and what a CTA does in which one ran out.
 #pragma once
 
 #include "common.cuh"
+#include "grouped.h"
 
 namespace moe {
-
-// CTAs that gave up on this device, and the number of the last one's grid (plus
-// one; the replays of a graph's node share theirs).  The count is never taken
-// back: each stream that asks compares it with what it was told before.
-static __device__ uint32_t g_gave_up;
-static __device__ unsigned long long g_gave_up_grid;
 
 // A CTA's bounded waits.
 struct Waits {
@@ -51,10 +44,10 @@ __device__ __forceinline__ bool wait_bar_warp(uint64_t* bar, uint32_t parity, Wa
 // CTA count on the even one's barriers, of which the phases that miss a share
 // stay open.  All of them take microseconds; the CTA keeps its memories for
 // another 10 ms.
-__device__ __forceinline__ void report_and_settle() {
+__device__ __forceinline__ void report_and_settle(GaveUp* gave_up) {
   if (threadIdx.x == 0) {
-    *static_cast<volatile unsigned long long*>(&g_gave_up_grid) = this_grid();
-    atomicAdd(&g_gave_up, 1u);
+    *static_cast<volatile unsigned long long*>(&gave_up->grid) = this_grid();
+    atomicAdd(&gave_up->count, 1u);
   }
   const long long t0 = clock64();
   while (clock64() - t0 < kSettleCycles) __nanosleep(1000);

@@ -1,6 +1,8 @@
 """Waits of the 8-bit products and of the layer for a few tokens that run out: as for the 16-bit operators, the kernels
 return, nothing outside the outputs is touched, the host reads MOE_ETIMEOUT, and the next calls are right."""
 
+import time
+
 import pytest
 import torch
 
@@ -86,3 +88,20 @@ def test_one_operators_timeout_is_told_once():
         moe.check(moe.moe_token_layer(*largs[:4], ly, ws))
     assert moe.moe_grouped_sync() == moe.MOE_ETIMEOUT
     assert moe.moe_grouped_sync() == moe.MOE_OK
+
+
+def test_asking_is_one_copy():
+    """Whatever kinds of kernels report: about as long as one blocking copy of four bytes, not as several."""
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+
+    def shortest(f):
+        best = 1.0
+        for _ in range(20):
+            start = time.perf_counter()
+            for _ in range(50):
+                f()
+            best = min(best, (time.perf_counter() - start) / 50)
+        return best
+
+    shortest(moe.moe_grouped_sync)
+    assert shortest(moe.moe_grouped_sync) <= 1.8 * shortest(one.cpu)

@@ -476,6 +476,11 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
   constexpr int kSize = kW8 ? 1 : 2;
   constexpr int kStageBytes = kColsDown * kColBytes, kColValues = kCol / kSize;
   prepare(p, maps, P, smem, S);
+  // CTAs that start after their launch gave up do nothing, or each wave of them would wait as long
+  if (tid == 64 && *static_cast<volatile unsigned long long*>(&p.gave_up->grid) == this_grid()) {
+    S.waits.abort = 2;
+    atomicAdd(&p.gave_up->count, 1u);
+  }
   // ids and weights are older than the first kernel, which let this one start after its own wait
   list_slots(p, P, smem, S);
   const Slot* slots = reinterpret_cast<const Slot*>(smem + P.at_slots);
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
                 d0, max(slots[at.slot].expert, 0), &full[s], policy);
   };
   Place at;
-  at.left = end - first;
+  at.left = S.waits.abort == 2 ? 0 : end - first;
   {
     const bool shared = first >= n_routed * per;
     const int i = shared ? first - n_routed * per : first, n = max(shared ? per_shared : per, 1), s = i / n;
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
     }
   if (split > 1) cluster_sync();   // the others may still read this CTA's sums
   __syncthreads();
-  if (S.waits.abort) report_and_settle(p.gave_up);
+  if (S.waits.abort == 1) report_and_settle(p.gave_up);
 }
 
 // ------------------------------------------------------------------ launches

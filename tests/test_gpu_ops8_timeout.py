@@ -105,3 +105,43 @@ def test_asking_is_one_copy():
 
     shortest(moe.moe_grouped_sync)
     assert shortest(moe.moe_grouped_sync) <= 1.8 * shortest(one.cpu)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_launch_gives_up_once(captured):
+    """The second kernel's 4,096 CTAs start in more than ten waves, of which the first gives up; each wave that did so by
+    itself would hold its memories for 10 ms."""
+    t, k, E, d, f = 32, 8, 64, 65536, 16
+    x, ids, gates, routed, _ = layer_case(t, k, E, d, f, 0)
+    whole_w, ws = guarded(torch.uint8, 2 * t * k * f)
+    whole_y, y = guarded(BF16, t, d)
+
+    def call():
+        moe.check(moe.moe_token_layer(x, ids, gates, routed, y, ws))
+
+    call()
+    torch.cuda.synchronize()
+    want = y.clone()
+    moe.moe_grouped_sync()
+    graph = torch.cuda.CUDAGraph()
+    with Stalled():
+        if captured:
+            with torch.cuda.graph(graph):
+                call()
+        for _ in range(2):   # the replays of a graph's node are one launch to the kernels: the second does nothing
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            graph.replay() if captured else call()
+            end.record()
+            torch.cuda.synchronize()
+            assert start.elapsed_time(end) < 60
+            if not captured:
+                assert moe.moe_grouped_sync() == moe.MOE_ETIMEOUT
+    if captured:
+        assert moe.moe_grouped_sync() == moe.MOE_ETIMEOUT
+    assert moe.moe_grouped_sync() == moe.MOE_OK
+    for whole in (whole_w, whole_y):
+        assert torch.all(whole[:GUARD] == 0x35) and torch.all(whole[-GUARD:] == 0x35)
+    call()
+    moe.check(moe.moe_grouped_sync())
+    assert torch.equal(y, want)

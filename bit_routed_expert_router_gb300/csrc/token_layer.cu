@@ -3,9 +3,11 @@
 //   up     a[i] = gate GELU(g) u,  [g, u] = Wgu[e] x[t]     for the tokens of each picked expert, rounded to the call's type
 //   down   y[t] = sum_e Wd[e] a[e, t]                       over the experts that t names, and the shared one
 //
-// a is rounded because it is an operand of 16-bit products: with its remainder as a
-// second operand the output's error would fall from 1.4 roundings of its type to
-// one, for twice the second kernel's products and workspace.
+// a is rounded because it is an operand of 16-bit products and two bytes of the
+// workspace: the output's error is 1.4 roundings of its type instead of one.  (As two
+// digits, a high and a low operand with an exponent for each eight values in the same
+// two bytes, which is 2^-13: one token 27.4 -> 30.4 us, in 8 bits 21.6 -> 27.8.)  What
+// leaves fp16's range takes another form in the same place, see Packed.
 //
 // The weights of the picked experts are read once and nothing else is of any
 // size, so both kernels stream them.  A warp works by itself: one of its lanes
@@ -41,6 +43,7 @@
 // memory set as such the second starts early, but takes HBM from the first: 28.5 us
 // at 27.9), 1.5 us of tails; in 8 bits the widening.
 #include <algorithm>
+#include <type_traits>
 
 #include "allow_smem.h"
 #include "gelu16.cuh"
@@ -145,13 +148,109 @@ struct TokenWords {
           v[i][h][j] = kWhole || at < k ? __ldcg(reinterpret_cast<const uint4*>(row + at)) : make_uint4(0, 0, 0, 0);
         }
   }
+  // what the sums of this lane's column `column` are to be multiplied by
+  __device__ __forceinline__ float unit(int) const { return 1.f; }
+};
+
+// ------------------------------------------------------------------ a in fp16
+//
+// Eight features of a token (a unit's, 16 bytes) are fp16 values if the largest is 0 or from 2^-13 on in fp16's range: none is
+// off by more than half a step or 2^-12 of the largest.  Others are packed, which the last value's exponent tells (infinity's,
+// which no value has): under it, in its fraction, lies e = k + 127 > 0, with 2^k <= |v| < 2^(k+1) for the largest once rounded; the
+// others' words hold integers v 2^(12-k), 14 bits, and above each of them two bits of the last one's.  To a product that takes
+// it for a value the last one's word is NaN, and so is the product.  (All of one token's packed: 28 -> 44 us, of seven tokens' 85
+// -> 143.)
+struct Packed {
+  static constexpr uint32_t kMark = 0x7C00;
+  static constexpr uint32_t kSmall = 0x39000000u, kLarge = 0x477FF000u;   // 2^-13; 65520, which would round to infinity
+  static constexpr int kLeast = 27, kMost = 254;   // of e; below 2^-100 values lose bits, then become 0
+  static constexpr uint32_t kNotFinite = 255;      // e: the integers 1, -1, 2 are infinity, -infinity, NaN, and 0 what is finite
+                                                   // (no sum that it goes into is)
+  static __device__ __forceinline__ bool needed(uint32_t top) { return top && top - kSmall >= kLarge - kSmall; }
+  // e from the largest magnitude's bits
+  static __device__ __forceinline__ uint32_t exponent(uint32_t top) {
+    if (top >= 0x7F800000u) return kNotFinite;
+    return min(max((top + (1u << 10)) >> 23, static_cast<uint32_t>(kLeast)), static_cast<uint32_t>(kMost));
+  }
+  static __device__ __forceinline__ int integer(float v, uint32_t e) {
+    if (e == kNotFinite) return isnan(v) ? 2 : !isinf(v) ? 0 : v > 0.f ? 1 : -1;
+    return min(__float2int_rn(v * __uint_as_float((kMost + 12 - e) << 23)), 8191);
+  }
+  // the word of feature i from its integer and the last feature's
+  static __device__ __forceinline__ uint16_t word(int i, int own, int last, uint32_t e) {
+    return static_cast<uint16_t>(i == 7 ? kMark | e : (own & 0x3FFF) | (last >> 2 * i & 3) << 14);
+  }
+  static __device__ __forceinline__ bool is(const uint4& v) { return (v.w >> 16 & kMark) == kMark; }
+  // e of eight words, packed or not (of fp16's smallest values that of 2^-15); 0: zeros, or not finite
+  static __device__ __forceinline__ int exponent(const uint4& v) {
+    if (is(v)) return (v.w >> 16 & 0x3FF) == kNotFinite ? 0 : v.w >> 16 & 0x3FF;
+    const uint32_t m = 0x7FFF7FFF, top = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    return top ? 112 + (max(top >> 16, top & 0xFFFF) >> 10) : 0;
+  }
+  // two of their values each, times a power of two, as fp16
+  static __device__ __forceinline__ uint4 scaled(const uint4& v, float by) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t out[4];
+    const auto pair = [&](int i, float lo, float hi) {
+      const __half2 two = __floats2half2_rn(lo, hi);
+      out[i] = *reinterpret_cast<const uint32_t*>(&two);
+    };
+    if (!is(v)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pair(i, half_lo(w[i]) * by, half_hi(w[i]) * by);
+    } else {
+      const uint32_t e = v.w >> 16 & 0x3FF;
+      int m[8];
+      uint32_t last = 0;
+#pragma unroll
+      for (int i = 0; i < 7; ++i) {
+        const uint32_t bits = i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFF;
+        last |= bits >> 14 << 2 * i;
+        m[i] = static_cast<int>(bits << 18) >> 18;
+      }
+      m[7] = static_cast<int>(last << 18) >> 18;
+      if (e != kNotFinite) {
+        const float step = __uint_as_float((e - 12) << 23) * by;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pair(i, static_cast<float>(m[2 * i]) * step, static_cast<float>(m[2 * i + 1]) * step);
+      } else {
+        const auto value = [](int m) { return m == 0 ? 0.f : __int_as_float(m == 2 ? 0x7FC00000 : m > 0 ? 0x7F800000 : 0xFF800000); };
+#pragma unroll
+        for (int i = 0; i < 4; ++i) pair(i, value(m[2 * i]), value(m[2 * i + 1]));
+      }
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+  }
+};
+
+// TokenWords of a of which some may be packed: `scale` makes them the values by the power of two that brings the largest of this
+// lane's token under 2^15; `units` takes it out of the sums again.  What is 2^-29 of the largest loses bits.
+template <bool kW8, int kCols>
+struct ScaledWords : TokenWords<kW8, kCols> {
+  using Words = TokenWords<kW8, kCols>;
+  float units[2];
+
+  __device__ __forceinline__ uint4& word(int i) { return this->v[i / (2 * Words::kWords)][i / Words::kWords % 2][i % Words::kWords]; }
+  __device__ __forceinline__ void scale(int lane) {
+    int e = Packed::kLeast;
+#pragma unroll
+    for (int i = 0; i < kCols * 2 * Words::kWords; ++i) e = max(e, Packed::exponent(word(i)));
+    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
+    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2));
+    const float by = __int_as_float((268 - e) << 23);   // 2^(14 - k)
+#pragma unroll
+    for (int i = 0; i < kCols * 2 * Words::kWords; ++i) word(i) = Packed::scaled(word(i), by);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) units[i] = __int_as_float((__shfl_sync(0xFFFFFFFFu, e, 8 * (lane & 3) + 4 * i) - 14) << 23);
+  }
+  __device__ __forceinline__ float unit(int column) const { return units[column]; }
 };
 
 // acc += 16 weight rows of staged loads of k values times the token rows.  With e4m3 weights `scale` holds the scales of the
 // chunk's blocks of 128 (its loads, these from `block` on): lane i that of rows 0 .. 7, lane 16 + i of rows 8 .. 15.
-template <bool kBf16, bool kW8, int kCols>
-__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const TokenWords<kW8, kCols>& x, int k, float scale,
-                                               int block, int lane) {
+template <bool kBf16, bool kW8, int kCols, typename Words>
+__device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* stage, const Words& x, int k, float scale, int block,
+                                               int lane) {
   const int r = row_of(lane >> 2), t = lane & 3;
   const uint8_t* row = stage + r * kCol;
   float part[2][4] = {};
@@ -164,7 +263,7 @@ __device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* s
       const uint4 w0 = *reinterpret_cast<const uint4*>(from), w1 = *reinterpret_cast<const uint4*>(from + 8 * kCol);
       const uint4 b0 = x.v[i][h][0];
       if (kW8) {
-        const uint4 b1 = x.v[i][h][TokenWords<kW8, kCols>::kWords - 1];
+        const uint4 b1 = x.v[i][h][Words::kWords - 1];
         const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
         const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -180,14 +279,14 @@ __device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* s
       const float lo = __shfl_sync(0xFFFFFFFFu, scale, block + i), hi = __shfl_sync(0xFFFFFFFFu, scale, 16 + block + i);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        acc[v] = fmaf(part[0][v] + part[1][v], v < 2 ? lo : hi, acc[v]);
+        acc[v] = fmaf((part[0][v] + part[1][v]) * x.unit(v & 1), v < 2 ? lo : hi, acc[v]);
         part[0][v] = part[1][v] = 0.f;
       }
     }
   }
   if (!kW8)   // tensor cores truncate: their sums go on for a chunk only
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] += part[0][v] + part[1][v];
+    for (int v = 0; v < 4; ++v) acc[v] = fmaf(part[0][v] + part[1][v], x.unit(v & 1), acc[v]);
 }
 
 __device__ __forceinline__ bool elect_one() {
@@ -406,7 +505,7 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
       float sc = 0.f;
       if (kW8 && kCol * (lane & 15) < k) sc = __ldg(scale + k0 / 128 + (lane & 15));
       if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
-      chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes, tokens, k, sc, 0, lane);
+      chunk_products<kBf16, kW8, kTokensUp>(acc, stages + s * kStageBytes, tokens, k, sc, 0, lane);
       __syncwarp();
       load();
     }
@@ -421,23 +520,43 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
       const float4 v = s_acc[buf][team][lane];
       acc[0] += v.x, acc[1] += v.y, acc[2] += v.z, acc[3] += v.w;
     }
-    // this lane: gate and up of one feature, columns 2 (lane % 4) and the next
+    // this lane: gate and up of one feature, columns 2 (lane % 4) and the next; the eight features of a column are the lanes that
+    // differ in lane / 4
     uint16_t* a = p.a + (at.slot.expert < 0 ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
                   static_cast<long long>(at.slot.base) * f + f0 + row_of(g);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int col = 2 * (lane & 3) + i;
-      if (!ok || col >= rows) continue;
-      float gate = 1.f;
-      if (at.slot.expert >= 0) {
-        const int* ids = reinterpret_cast<const int*>(smem + P.at_ids);
-        const float* gates = reinterpret_cast<const float*>(smem + P.at_gates);
-        const int t = nth_bit(at.slot.mask, col);
-        gate = 0.f;
-        for (int j = 0; j < p.k; ++j) gate += ids[t * p.k + j] == at.slot.expert ? gates[t * p.k + j] : 0.f;
+      const bool there = ok && col < rows;
+      if (kBf16 && !there) continue;
+      float v = 0.f;
+      if (there) {
+        float gate = 1.f;
+        if (at.slot.expert >= 0) {
+          const int* ids = reinterpret_cast<const int*>(smem + P.at_ids);
+          const float* gates = reinterpret_cast<const float*>(smem + P.at_gates);
+          const int t = nth_bit(at.slot.mask, col);
+          gate = 0.f;
+          for (int j = 0; j < p.k; ++j) gate += ids[t * p.k + j] == at.slot.expert ? gates[t * p.k + j] : 0.f;
+        }
+        v = gate * (gelu16(acc[i], p.gelu) * acc[2 + i]);
       }
-      const float v = gate * (gelu16(acc[i], p.gelu) * acc[2 + i]);
-      a[static_cast<long long>(col) * f] = kBf16 ? float_to_bf16_bits(v) : __half_as_ushort(__float2half_rn(v));
+      uint16_t word = kBf16 ? float_to_bf16_bits(v) : __half_as_ushort(__float2half_rn(v));
+      if (!kBf16) {
+        uint32_t top = __float_as_uint(v) & 0x7FFFFFFFu;
+        uint32_t enough = __ballot_sync(0xFFFFFFFFu, top >= Packed::kSmall || !there);   // of a column: one is enough
+        enough |= enough >> 16;
+        enough |= enough >> 8;
+        enough |= enough >> 4;
+        if (__any_sync(0xFFFFFFFFu, top >= Packed::kLarge) || (enough & 15) != 15) {
+#pragma unroll
+          for (int d = 4; d < 32; d *= 2) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+          const uint32_t e = Packed::exponent(top);
+          const int own = Packed::integer(v, e), last = __shfl_sync(0xFFFFFFFFu, own, 28 + (lane & 3));
+          if (Packed::needed(top)) word = Packed::word(row_of(g), own, last, e);
+        }
+      }
+      if (there) a[static_cast<long long>(col) * f] = word;
     }
   }
   __syncthreads();
@@ -476,8 +595,9 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
   constexpr int kSize = kW8 ? 1 : 2;
   constexpr int kStageBytes = kColsDown * kColBytes, kColValues = kCol / kSize;
   prepare(p, maps, P, smem, S);
-  // CTAs that start after their launch gave up do nothing, or each wave of them would wait as long
-  if (tid == 64 && *static_cast<volatile unsigned long long*>(&p.gave_up->grid) == this_grid()) {
+  // CTAs that start after their launch gave up do nothing, or each wave of them would wait as long (asked by the warp that is the
+  // last to have pairs to list: by the third one 19 tokens took 0.3 us more)
+  if (tid == kThreads - 32 && *static_cast<volatile unsigned long long*>(&p.gave_up->grid) == this_grid()) {
     S.waits.abort = 2;
     atomicAdd(&p.gave_up->count, 1u);
   }
@@ -524,6 +644,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
     at.slot = shared ? n_routed + s : s;
     at.col = i - s * n;
   }
+  const Place start = at;
   Place next = at;
   int loads = 0;
   const auto load_next = [&] {
@@ -537,46 +658,63 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
   pdl_wait();      // a; and y may be in use until here
   pdl_trigger();
 
-  bool ok = true;
-  float acc[4] = {};
+  bool ok = true, odd = false;
+  int it = 0;
   const int db = divide_up(p.d, 128);
-  for (int it = 0; at.left > 0; ++it) {
-    const int s = it % kStages, k0 = at.col * kColValues;
-    const bool shared = at.slot >= n_routed;
-    const Slot slot = slots[at.slot];
-    const int f = shared ? p.fs : p.f, k = min(at.cols(of_slot(at)) * kColValues, f - k0);
-    const uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
-                        static_cast<long long>(slot.base + min(g, __popc(slot.mask) - 1)) * f + k0;
+  const auto add = [&](auto careful) {
+    constexpr bool kCareful = decltype(careful)::value;
     constexpr int kTokenCols = tokens_down(kW8);
-    TokenWords<kW8, kTokenCols> tokens;
-    tokens.load(a, k, lane);
-    float sc = 0.f;
-    if (kW8 && kCol * (lane & 15) < k) {
-      const long long block = (shared ? 0LL : static_cast<long long>(slot.expert) * db) + d0 / 128;
-      sc = __ldg((shared ? p.shared.down_scale : p.routed.down_scale) + block * divide_up(f, 128) + k0 / 128 + (lane & 15));
-    }
-    if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
-#pragma unroll
-    for (int c = 0; c < kColsDown; c += kTokenCols) {
-      const int done = c * kColValues;
-      if (c) {
-        if (done >= k) break;
-        tokens.load(a + done, k - done, lane);
+    float acc[4] = {};
+    for (; at.left > 0; ++it) {
+      const int s = it % kStages, k0 = at.col * kColValues;
+      const bool shared = at.slot >= n_routed;
+      const Slot slot = slots[at.slot];
+      const int f = shared ? p.fs : p.f, k = min(at.cols(of_slot(at)) * kColValues, f - k0);
+      const uint16_t* a = p.a + (shared ? static_cast<long long>(p.t) * p.k * p.f : 0LL) +
+                          static_cast<long long>(slot.base + min(g, __popc(slot.mask) - 1)) * f + k0;
+      std::conditional_t<kCareful, ScaledWords<kW8, kTokenCols>, TokenWords<kW8, kTokenCols>> tokens;
+      tokens.load(a, k, lane);
+      float sc = 0.f;
+      if (kW8 && kCol * (lane & 15) < k) {
+        const long long block = (shared ? 0LL : static_cast<long long>(slot.expert) * db) + d0 / 128;
+        sc = __ldg((shared ? p.shared.down_scale : p.routed.down_scale) + block * divide_up(f, 128) + k0 / 128 + (lane & 15));
       }
-      chunk_products<kBf16, kW8>(acc, stages + s * kStageBytes + c * kColBytes, tokens, k - done, sc, c, lane);
+      if (!(ok = wait_bar_warp(&full[s], (it / kStages) & 1, &S.waits))) break;
+#pragma unroll
+      for (int c = 0; c < kColsDown; c += kTokenCols) {
+        const int done = c * kColValues;
+        if (c) {
+          if (done >= k) break;
+          tokens.load(a + done, k - done, lane);
+        }
+        if constexpr (kCareful) tokens.scale(lane);
+        chunk_products<kBf16, kW8, kTokenCols>(acc, stages + s * kStageBytes + c * kColBytes, tokens, k - done, sc, c, lane);
+      }
+      __syncwarp();
+      load_next();
+      const int was = at.slot;
+      advance(at);
+      if (at.slot != was || at.left <= 0) {   // two rows of columns 2 (lane % 4) and the next
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int col = 2 * (lane & 3) + (v & 1);
+          if (col < __popc(slot.mask)) own[nth_bit(slot.mask, col) * 16 + row_of(g) + 8 * (v >> 1)] += acc[v];
+          odd |= isnan(acc[v]);
+          acc[v] = 0.f;
+        }
+      }
     }
+  };
+  add(std::false_type{});
+  // fp16: sums that are NaN may have met packed values; once more, with care (asked of every chunk's values beforehand, or with the
+  // care in the same loop, that is 3 to 5 % of the layer)
+  if (!kBf16 && ok && __any_sync(0xFFFFFFFFu, odd)) {
+    at = next = start;
     __syncwarp();
-    load_next();
-    const int was = at.slot;
-    advance(at);
-    if (at.slot != was || at.left <= 0) {   // two rows of columns 2 (lane % 4) and the next
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int col = 2 * (lane & 3) + (v & 1);
-        if (col < __popc(slot.mask)) own[nth_bit(slot.mask, col) * 16 + row_of(g) + 8 * (v >> 1)] += acc[v];
-        acc[v] = 0.f;
-      }
-    }
+    for (int i = lane; i < p.t * 16; i += 32) own[i] = 0.f;
+    for (int i = 0; i < kStages; ++i) load_next();
+    __syncwarp();
+    add(std::true_type{});
   }
   __syncthreads();
   // the warps' sums; each CTA's are then in the first warp's place

@@ -207,3 +207,143 @@ def test_the_most_pairs_and_experts():
     """32 tokens that name 32 experts each, of 1024."""
     args = case(32, 32, 1024, 64, 32, 48, F16)
     check(call(*args), *args, moe.MOE_GELU_ERF)
+
+
+def formula(x, ids, gates, routed, shared, variant):
+    rw, sw = wide(routed), wide(shared) if shared else None
+
+    def ffn(xt, gu, down):
+        h = gu @ xt
+        f = down.shape[1]
+        return down @ (gelu(h[:f], variant) * h[f:])
+
+    y = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+    for t in range(x.shape[0]):
+        for j in range(ids.shape[1]):
+            e = int(ids[t, j])
+            if 0 <= e < rw[0].shape[0]:
+                y[t] += gates[t, j].double() * ffn(x[t].double(), rw[0][e], rw[1][e])
+        if shared:
+            y[t] += ffn(x[t].double(), *sw)
+    return y
+
+
+def between(dtype):
+    """What lies between the two products is off by half a step of its type at most (packed fp16: 2^-13 of the largest of its
+    eight features, of sqrt(8) times their root mean square, which is less).  The down product spreads these errors as it
+    spreads the values (Gaussian weights, hundreds of outputs: within a quarter); those of the fp32 sums are a hundredth of
+    them."""
+    assert 2.0 ** -13 * 8 ** 0.5 < torch.finfo(dtype).eps / 2
+    return 1.25 * torch.finfo(dtype).eps / 2
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("size,gate", [(1000.0, 1.0), (1000.0, 1e-4), (1.0, 1e-6), (0.01, 1.0), (1e-4, 1e-3), (30.0, 1e4)])
+def test_values_between_the_products_past_16_bits(size, gate, dtype, eight):
+    """GELU(g) u and its product with the gate from 1e-12 to 1e6."""
+    x, ids, gates, routed, shared = case(5, 3, 6, 272, 304, 272, dtype, eight, seed=81)
+    x, gates = (x.float() * size).to(dtype), gates * gate
+    for sh in (shared, None):
+        want = formula(x, ids, gates, routed, sh, moe.MOE_GELU_ERF)
+        y = call(x, ids, gates, routed, sh, out=F32)
+        err = (y.double() - want).norm(dim=1) / want.norm(dim=1)
+        assert torch.all(err <= between(dtype)), float(err.max())
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_small_features_beside_large_ones(dtype, eight):
+    """Features of very different size, blocks of eight one after the other; outputs that weigh the small ones only."""
+    t, d, f = 4, 256, 432
+    x, ids, gates, routed, _ = case(t, 2, 4, d, f, 0, dtype, False, seed=82)
+    gu, down = routed[0].clone(), routed[1].clone()
+    small = torch.arange(f, device="cuda") // 8 % 2 == 1
+    gu[:, :f][:, small] *= 2.0 ** -6       # g and u: GELU(g) u is about 2^-12 of the others
+    gu[:, f:][:, small] *= 2.0 ** -6
+    down[:, :64, ~small] = 0               # the first outputs see the small features only
+    down[:, 64:128] = 0
+    down[:, 64:128, 8:16] = 1              # the next ones eight of them
+    if eight:
+        one = lambda n, k: torch.ones(4, blocks(n), blocks(k), device="cuda")  # noqa: E731
+        routed = ((gu.float() * 64).to(E4M3), down.to(E4M3), one(2 * f, d) / 64, one(d, f))
+    else:
+        routed = gu, down
+    want = formula(x, ids, gates, routed, None, moe.MOE_GELU_ERF)
+    y = call(x, ids, gates, routed, None, out=F32)
+    for lo, hi in ((0, 64), (64, 65), (128, 256)):
+        err, size = (y.double() - want)[:, lo:hi].norm(dim=1), want[:, lo:hi].norm(dim=1)
+        if lo == 64:   # one sum of eight values, which may cancel: the bound is of their magnitudes
+            size = size.clamp(min=float(want[:, 64].abs().mean()))
+            err = err / 8 ** 0.5
+        assert torch.all(err <= 2 * between(dtype) * size), float((err / size).max())
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_infinities_keep_their_signs(dtype, eight):
+    """An infinite token value, and one that only the product makes infinite: infinities where the formula has them."""
+    x, ids, gates, routed, _ = case(6, 2, 4, 256, 64, 0, dtype, eight, seed=83)
+    x[2, 7] = float("inf")
+    if not eight:
+        routed[0][1, 64 + 9, 5] = float("-inf")
+        routed[1][:, 100, 9] = 0     # no weight there: NaN
+    y = call(x, ids, gates, routed, None, out=F32)
+    want = formula(x, ids, gates, routed, None, moe.MOE_GELU_ERF)
+    assert torch.equal(torch.isfinite(y), torch.isfinite(want))
+    inf = torch.isinf(want)
+    assert torch.equal(torch.isnan(y), torch.isnan(want))
+    assert torch.equal(y[inf], want[inf].float())
+
+
+@pytest.mark.parametrize("t", [2, 8, 9, 32])
+@pytest.mark.parametrize("dtype,eight", [(BF16, False), (F16, False), (BF16, True), (F16, True)])
+def test_full_shape_layers_of_more_tokens(t, dtype, eight):
+    args = case(t, 8, 128, 2816, 704, 2816, dtype, eight, seed=84)
+    want = formula(*args, moe.MOE_GELU_ERF)
+    err = (call(*args, out=F32).double() - want).norm(dim=1) / want.norm(dim=1)
+    assert torch.all(err <= between(dtype)), float(err.max())
+    half = torch.finfo(dtype).eps / 2
+    y = call(*args)
+    assert torch.all((y.double() - want).norm(dim=1) <= (half + between(dtype)) * want.norm(dim=1))
+
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("t", [1, 12])
+def test_rows_of_plain_and_packed_values(t, eight):
+    """fp16: blocks of eight features inside and outside of the type's range side by side, other ones for each token; the rows
+    that need no packing are bit for bit what they are alone."""
+    d, f, fs = 256, 432, 400
+    x, ids, gates, routed, shared = case(t, 2, 4, d, f, fs, F16, eight, seed=85)
+    x[1::3] *= 300.0
+    x[2::3] *= 0.004
+    want = formula(x, ids, gates, routed, shared, moe.MOE_GELU_TANH)
+    y = call(x, ids, gates, routed, shared, out=F32, variant=moe.MOE_GELU_TANH)
+    err = (y.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert torch.all(err <= between(F16)), float(err.max())
+    alone = call(x[::3].contiguous(), ids[::3].contiguous(), gates[::3].contiguous(), routed, shared, out=F32, variant=moe.MOE_GELU_TANH)
+    assert (y[::3] - alone).norm() <= 1e-5 * alone.norm()   # (chunks may end elsewhere)
+
+
+@pytest.mark.parametrize("eight", [False, True])
+def test_the_largest_and_smallest_fp32_values(eight):
+    """GELU(g) u up to 1e33 and down to 1e-25 in one call, by way of the router's tokens and the weights' scales; features that
+    are zero beside them."""
+    d, f = 128, 80
+    x, ids, gates, routed, _ = case(3, 1, 3, d, f, 0, F16, True, seed=86)
+    ids[:, 0] = torch.arange(3)
+    gates[:] = 1
+    gu, down, su, sd = routed
+    gu.view(torch.uint8)[:, 32:48] = 0
+    su[0] *= 1e16
+    su[1] *= 1e-12
+    sd[0] *= 1e-16
+    if not eight:   # fp16 weights hold no such scales: as large as they come
+        wide_gu = wide_weights(gu, su)
+        wide_gu[0] *= 1e4 / wide_gu[0].abs().max()
+        wide_gu[1] *= 1e-4 / wide_gu[1].abs().max()
+        routed = wide_gu.to(F16), wide_weights(down, sd.clamp(min=sd[1:].min())).to(F16)
+    want = formula(x, ids, gates, routed, None, moe.MOE_GELU_ERF)
+    y = call(x, ids, gates, routed, None, out=F32)
+    err = (y.double() - want).norm(dim=1) / want.norm(dim=1)
+    assert torch.all(err <= between(F16)), float(err.max())

@@ -262,3 +262,52 @@ def test_few_and_many_tiles_give_the_same_sums():
     moe.check(moe.moe_grouped_mm8(x, sx, off, w, sw, y))
     moe.check(moe.moe_grouped_mm8(x, sx, off, w.view(torch.uint8)[:, :256].contiguous().view(E4M3), sw[:, :2].contiguous(), few))
     assert torch.equal(few, y[:, :256])
+
+
+@pytest.mark.parametrize("variant", [moe.MOE_GELU_ERF, moe.MOE_GELU_TANH])
+@pytest.mark.parametrize("f", [176, 304, 128])
+@pytest.mark.parametrize("k", [384, 272])
+def test_non_finite_values_stay_in_their_blocks_when_gated(f, k, variant):
+    """A NaN or an infinity in a row, in a gate or up row of an expert, in a scale on either side of where the up rows pass
+    from one block of scales to the next: the blocks that the formula says, everything else bit for bit as without."""
+    counts = [20, 33, 150]
+    x, sx, off, w, sw = case(counts, 2 * f, k, seed=f + k)
+    sx = sx * 2.0 ** -6 * k ** -0.5
+    m, expert = x.shape[0], torch.arange(3, device="cuda").repeat_interleave(torch.tensor(counts, device="cuda"))
+    pad = lambda t: torch.nn.functional.pad(t, (0, -f % 128)).view(m, blocks(f), 128)  # noqa: E731
+
+    def run(x, sx, w, sw):
+        a, sa = torch.zeros(m, f, device="cuda").to(E4M3), torch.zeros(m, blocks(f), device="cuda")
+        moe.check(moe.moe_grouped_geglu8(x, sx, off, w, sw, a, sa, gelu_variant=variant))
+        return a, sa
+
+    def spoil(which, at, value):
+        v = [x.clone(), sx.clone(), w.clone(), sw.clone()]
+        (v[which].view(torch.uint8) if v[which].dtype == E4M3 else v[which])[at] = value
+        return v
+
+    clean_a, clean_s = run(x, sx, w, sw)
+    nan, inf = float("nan"), float("inf")
+    up = blocks(2 * f) - 1
+    cases = [(0, (25, 130), 0x7F), (1, (40, 1), nan), (2, (1, 40, 3), 0xFF), (2, (1, f + 100, 200), 0x7F),
+             (3, (2, f // 128, 1), nan), (3, (2, up, 0), nan), (3, (2, up, 2), inf), (3, (0, up - 1, 1), inf), (1, (60, 2), inf)]
+    for which, at, value in cases:
+        bad = spoil(which, at, value)
+        a, sa = run(*bad)
+        h = torch.zeros(m, 2 * f, dtype=torch.float64, device="cuda")
+        for b in range(blocks(k)):   # the factors of a block's sum, not of its products: infinity times 0 is NaN
+            part = slice(128 * b, min(128 * b + 128, k))
+            sums = torch.einsum("rk,rnk->rn", bad[0][:, part].double(), bad[2].double()[expert][:, :, part])
+            h += bad[1][:, b, None].double() * bad[3].double()[expert][:, :, b].repeat_interleave(128, 1)[:, :2 * f] * sums
+        v = gelu(h[:, :f], variant) * h[:, f:]
+        has_nan, has_inf = pad(torch.isnan(v)).any(-1), pad(torch.isinf(v)).any(-1)
+        assert has_nan.any() or has_inf.any()
+        hit = has_nan | has_inf
+        wide = lambda t: t.repeat_interleave(128, 1)[:, :f]  # noqa: E731
+        assert torch.all(torch.isnan(sa[has_nan])) and torch.all(torch.isnan(a.float()[wide(has_nan)]))
+        only = has_inf & ~has_nan
+        assert torch.all(torch.isinf(sa[only]))
+        spot = wide(only) & torch.isinf(v)
+        assert torch.all(torch.isnan(a.float()[spot])) and torch.all(a.float()[wide(only) & ~spot] == 0)
+        assert torch.equal(sa[~hit], clean_s[~hit])
+        assert torch.equal(a.view(torch.uint8)[wide(~hit)], clean_a.view(torch.uint8)[wide(~hit)])

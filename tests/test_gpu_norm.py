@@ -326,3 +326,40 @@ def test_products_of_row_and_weight_past_fp32(m, size, weight, eps):
     want = normed(h, w, eps)
     near16(y, want, BF16)
     near8(y8, s, want)
+
+
+def parts_of(m, d):
+    """CTAs of the gradient's row kernel: each sums every parts-th row, and their sums are added 64 at a time."""
+    words = d // 8
+    warps = (words + 63) // 64 if words > 512 else (words + 31) // 32
+    return min(m, 512, torch.cuda.get_device_properties(0).multi_processor_count * max(1, 32 // warps))
+
+
+@pytest.mark.parametrize("m,d", [(20001, 264), (9000, 2816), (40000, 64), (3000, 8200), (700, 16384)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_weight_gradients_of_many_rows_of_one_sign(m, d, dtype):
+    """dy x > 0: what long fp32 sums lose adds up.  A column takes ceil(m / parts) additions in a CTA, ceil(parts / 64) in a
+    thread of the second kernel and 64 there, each half a step of a sum that is the whole one at most, and a term its own
+    roundings (ROUNDED for 1 / sqrt, two products)."""
+    g = gen(m + d)
+    h, dy = (torch.rand(m, d, generator=g, device="cuda") + 0.5).to(dtype), (torch.rand(m, d, generator=g, device="cuda") + 0.5).to(dtype)
+    w = rand(g, dtype, d)
+    _, dw = call_grad(h, dy, None, w)
+    x = normed(h, None)
+    want = (dy.double() * x).sum(0)
+    parts = parts_of(m, d)
+    n = -(-m // parts) + -(-parts // 64) + 64
+    assert torch.all((dw.double() - want).abs() <= (n * 2.0 ** -24 + ROUNDED + 2 * 2.0 ** -24) * want)
+
+
+@pytest.mark.parametrize("m,d", [(7, 2816), (2500, 264), (40, 8200), (301, 16384)])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_the_normed_rows_in_deltas_place(m, d, dtype):
+    g = gen(91)
+    h, delta, w = rand(g, dtype, m, d, scale=2), rand(g, dtype, m, d), rand(g, dtype, d)
+    y, r, y8, s = torch.empty_like(h), torch.empty_like(h), torch.empty(m, d, dtype=E4M3, device="cuda"), torch.empty(m, (d + 127) // 128, device="cuda")
+    moe.check(moe.moe_rmsnorm(h, y, y8, s, delta=delta, h_out=r, weight=w))
+    y8b, sb = torch.empty_like(y8), torch.empty_like(s)
+    moe.check(moe.moe_rmsnorm(h, delta, y8b, sb, delta=delta, h_out=h, weight=w))   # y in delta's place, h_out in h's
+    assert torch.equal(delta, y) and torch.equal(h, r)
+    assert torch.equal(y8.view(torch.uint8), y8b.view(torch.uint8)) and torch.equal(s, sb)

@@ -52,7 +52,8 @@ __device__ GaveUp g_gave_up;
 constexpr int kMaxE = 1024;
 constexpr int kStageBytes = 32768;   // 128 features x 64 and up to 128 columns x 64, 16 bits
 constexpr int kHalf = 16384;
-constexpr int kEpiPitch16 = 48;      // bytes between staged rows of 32 bytes, as kEpiPitch
+constexpr int kEpiPitch = 80;        // bytes between staged rows of 64 and of 32 bytes: multiples of 16, and the
+constexpr int kEpiPitch16 = 48;      // 16-byte words of eight rows hit all 32 banks
 constexpr int kEpiWarps = 8;         // two for each quarter of the tensor-memory lanes, 32 columns in turn
 constexpr int kEpiBytes = 4 * 16 * kEpiPitch16;
 constexpr int kUWarps = 4;           // adapters: warps that stage u
@@ -342,6 +343,36 @@ __device__ __forceinline__ bool split_f16(const uint4& v, uint4& hi, uint4& lo) 
 }
 
 // ------------------------------------------------------------------ the persistent kernel
+
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 w;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+  return w;
+}
+
+// The stores of one warp: 32 columns of its accumulator lanes as fragments,
+// turned through the warp's own shared memory so that every lane stores 16
+// bytes.  All of a tensor's fragments are staged before the first is read
+// back: one warp barrier each way, and four independent loads and stores.
+
+// 32 features x 32 columns of 16-bit values: 64 contiguous bytes of a column.
+__device__ __forceinline__ void store_32x32(uint32_t buf, const float (&v)[2][16], int bf16, uint16_t* out, long long ld,
+                                            int cols, int feats, int lane) {
+  __syncwarp();   // earlier reads of this buffer are done
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    stmatrix4_trans(buf + j * 8 * kEpiPitch + (lane & 7) * kEpiPitch + (lane >> 3) * 16,
+                    pack16(v[0][4 * j], v[0][4 * j + 1], bf16), pack16(v[0][4 * j + 2], v[0][4 * j + 3], bf16),
+                    pack16(v[1][4 * j], v[1][4 * j + 1], bf16), pack16(v[1][4 * j + 2], v[1][4 * j + 3], bf16));
+  __syncwarp();
+  const int f = 8 * (lane & 3);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = 8 * j + (lane >> 2);
+    const uint4 w = lds128(buf + c * kEpiPitch + (lane & 3) * 16);
+    if (c < cols && f < feats) *reinterpret_cast<uint4*>(out + c * ld + f) = w;
+  }
+}
 
 // One feature a lane of 32 fp32 columns: each store of the warp is 128 contiguous bytes of a column.
 __device__ __forceinline__ void store_f32(const float (&v)[32], float* out, long long ld, int cols, int feats, int lane) {

@@ -179,9 +179,6 @@ __device__ __forceinline__ void take_registers() {
 // 384 threads are launched with 168 registers each: 128 x 40 + 256 x 232 are the same 64,512.
 constexpr int kFewRegs = 40, kManyRegs = 232;
 
-__device__ __forceinline__ float lo_f32(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_f32(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
 // 16 columns of this thread's accumulator lane: issued, and waited for.  The wait takes the registers, so that nothing uses them
 // before it.
 struct Cols16 {
@@ -200,12 +197,6 @@ struct Cols16 {
   }
   __device__ __forceinline__ uint64_t pair(int i) const { return static_cast<uint64_t>(r[2 * i + 1]) << 32 | r[2 * i]; }
 };
-
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 
 // GELU(g) u of two features.  The tanh form: g / (1 + 2^z) u, z = -2 log2(e) sqrt(2 / pi) (g + 0.044715 g^3); past fp32's range
 // 2^z is infinite and the quotient 0.

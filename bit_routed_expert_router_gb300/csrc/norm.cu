@@ -17,6 +17,7 @@
 #include <algorithm>
 
 #include "allow_smem.h"
+#include "f32x2.cuh"
 #include "ops8.h"
 #include "quant8.cuh"
 
@@ -27,32 +28,12 @@ namespace {
 // Eight values as four pairs: the arithmetic on them is two values an instruction (f32x2).
 struct Eight {
   uint64_t p[4];
-  __device__ __forceinline__ float lo(int i) const { return __uint_as_float(static_cast<uint32_t>(p[i])); }
-  __device__ __forceinline__ float hi(int i) const { return __uint_as_float(static_cast<uint32_t>(p[i] >> 32)); }
+  __device__ __forceinline__ float lo(int i) const { return lo_f32(p[i]); }
+  __device__ __forceinline__ float hi(int i) const { return hi_f32(p[i]); }
 };
 
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  return static_cast<uint64_t>(__float_as_uint(hi)) << 32 | __float_as_uint(lo);
-}
-__device__ __forceinline__ uint64_t both(float v) { return pair(v, v); }
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float sum2(uint64_t v) {
-  return __uint_as_float(static_cast<uint32_t>(v)) + __uint_as_float(static_cast<uint32_t>(v >> 32));
-}
+__device__ __forceinline__ uint64_t both(float v) { return pack_f32x2(v, v); }
+__device__ __forceinline__ float sum2(uint64_t v) { return lo_f32(v) + hi_f32(v); }
 
 template <bool kBf16>
 __device__ __forceinline__ Eight widen(uint4 v) {
@@ -60,7 +41,7 @@ __device__ __forceinline__ Eight widen(uint4 v) {
   Eight o;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    o.p[i] = kBf16 ? pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)) : pair(half_lo(w[i]), half_hi(w[i]));
+    o.p[i] = kBf16 ? pack_f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u)) : pack_f32x2(half_lo(w[i]), half_hi(w[i]));
   return o;
 }
 
@@ -153,10 +134,10 @@ __global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(
             d = widen<kBf16>(d16[q]);
           } else {
             const float4 a = d32[q][0], b = d32[q][1];
-            d = {{pair(a.x, a.y), pair(a.z, a.w), pair(b.x, b.y), pair(b.z, b.w)}};
+            d = {{pack_f32x2(a.x, a.y), pack_f32x2(a.z, a.w), pack_f32x2(b.x, b.y), pack_f32x2(b.z, b.w)}};
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[q][j].p[k] = add2(v[q][j].p[k], d.p[k]);
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = add_f32x2(v[q][j].p[k], d.p[k]);
           const uint4 stored = narrow<kBf16>(v[q][j]);
           *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.h_out) + r * p.ldo + c) = stored;
           v[q][j] = widen<kBf16>(stored);
@@ -172,7 +153,7 @@ __global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(
 #pragma unroll
     for (int j = 0; j < kV; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) two = fma2(v[q][j].p[k], v[q][j].p[k], two);
+      for (int k = 0; k < 4; ++k) fma_f32x2(two, v[q][j].p[k], v[q][j].p[k]);
     sum[q] = warp_sum(sum2(two));
   }
   if (warps > 1) {
@@ -196,10 +177,10 @@ __global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(
       if (p.y && in) {
         Eight y;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) y.p[k] = mul2(v[q][j].p[k], both(rstd));
+        for (int k = 0; k < 4; ++k) y.p[k] = mul_f32x2(v[q][j].p[k], both(rstd));
         if (p.weight)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) y.p[k] = mul2(y.p[k], f(k));
+          for (int k = 0; k < 4; ++k) y.p[k] = mul_f32x2(y.p[k], f(k));
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.ldy + c) = narrow<kBf16>(y);
       }
       if (p.y8) {
@@ -208,11 +189,11 @@ __global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(
           const float power = rstd < kLargest ? __uint_as_float(__float_as_uint(rstd) & 0x7F800000u) : rstd;
           rest = __uint_as_float((__float_as_uint(rstd) & 0x007FFFFFu) | 0x3F800000u);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], both(power));
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul_f32x2(v[q][j].p[k], both(power));
         }
         if (p.weight)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], f(k));
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul_f32x2(v[q][j].p[k], f(k));
         float top = 0.f;   // of the 16 lanes that hold a group; words past the row are 0
 #pragma unroll
         for (int k = 0; k < 4; ++k) top = max_abs(max_abs(top, v[q][j].lo(k)), v[q][j].hi(k));
@@ -226,12 +207,12 @@ __global__ void __launch_bounds__(kR == 2 ? 512 : 1024, kR == 2 ? 3 : 1) k_norm(
         } else {   // the least scale, or values that are not finite
           s = scale8(least);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul2(v[q][j].p[k], both(rest));
+          for (int k = 0; k < 4; ++k) v[q][j].p[k] = mul_f32x2(v[q][j].p[k], both(rest));
         }
         if (in) {
           Eight a;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) a.p[k] = mul2(v[q][j].p[k], both(s.inverse));
+          for (int k = 0; k < 4; ++k) a.p[k] = mul_f32x2(v[q][j].p[k], both(s.inverse));
           *reinterpret_cast<uint2*>(p.y8 + r * p.ldy8 + c) =
               make_uint2(to_e4m3x4(a.lo(0), a.hi(0), a.lo(1), a.hi(1)), to_e4m3x4(a.lo(2), a.hi(2), a.lo(3), a.hi(3)));
           if ((i & 15) == 0) p.scale[static_cast<long long>(r) * ((p.d + 127) / 128) + i / 16] = s.scale;
@@ -311,8 +292,8 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 2 : 1) k_norm_grad
       fetch(j);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        ss2 = fma2(a[j].p[k], a[j].p[k], ss2);
-        dot2 = fma2(mul2(b[j].p[k], w[j].p[k]), a[j].p[k], dot2);
+        fma_f32x2(ss2, a[j].p[k], a[j].p[k]);
+        fma_f32x2(dot2, mul_f32x2(b[j].p[k], w[j].p[k]), a[j].p[k]);
       }
     }
     if (!kAgain) load(r + kStages * gridDim.x, s);
@@ -332,8 +313,10 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 2 : 1) k_norm_grad
       if (kAgain) fetch(j);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        dw[j].p[k] = fma2(b[j].p[k], mul2(a[j].p[k], both(rstd)), dw[j].p[k]);
-        o[j].p[k] = add2(o[j].p[k], fma2(mul2(b[j].p[k], w[j].p[k]), both(rstd), mul2(a[j].p[k], both(-mean))));
+        fma_f32x2(dw[j].p[k], b[j].p[k], mul_f32x2(a[j].p[k], both(rstd)));
+        uint64_t own = mul_f32x2(a[j].p[k], both(-mean));
+        fma_f32x2(own, mul_f32x2(b[j].p[k], w[j].p[k]), both(rstd));
+        o[j].p[k] = add_f32x2(o[j].p[k], own);
       }
       if (i < n_words) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.dh) + r * p.lddh + 8 * i) = narrow<kBf16>(o[j]);
     }

@@ -1,5 +1,5 @@
-// tcgen05, TMA and cluster primitives of the 16-bit grouped products
-// (grouped_mm.cu): inline PTX only, one function per instruction form used.
+// tcgen05, TMA and cluster primitives of the grouped products and of the
+// layer for a few tokens: inline PTX only, one function per instruction form used.
 #pragma once
 
 #include <cuda.h>

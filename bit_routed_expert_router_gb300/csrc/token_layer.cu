@@ -49,12 +49,17 @@
 #include "gelu16.cuh"
 #include "grouped.h"
 #include "ops8.h"
+#include "tc16.cuh"
 #include "tensor_map.h"
 #include "waits.cuh"
 
 namespace moe {
 
 namespace {
+
+using tc16::cluster_rank;
+using tc16::cluster_sync;
+using tc16::elect_one;
 
 constexpr int kTeams = 8, kWarpsDown = 8;          // units that a CTA of the first kernel has at hand; warps of the second's
 // Warps of a team, which take a unit's chunks in turn where it has several.  Widening e4m3 is a chain of four instructions: with
@@ -287,12 +292,6 @@ __device__ __forceinline__ void chunk_products(float (&acc)[4], const uint8_t* s
   if (!kW8)   // tensor cores truncate: their sums go on for a chunk only
 #pragma unroll
     for (int v = 0; v < 4; ++v) acc[v] = fmaf(part[0][v] + part[1][v], x.unit(v & 1), acc[v]);
-}
-
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-  return one != 0;
 }
 
 // Once read, they leave L2 first: what else lies there (the kernels' code, the tokens) stays.
@@ -564,16 +563,6 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
 }
 
 // ------------------------------------------------------------------ down
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 
 __device__ __forceinline__ float ld_rank(const float* at, uint32_t rank) {
   uint32_t a;

@@ -260,8 +260,8 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 512 ? 2 : 1) k_norm_grad
 #pragma unroll
   for (int s = 0; s < kStages; ++s) load(blockIdx.x + s * gridDim.x, s);
   // A row's values stay in registers between its sums and its outputs where a thread has one word of them; two would spill
-  // or leave room for one CTA an SM, so they are read again, and the weight is kept as it is (2000 rows of 5632 22.9 -> 21.4 us,
-  // 700 of 16384 40.3 -> 24.0).
+  // (2000 rows of 5632 34.4 us, 700 of 16,384 39.9) or leave room for one CTA an SM (22.9 us, the former), so they are read
+  // again, and the weight is kept as it is (21.4 and 24.4; all bf16 with dres).
   constexpr bool kAgain = kV > 1;
   Eight dw[kV], w[kV];
   uint4 w_raw[kV];
@@ -402,7 +402,6 @@ bool launch_grad_rows(const NormGradParams& p, int nt, cudaStream_t s) {
 template <bool kBf16>
 bool launch_grad_of(const NormGradParams& p, cudaStream_t s) {
   const int words = p.d / 8, nt = (words + 31) / 32 * 32;
-  if (nt <= 384) return launch_grad_rows<kBf16, 1, 384>(p, nt, s);
   if (nt <= 512) return launch_grad_rows<kBf16, 1, 512>(p, nt, s);
   const int half = (words + 63) / 64 * 32;   // two words a thread
   return half <= 512 ? launch_grad_rows<kBf16, 2, 512>(p, half, s) : launch_grad_rows<kBf16, 2, 1024>(p, half, s);

@@ -1,12 +1,14 @@
 // A routed layer and its shared expert for up to 32 tokens, in two kernels:
 //
-//   up     a[i] = gate GELU(g) u,  [g, u] = Wgu[e] x[t]     for the tokens of each picked expert, rounded to the call's type
+//   up     a[i] = gate GELU(g) u,  [g, u] = Wgu[e] x[t]     for the tokens of each picked expert, in 16 bits
 //   down   y[t] = sum_e Wd[e] a[e, t]                       over the experts that t names, and the shared one
 //
 // a is rounded because it is an operand of 16-bit products and two bytes of the
-// workspace: the output's error is 1.4 roundings of its type instead of one.  (As two
-// digits, a high and a low operand with an exponent for each eight values in the same
-// two bytes, which is 2^-13: one token 27.4 -> 30.4 us, in 8 bits 21.6 -> 27.8.)  What
+// workspace.  With 16-bit weights it has their type: the output's error is 1.4 roundings
+// of it instead of one.  With e4m3 weights, which are exact in either type, it is fp16
+// whatever the call's: one rounding of bf16, and they are widened to it in a third of
+// the instructions.  (As two digits, a high and a low operand with an exponent for each
+// eight values in the same two bytes, which is 2^-13: one token 27.4 -> 30.4 us.)  What
 // leaves fp16's range takes another form in the same place, see Packed.
 //
 // The weights of the picked experts are read once and nothing else is of any
@@ -70,6 +72,8 @@ constexpr int kCol = 128, kColBytes = 16 * kCol;  // bytes of a weight row that 
 // Loads of a chunk: neighbours in their rows, which the memory likes (chunks of 256 bytes of a row 34 us for one token, 104 for
 // seven, when those of 512 took 29.8 and 87.9; in the second kernel 768 bytes instead of 512 27.6 -> 27.1 and 83.5 -> 83.1).
 constexpr int kColsUp = 4, kColsDown = 6;
+// The type of a: fp16, or bf16.
+constexpr bool half_a(bool bf16, bool w8) { return w8 || !bf16; }
 // Of these, loads whose token values a lane holds at a time (registers: two CTAs of the second kernel an SM).
 constexpr int kTokensUp = kColsUp;
 constexpr int tokens_down(bool w8) { return w8 ? 3 : kColsDown; }
@@ -527,7 +531,8 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
     for (int i = 0; i < 2; ++i) {
       const int col = 2 * (lane & 3) + i;
       const bool there = ok && col < rows;
-      if (kBf16 && !there) continue;
+      constexpr bool kHalf = half_a(kBf16, kW8);
+      if (!kHalf && !there) continue;
       float v = 0.f;
       if (there) {
         float gate = 1.f;
@@ -540,8 +545,8 @@ __global__ void __launch_bounds__(32 * kTeams * team_of(kW8), 1)
         }
         v = gate * (gelu16(acc[i], p.gelu) * acc[2 + i]);
       }
-      uint16_t word = kBf16 ? float_to_bf16_bits(v) : __half_as_ushort(__float2half_rn(v));
-      if (!kBf16) {
+      uint16_t word = kHalf ? __half_as_ushort(__float2half_rn(v)) : float_to_bf16_bits(v);
+      if (kHalf) {
         uint32_t top = __float_as_uint(v) & 0x7FFFFFFFu;
         uint32_t enough = __ballot_sync(0xFFFFFFFFu, top >= Packed::kSmall || !there);   // of a column: one is enough
         enough |= enough >> 16;
@@ -653,6 +658,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
   const auto add = [&](auto careful) {
     constexpr bool kCareful = decltype(careful)::value;
     constexpr int kTokenCols = tokens_down(kW8);
+    constexpr bool kHalf = half_a(kBf16, kW8);
     float acc[4] = {};
     for (; at.left > 0; ++it) {
       const int s = it % kStages, k0 = at.col * kColValues;
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
           tokens.load(a + done, k - done, lane);
         }
         if constexpr (kCareful) tokens.scale(lane);
-        chunk_products<kBf16, kW8, kTokenCols>(acc, stages + s * kStageBytes + c * kColBytes, tokens, k - done, sc, c, lane);
+        chunk_products<!kHalf, kW8, kTokenCols>(acc, stages + s * kStageBytes + c * kColBytes, tokens, k - done, sc, c, lane);
       }
       __syncwarp();
       load_next();
@@ -697,7 +703,7 @@ __global__ void __launch_bounds__(32 * kWarpsDown, 2) k_layer_down(const __grid_
   add(std::false_type{});
   // fp16: sums that are NaN may have met packed values; once more, with care (asked of every chunk's values beforehand, or with the
   // care in the same loop, that is 3 to 5 % of the layer)
-  if (!kBf16 && ok && __any_sync(0xFFFFFFFFu, odd)) {
+  if (half_a(kBf16, kW8) && ok && __any_sync(0xFFFFFFFFu, odd)) {
     at = next = start;
     __syncwarp();
     for (int i = lane; i < p.t * 16; i += 32) own[i] = 0.f;

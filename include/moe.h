@@ -602,10 +602,11 @@ typedef struct {
  *   workspace   at least 2 t (top_k f + f_shared) bytes, 16-byte aligned, contents
  *               undefined before and after; calls that may run at the same time need
  *               one each
- * Sums are fp32; gates * GELU(g) u is rounded to dtype once before the down
- * product, y once at the end.  (fp16: eight features of a token whose largest
- * value lies outside of 2^-13 .. 65504 are held to 2^-13 of it instead, whatever
- * its size, for a second reading of the weights of that part.)  Non-finite weights of an expert reach the tokens that
+ * Sums are fp32; gates * GELU(g) u is rounded once before the down product, to
+ * dtype, or with e4m3 weights to fp16, and y once at the end.  (fp16: eight
+ * features of a token whose largest value lies outside of 2^-13 .. 65504 are held to
+ * 2^-13 of it instead, whatever its size, for a second reading of the weights of
+ * that part.)  Non-finite weights of an expert reach the tokens that
  * name it only.  y may be x; nothing else may overlap.  moe_grouped_sync reports a
  * bounded wait that ran out. */
 moe_status moe_token_layer(int dtype, int gelu_variant, const void *x, int64_t ldx, int t, const int32_t *ids,

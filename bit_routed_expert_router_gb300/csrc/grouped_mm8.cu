@@ -24,11 +24,14 @@
 // expert's gate/up, 4096 rows: 144 and 90 us).
 //
 // What bounds it: few rows an expert, HBM (gated, 33 tokens of 128 experts, 2816 to
-// 704 features: 67 us, 6.66 TB/s).  Many, tensor memory: a block's MMAs take 540
-// cycles, its reads and additions 340, both at once 1,040 (shared expert's gate/up,
-// 4096 rows, 2816 to 5632: 59 us, 2.19 PFLOP/s; gated, 4096 tokens: 169 us, 1.54).
-// Pairs of CTAs on 256 rows, which load a third less, take 58.9 us and, with ragged
-// groups, 209.
+// 704 features: 67 us, 6.66 TB/s).  Many (shared expert's gate/up, 4096 rows, 2816 to
+// 5632: 60 us, 2.17 PFLOP/s), the blocks: of 1,036 cycles an adding warp waits 220 for
+// the accumulator, takes 107 for the factors, 443 to read and add, 146 for its share of
+// a tile's end (3,200: stores) and 120 for the loop and what the two sides cost each
+// other; alone the MMAs take 540, the reads 340, without the adding a block takes 907,
+// without the loads 755.  Gated, 4096 tokens: 172 us, 1.51 PFLOP/s, in bursts; in a long
+// row of calls 188 at the 1.78 GHz that the power cap leaves.  Pairs of CTAs on 256
+// rows, which load a third less, take 58.9 us and, with ragged groups, 209.
 #include <algorithm>
 #include <cstddef>
 

@@ -10,9 +10,9 @@
 // value is read once, a row stays in registers between its sum and its outputs,
 // eight values (16 bytes) a thread.
 //
-// 4096 rows of 2816, delta in 16 bits, out in 8 bits: 15.0 us, 5.4 TB/s (80 % of a
-// copy's rate).  Their gradient with dres: 19.6 us, of which 16.0 are the rows'
-// (5.8 TB/s) and the rest the sum of the weight gradient's parts after them.  One
+// 4096 rows of 2816, delta in 16 bits, out in 8 bits: 15.3 us, 5.3 TB/s (78 % of a
+// copy's rate).  Their gradient with dres: 19.7 us, of which 16.0 are the rows'
+// (5.7 TB/s) and the rest the sum of the weight gradient's parts after them.  One
 // row: 1.7 us in a graph, a launch.
 #include <algorithm>
 

@@ -38,12 +38,12 @@
 // weights while others still run.
 //
 // 128 experts of 2816 x 704, 8 of them a token, and a shared one of 2816 x 2816: 7
-// tokens 83.1 us in a graph, HBM; one token 27.1 us (143 MB, 5.3 TB/s), in 8 bits 21.9
-// (71 MB, 3.3 TB/s).  What nothing hides there: 2.3 us from the start to the first
-// weights, 2.7 us from one kernel's last sums to the other's first weights (with
+// tokens 85 us in a graph, HBM; one token 27.4 us (143 MB, 5.2 TB/s), in 8 bits 20.4
+// (71 MB, 3.5 TB/s).  What nothing hides there: 2.3 us from the start to the first
+// weights, 3 us from one kernel's last sums to the other's first weights (with
 // stages of 64 KB, which fit beside the first kernel's, and all of the SM's shared
 // memory set as such the second starts early, but takes HBM from the first: 28.5 us
-// at 27.9), 1.5 us of tails; in 8 bits the widening.
+// at 27.9), 1 us of tails; in 8 bits the first kernel's widening.
 #include <algorithm>
 #include <type_traits>
 

@@ -547,6 +547,8 @@ moe_status moe_rmsnorm(int dtype, const void *h, int64_t ldh, const void *delta,
  * the gradient dy of y
  *   dh = dres + (dy weight - x mean(dy weight x)) / sqrt(mean(h^2) + eps)
  *   dweight = sum over the rows of dy x         (fp32 [d], 16-byte aligned, or NULL)
+ * Sums and products are fp32's: rows whose h^2 or dy weight h leave its range get
+ * gradients that are not finite, or without the mean's part.
  * dres is the gradient that reaches r past the norm, or NULL; dh is the gradient
  * of h and of delta.  dh may be h, dy or dres.  All rows are of dtype.
  * workspace (with dweight): at least 4 d min(m, 512) bytes, 16-byte aligned,
@@ -564,7 +566,8 @@ moe_status moe_rmsnorm_grad(int dtype, const void *h, int64_t ldh, const void *d
  * to 65536, k a multiple of 16 from 16 to 65536, weights contiguous and 16-byte
  * aligned; y [m][ldy] of out_dtype (MOE_BF16, MOE_F16, MOE_F32).  Rows before
  * offsets[0] and from offsets[n_experts] on are not written.  Each block's products
- * are summed by themselves, the blocks in fp32 with rounding.  No output may overlap
+ * are summed by themselves, the blocks in fp32 with rounding; the product of a
+ * block's two scales is taken first.  No output may overlap
  * an input.  moe_grouped_sync reports a bounded wait that ran out. */
 moe_status moe_grouped_mm8(const void *x, int64_t ldx, const float *sx, int m, const int32_t *offsets, int n_experts,
                            const void *w, const float *sw, int n, int k, void *y, int64_t ldy, int out_dtype,
